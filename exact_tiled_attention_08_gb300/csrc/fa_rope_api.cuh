@@ -1,0 +1,211 @@
+// Host side of the head norm and rotation entry points (declared in fa.h;
+// included by fa_ops.cu; uses the checks of fa_lib.cu).
+#pragma once
+
+#include <algorithm>
+
+namespace {
+
+constexpr int kRopeBwdCtas = 152 * 4;  // CTAs of the backward, each with a row of weight gradient sums
+
+fa_status check_rows(const fa_rows& r) {
+  if (!aligned16(r.ptr) || r.batch % 8 || r.token % 8 || r.head % 8) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+// written rows: no two of them may share memory
+bool rows_disjoint(const fa_rows& r, int B, int N, int heads, int d) {
+  struct Dim {
+    long long stride, size;
+  } dim[3] = {{r.batch, B}, {r.token, N}, {r.head, heads}};
+  std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  long long extent = d;
+  for (const Dim& x : dim) {
+    if (x.size == 1) continue;
+    if (x.stride < extent) return false;
+    extent = x.stride * (x.size - 1) + extent;
+  }
+  return true;
+}
+
+fa::RopeRows rope_rows(const fa_rows* r) {
+  fa::RopeRows x{};
+  if (r && r->ptr) x = {static_cast<const __nv_bfloat16*>(r->ptr), r->batch, r->token, r->head};
+  return x;
+}
+
+bool present(const fa_rows* r) { return r && r->ptr; }
+
+// checks that the forward and the backward share
+fa_status check_rope(const double* inv_freq, int B, int N, int H, int Hkv, int d, int rotary_dim, int norm, float eps,
+                     float factor, int interleaved) {
+  if (H < 1 || Hkv < 1) return FA_ERR_INVALID_ARG;
+  fa_status st = check_shape(B, H, N, d);
+  if (st == FA_OK) st = check_shape(B, Hkv, N, d);
+  if (st != FA_OK) return st;
+  if ((long long)H + 2LL * Hkv > 0x3fffffffLL || (long long)B * N > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > d) return FA_ERR_INVALID_ARG;
+  if (rotary_dim % 16) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim > 0 && !inv_freq) return FA_ERR_INVALID_ARG;
+  if ((norm != 0 && norm != 1) || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(factor) || (norm && (!std::isfinite(eps) || eps < 0.f))) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (!p) continue;
+    const fa_status st = check_device_ptrs({p});
+    if (st != FA_OK) return st;
+  }
+  return FA_OK;
+}
+
+// work units of a launch: groups of tokens (one pass of a CTA's warps) times
+// groups of heads
+void rope_units(fa::RopeParams& p, int d) {
+  const long long per_cta = (fa::kRopeThreads / 32) * (32 / (d / 8));
+  const long long groups = (p.tokens + per_cta - 1) / per_cta;
+  const int heads = p.H + 2 * p.Hkv;
+  p.head_step = 8;
+  p.head_groups = (heads + p.head_step - 1) / p.head_step;
+  p.units = groups * p.head_groups;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const float* q_weight,
+                      const float* k_weight, const double* inv_freq, const int* positions, const int* starts,
+                      void* q_out, void* k_out, void* v_out, int B, int N, int H, int Hkv, int C, int d,
+                      int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream) {
+  if (present(q) != (q_out != nullptr) || present(k) != (k_out != nullptr) || present(v) != (v_out != nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (!q_out && !k_out && !v_out) return FA_ERR_INVALID_ARG;
+  fa_status st = check_rope(inv_freq, B, N, H, Hkv, d, rotary_dim, norm, eps, factor, interleaved);
+  if (st != FA_OK) return st;
+  if (C < N) return FA_ERR_INVALID_ARG;
+  for (const fa_rows* r : {q, k, v})
+    if (present(r) && (st = check_rows(*r)) != FA_OK) return st;
+  if (!all_aligned16({q_weight, k_weight, inv_freq, positions, starts, q_out, k_out, v_out})) return FA_ERR_MISALIGNED;
+  if ((st = check_device_ptrs_given({q ? q->ptr : nullptr, k ? k->ptr : nullptr, v ? v->ptr : nullptr, q_weight,
+                                     k_weight, inv_freq, positions, starts, q_out, k_out, v_out})) != FA_OK)
+    return st;
+  fa::RopeParams p{};
+  p.q = rope_rows(q);
+  p.k = rope_rows(k);
+  p.v = rope_rows(v);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.starts = starts;
+  p.N = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.C = C;
+  p.rot = rotary_dim;
+  p.tokens = (long long)B * N;
+  p.eps = eps;
+  p.factor = factor;
+  p.norm = norm;
+  rope_units(p, d);
+  const unsigned grid = (unsigned)std::min<long long>(p.units, 152LL * 8);
+  if (d == 128) {
+    if (interleaved)
+      fa::fa_rope_fwd_kernel<128, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    else
+      fa::fa_rope_fwd_kernel<128, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  } else {
+    if (interleaved)
+      fa::fa_rope_fwd_kernel<64, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    else
+      fa::fa_rope_fwd_kernel<64, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_rope_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
+  if (check_shape(B, H, N, d) != FA_OK || check_shape(B, Hkv, N, d) != FA_OK) return 0;
+  return (size_t)kRopeBwdCtas * 2 * d * sizeof(float);
+}
+
+fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight, const float* k_weight,
+                      const double* inv_freq, const int* positions, const void* dq_out, const void* dk_out,
+                      const void* dv_out, const fa_rows* dq, const fa_rows* dk, const fa_rows* dv, float* dq_weight,
+                      float* dk_weight, void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d,
+                      int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream) {
+  if (present(dq) != (dq_out != nullptr) || present(dk) != (dk_out != nullptr) || present(dv) != (dv_out != nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (!dq_out && !dk_out && !dv_out) return FA_ERR_INVALID_ARG;
+  fa_status st = check_rope(inv_freq, B, N, H, Hkv, d, rotary_dim, norm, eps, factor, interleaved);
+  if (st != FA_OK) return st;
+  const bool need_q = norm && dq_out, need_k = norm && dk_out;
+  if ((need_q && !present(q)) || (need_k && !present(k))) return FA_ERR_INVALID_ARG;
+  // a weight has a gradient only where the norm runs on its rows
+  if ((dq_weight && !need_q) || (dk_weight && !need_k)) return FA_ERR_INVALID_ARG;
+  const bool weights = dq_weight || dk_weight;
+  if (weights && (!workspace || ws_bytes < fa_rope_bwd_workspace_bytes(B, H, Hkv, N, d))) return FA_ERR_INVALID_ARG;
+  if ((need_q && (st = check_rows(*q)) != FA_OK) || (need_k && (st = check_rows(*k)) != FA_OK)) return st;
+  for (const fa_rows* r : {dq, dk, dv}) {
+    if (!present(r)) continue;
+    if ((st = check_rows(*r)) != FA_OK) return st;
+    if (!rows_disjoint(*r, B, N, r == dq ? H : Hkv, d)) return FA_ERR_INVALID_ARG;
+  }
+  if (!all_aligned16({q_weight, k_weight, inv_freq, positions, dq_out, dk_out, dv_out, dq_weight, dk_weight,
+                      weights ? workspace : nullptr}))
+    return FA_ERR_MISALIGNED;
+  if ((st = check_device_ptrs_given({need_q ? q->ptr : nullptr, need_k ? k->ptr : nullptr, q_weight, k_weight,
+                                     inv_freq, positions, dq_out, dk_out, dv_out, dq ? dq->ptr : nullptr,
+                                     dk ? dk->ptr : nullptr, dv ? dv->ptr : nullptr, dq_weight, dk_weight,
+                                     weights ? workspace : nullptr})) != FA_OK)
+    return st;
+  fa::RopeParams p{};
+  if (need_q) p.q = rope_rows(q);
+  if (need_k) p.k = rope_rows(k);
+  p.dq = rope_rows(dq);
+  p.dk = rope_rows(dk);
+  p.dv = rope_rows(dv);
+  p.q_out = static_cast<__nv_bfloat16*>(const_cast<void*>(dq_out));
+  p.k_out = static_cast<__nv_bfloat16*>(const_cast<void*>(dk_out));
+  p.v_out = static_cast<__nv_bfloat16*>(const_cast<void*>(dv_out));
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.partials = weights ? static_cast<float*>(workspace) : nullptr;
+  p.N = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.C = N;
+  p.rot = rotary_dim;
+  p.tokens = (long long)B * N;
+  p.eps = eps;
+  p.factor = factor;
+  p.norm = norm;
+  rope_units(p, d);
+  const unsigned grid = (unsigned)std::min<long long>(p.units, kRopeBwdCtas);
+  if (d == 128) {
+    if (interleaved)
+      fa::fa_rope_bwd_kernel<128, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    else
+      fa::fa_rope_bwd_kernel<128, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  } else {
+    if (interleaved)
+      fa::fa_rope_bwd_kernel<64, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    else
+      fa::fa_rope_bwd_kernel<64, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  }
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (weights) {
+    fa::fa_rope_dw_kernel<<<2 * d / 8, 256, 0, stream>>>(p.partials, (int)grid, d, dq_weight, dk_weight);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -33,6 +34,13 @@ _STATUS_NAMES = {
     FA_ERR_CUDA: "FA_ERR_CUDA",
     FA_ERR_TIMEOUT: "FA_ERR_TIMEOUT",
 }
+
+
+class FaRows(ctypes.Structure):
+    """``fa_rows`` of the C ABI: a token-major tensor's address and strides in elements."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong),
+                ("head", ctypes.c_longlong)]
 
 
 class FaError(RuntimeError):
@@ -70,6 +78,25 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fa_bwd_deterministic.restype = i
     lib.fa_bwd_static_scratch.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp]
     lib.fa_bwd_static_scratch.restype = i
+    lib.fa_cross_fwd_workspace_bytes.argtypes = [i] * 6
+    lib.fa_cross_fwd_workspace_bytes.restype = sz
+    lib.fa_cross_fwd.argtypes = [vp] * 7 + [sz] + [i] * 6 + [f, vp]
+    lib.fa_cross_fwd.restype = i
+    lib.fa_cross_bwd_workspace_bytes.argtypes = [i] * 6
+    lib.fa_cross_bwd_workspace_bytes.restype = sz
+    lib.fa_cross_bwd.argtypes = [vp] * 11 + [sz] + [i] * 6 + [f, vp]
+    lib.fa_cross_bwd.restype = i
+    lib.fa_tree_fwd_workspace_bytes.argtypes = [i] * 6
+    lib.fa_tree_fwd_workspace_bytes.restype = sz
+    lib.fa_tree_fwd.argtypes = [vp] * 9 + [sz] + [i] * 6 + [f, vp]
+    lib.fa_tree_fwd.restype = i
+    rows = ctypes.POINTER(FaRows)
+    lib.fa_rope_fwd.argtypes = [rows] * 3 + [vp] * 8 + [i] * 8 + [f, f, i, vp]
+    lib.fa_rope_fwd.restype = i
+    lib.fa_rope_bwd_workspace_bytes.argtypes = [i] * 5
+    lib.fa_rope_bwd_workspace_bytes.restype = sz
+    lib.fa_rope_bwd.argtypes = [rows] * 2 + [vp] * 7 + [rows] * 3 + [vp] * 3 + [sz] + [i] * 7 + [f, f, i, vp]
+    lib.fa_rope_bwd.restype = i
     lib.fa_check_device_status.argtypes = [vp]
     lib.fa_check_device_status.restype = i
     lib.fa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
@@ -283,6 +310,243 @@ def fa_bwd_static_scratch(q, k, v, o, dout, lse, dq, dk, dv, scale: float, causa
 
 
 # ---------------------------------------------------------------------------
+# cross attention, attention over a cache, head norm and rotation
+# ---------------------------------------------------------------------------
+def _given(t, name: str, dtype, shape, device) -> int:
+    """Address of an optional tensor (0 for None), checked."""
+    if t is None:
+        return 0
+    _check(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _workspace(workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _cross_shapes(q, k, v):
+    B, H, Nq, d = _shape4(q, "q")
+    _, Hkv, Nk, _ = _shape4(k, "k")
+    dev = q.device
+    _check(q, "q", torch.bfloat16, (B, H, Nq, d), dev)
+    _check(k, "k", torch.bfloat16, (B, Hkv, Nk, d), dev)
+    _check(v, "v", torch.bfloat16, (B, Hkv, Nk, d), dev)
+    return B, H, Hkv, Nq, Nk, d, dev
+
+
+def fa_cross_fwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return int(load_library().fa_cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d))
+
+
+def fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale: float, stream=None) -> None:
+    """Attention of q [B,H,Nq,d] to k, v [B,Hkv,Nk,d] of another length; key_lens
+    int32 [B] (or None: all Nk); o like q, lse [B,H,Nq] fp32."""
+    B, H, Hkv, Nq, Nk, d, dev = _cross_shapes(q, k, v)
+    _check(o, "o", torch.bfloat16, (B, H, Nq, d), dev)
+    _check(lse, "lse", torch.float32, (B, H, Nq), dev)
+    lens = _given(key_lens, "key_lens", torch.int32, (B,), dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    with _on_device(dev):
+        st = load_library().fa_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(), lse.data_ptr(),
+                                         ws, ws_bytes, B, H, Hkv, Nq, Nk, d, float(scale),
+                                         _stream_handle(stream, dev))
+    _raise(st, "fa_cross_fwd")
+
+
+def fa_cross_bwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return int(load_library().fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d))
+
+
+def fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale: float, stream=None) -> None:
+    """dQ, dK, dV of fa_cross_fwd by recomputation; dk, dv like k, v."""
+    B, H, Hkv, Nq, Nk, d, dev = _cross_shapes(q, k, v)
+    for t, name in ((o, "o"), (dout, "dout"), (dq, "dq")):
+        _check(t, name, torch.bfloat16, (B, H, Nq, d), dev)
+    for t, name in ((dk, "dk"), (dv, "dv")):
+        _check(t, name, torch.bfloat16, (B, Hkv, Nk, d), dev)
+    _check(lse, "lse", torch.float32, (B, H, Nq), dev)
+    lens = _given(key_lens, "key_lens", torch.int32, (B,), dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    with _on_device(dev):
+        st = load_library().fa_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(),
+                                         dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                         ws, ws_bytes, B, H, Hkv, Nq, Nk, d, float(scale),
+                                         _stream_handle(stream, dev))
+    _raise(st, "fa_cross_bwd")
+
+
+def fa_tree_fwd_workspace_bytes(B: int, H: int, Hkv: int, T: int, C: int, d: int) -> int:
+    return int(load_library().fa_tree_fwd_workspace_bytes(B, H, Hkv, T, C, d))
+
+
+def fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace, scale: float,
+                stream=None) -> None:
+    """Attention of T new tokens q [B,H,T,d] over a cache [B,Hkv,C,d] that holds
+    cache_lens[b] tokens and then the new ones.  draft_lens int32 [B] (or
+    None: T); draft_masks int64 [B,T], bit t of word n: token n sees token t
+    (or None: each sees the ones before it and itself; see tree_masks)."""
+    B, H, Hkv, T, C, d, dev = _cross_shapes(q, k_cache, v_cache)
+    _check(o, "o", torch.bfloat16, (B, H, T, d), dev)
+    _check(lse, "lse", torch.float32, (B, H, T), dev)
+    _check(cache_lens, "cache_lens", torch.int32, (B,), dev)
+    drafts = _given(draft_lens, "draft_lens", torch.int32, (B,), dev)
+    masks = _given(draft_masks, "draft_masks", torch.int64, (B, T), dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    with _on_device(dev):
+        st = load_library().fa_tree_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cache_lens.data_ptr(),
+                                        drafts, masks, o.data_ptr(), lse.data_ptr(), ws, ws_bytes, B, H, Hkv, T, C, d,
+                                        float(scale), _stream_handle(stream, dev))
+    _raise(st, "fa_tree_fwd")
+
+
+def tree_masks(parents: torch.Tensor) -> torch.Tensor:
+    """draft_masks of fa_tree_fwd for trees given by parents int [B,T]: parents[b,n]
+    is the token that n was drafted after (always an earlier one), or -1 for
+    one that follows the request's own tokens.  On the tensor's device."""
+    if parents.dim() != 2 or parents.dtype not in (torch.int32, torch.int64):
+        raise ValueError("parents must be int32 or int64 [B, T]")
+    B, T = parents.shape
+    if T > 64:
+        raise ValueError("at most 64 drafted tokens have masks")
+    place = torch.arange(T, device=parents.device)
+    if bool(((parents < -1) | (parents >= place)).any()):
+        raise ValueError("a parent must be -1 or an earlier token")
+    words = torch.zeros((B, T), dtype=torch.int64, device=parents.device)
+    for n in range(T):
+        up = torch.gather(words, 1, parents[:, n:n + 1].long().clamp(min=0))[:, 0]
+        words[:, n] = torch.where(parents[:, n] >= 0, up, 0) | (1 << n if n < 63 else -(1 << 63))
+    return words
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, scale: float = 1.0,
+                     trained_len: int = 0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(inv_freq, factor) of fa_rope_fwd: frequencies base^(-2i/rotary_dim) in fp64, and
+    the factor of the rotated values.  For contexts ``scale`` times the trained one:
+    ``"linear"`` divides every frequency by scale; ``"base"`` raises the base to
+    base * scale^(rotary_dim / (rotary_dim - 2)), which slows the lowest frequency
+    by scale and leaves the highest; ``"parts"`` keeps frequencies that turn at
+    least ``fast`` times over trained_len positions, divides by scale those that
+    turn at most ``slow`` times, blends between, with factor 0.1 ln(scale) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not base > 1.0 or not scale >= 1.0:
+        raise ValueError("base must be above 1 and scale at least 1")
+    factor = 1.0
+    if scaling == "base":
+        if rotary_dim == 2:
+            raise ValueError("scaling by the base needs rotary_dim above 2")
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    if scaling == "linear":
+        freq = freq / scale
+    elif scaling == "parts":
+        if trained_len < 1 or not fast > slow > 0:
+            raise ValueError("scaling by parts needs trained_len and fast > slow > 0")
+        turns = trained_len * freq / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1.0 - keep) / scale)
+        factor = 0.1 * math.log(scale) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(device), factor
+
+
+def _rows(t, name: str, shape, device):
+    """``fa_rows`` of a [B, N, heads, d] tensor whose d values lie next to each other (None: no such rows)."""
+    if t is None:
+        return None
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 and shape[3] != 1:
+        raise ValueError(f"{name} must have its last dimension contiguous")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    # (the stride of a dimension of one is any number: it is never used)
+    return FaRows(t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+
+
+def _rope_sizes(q, k, v, names):
+    """B, N, H, Hkv, d and device of the token-major tensors that are given."""
+    first = next((t for t in (q, k, v) if t is not None), None)
+    if first is None:
+        raise ValueError(f"one of {', '.join(names)} must be given")
+    for t, name in zip((q, k, v), names):
+        if t is not None and t.dim() != 4:
+            raise ValueError(f"{name} must be [B, N, heads, d], got {tuple(t.shape)}")
+    B, N, _, d = first.shape
+    kv = k if k is not None else v
+    return B, N, (q.shape[2] if q is not None else 1), (kv.shape[2] if kv is not None else 1), d, first.device
+
+
+def fa_rope_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, starts, q_out, k_out, v_out, *, eps=None,
+                factor: float = 1.0, interleaved: bool = False, stream=None) -> None:
+    """RMS norm of each head (with eps; None: no norm) and rotation of the first
+    2 * len(inv_freq) values by position: q [B,N,H,d], k and v [B,N,Hkv,d] (any
+    strides with d contiguous) into q_out [B,H,N,d] and rows starts[b].. of
+    k_out, v_out [B,Hkv,C,d].  q, k or v may be None with its output; weights
+    fp32 [d] or None; inv_freq fp64 or None (no rotation); positions int32
+    [B,N] or None (starts[b] + n); starts int32 [B] or None (0)."""
+    B, N, H, Hkv, d, dev = _rope_sizes(q, k, v, ("q", "k", "v"))
+    rq, rk, rv = _rows(q, "q", (B, N, H, d), dev), _rows(k, "k", (B, N, Hkv, d), dev), _rows(v, "v", (B, N, Hkv, d), dev)
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights need eps: without it there is no norm")
+    cache = k_out if k_out is not None else v_out
+    C = _shape4(cache, "k_out")[2] if cache is not None else N
+    args = (_given(q_weight, "q_weight", torch.float32, (d,), dev), _given(k_weight, "k_weight", torch.float32, (d,), dev),
+            0 if inv_freq is None else _given(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev),
+            _given(positions, "positions", torch.int32, (B, N), dev), _given(starts, "starts", torch.int32, (B,), dev),
+            _given(q_out, "q_out", torch.bfloat16, (B, H, N, d), dev),
+            _given(k_out, "k_out", torch.bfloat16, (B, Hkv, C, d), dev),
+            _given(v_out, "v_out", torch.bfloat16, (B, Hkv, C, d), dev))
+    with _on_device(dev):
+        st = load_library().fa_rope_fwd(rq, rk, rv, *args, B, N, H, Hkv, C, d,
+                                        0 if inv_freq is None else 2 * inv_freq.numel(), int(eps is not None),
+                                        float(eps or 0.0), float(factor), int(bool(interleaved)),
+                                        _stream_handle(stream, dev))
+    _raise(st, "fa_rope_fwd")
+
+
+def fa_rope_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int) -> int:
+    return int(load_library().fa_rope_bwd_workspace_bytes(B, H, Hkv, N, d))
+
+
+def fa_rope_bwd(q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, dv_out, dq, dk, dv, dq_weight,
+                dk_weight, workspace=None, *, eps=None, factor: float = 1.0, interleaved: bool = False,
+                stream=None) -> None:
+    """Gradients of fa_rope_fwd (without starts): dq_out [B,H,N,d], dk_out and dv_out
+    [B,Hkv,N,d] into token-major dq, dk, dv like q, k, v, and fp32 dq_weight,
+    dk_weight [d] (or None).  q and k are read only with eps; any of the three
+    gradients may be None with its output; workspace is needed for weights."""
+    B, N, H, Hkv, d, dev = _rope_sizes(dq, dk, dv, ("dq", "dk", "dv"))
+    outs = (_rows(dq, "dq", (B, N, H, d), dev), _rows(dk, "dk", (B, N, Hkv, d), dev),
+            _rows(dv, "dv", (B, N, Hkv, d), dev))
+    if eps is None and any(t is not None for t in (q_weight, k_weight, dq_weight, dk_weight)):
+        raise ValueError("weights need eps: without it there is no norm")
+    rq = _rows(q, "q", (B, N, H, d), dev) if eps is not None and dq is not None else None
+    rk = _rows(k, "k", (B, N, Hkv, d), dev) if eps is not None and dk is not None else None
+    args = (_given(q_weight, "q_weight", torch.float32, (d,), dev), _given(k_weight, "k_weight", torch.float32, (d,), dev),
+            0 if inv_freq is None else _given(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev),
+            _given(positions, "positions", torch.int32, (B, N), dev),
+            _given(dq_out, "dq_out", torch.bfloat16, (B, H, N, d), dev),
+            _given(dk_out, "dk_out", torch.bfloat16, (B, Hkv, N, d), dev),
+            _given(dv_out, "dv_out", torch.bfloat16, (B, Hkv, N, d), dev))
+    grads = (_given(dq_weight, "dq_weight", torch.float32, (d,), dev),
+             _given(dk_weight, "dk_weight", torch.float32, (d,), dev))
+    ws, ws_bytes = (0, 0) if workspace is None else _workspace(workspace, dev)
+    with _on_device(dev):
+        st = load_library().fa_rope_bwd(rq, rk, *args, *outs, *grads, ws, ws_bytes, B, N, H, Hkv, d,
+                                        0 if inv_freq is None else 2 * inv_freq.numel(), int(eps is not None),
+                                        float(eps or 0.0), float(factor), int(bool(interleaved)),
+                                        _stream_handle(stream, dev))
+    _raise(st, "fa_rope_bwd")
+
+
+# ---------------------------------------------------------------------------
 # conveniences that allocate the outputs with torch and call the entry points.
 # With check_status (the default) they wait for the work and raise FaError if
 # a kernel reported a timeout, so what they return is known to be valid; pass
@@ -329,3 +593,45 @@ def attention_backward(q, k, v, o, dout, lse, scale: float, causal: bool = False
     if check_status:
         _checked(stream, q.device, "attention_backward")
     return dq, dk, dv
+
+
+def cross_attention_forward(q, k, v, scale: float, key_lens=None, workspace=None, stream=None,
+                            check_status: bool = True):
+    B, H, Nq, d = _shape4(q, "q")
+    _, Hkv, Nk, _ = _shape4(k, "k")
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(fa_cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
+    fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale, stream)
+    if check_status:
+        _checked(stream, q.device, "cross_attention_forward")
+    return o, lse
+
+
+def cross_attention_backward(q, k, v, o, dout, lse, scale: float, key_lens=None, workspace=None, stream=None,
+                             check_status: bool = True):
+    B, H, Nq, d = _shape4(q, "q")
+    _, Hkv, Nk, _ = _shape4(k, "k")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if workspace is None:
+        workspace = torch.empty(fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
+    fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale, stream)
+    if check_status:
+        _checked(stream, q.device, "cross_attention_backward")
+    return dq, dk, dv
+
+
+def tree_attention_forward(q, k_cache, v_cache, cache_lens, scale: float, draft_lens=None, draft_masks=None,
+                           workspace=None, stream=None, check_status: bool = True):
+    """Rows of tokens that a request does not have come out as O = 0, LSE = -inf."""
+    B, H, T, d = _shape4(q, "q")
+    _, Hkv, C, _ = _shape4(k_cache, "k_cache")
+    o = torch.zeros_like(q)
+    lse = torch.full((B, H, T), -math.inf, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(fa_tree_fwd_workspace_bytes(B, H, Hkv, T, C, d), dtype=torch.uint8, device=q.device)
+    fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace, scale, stream)
+    if check_status:
+        _checked(stream, q.device, "tree_attention_forward")
+    return o, lse

@@ -226,6 +226,145 @@ fa_status fa_bwd_static_scratch(const void* q, const void* k, const void* v, con
                                 float scale, int causal, cudaStream_t stream);
 
 /*
+ * Cross attention: queries [B][H][Nq][d] over keys and values [B][Hkv][Nk][d]
+ * of another length (an encoder's states), O = softmax(scale Q K^T) V.
+ * Query head h uses key/value head h / (H / Hkv); H is a multiple of Hkv.
+ * There is no causal mask.
+ *
+ *   q        in:  bf16 [B][H][Nq][d]
+ *   k, v     in:  bf16 [B][Hkv][Nk][d]
+ *   key_lens in:  int32 [B] device array: request b has keys 0 .. key_lens[b]-1
+ *                 (values outside [0, Nk] are taken as 0 and Nk), or null: Nk
+ *                 for every request.  What K and V hold behind a request's
+ *                 keys is never used, NaN and infinities included.
+ *   o        out: bf16 [B][H][Nq][d];  lse out: fp32 [B][H][Nq].
+ *                 A row without keys (or whose scores are all -inf) gives
+ *                 O = 0 and LSE = -inf.
+ *   workspace     device scratch of ws_bytes >= fa_cross_fwd_workspace_bytes(),
+ *                 16-byte aligned, contents on entry ignored; calls that may
+ *                 overlap on the GPU need one each.
+ * Limits: those of fa_fwd with B * Hkv for B * H and, for N, both
+ * (H / Hkv) * Nq and Nk.  The results are the same from run to run.
+ */
+size_t fa_cross_fwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
+fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* key_lens, void* o, float* lse,
+                       void* workspace, size_t ws_bytes, int B, int H, int Hkv, int Nq, int Nk, int d, float scale,
+                       cudaStream_t stream);
+
+/*
+ * Backward pass of fa_cross_fwd by recomputation: P = exp(S - LSE),
+ * dV = P^T dO, dS = P o (dO V^T - rowsum(dO o O)), dQ = scale dS K,
+ * dK = scale dS^T Q, dK and dV summed over the query heads that share them.
+ *
+ *   q, o, dout, lse  in:  as for fa_cross_fwd; o and lse as it wrote them
+ *   dq               out: bf16 [B][H][Nq][d]
+ *   dk, dv           out: bf16 [B][Hkv][Nk][d]; zero behind a request's keys
+ *   workspace        as for fa_cross_fwd, of fa_cross_bwd_workspace_bytes()
+ * dQ is summed with fp32 atomics, so it is not bitwise repeatable from run to
+ * run; dK and dV are.
+ */
+size_t fa_cross_bwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
+fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* key_lens, const void* o,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                       size_t ws_bytes, int B, int H, int Hkv, int Nq, int Nk, int d, float scale,
+                       cudaStream_t stream);
+
+/*
+ * Attention of T new tokens per request over a key/value cache that already
+ * holds them: one token (T = 1), a run of tokens, or a tree of drafted ones.
+ * Request b has cache_lens[b] tokens of its own in rows 0 .. cache_lens[b]-1 of
+ * the cache and its drafted tokens in the rows after them, in order.  Every
+ * new token sees the request's own tokens; of the drafted ones, token n sees
+ * token t when bit t of draft_masks[b][n] is set (its ancestors and itself
+ * in a tree), or, without masks, when t <= n.
+ *
+ *   q            in:  bf16 [B][H][T][d]
+ *   k_cache, v_cache  in: bf16 [B][Hkv][C][d], C rows of capacity; rows behind
+ *                     a request's last drafted token are never used
+ *   cache_lens   in:  int32 [B] (taken into [0, C])
+ *   draft_lens   in:  int32 [B], or null: request b has draft_lens[b] <= T
+ *                     drafted tokens, else T; never more than fit in C rows
+ *   draft_masks  in:  64-bit words [B][T], or null (each token sees the ones
+ *                     before it); bits of tokens that do not exist are ignored
+ *   o, lse       out: as for fa_cross_fwd; rows of tokens >= the request's
+ *                     number of drafted tokens are left as they were
+ *   T            any with draft_masks null; at most 64 with them
+ *                (FA_ERR_UNSUPPORTED)
+ *   workspace    as for fa_cross_fwd, of fa_tree_fwd_workspace_bytes()
+ * Limits: those of fa_cross_fwd with T for Nq and C for Nk.
+ */
+size_t fa_tree_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d);
+fa_status fa_tree_fwd(const void* q, const void* k_cache, const void* v_cache, const int* cache_lens,
+                      const int* draft_lens, const unsigned long long* draft_masks, void* o, float* lse,
+                      void* workspace, size_t ws_bytes, int B, int H, int Hkv, int T, int C, int d, float scale,
+                      cudaStream_t stream);
+
+/*
+ * Rows of a token-major tensor, as a projection leaves them: the d values of
+ * head h of token n of request b start at ptr + b batch + n token + h head
+ * (elements; every stride a multiple of 8, ptr on a 16-byte boundary).
+ */
+typedef struct {
+  void* ptr;
+  long long batch, token, head;
+} fa_rows;
+
+/*
+ * Head norm and rotary positions: each query and key row x becomes
+ *   u = weight o x / sqrt(mean(x^2) + eps)   (norm = 1; weight null: ones)
+ *   u = x                                    (norm = 0)
+ * and the first rotary_dim values of u are rotated in pairs by the angle
+ * position * inv_freq[i] and multiplied by `factor`:
+ *   (a, b) -> factor (a cos - b sin, a sin + b cos),
+ * with pairs (i, i + rotary_dim / 2) (interleaved = 0) or (2 i, 2 i + 1)
+ * (interleaved = 1); values from rotary_dim on stay as they are.  Rows go from
+ * token-major tensors to head-major ones, as the attention entry points read
+ * them; value rows are moved along unchanged.  Angles keep their precision at
+ * any 32-bit position.  Arithmetic is fp32, rounded once.
+ *
+ *   q, k, v      in:  bf16 rows, B requests of N tokens, H heads (q) and Hkv
+ *                heads (k, v); a null q, k or v (ptr null, and its output null)
+ *                leaves that tensor out
+ *   q_weight, k_weight  in: fp32 [d] or null
+ *   inv_freq     in:  fp64 [rotary_dim / 2] (radians per position); may be null
+ *                when rotary_dim is 0
+ *   positions    in:  int32 [B][N], or null: starts[b] + n
+ *   starts       in:  int32 [B], or null (0): row of k_out and v_out that token 0
+ *                of request b goes to (its length in a cache)
+ *   q_out        out: bf16 [B][H][N][d]
+ *   k_out, v_out out: bf16 [B][Hkv][C][d], rows starts[b] .. starts[b] + N - 1;
+ *                rows outside [0, C) are not written, other rows stay as they were
+ *   rotary_dim   a multiple of 16, 0 <= rotary_dim <= d (others:
+ *                FA_ERR_UNSUPPORTED); C >= N
+ *   eps          finite, >= 0; factor finite
+ * No input may overlap an output.
+ */
+fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const float* q_weight,
+                      const float* k_weight, const double* inv_freq, const int* positions, const int* starts,
+                      void* q_out, void* k_out, void* v_out, int B, int N, int H, int Hkv, int C, int d,
+                      int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream);
+
+/*
+ * Backward pass of fa_rope_fwd (with starts null and C = N).
+ *
+ *   q, k         in:  the forward's inputs; not read (may be null) when norm = 0
+ *   dq_out, dk_out, dv_out  in: bf16 [B][H][N][d], [B][Hkv][N][d]: the gradients
+ *                of its outputs, as the attention backward passes write them
+ *   dq, dk, dv   out: bf16 rows like q, k, v; a null one leaves that tensor out
+ *                (its gradient then null too).  The rows may not overlap.
+ *   dq_weight, dk_weight  out: fp32 [d], summed over all rows; may be null
+ *   workspace    device scratch of ws_bytes >= fa_rope_bwd_workspace_bytes(),
+ *                16-byte aligned; may be null when no weight gradient is asked for
+ * The results are the same from run to run.
+ */
+size_t fa_rope_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d);
+fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight, const float* k_weight,
+                      const double* inv_freq, const int* positions, const void* dq_out, const void* dk_out,
+                      const void* dv_out, const fa_rows* dq, const fa_rows* dk, const fa_rows* dv, float* dq_weight,
+                      float* dk_weight, void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d,
+                      int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream);
+
+/*
  * Synchronizes `stream`, then returns and clears the current device's status
  * word: FA_OK, or FA_ERR_TIMEOUT if a kernel of this library gave up waiting
  * on one of its barriers since the last check (its outputs are then
