@@ -39,15 +39,6 @@ struct CrossView {
   }
 };
 
-struct CrossFwdParams {
-  CrossView view;
-  const __nv_bfloat16 *q, *k, *v;
-  __nv_bfloat16* o;
-  float* lse;
-  int B;
-  float scale;
-};
-
 struct CrossBwdParams {
   CrossView view;
   const __nv_bfloat16 *q, *k, *v, *o, *dout;
@@ -79,36 +70,6 @@ struct LaneRow {
     for (int i = 0; i < E; ++i) row[lane * E + i] = __float2bfloat16(x[i] * f);
   }
 };
-
-// one warp per query row
-template <int D>
-__global__ void __launch_bounds__(256) fa_cross_fwd_kernel(const CrossFwdParams p) {
-  const CrossView& v = p.view;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)p.B * v.Hkv * v.R) return;
-  const long long bk = row / v.R;
-  const int b = (int)(bk / v.Hkv), n = (int)(row - bk * v.R) % v.Nq;
-  const int len = v.len(b), dr = v.drafted(b, len);
-  if (v.T && n >= dr) return;
-  LaneRow<D> q, kv, acc{};
-  q.load(p.q + row * D, lane);
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int j = 0; j < len + dr; ++j) {
-    if (j >= len && !v.sees(b, n, j - len)) continue;
-    kv.load(p.k + (bk * v.Nk + j) * D, lane);
-    const float s = q.dot(kv) * p.scale;
-    const float mn = fmaxf(m, s), ref = mn == -CUDART_INF_F ? 0.f : mn;
-    const float a = __expf(m - ref), w = __expf(s - ref);
-    kv.load(p.v + (bk * v.Nk + j) * D, lane);
-#pragma unroll
-    for (int i = 0; i < LaneRow<D>::E; ++i) acc.x[i] = fmaf(w, kv.x[i], acc.x[i] * a);
-    l = l * a + w;
-    m = mn;
-  }
-  acc.store(p.o + row * D, lane, l == 0.f ? 0.f : 1.f / l);
-  if (lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : m + __logf(l);
-}
 
 // one warp per query row: dQ, and delta for the pass over the keys
 template <int D>

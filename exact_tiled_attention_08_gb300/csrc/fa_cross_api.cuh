@@ -2,6 +2,8 @@
 // (declared in fa.h; included by fa_ops.cu; uses the checks of fa_lib.cu).
 #pragma once
 
+#include <algorithm>
+
 namespace {
 
 // shape checks of the cross attention entry points; `R` receives the query
@@ -31,19 +33,95 @@ fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   return v;
 }
 
-fa_status run_cross_fwd(const fa::CrossFwdParams& p, int d, cudaStream_t stream) {
-  const long long blocks = ((long long)p.B * p.view.Hkv * p.view.R + 7) / 8;
-  if (blocks > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  if (d == 128)
-    fa::fa_cross_fwd_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  else
-    fa::fa_cross_fwd_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+// Grid and workspace of the forward: CTAs (at most one per SM, and one per key
+// block), and two parts per CTA where an item can be cut (more than one block).
+struct CrossFwdPlan {
+  int row_tiles, part_rows, ctas;
+  bool pair, cuts;
+  size_t lse_at, o_at, total;
+  static CrossFwdPlan of(int B, int Hkv, int R, int Nk, int d) {
+    CrossFwdPlan w;
+    w.pair = R > 128;
+    w.row_tiles = w.pair ? (R + 255) / 256 : 1;
+    w.part_rows = w.pair ? 256 : R;
+    const long long blocks = (long long)B * Hkv * w.row_tiles * ((Nk + 127LL) / 128);
+    w.ctas = (int)std::min<long long>(blocks, fa::kCrossMaxCtas);
+    w.cuts = Nk > 128;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t rows = w.cuts ? (size_t)2 * w.ctas * w.part_rows : 0;
+    w.lse_at = up(w.ctas * sizeof(fa::CrossMeta));
+    w.o_at = w.lse_at + up(rows * sizeof(float));
+    w.total = w.o_at + up(rows * d * sizeof(float)) + 256;  // (the base is brought to a 256-byte boundary)
+    return w;
+  }
+};
+
+template <int D, bool TREE, bool PAIR>
+fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                           const fa::CrossFwdParams& p, const CrossFwdPlan& plan, cudaStream_t stream) {
+  using C = fa::CrossCfg<D>;
+  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, PAIR>;
+  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
+  // the warpgroups re-divide the block's registers (setmaxnreg); that only
+  // works if the block really gets kLaunchRegs per thread
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != C::kLaunchRegs) return FA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return FA_ERR_CUDA;
+  const int grid = std::min(plan.ctas, sms);
+  kernel<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (plan.cuts) {
+    const dim3 rows((unsigned)grid, (unsigned)((plan.part_rows + 7) / 8));
+    fa::fa_cross_combine_kernel<D, TREE, PAIR><<<rows, 256, 0, stream>>>(p, grid);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+fa_status run_cross_fwd(const fa::CrossView& view, const void* q, const void* k, const void* v, void* o, float* lse,
+                        void* workspace, int B, int d, float scale, cudaStream_t stream) {
+  const CrossFwdPlan plan = CrossFwdPlan::of(B, view.Hkv, view.R, view.Nk, d);
+  CUtensorMap mq, mk, mv;
+  if (!encode_bhnd(&mq, q, B * view.Hkv, view.R, d) || !encode_bhnd(&mk, k, B * view.Hkv, view.Nk, d) ||
+      !encode_bhnd(&mv, v, B * view.Hkv, view.Nk, d))
+    return FA_ERR_CUDA;
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+  fa::CrossFwdParams p{};
+  p.view = view;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.meta = reinterpret_cast<fa::CrossMeta*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + plan.lse_at);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_at);
+  p.part_rows = plan.part_rows;
+  p.B = B;
+  p.row_tiles = plan.row_tiles;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = wait_limit_ns();
+  p.debug_stall = g_debug_stall.load();
+  p.o_align32 = aligned32(o);
+  const bool tree = view.T > 0;
+  if (d == 128) {
+    if (tree)
+      return plan.pair ? launch_cross_fwd<128, true, true>(mq, mk, mv, p, plan, stream)
+                       : launch_cross_fwd<128, true, false>(mq, mk, mv, p, plan, stream);
+    return plan.pair ? launch_cross_fwd<128, false, true>(mq, mk, mv, p, plan, stream)
+                     : launch_cross_fwd<128, false, false>(mq, mk, mv, p, plan, stream);
+  }
+  if (tree)
+    return plan.pair ? launch_cross_fwd<64, true, true>(mq, mk, mv, p, plan, stream)
+                     : launch_cross_fwd<64, true, false>(mq, mk, mv, p, plan, stream);
+  return plan.pair ? launch_cross_fwd<64, false, true>(mq, mk, mv, p, plan, stream)
+                   : launch_cross_fwd<64, false, false>(mq, mk, mv, p, plan, stream);
 }
 
 size_t cross_fwd_workspace(int B, int H, int Hkv, int Nq, int Nk, int d) {
   int R;
-  return check_cross_shape(B, H, Hkv, Nq, Nk, d, &R) == FA_OK ? 256 : 0;
+  if (check_cross_shape(B, H, Hkv, Nq, Nk, d, &R) != FA_OK) return 0;
+  return CrossFwdPlan::of(B, Hkv, R, Nk, d).total;
 }
 
 }  // namespace
@@ -66,17 +144,9 @@ fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* k
   if (!all_aligned16({q, k, v, key_lens, o, lse, workspace})) return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, lse, workspace})) != FA_OK) return st;
   if (key_lens && (st = check_device_ptrs({key_lens})) != FA_OK) return st;
-  fa::CrossFwdParams p{};
-  p.view = cross_view(H, Hkv, Nq, Nk);
-  p.view.lens = key_lens;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.B = B;
-  p.scale = scale;
-  return run_cross_fwd(p, d, stream);
+  fa::CrossView view = cross_view(H, Hkv, Nq, Nk);
+  view.lens = key_lens;
+  return run_cross_fwd(view, q, k, v, o, lse, workspace, B, d, scale, stream);
 }
 
 size_t fa_cross_bwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
@@ -145,20 +215,12 @@ fa_status fa_tree_fwd(const void* q, const void* k_cache, const void* v_cache, c
   if ((st = check_device_ptrs({q, k_cache, v_cache, cache_lens, o, lse, workspace})) != FA_OK) return st;
   if (draft_lens && (st = check_device_ptrs({draft_lens})) != FA_OK) return st;
   if (draft_masks && (st = check_device_ptrs({draft_masks})) != FA_OK) return st;
-  fa::CrossFwdParams p{};
-  p.view = cross_view(H, Hkv, T, C);
-  p.view.lens = cache_lens;
-  p.view.drafts = draft_lens;
-  p.view.masks = draft_masks;
-  p.view.T = T;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k_cache);
-  p.v = static_cast<const __nv_bfloat16*>(v_cache);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.B = B;
-  p.scale = scale;
-  return run_cross_fwd(p, d, stream);
+  fa::CrossView view = cross_view(H, Hkv, T, C);
+  view.lens = cache_lens;
+  view.drafts = draft_lens;
+  view.masks = draft_masks;
+  view.T = T;
+  return run_cross_fwd(view, q, k_cache, v_cache, o, lse, workspace, B, d, scale, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,771 @@
+// Forward kernel for keys of another length than the queries: cross attention
+// and attention over a cache (see CrossView in fa_cross.cuh).
+//
+// The arithmetic and the pipeline are those of fa_fwd_kernel: TMA fills a ring
+// of K and V tiles, one thread issues S = Q K^T, one O += P V, and two softmax
+// warpgroups hold a row of scores per thread.  What differs:
+//
+// Work.  The keys of every (request, key/value head, row tile) are cut into
+// blocks of 128, all of them form one sequence, and CTA c of G takes the
+// blocks [c Tot / G, (c + 1) Tot / G) of it: the CTAs' shares differ by one
+// block whatever the requests' lengths, and few rows over many keys use every
+// SM.  An item that lies within one CTA's share is written directly; one cut by
+// a share's end leaves a normalised fp32 O and a log-sum-exp per row and part
+// (at most two parts per CTA) that fa_cross_combine_kernel joins in CTA order.
+//
+// The two softmax warpgroups.  With more than 128 rows per key/value head
+// (PAIR) they take two row tiles that share each key block, as in
+// fa_fwd_kernel.  With up to 128 rows (ALT) there is one row tile and they take
+// its key blocks in turn, each with its own maximum, sum and accumulator; at
+// the end warpgroup 0 joins the two, reading O_1 from the same TMEM lanes.
+//
+// Keys behind a request's length.  Their scores become -inf; their rows of V
+// (which may hold anything, and 0 times NaN is NaN) are zeroed in shared
+// memory by warp 11 before the last block's P V.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "fa_cross.cuh"
+#include "fa_fwd.cuh"
+
+namespace fa {
+
+constexpr int kCrossMaxCtas = 152;  // the grid's bound: one CTA per SM
+
+struct CrossMeta {   // of each CTA, for the combine kernel
+  int split;         // its last item goes on in the next CTA
+  int b, it;         // that item
+  int n;             // its key blocks
+  long long first;   // its first block in the sequence
+  long long total;   // blocks of the sequence
+};
+
+struct CrossFwdParams {
+  CrossView view;
+  __nv_bfloat16* o;
+  float* lse;
+  CrossMeta* meta;       // [grid]
+  float* part_lse;       // [2 grid][part_rows], base 2
+  float* part_o;         // [2 grid][part_rows][d]
+  int part_rows;         // rows of a part: 256 (PAIR) or R (ALT)
+  int B;
+  int row_tiles;         // row tiles (PAIR: pairs of them) per key/value head
+  float scale_log2;
+  uint64_t wait_limit_ns;
+  int debug_stall;
+  int o_align32;
+};
+
+// key blocks of a request: at least one, so that rows without keys are written
+__device__ __forceinline__ int cross_blocks(int keys) { return keys > 128 ? (keys + 127) >> 7 : 1; }
+
+// A CTA's place in the sequence of blocks.
+struct CrossPlace {
+  int b, it, j;    // request, item of it (head, row tile), key block
+  long long left;  // blocks of the CTA from there on
+};
+
+// A run of key blocks of one item.
+struct CrossSeg {
+  int b, it, j0, j1, n;
+  int len, keys;  // the request's own keys; with its drafts
+  __device__ __forceinline__ bool first() const { return j0 == 0; }
+  __device__ __forceinline__ bool last() const { return j1 == n; }
+  // the last block's rows of V behind the keys hold anything (past Nk the TMA fills zeros)
+  __device__ __forceinline__ bool dirty(const CrossView& v) const { return last() && keys < (n << 7) && keys < v.Nk; }
+};
+
+__device__ __forceinline__ bool cross_next(const CrossView& v, int items, CrossPlace& at, CrossSeg& s) {
+  if (at.left <= 0) return false;
+  s.b = at.b;
+  s.it = at.it;
+  s.len = v.len(at.b);
+  s.keys = s.len + v.drafted(at.b, s.len);
+  s.n = cross_blocks(s.keys);
+  s.j0 = at.j;
+  s.j1 = (int)min((long long)s.n, at.j + at.left);
+  at.left -= s.j1 - s.j0;
+  at.j = s.j1;
+  if (at.j == s.n) {
+    at.j = 0;
+    if (++at.it == items) {
+      at.it = 0;
+      ++at.b;
+    }
+  }
+  return true;
+}
+
+// Where CTA `cta` of at most `ctas` starts, by all of the block's threads.
+// `scratch`: kThreads long longs of shared memory.  Returns the blocks of the
+// sequence; the CTAs past it (more CTAs than blocks) get nothing.
+template <int kThreads>
+__device__ __forceinline__ long long cross_schedule(const CrossView& v, int B, int items, int cta, int ctas,
+                                                    long long* scratch, CrossPlace* place) {
+  const int tid = threadIdx.x;
+  const int chunk = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, tid * chunk), b1 = min(B, b0 + chunk);
+  auto blocks = [&](int b) {
+    const int len = v.len(b);
+    return cross_blocks(len + v.drafted(b, len));
+  };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += blocks(b);
+  scratch[tid] = mine;
+  __syncthreads();
+  for (int o = 1; o < kThreads; o <<= 1) {  // inclusive scan
+    const long long add = tid >= o ? scratch[tid - o] : 0;
+    __syncthreads();
+    scratch[tid] += add;
+    __syncthreads();
+  }
+  const long long total = scratch[kThreads - 1] * items;
+  if (total < ctas) ctas = (int)total;
+  const long long start = cta < ctas ? cta * total / ctas : total;
+  const long long end = cta < ctas ? (cta + 1) * total / ctas : total;
+  if (cta >= ctas) {
+    if (tid == 0) *place = {0, 0, 0, 0};
+  } else {
+    long long at = (scratch[tid] - mine) * items;
+    if (start >= at && start < scratch[tid] * items) {
+      for (int b = b0; b < b1; ++b) {
+        const int n = blocks(b);
+        if (start < at + (long long)n * items) {
+          const long long off = start - at;
+          *place = {b, (int)(off / n), (int)(off % n), end - start};
+          break;
+        }
+        at += (long long)n * items;
+      }
+    }
+  }
+  return total;
+}
+
+template <int D>
+struct CrossCfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kThreads = 384;
+  static constexpr int kLaunchRegs = 168;
+  static constexpr uint32_t kSoftRegs = D == 64 ? 216 : 208;
+  static constexpr uint32_t kMiscRegs = 3 * kLaunchRegs - 2 * kSoftRegs;
+  static_assert(kSoftRegs % 8 == 0 && kMiscRegs % 8 == 0 && kMiscRegs >= 24 && kSoftRegs > kLaunchRegs,
+                "2 kSoftRegs + kMiscRegs = the three warpgroups' launch budget");
+  static constexpr bool kDualS = D == 64;
+  static constexpr int kSlots = D == 128 ? 5 : 12;
+  // Ring slot and use of key block g's K (kv = 0) or V tile (g counts over the
+  // CTA's segments).  PAIR: one ring, K_g and V_g in turn.  ALT: K and V have
+  // slots of their own (3 and 2 at d = 128): there the S issuer may be several
+  // blocks ahead of the P V issuer, and a wait on the phase of a slot that K
+  // and V share could take the phase before last for its own.
+  static constexpr int kAltK = (kSlots + 1) / 2, kAltV = kSlots / 2;
+  template <bool PAIR>
+  static __device__ __forceinline__ int slot(int kv, int g) {
+    if (PAIR) return (2 * g + kv) % kSlots;
+    return kv ? kAltK + g % kAltV : g % kAltK;
+  }
+  template <bool PAIR>
+  static __device__ __forceinline__ int use(int kv, int g) {
+    if (PAIR) return (2 * g + kv) / kSlots;
+    return g / (kv ? kAltV : kAltK);
+  }
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kSCol = 0, kPCol0 = 128, kPCol1 = 192, kOCol0 = 256, kOCol1 = 256 + D;
+  static constexpr uint32_t kSCol1 = kDualS ? kOCol1 + D : kSCol;
+  static_assert((kDualS ? kSCol1 + 128 : kOCol1 + D) <= kTmemCols, "tensor memory budget");
+  static constexpr int kMergeBytes = 3 * 128 * 4;
+  static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + kMergeBytes + 512;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(kSlots * kTileBytes >= kThreads * 8, "the schedule's scan uses the ring");
+};
+
+struct CrossBarriers {
+  uint64_t q_full[2], q_empty[2];  // PAIR: both tiles by [0]; ALT: the segments' queries in turn
+  uint64_t kv_full[12], kv_empty[12];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  // an item's last V tile has landed: warp 11 may zero its rows behind the
+  // keys; they are zero.  (The P V issuer asks: warp 11 could not wait for the
+  // tile's own barrier, whose phases go on while it waits for nothing.)
+  uint64_t v_ask, v_clean;
+  uint64_t merge_ready, merge_free;    // ALT: warpgroup 1's sums are in place; O_1 has been read
+  uint64_t drain[2];
+  uint64_t never;
+  CrossPlace place;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(CrossBarriers) <= 512, "barriers overflow their shared-memory slot");
+
+enum : int { kSiteCrossQEmpty = 40, kSiteCrossKvEmpty, kSiteCrossQ, kSiteCrossK, kSiteCrossSFree, kSiteCrossV,
+             kSiteCrossClean, kSiteCrossP, kSiteCrossS, kSiteCrossPv, kSiteCrossMerge, kSiteCrossTail };
+
+// the maximum of 64 scores: a tree of 3-input maxima
+__device__ __forceinline__ float cross_max64(const uint32_t* x, const uint32_t* y) {
+  float t1[22];
+#pragma unroll
+  for (int i = 0; i < 21; ++i) {
+    const int e = 3 * i;
+    t1[i] = max3(__uint_as_float(e < 32 ? x[e] : y[e - 32]), __uint_as_float(e + 1 < 32 ? x[e + 1] : y[e - 31]),
+                 __uint_as_float(e + 2 < 32 ? x[e + 2] : y[e - 30]));
+  }
+  t1[21] = __uint_as_float(y[31]);
+  float t2[8];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) t2[i] = max3(t1[3 * i], t1[3 * i + 1], t1[3 * i + 2]);
+  t2[7] = t1[21];
+  return max3(max3(t2[0], t2[1], t2[2]), max3(t2[3], t2[4], t2[5]), fmaxf(t2[6], t2[7]));
+}
+
+// 32 bits of what a row sees, from key `rel` keys behind the request's own
+__device__ __forceinline__ uint32_t cross_bits(unsigned long long mask, int rel) {
+  if (rel <= -32) return 0xffffffffu;
+  if (rel < 0) return ((1u << -rel) - 1u) | (uint32_t)(mask << -rel);
+  return rel < 64 ? (uint32_t)(mask >> rel) : 0u;
+}
+
+// TREE: drafted tokens behind the request's own.  PAIR: two row tiles per item.
+template <int D, bool TREE, bool PAIR>
+__global__ void __launch_bounds__(384, 1)
+    fa_cross_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const CrossFwdParams p) {
+  using C = CrossCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * C::kTileBytes;
+  float* sMerge = reinterpret_cast<float*>(sKV + C::kSlots * C::kTileBytes);  // [3][128]
+  CrossBarriers* bar = reinterpret_cast<CrossBarriers*>(reinterpret_cast<uint8_t*>(sMerge) + C::kMergeBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const CrossView& v = p.view;
+  const int items = v.Hkv * p.row_tiles;
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar->q_full[t], 1);
+      mbar_init(&bar->q_empty[t], 1);
+      mbar_init(&bar->s_full[t], 1);
+      mbar_init(&bar->s_free[t], 128);
+      mbar_init(&bar->p_full[t], 128);
+      mbar_init(&bar->pv_done[t], 1);
+      mbar_init(&bar->drain[t], 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bar->kv_full[s], 1);
+      mbar_init(&bar->kv_empty[s], 1);
+    }
+    mbar_init(&bar->v_clean, 1);
+    mbar_init(&bar->v_ask, 1);
+    mbar_init(&bar->merge_ready, 128);
+    mbar_init(&bar->merge_free, 128);
+    mbar_init(&bar->never, 1);
+    bar->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&bar->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+  }
+  const long long total = cross_schedule<C::kThreads>(v, p.B, items, blockIdx.x, gridDim.x,
+                                                      reinterpret_cast<long long*>(sKV), &bar->place);
+  fence_async_shared();  // the ring's first copies follow the scan's plain writes
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
+  CrossPlace at = bar->place;  // every role walks the same segments
+  CrossSeg w;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<C::kMiscRegs>();
+    if (warp == 9) {
+      // ------------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        int loads = 0, nq = 0;  // K and V tiles, in turn
+        bool ok = true;
+        auto load_kv = [&](int j, int kv, int bk) -> bool {
+          const int g = loads >> 1, s = C::template slot<PAIR>(kv, g);
+          const CUtensorMap* map = kv ? &map_v : &map_k;
+          if (!wait_bounded_inl(&bar->kv_empty[s], (C::template use<PAIR>(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty))
+            return false;
+          mbar_arrive_expect_tx(&bar->kv_full[s], C::kTileBytes);
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_3d(sKV + s * C::kTileBytes + a * 16384, map, &bar->kv_full[s], a * 64, j * 128, bk);
+          ++loads;
+          return true;
+        };
+        while (ok && cross_next(v, items, at, w)) {
+          const int kvh = w.it / p.row_tiles;
+          const int row0 = (w.it - kvh * p.row_tiles) * (PAIR ? 256 : 128);
+          const int bk = w.b * v.Hkv + kvh;
+          // the first key block needs only ring slots: it goes out before the
+          // queries, whose buffer an earlier segment may still be reading
+          ok = load_kv(w.j0, 0, bk) && load_kv(w.j0, 1, bk);
+          if (!ok) break;
+          const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+          if (use > 0 && !(ok = wait_bounded_inl(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty))) break;
+          const int tiles = PAIR && row0 + 128 < v.R ? 2 : 1;
+          mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
+          for (int t = 0; t < tiles; ++t)
+            for (int a = 0; a < C::kAtoms; ++a)
+              tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
+                          row0 + 128 * t, bk);
+          ++nq;
+          for (int j = w.j0 + 1; ok && j < w.j1; ++j) ok = load_kv(j, 0, bk) && load_kv(j, 1, bk);
+        }
+        // every copy this thread started must land before the CTA can exit
+        for (int s = 0; s < 2; ++s) {
+          const int uses = PAIR ? (s ? 0 : nq) : (nq + 1 - s) >> 1;
+          if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
+        }
+        for (int s = 0; s < C::kSlots; ++s) {
+          // loads into slot s: of all in turn (PAIR), or of the K or V tiles
+          const bool vslot = !PAIR && s >= C::kAltK;
+          const int n = PAIR ? loads : (vslot ? loads >> 1 : (loads + 1) >> 1);
+          const int at0 = vslot ? s - C::kAltK : s, step = PAIR ? C::kSlots : (vslot ? C::kAltV : C::kAltK);
+          if (n > at0) wait_drain_inl(&bar->kv_full[s], ((n - 1 - at0) / step) & 1, kDrainLimitNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // ------------------------------------------------------------------ S issuer
+      // g counts key blocks over all segments
+      if (lane == 0) {
+        const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+        int s_uses[2] = {0, 0}, g = 0, nq = 0;
+        bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
+        while (ok && cross_next(v, items, at, w)) {
+          const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+          if (!wait_bounded_inl(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
+          ++nq;
+          const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128);
+          const bool two = PAIR && row0 + 128 < v.R;
+          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+            const int ks = C::template slot<PAIR>(0, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK))) break;
+            const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (PAIR ? (t == 0 || two) : (((j - w.j0) & 1) == t)) {
+                const int sb = C::kDualS ? t : 0;
+                if (s_uses[sb] > 0 && !wait_bounded_inl(&bar->s_free[sb], (s_uses[sb] - 1) & 1, ctx, kSiteCrossSFree)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                const uint64_t qd = sdesc_sw128(sq + (PAIR ? t : qs) * C::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                  mma_bf16_ss(tmem + (sb ? C::kSCol1 : C::kSCol), qd + off, kdesc + off, id_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&bar->s_full[t]);
+                ++s_uses[sb];
+              }
+            }
+            if (!ok) break;
+            mma_commit(&bar->kv_empty[ks]);
+          }
+          if (!ok) break;
+          mma_commit(&bar->q_empty[qs]);  // the segment's queries have been read
+        }
+        mma_commit(&bar->drain[0]);
+        wait_drain_inl(&bar->drain[0], 0, kDrainLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ------------------------------------------------------------------ P V issuer
+      // O_t += P_t(j) V_j once the softmax of tile t wrote P_t(j)
+      if (lane == 0) {
+        const uint32_t skv = smem_u32(sKV);
+        constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+        int g = 0, cleaned = 0;
+        int pv_uses[2] = {0, 0};
+        bool ok = true;
+        while (ok && cross_next(v, items, at, w)) {
+          const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128);
+          const bool two = PAIR && row0 + 128 < v.R;
+          const bool dirty = w.dirty(v);
+          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+            const int vs = C::template slot<PAIR>(1, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[vs], C::template use<PAIR>(1, g) & 1, ctx, kSiteCrossV))) break;
+            bool clean = !(dirty && j == w.n - 1);
+            if (!clean) mbar_arrive(&bar->v_ask);
+            const uint64_t vdesc = sdesc_sw128(skv + vs * C::kTileBytes, 16384, 1024);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (PAIR ? (t == 0 || two) : (((j - w.j0) & 1) == t)) {
+                if (!wait_bounded_inl(&bar->p_full[t], pv_uses[t] & 1, ctx, kSiteCrossP)) {
+                  ok = false;
+                  break;
+                }
+                if (!clean) {
+                  if (!(ok = wait_bounded_inl(&bar->v_clean, cleaned & 1, ctx, kSiteCrossClean))) break;
+                  ++cleaned;
+                  clean = true;
+                }
+                tc_fence_after();
+                const bool add = j > w.j0 + (PAIR ? 0 : 1);  // not the tile's first block of the segment
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_bf16_ts(tmem + (t ? C::kOCol1 : C::kOCol0), tmem + (t ? C::kPCol1 : C::kPCol0) + kk * 8,
+                              vdesc + (uint32_t)((kk * 2048) >> 4), id_pv, (add || kk > 0) ? 1u : 0u);
+                mma_commit(&bar->pv_done[t]);
+                ++pv_uses[t];
+              }
+            }
+            if (!ok) break;
+            mma_commit(&bar->kv_empty[vs]);
+          }
+        }
+        mma_commit(&bar->drain[1]);
+        wait_drain_inl(&bar->drain[1], 0, kDrainLimitNs);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ warp 11: rows of V behind the keys
+      int g = 0, cleaned = 0;
+      bool ok = true;
+      CrossMeta meta{0, 0, 0, 0, 0, total};
+      long long place = (long long)blockIdx.x * total / min((long long)gridDim.x, total);
+      while (ok && cross_next(v, items, at, w)) {
+        if (w.dirty(v)) {
+          const int vs = C::template slot<PAIR>(1, g + w.j1 - 1 - w.j0);
+          ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
+          if (!ok) break;
+          ++cleaned;
+          uint8_t* tile = sKV + vs * C::kTileBytes;
+          const int row = w.keys - (w.n - 1) * 128;  // first row behind the keys
+          for (int a = 0; a < C::kAtoms; ++a)
+            for (int c = row * 8 + lane; c < 128 * 8; c += 32)
+              *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->v_clean);
+        }
+        g += w.j1 - w.j0;
+        if (w.first() && !w.last()) meta = {1, w.b, w.it, w.n, place, total};
+        place += w.j1 - w.j0;
+      }
+      if (!ok) meta.split = 0;
+      if (lane == 0) p.meta[blockIdx.x] = meta;
+    }
+  } else {
+    setmaxnreg_inc<C::kSoftRegs>();
+    // ------------------------------------------------------------------ softmax warpgroups
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + ((C::kDualS && t) ? C::kSCol1 : C::kSCol) + lane_off;
+    const uint32_t tP = tmem + (t ? C::kPCol1 : C::kPCol0) + lane_off;
+    const uint32_t tO = tmem + (t ? C::kOCol1 : C::kOCol0) + lane_off;
+    const float cj = p.scale_log2;
+    int uses = 0;   // blocks this tile has processed over all segments
+    int merges = 0;  // ALT: segments whose two accumulators were joined
+    bool alive = true;
+    while (alive && cross_next(v, items, at, w)) {
+      const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0);
+      if (PAIR ? (row0 >= v.R) : (t == 1 && w.j1 - w.j0 < 2)) continue;  // nothing for this tile
+      const int row = row0 + r;
+      // TREE: what the row's token sees of the drafts
+      unsigned long long mask = 0;
+      int last_key = w.keys - 1;
+      if constexpr (TREE) {
+        const int tok = row % v.Nq;
+        if (v.masks)
+          mask = __ldg(v.masks + (long long)w.b * v.T + tok) &
+                 (w.keys - w.len >= 64 ? ~0ull : (1ull << (w.keys - w.len)) - 1ull);
+        else
+          last_key = min(last_key, w.len + tok);
+      }
+      float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
+      // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
+      // block's largest one, so that l + lcorr normalises O (see fa_fwd_kernel)
+      float l = 0.f, lcorr = 0.f;
+      const int jfirst = w.j0 + (PAIR ? 0 : t);
+      for (int j = jfirst; j < w.j1; j += PAIR ? 1 : 2, ++uses) {
+        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+        float mx_a = 0.f;
+        if constexpr (C::kDualS) {  // two halves: the first's maximum is taken while the second loads
+          tmem_ld32(tS, sr[0]);
+          tmem_ld32(tS + 32, sr[1]);
+          tmem_wait_ld();
+          reg_fence32(sr[0]);
+          reg_fence32(sr[1]);
+          tmem_ld32(tS + 64, sr[2]);
+          tmem_ld32(tS + 96, sr[3]);
+          mx_a = cross_max64(sr[0], sr[1]);
+          tmem_wait_ld();
+          reg_fence32(sr[2]);
+          reg_fence32(sr[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+        }
+        // the scores are in registers: the next scores may now overwrite S
+        tc_fence_before();
+        mbar_arrive(&bar->s_free[C::kDualS ? t : 0]);
+
+        const int kbase = j * 128;
+        const bool cut = kbase + 128 > (TREE ? w.len : w.keys);
+        if (cut) {
+          if (TREE && v.masks) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = cross_bits(mask, kbase + 32 * c - w.len);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-CUDART_INF_F);
+            }
+          } else {
+            const int last = last_key - kbase;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > last) sr[c >> 5][c & 31] = __float_as_uint(-CUDART_INF_F);
+          }
+        }
+        float mx;
+        if constexpr (C::kDualS) {
+          mx = fmaxf(cut ? cross_max64(sr[0], sr[1]) : mx_a, cross_max64(sr[2], sr[3]));
+        } else {
+          mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
+        }
+        const float m_new = fmaxf(m, mx * cj);
+        // conditional rescale: the reference moves only when the row maximum
+        // rose by more than the threshold (always from -inf: no key so far)
+        float alpha = 1.f;
+        bool rescale_warp = false;
+        if (j == jfirst) {
+          m = m_new;
+        } else {
+          const bool need = (m_new - m) > kRescaleThresholdLog2;
+          rescale_warp = __any_sync(0xffffffffu, need);
+          if (need) {
+            alpha = ex2_approx(m - m_new);
+            m = m_new;
+          }
+        }
+        const float ref = m == -CUDART_INF_F ? 0.f : m;  // a row without keys so far: every P is 2^-inf = 0
+        const float2 c2 = make_float2(cj, cj);
+        const float2 mneg2 = make_float2(-ref, -ref);
+        float2 acc[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
+        {
+          const float pbm = ex2_approx(fmaf(mx, cj, -ref));
+          const float pbm_r = __uint_as_float(pack_bf16x2(pbm, 0.f) << 16);
+          lcorr = lcorr * alpha + (pbm_r - pbm);
+        }
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
+                                        c2, mneg2);
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            pk[c][i] = pack_bf16x2(p0, p1);
+            acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+          }
+        }
+        const float2 accs = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        l = l * alpha + (accs.x + accs.y);
+        // P_t and O_t are in use until the tile's previous product has completed
+        // (a segment's first block: its predecessor's epilogue has waited for
+        // it; ALT: O_1 also until warpgroup 0 has read it)
+        if (j > jfirst) {
+          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+        } else if (!PAIR && t == 1 && merges > 0) {
+          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_free, (merges - 1) & 1, ctx, kSiteCrossMerge))) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        if (rescale_warp) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + 32 * c, ov);
+            tmem_wait_ld();
+            reg_fence32(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(tO + 32 * c, ov);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(tP + 16 * c, pk[c]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[t]);
+      }
+      if (!alive) break;
+      if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      // ---- end of the segment
+      const bool join = !PAIR && w.j1 - w.j0 >= 2;
+      float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
+      if (join) {
+        if (t == 1) {
+          sMerge[r] = m;
+          sMerge[128 + r] = l;
+          sMerge[256 + r] = lo;
+          tc_fence_before();
+          mbar_arrive(&bar->merge_ready);
+          ++merges;
+          continue;
+        }
+        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_ready, merges & 1, ctx, kSiteCrossMerge))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        ++merges;
+        const float m1 = sMerge[r], mm = fmaxf(m, m1), ref = mm == -CUDART_INF_F ? 0.f : mm;
+        a0 = ex2_approx(m - ref);
+        a1 = ex2_approx(m1 - ref);
+        l = l * a0 + sMerge[128 + r] * a1;
+        lo = lo * a0 + sMerge[256 + r] * a1;
+        m = mm;
+      }
+      const float inv = lo == 0.f ? 0.f : 1.f / lo;
+      a0 *= inv;
+      a1 *= inv;
+      const float lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+      const bool whole = w.first() && w.last();
+      bool write = row < v.R;
+      if (TREE) write = write && (row % v.Nq) < w.keys - w.len;
+      const int kvh = w.it / p.row_tiles;
+      const size_t grow = ((size_t)w.b * v.Hkv + kvh) * v.R + row;
+      const size_t prow = ((size_t)2 * blockIdx.x + (w.first() ? 1 : 0)) * p.part_rows + (PAIR ? 128 * t : 0) + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32], ow[32];
+        tmem_ld32(tO + 32 * c, ov);
+        if (join) tmem_ld32(tmem + C::kOCol1 + lane_off + 32 * c, ow);
+        tmem_wait_ld();
+        reg_fence32(ov);
+        if (join) {
+          reg_fence32(ow);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = __float_as_uint(fmaf(__uint_as_float(ow[i]), a1, __uint_as_float(ov[i]) * a0));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a0);
+        }
+        if (join && c == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&bar->merge_free);
+        }
+        if (write && whole) {
+          __nv_bfloat16* orow = p.o + grow * D + 32 * c;
+          uint32_t w16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w16[e] = pack_bf16x2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
+          if (p.o_align32) {
+            st_global_v8(orow, w16);
+            st_global_v8(orow + 16, w16 + 8);
+          } else {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4)
+              reinterpret_cast<uint4*>(orow)[v4] =
+                  make_uint4(w16[4 * v4], w16[4 * v4 + 1], w16[4 * v4 + 2], w16[4 * v4 + 3]);
+          }
+        } else if (write) {
+          float* prow_o = p.part_o + prow * D + 32 * c;
+#pragma unroll
+          for (int v8 = 0; v8 < 4; ++v8) st_global_v8(prow_o + 8 * v8, ov + 8 * v8);
+        }
+        __syncwarp();  // the next tensor memory load is a whole warp's
+      }
+      if (write) {
+        if (whole)
+          p.lse[grow] = lse2 * 0.6931471805599453f;
+        else
+          p.part_lse[prow] = lse2;
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the parts of the items that share ends cut: block x takes the item that
+// begins in CTA x's share and goes on behind it, one warp per row.  O = sum of
+// the parts' O weighted by 2^(their LSE - the largest), in CTA order.
+template <int D, bool TREE, bool PAIR>
+__global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdParams p, int ctas) {
+  const CrossMeta meta = p.meta[blockIdx.x];
+  if (!meta.split) return;
+  const CrossView& v = p.view;
+  const int lane = threadIdx.x & 31, local = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int kvh = meta.it / p.row_tiles;
+  const int row = (meta.it - kvh * p.row_tiles) * (PAIR ? 256 : 128) + local;
+  if (local >= p.part_rows || row >= v.R) return;
+  if (TREE) {
+    const int len = v.len(meta.b);
+    if (row % v.Nq >= v.drafted(meta.b, len)) return;
+  }
+  const long long g = min((long long)ctas, meta.total);
+  const int parts = (int)(((meta.first + meta.n) * g - 1) / meta.total) - (int)blockIdx.x + 1;
+  // part i: the last segment of CTA x, then the first of each CTA after it
+  auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local; };
+  float mx = -CUDART_INF_F;
+  for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_lse[part(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+  constexpr int E = D / 32;
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float wt = ex2_approx(p.part_lse[part(i)] - ref);
+    sum += wt;
+    const float* o = p.part_o + part(i) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[e], acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const size_t grow = ((size_t)meta.b * v.Hkv + kvh) * v.R + row;
+  uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace fa

@@ -5,6 +5,7 @@
 #include "fa_lib.cu"
 
 #include "fa_cross.cuh"
+#include "fa_cross_fwd.cuh"
 #include "fa_rope.cuh"
 #include "fa_cross_api.cuh"
 #include "fa_rope_api.cuh"

@@ -94,6 +94,8 @@ CROSS = [
     (1, 1, 1, 700, 6000, None),      # few rows of blocks, many keys
     (5, 16, 8, 40, 260, [1, 255, 256, 257, 260]),
     (2, 40, 40, 130, 384, [384, 130]),  # more items than SMs
+    (4, 40, 40, 2, 1500, [1500, 700, 1499, 64]),  # many key blocks a CTA
+    (2, 40, 20, 130, 1111, None),
 ]
 
 
@@ -251,6 +253,7 @@ TREE = [
     (1, 2, 1, 3, 30000, [29000], None, True),
     (2, 2, 2, 8, 64, [60, 64], None, False),     # drafts that do not fit are not there
     (40, 16, 8, 2, 300, list(range(0, 280, 7)), None, True),
+    (20, 16, 8, 3, 4000, [3990 - 7 * i for i in range(20)], None, True),  # many key blocks a CTA
 ]
 
 
