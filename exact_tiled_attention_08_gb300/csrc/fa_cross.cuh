@@ -8,7 +8,6 @@
 #pragma once
 
 #include <cuda_bf16.h>
-#include <math_constants.h>
 
 #include "sm103_ptx.cuh"
 
@@ -38,90 +37,5 @@ struct CrossView {
     return masks ? ((__ldg(masks + (long long)b * T + n) >> t) & 1) : t <= n;
   }
 };
-
-struct CrossBwdParams {
-  CrossView view;
-  const __nv_bfloat16 *q, *k, *v, *o, *dout;
-  const float* lse;
-  __nv_bfloat16 *dq, *dk, *dv;
-  float* delta;
-  int B;
-  float scale;
-};
-
-template <int D>
-struct LaneRow {
-  static constexpr int E = D / 32;
-  float x[E];
-  __device__ __forceinline__ void load(const __nv_bfloat16* row, int lane) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __bfloat162float(row[lane * E + i]);
-  }
-  __device__ __forceinline__ float dot(const LaneRow& o) const {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(x[i], o.x[i], s);
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    return s;
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* row, int lane, float f) const {
-#pragma unroll
-    for (int i = 0; i < E; ++i) row[lane * E + i] = __float2bfloat16(x[i] * f);
-  }
-};
-
-// one warp per query row: dQ, and delta for the pass over the keys
-template <int D>
-__global__ void __launch_bounds__(256) fa_cross_dq_kernel(const CrossBwdParams p) {
-  const CrossView& v = p.view;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)p.B * v.Hkv * v.R) return;
-  const long long bk = row / v.R;
-  const int len = v.len((int)(bk / v.Hkv));
-  LaneRow<D> q, o, go, k, x, acc{};
-  q.load(p.q + row * D, lane);
-  o.load(p.o + row * D, lane);
-  go.load(p.dout + row * D, lane);
-  const float delta = go.dot(o), lse = p.lse[row];
-  if (lane == 0) p.delta[row] = delta;
-  for (int j = 0; j < len; ++j) {
-    k.load(p.k + (bk * v.Nk + j) * D, lane);
-    x.load(p.v + (bk * v.Nk + j) * D, lane);
-    const float ds = __expf(q.dot(k) * p.scale - lse) * (go.dot(x) - delta);
-#pragma unroll
-    for (int i = 0; i < LaneRow<D>::E; ++i) acc.x[i] = fmaf(ds, k.x[i], acc.x[i]);
-  }
-  acc.store(p.dq + row * D, lane, p.scale);
-}
-
-// one warp per key row: dK and dV
-template <int D>
-__global__ void __launch_bounds__(256) fa_cross_dkv_kernel(const CrossBwdParams p) {
-  const CrossView& v = p.view;
-  const long long key = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (key >= (long long)p.B * v.Hkv * v.Nk) return;
-  const long long bk = key / v.Nk;
-  LaneRow<D> q, go, k, x, dk{}, dv{};
-  if (key - bk * v.Nk < v.len((int)(bk / v.Hkv))) {
-    k.load(p.k + key * D, lane);
-    x.load(p.v + key * D, lane);
-    for (long long row = bk * v.R; row < (bk + 1) * v.R; ++row) {
-      q.load(p.q + row * D, lane);
-      go.load(p.dout + row * D, lane);
-      const float pr = __expf(q.dot(k) * p.scale - p.lse[row]);
-      const float ds = pr * (go.dot(x) - p.delta[row]);
-#pragma unroll
-      for (int i = 0; i < LaneRow<D>::E; ++i) {
-        dk.x[i] = fmaf(ds, q.x[i], dk.x[i]);
-        dv.x[i] = fmaf(pr, go.x[i], dv.x[i]);
-      }
-    }
-  }
-  dk.store(p.dk + key * D, lane, p.scale);
-  dv.store(p.dv + key * D, lane, 1.f);
-}
 
 }  // namespace fa

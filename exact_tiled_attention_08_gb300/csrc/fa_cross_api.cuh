@@ -124,6 +124,83 @@ size_t cross_fwd_workspace(int B, int H, int Hkv, int Nq, int Nk, int d) {
   return CrossFwdPlan::of(B, Hkv, R, Nk, d).total;
 }
 
+// workspace of the backward: plan, dQ accumulator, delta and LSE log2(e) padded
+// to whole blocks, runs of cut items
+struct CrossBwdWorkspace {
+  size_t dq_at, delta_at, lse_at, runs_at, total;
+  static CrossBwdWorkspace of(int B, int Hkv, int R, int d) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t bk = (size_t)B * Hkv, rpad = ((size_t)R + 127) / 128 * 128;
+    CrossBwdWorkspace w;
+    w.dq_at = up(sizeof(fa::CrossBwdPlan));
+    w.delta_at = w.dq_at + up(bk * R * d * sizeof(float));
+    w.lse_at = w.delta_at + up(bk * rpad * sizeof(float));
+    w.runs_at = w.lse_at + up(bk * rpad * sizeof(float));
+    // (an item of one query block is never cut)
+    w.total = w.runs_at + (R > 128 ? (size_t)fa::kCrossBwdSlots * 2 * 128 * d * sizeof(float) : 0) + 256;
+    return w;
+  }
+};
+
+template <int D>
+fa_status run_cross_bwd(const fa::CrossView& view, const void* q, const void* k, const void* v, const void* o,
+                        const void* dout, const float* lse, void* dq, void* dk, void* dv, void* workspace, int B,
+                        float scale, cudaStream_t stream) {
+  using C = fa::BwdCfg<D, true>;
+  const int BK = B * view.Hkv, R = view.R, nqb = (R + 127) / 128, rpad = nqb * 128;
+  const CrossBwdWorkspace w = CrossBwdWorkspace::of(B, view.Hkv, R, D);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+  float* dq_acc = reinterpret_cast<float*>(ws + w.dq_at);
+  float* delta = reinterpret_cast<float*>(ws + w.delta_at);
+  float* lse2 = reinterpret_cast<float*>(ws + w.lse_at);
+  CUtensorMap mq, mk, mv, mdo, ml, mdel, mdq;
+  if (!encode_bhnd(&mq, q, BK, R, D) || !encode_bhnd(&mk, k, BK, view.Nk, D) || !encode_bhnd(&mv, v, BK, view.Nk, D) ||
+      !encode_bhnd(&mdo, dout, BK, R, D) || !encode_f32_rows(&ml, lse2, BK, rpad, 128) ||
+      !encode_f32_rows(&mdel, delta, BK, rpad, 128) || !encode_dq_acc(&mdq, dq_acc, BK, R, D))
+    return FA_ERR_CUDA;
+  auto kernel = fa::fa_cross_bwd_kernel<D>;
+  if (set_smem(kernel, fa::kCrossBwdSmemBytes<D>) != cudaSuccess) return FA_ERR_CUDA;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != C::kLaunchRegs) return FA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return FA_ERR_CUDA;
+  const long long rows = (long long)BK * rpad, per_block = 256 / (D / 8);
+  const long long prep = std::min((rows + per_block - 1) / per_block, 152LL * 16);
+  fa::fa_cross_bwd_prep_kernel<D><<<(unsigned)prep, 256, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, delta, lse2, dq_acc, R, rpad,
+      rows);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  fa::CrossBwdPostParams post{};
+  fa::CrossBwdParams& p = post.p;
+  p.view = view;
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.plan = reinterpret_cast<fa::CrossBwdPlan*>(ws);
+  p.runs = reinterpret_cast<float*>(ws + w.runs_at);
+  p.B = B;
+  p.nqb = nqb;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = scale;
+  p.wait_limit_ns = wait_limit_ns();
+  p.debug_stall = g_debug_stall.load();
+  p.out_align32 = aligned32(dk) && aligned32(dv);
+  // one CTA per SM, and no more than there are query blocks to hand out
+  const long long blocks = (long long)BK * ((view.Nk + 127LL) / 128) * std::min(nqb, fa::kCrossBwdMaxParts);
+  const int grid = (int)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
+  kernel<<<(unsigned)grid, C::kThreads, fa::kCrossBwdSmemBytes<D>, stream>>>(mq, mk, mv, mdo, ml, mdel, mdq, p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  post.dq_acc = dq_acc;
+  post.dq = static_cast<__nv_bfloat16*>(dq);
+  post.n8 = (long long)BK * R * D / 8;
+  post.ctas = grid;
+  const long long convert = std::min((post.n8 + 255) / 256, 152LL * 16);
+  const long long post_grid = 8LL * grid + (view.lens ? BK : 0) + convert;
+  fa::fa_cross_bwd_post_kernel<D><<<(unsigned)post_grid, 256, 0, stream>>>(post);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,7 +229,7 @@ fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* k
 size_t fa_cross_bwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
   int R;
   if (check_cross_shape(B, H, Hkv, Nq, Nk, d, &R) != FA_OK) return 0;
-  return (size_t)B * Hkv * R * sizeof(float);
+  return CrossBwdWorkspace::of(B, Hkv, R, d).total;
 }
 
 fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* key_lens, const void* o,
@@ -168,31 +245,11 @@ fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* k
   if (!all_aligned16({q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace})) return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, workspace})) != FA_OK) return st;
   if (key_lens && (st = check_device_ptrs({key_lens})) != FA_OK) return st;
-  fa::CrossBwdParams p{};
-  p.view = cross_view(H, Hkv, Nq, Nk);
-  p.view.lens = key_lens;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
-  p.o = static_cast<const __nv_bfloat16*>(o);
-  p.dout = static_cast<const __nv_bfloat16*>(dout);
-  p.lse = lse;
-  p.dq = static_cast<__nv_bfloat16*>(dq);
-  p.dk = static_cast<__nv_bfloat16*>(dk);
-  p.dv = static_cast<__nv_bfloat16*>(dv);
-  p.delta = static_cast<float*>(workspace);
-  p.B = B;
-  p.scale = scale;
-  const long long rows = ((long long)B * Hkv * R + 7) / 8, keys = ((long long)B * Hkv * Nk + 7) / 8;
-  if (rows > 0x7fffffffLL || keys > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  if (d == 128) {
-    fa::fa_cross_dq_kernel<128><<<(unsigned)rows, 256, 0, stream>>>(p);
-    fa::fa_cross_dkv_kernel<128><<<(unsigned)keys, 256, 0, stream>>>(p);
-  } else {
-    fa::fa_cross_dq_kernel<64><<<(unsigned)rows, 256, 0, stream>>>(p);
-    fa::fa_cross_dkv_kernel<64><<<(unsigned)keys, 256, 0, stream>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  fa::CrossView view = cross_view(H, Hkv, Nq, Nk);
+  view.lens = key_lens;
+  if (d == 128)
+    return run_cross_bwd<128>(view, q, k, v, o, dout, lse, dq, dk, dv, workspace, B, scale, stream);
+  return run_cross_bwd<64>(view, q, k, v, o, dout, lse, dq, dk, dv, workspace, B, scale, stream);
 }
 
 size_t fa_tree_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d) {

@@ -6,6 +6,7 @@
 
 #include "fa_cross.cuh"
 #include "fa_cross_fwd.cuh"
+#include "fa_cross_bwd.cuh"
 #include "fa_rope.cuh"
 #include "fa_cross_api.cuh"
 #include "fa_rope_api.cuh"
