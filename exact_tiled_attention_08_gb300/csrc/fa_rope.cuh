@@ -16,9 +16,11 @@
 // 32 bits are the angle to 2^-32 of a turn at any 32-bit position.
 //
 // Both are bound by memory: a row is read once and written once.  A lane holds
-// 8 values (16 bytes), D / 8 lanes a row, so a warp moves 32 * 16 bytes per
-// access; the cosines and sines of a token are computed once per warp and used
-// for `head_step` heads.  Statistics and rotation are fp32, rounded once.
+// 8 values of a row, D / 8 lanes a row; it holds whole pairs (in the half layout
+// 4 values of each half, two 8-byte accesses), so that the rotation needs no
+// other lane, and keeps 4 cosines and sines for the heads of its token.  The
+// rows of kRopeUnroll heads are loaded before the first is used.  Statistics
+// and rotation are fp32, rounded once.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,26 +45,11 @@ struct RopeParams {
   float* partials;                       // backward: [gridDim.x][2][d] sums of the weight gradients
   int N, H, Hkv, C, rot;
   long long tokens;     // B * N
-  int head_step;        // heads handled by one unit of work
-  int head_groups;      // ceil((H + Hkv + Hkv) / head_step)
-  long long units;      // token groups * head_groups
+  int head_step;        // heads (of H + Hkv + Hkv) that a warp takes for its tokens
+  long long units;      // warps' units of work: token groups * ceil(heads / head_step)
   float eps, factor;
   int norm;
 };
-
-// a token's 8 values from and to bf16
-__device__ __forceinline__ void rope_unpack(const uint4& a, float (&x)[8]) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ uint4 rope_pack(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
 
 // freq / 2 pi as a binary fraction of a turn (whole turns dropped)
 __device__ __forceinline__ unsigned long long rope_turns(double freq) {
@@ -79,52 +66,64 @@ __device__ __forceinline__ void rope_angle(unsigned long long turns, int pos, fl
   s *= f;
 }
 
-// The rotation of a lane's 8 values.  kInterleaved: 4 pairs of its own;
-// otherwise 8 values whose partners another lane holds (`peer`), the sine
-// carrying the sign of this lane's half.
-template <bool kInterleaved>
-struct RopeTurn {
-  static constexpr int kAngles = kInterleaved ? 4 : 8;
-  float c[kAngles], s[kAngles];
-  int peer;     // lane of the partner values
-  bool active;  // the lane's values are in the rotated part
-
-  __device__ __forceinline__ void setup(const unsigned long long* turns, int rot, int sub, int lane, int pos, float f) {
-    const int half = rot >> 4;  // lanes of half the rotated part
-    active = 8 * sub < rot;
-    peer = lane;
-    if (!active) return;
-    if (kInterleaved) {
+// 8 values of a row: 4 from element e0 and 4 from e1
+struct RopeLane {
+  float x[8];
+  __device__ __forceinline__ void unpack(const uint2& lo, const uint2& hi) {
+    const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-      for (int i = 0; i < kAngles; ++i) rope_angle(turns[4 * sub + i], pos, f, c[i], s[i]);
-    } else {
-      const bool low = sub < half;
-      peer = low ? lane + half : lane - half;
-      const int first = 8 * (low ? sub : sub - half);
-#pragma unroll
-      for (int i = 0; i < kAngles; ++i) {
-        rope_angle(turns[first + i], pos, f, c[i], s[i]);
-        if (low) s[i] = -s[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  // every lane of the warp takes part
+};
+
+struct RopeRaw {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ RopeRaw rope_load(const __nv_bfloat16* row, int e0, int e1, bool valid) {
+  RopeRaw r{make_uint2(0, 0), make_uint2(0, 0)};
+  if (valid) {
+    r.lo = __ldg(reinterpret_cast<const uint2*>(row + e0));
+    r.hi = __ldg(reinterpret_cast<const uint2*>(row + e1));
+  }
+  return r;
+}
+__device__ __forceinline__ void rope_store(__nv_bfloat16* row, int e0, int e1, const RopeLane& v) {
+  *reinterpret_cast<uint2*>(row + e0) = make_uint2(pack_bf16x2(v.x[0], v.x[1]), pack_bf16x2(v.x[2], v.x[3]));
+  *reinterpret_cast<uint2*>(row + e1) = make_uint2(pack_bf16x2(v.x[4], v.x[5]), pack_bf16x2(v.x[6], v.x[7]));
+}
+
+// The rotation of a lane's values for one token: pairs (x[i], x[4 + i]) of the
+// halves, or (x[2 i], x[2 i + 1]) interleaved.
+template <bool kInterleaved>
+struct RopeTurn {
+  float c[4], s[4];
+  bool active;  // the lane's values are in the rotated part
+
+  // a lane's elements: e0 .. e0 + 3 and e1 .. e1 + 3
+  static __device__ __forceinline__ void place(int rot, int sub, int& e0, int& e1) {
+    const bool pairs = !kInterleaved && 8 * sub < rot;
+    e0 = pairs ? 4 * sub : 8 * sub;
+    e1 = pairs ? (rot >> 1) + 4 * sub : 8 * sub + 4;
+  }
+  __device__ __forceinline__ void setup(const unsigned long long* turns, int rot, int sub, int pos, float f) {
+    active = 8 * sub < rot;
+    if (!active) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rope_angle(turns[4 * sub + i], pos, f, c[i], s[i]);
+  }
   template <bool kBack>
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
-    if (kInterleaved) {
-      if (!active) return;
+  __device__ __forceinline__ void apply(RopeLane& v) const {
+    if (!active) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1], sn = kBack ? -s[i % kAngles] : s[i % kAngles];
-        x[2 * i] = fmaf(a, c[i % kAngles], -b * sn);
-        x[2 * i + 1] = fmaf(a, sn, b * c[i % kAngles]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], peer);
-        if (active) x[i] = fmaf(x[i], c[i % kAngles], kBack ? -(y * s[i % kAngles]) : y * s[i % kAngles]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      constexpr int kStep = kInterleaved ? 1 : 4;
+      float &a = v.x[kInterleaved ? 2 * i : i], &b = v.x[(kInterleaved ? 2 * i : i) + kStep];
+      const float sn = kBack ? -s[i] : s[i], a0 = a;
+      a = fmaf(a0, c[i], -b * sn);
+      b = fmaf(a0, sn, b * c[i]);
     }
   }
 };
@@ -137,139 +136,196 @@ __device__ __forceinline__ float rope_row_sum(float v) {
 }
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;
+// CTAs held by an SM.  (Measured, forward and backward with the norm, 16384 and
+// 8004 tokens of 48 heads: 3 and 2 take 78 and 71 us; 4 and 3, with their rows
+// spilled, 101 and 84 us.)
+constexpr int kRopeFwdPerSm = 3, kRopeBwdPerSm = 2;
 
-// the 8 weights of a lane (ones without a weight)
-__device__ __forceinline__ void rope_weights(const float* w, int sub, float (&out)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = w ? __ldg(w + 8 * sub + i) : 1.f;
+// the weights of a lane's values (ones without a weight)
+__device__ __forceinline__ void rope_weights(const float* w, int e0, int e1, float (&out)[8]) {
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  const float4 a = w ? __ldg(reinterpret_cast<const float4*>(w + e0)) : one;
+  const float4 b = w ? __ldg(reinterpret_cast<const float4*>(w + e1)) : one;
+  out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+  out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
 }
 
-template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_fwd_kernel(const RopeParams p) {
-  constexpr int kLanes = D / 8, kTokens = 32 / kLanes;  // lanes per row, tokens per warp
-  __shared__ unsigned long long turns[64];
-  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = rope_turns(p.inv_freq[i]);
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
-  const long long token_groups = (p.tokens + kTokens * (kRopeThreads / 32) - 1) / (kTokens * (kRopeThreads / 32));
-  for (long long unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-    const long long group = unit % token_groups;
-    const int h0 = (int)(unit / token_groups) * p.head_step;
-    const int h1 = min(h0 + p.head_step, p.H + 2 * p.Hkv);
-    const long long token = (group * (kRopeThreads / 32) + warp) * kTokens + mine;
-    const bool valid = token < p.tokens;
-    const int b = valid ? (int)(token / p.N) : 0;
-    const int n = valid ? (int)(token - (long long)b * p.N) : 0;
-    const int start = p.starts ? __ldg(p.starts + b) : 0;
-    const int pos = p.positions ? __ldg(p.positions + (valid ? token : 0)) : start + n;
-    const long long row = (long long)start + n;  // row of this token in k_out and v_out
-    const bool stored = valid && row >= 0 && row < p.C;
-    RopeTurn<kInterleaved> turn;
-    turn.setup(turns, p.rot, sub, lane, pos, p.factor);
-    for (int h = h0; h < h1; ++h) {
-      const int kind = h < p.H ? 0 : (h < p.H + p.Hkv ? 1 : 2);
-      const int head = kind == 0 ? h : (kind == 1 ? h - p.H : h - p.H - p.Hkv);
-      const RopeRows& in = kind == 0 ? p.q : (kind == 1 ? p.k : p.v);
-      if (!in.ptr) continue;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (valid)
-        raw = __ldg(reinterpret_cast<const uint4*>(in.ptr + b * in.batch + n * in.token + head * in.head) + sub);
-      if (kind < 2) {
-        float x[8];
-        rope_unpack(raw, x);
-        if (p.norm) {
-          float ss = 0.f, w[8];
+// A warp's tokens in a unit of work, one per D / 8 lanes.
+struct RopeToken {
+  int b, n, sub;
+  long long token;
+  bool valid;
+  int h0, h1;  // heads of q, k and v, counted on
+};
+template <int D>
+__device__ __forceinline__ RopeToken rope_token(const RopeParams& p, long long unit) {
+  constexpr int kLanes = D / 8, kTokens = 32 / kLanes;
+  const long long groups = (p.tokens + kTokens - 1) / kTokens;
+  const int lane = threadIdx.x & 31;
+  RopeToken t;
+  const int step = (int)(unit / groups);
+  t.token = (unit - step * groups) * kTokens + lane / kLanes;
+  t.sub = lane % kLanes;
+  t.valid = t.token < p.tokens;
+  t.b = t.valid ? (int)(t.token / p.N) : 0;
+  t.n = t.valid ? (int)(t.token - (long long)t.b * p.N) : 0;
+  t.h0 = step * p.head_step;
+  t.h1 = min(t.h0 + p.head_step, p.H + 2 * p.Hkv);
+  return t;
+}
+
+// heads [h0, h1) of one of q, k, v: norm, rotation and store
+template <int D, bool kInterleaved, bool kNorm, bool kTurn>
+__device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& turn, const __nv_bfloat16* in,
+                                               long long in_head, __nv_bfloat16* out, long long out_head, int h0,
+                                               int h1, int e0, int e1, bool valid, bool stored, const float* weight,
+                                               float eps) {
+  float w[8];
+  if (kNorm) rope_weights(weight, e0, e1, w);
+  RopeRaw raw[kRopeUnroll];  // the next rows, on their way
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-          const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + p.eps);
-          rope_weights(kind ? p.k_weight : p.q_weight, sub, w);
+  for (int u = 0; u < kRopeUnroll; ++u) raw[u] = rope_load(in + (h0 + u) * in_head, e0, e1, valid && h0 + u < h1);
+  for (int h = h0; h < h1; h += kRopeUnroll) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
-        }
-        turn.template apply<false>(x);
-        raw = rope_pack(x);
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      RopeLane v;
+      v.unpack(raw[u].lo, raw[u].hi);
+      raw[u] = rope_load(in + (h + u + kRopeUnroll) * in_head, e0, e1, valid && h + u + kRopeUnroll < h1);
+      if (kNorm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v.x[i], v.x[i], ss);
+        const float r = rsqrtf(rope_row_sum<D / 8>(ss) * (1.f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.x[i] *= r * w[i];
       }
-      if (kind == 0) {
-        if (valid) reinterpret_cast<uint4*>(p.q_out + (((long long)b * p.H + head) * p.N + n) * D)[sub] = raw;
-      } else if (stored) {
-        __nv_bfloat16* out = kind == 1 ? p.k_out : p.v_out;
-        reinterpret_cast<uint4*>(out + (((long long)b * p.Hkv + head) * p.C + row) * D)[sub] = raw;
-      }
+      if (kTurn) turn.template apply<false>(v);
+      if (stored && h + u < h1) rope_store(out + (h + u) * out_head, e0, e1, v);
     }
   }
 }
 
-// Backward.  The weight gradients are summed in registers over a CTA's rows,
-// over its warps in a fixed order, and over the CTAs by fa_rope_dw_kernel, so
-// they are the same from run to run.
-template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_bwd_kernel(const RopeParams p) {
-  constexpr int kLanes = D / 8, kTokens = 32 / kLanes;
+template <int D, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kernel(const RopeParams p) {
   __shared__ unsigned long long turns[64];
-  __shared__ float sums[kRopeThreads / 32][2][D];
   for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = rope_turns(p.inv_freq[i]);
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
-  const long long token_groups = (p.tokens + kTokens * (kRopeThreads / 32) - 1) / (kTokens * (kRopeThreads / 32));
+  for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); unit < p.units;
+       unit += (long long)gridDim.x * (kRopeThreads / 32)) {
+    const RopeToken t = rope_token<D>(p, unit);
+    const int start = p.starts ? __ldg(p.starts + t.b) : 0;
+    const int pos = p.positions ? __ldg(p.positions + (t.valid ? t.token : 0)) : start + t.n;
+    const long long row = (long long)start + t.n;  // row of this token in k_out and v_out
+    const bool stored = t.valid && row >= 0 && row < p.C;
+    int e0, e1;
+    RopeTurn<kInterleaved>::place(p.rot, t.sub, e0, e1);
+    RopeTurn<kInterleaved> turn;
+    if (t.h0 < p.H + p.Hkv) turn.setup(turns, p.rot, t.sub, pos, p.factor);
+    auto in = [&](const RopeRows& r) { return r.ptr + t.b * r.batch + t.n * r.token; };
+    if (p.q.ptr && t.h0 < p.H)
+      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, in(p.q), p.q.head,
+                                                   p.q_out + ((long long)t.b * p.H * p.N + t.n) * D,
+                                                   (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1, t.valid, t.valid,
+                                                   p.q_weight, p.eps);
+    const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D, next = (long long)p.C * D;
+    if (p.k.ptr)
+      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, in(p.k), p.k.head, p.k_out + cache, next, max(t.h0 - p.H, 0),
+                                                   min(t.h1 - p.H, p.Hkv), e0, e1, t.valid, stored, p.k_weight, p.eps);
+    if (p.v.ptr)
+      rope_fwd_heads<D, kInterleaved, false, false>(turn, in(p.v), p.v.head, p.v_out + cache, next,
+                                                    max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
+                                                    stored, nullptr, 0.f);
+  }
+}
+
+// heads [h0, h1) of one of q, k, v, backwards: dw gathers g o x^ of its rows
+template <int D, bool kInterleaved, bool kNorm, bool kTurn>
+__device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& turn, const __nv_bfloat16* dy,
+                                               long long dy_head, const __nv_bfloat16* in, long long in_head,
+                                               __nv_bfloat16* out, long long out_head, int h0, int h1, int e0, int e1,
+                                               bool valid, const float* weight, float eps, float (&dw)[8]) {
+  constexpr int U = kNorm ? kRopeUnroll / 2 : kRopeUnroll;  // (two rows each with the norm)
+  float w[8];
+  if (kNorm) rope_weights(weight, e0, e1, w);
+  RopeRaw raw[U], xraw[U];  // the next rows, on their way
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    raw[u] = rope_load(dy + (h0 + u) * dy_head, e0, e1, valid && h0 + u < h1);
+    if (kNorm) xraw[u] = rope_load(in + (h0 + u) * in_head, e0, e1, valid && h0 + u < h1);
+  }
+  for (int h = h0; h < h1; h += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool more = valid && h + u + U < h1;
+      RopeLane g;
+      g.unpack(raw[u].lo, raw[u].hi);
+      raw[u] = rope_load(dy + (h + u + U) * dy_head, e0, e1, more);
+      if (kTurn) turn.template apply<true>(g);
+      if (kNorm) {
+        RopeLane x;
+        x.unpack(xraw[u].lo, xraw[u].hi);
+        xraw[u] = rope_load(in + (h + u + U) * in_head, e0, e1, more);
+        // rows that are not there were loaded as zeros: they add nothing
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(x.x[i], x.x[i], ss);
+          dot = fmaf(g.x[i] * w[i], x.x[i], dot);
+        }
+        const float r = rsqrtf(rope_row_sum<D / 8>(ss) * (1.f / D) + eps);
+        dot = rope_row_sum<D / 8>(dot) * (1.f / D) * r;  // mean(w g x^)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x.x[i] = h + u < h1 && valid ? x.x[i] * r : 0.f;
+          dw[i] = fmaf(g.x[i], x.x[i], dw[i]);
+          g.x[i] = r * fmaf(-x.x[i], dot, g.x[i] * w[i]);
+        }
+      }
+      if (valid && h + u < h1) rope_store(out + (h + u) * out_head, e0, e1, g);
+    }
+  }
+}
+
+// Backward.  The weight gradients are summed in registers over a warp's rows,
+// over a CTA's warps in a fixed order, and over the CTAs by fa_rope_dw_kernel,
+// so they are the same from run to run.
+template <int D, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kernel(const RopeParams p) {
+  constexpr int kLanes = D / 8;
+  __shared__ unsigned long long turns[64];
+  __shared__ float sums[kNorm ? kRopeThreads / 32 : 1][2][D];
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = rope_turns(p.inv_freq[i]);
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-  for (long long unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-    const long long group = unit % token_groups;
-    const int h0 = (int)(unit / token_groups) * p.head_step;
-    const int h1 = min(h0 + p.head_step, p.H + 2 * p.Hkv);
-    const long long token = (group * (kRopeThreads / 32) + warp) * kTokens + mine;
-    const bool valid = token < p.tokens;
-    const int b = valid ? (int)(token / p.N) : 0;
-    const int n = valid ? (int)(token - (long long)b * p.N) : 0;
-    const int pos = p.positions ? __ldg(p.positions + (valid ? token : 0)) : n;
+  int e0, e1;
+  RopeTurn<kInterleaved>::place(p.rot, lane % kLanes, e0, e1);
+  for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + warp; unit < p.units;
+       unit += (long long)gridDim.x * (kRopeThreads / 32)) {
+    const RopeToken t = rope_token<D>(p, unit);
+    const int pos = p.positions ? __ldg(p.positions + (t.valid ? t.token : 0)) : t.n;
     RopeTurn<kInterleaved> turn;
-    turn.setup(turns, p.rot, sub, lane, pos, p.factor);
-    for (int h = h0; h < h1; ++h) {
-      const int kind = h < p.H ? 0 : (h < p.H + p.Hkv ? 1 : 2);
-      const int head = kind == 0 ? h : (kind == 1 ? h - p.H : h - p.H - p.Hkv);
-      const RopeRows& out = kind == 0 ? p.dq : (kind == 1 ? p.dk : p.dv);
-      if (!out.ptr) continue;
-      const __nv_bfloat16* dy = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
-      const int heads = kind == 0 ? p.H : p.Hkv;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (valid) raw = __ldg(reinterpret_cast<const uint4*>(dy + (((long long)b * heads + head) * p.N + n) * D) + sub);
-      if (kind < 2) {
-        float g[8];
-        rope_unpack(raw, g);
-        turn.template apply<true>(g);
-        if (p.norm) {
-          const RopeRows& in = kind ? p.k : p.q;
-          uint4 xraw = make_uint4(0, 0, 0, 0);
-          if (valid)
-            xraw = __ldg(reinterpret_cast<const uint4*>(in.ptr + b * in.batch + n * in.token + head * in.head) + sub);
-          float x[8], w[8];
-          rope_unpack(xraw, x);
-          rope_weights(kind ? p.k_weight : p.q_weight, sub, w);
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-          const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] *= r;
-            const float gx = valid ? g[i] * x[i] : 0.f;
-            if (kind) dw[1][i] += gx; else dw[0][i] += gx;
-            g[i] *= w[i];
-            dot = fmaf(g[i], x[i], dot);
-          }
-          dot = rope_row_sum<kLanes>(dot) * (1.f / D);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-x[i], dot, g[i]);
-        }
-        raw = rope_pack(g);
-      }
-      if (valid)
-        reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(out.ptr) + b * out.batch + n * out.token +
-                                 head * out.head)[sub] = raw;
-    }
+    if (t.h0 < p.H + p.Hkv) turn.setup(turns, p.rot, t.sub, pos, p.factor);
+    auto at = [&](const RopeRows& r) { return const_cast<__nv_bfloat16*>(r.ptr) + t.b * r.batch + t.n * r.token; };
+    const long long next = (long long)p.N * D, kv = ((long long)t.b * p.Hkv * p.N + t.n) * D;
+    if (p.dq.ptr && t.h0 < p.H)
+      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, p.q_out + ((long long)t.b * p.H * p.N + t.n) * D, next,
+                                                   at(p.q), p.q.head, at(p.dq), p.dq.head, t.h0, min(t.h1, p.H), e0,
+                                                   e1, t.valid, p.q_weight, p.eps, dw[0]);
+    if (p.dk.ptr)
+      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, p.k_out + kv, next, at(p.k), p.k.head, at(p.dk), p.dk.head,
+                                                   max(t.h0 - p.H, 0), min(t.h1 - p.H, p.Hkv), e0, e1, t.valid,
+                                                   p.k_weight, p.eps, dw[1]);
+    if (p.dv.ptr)
+      rope_bwd_heads<D, kInterleaved, false, false>(turn, p.v_out + kv, next, nullptr, 0, at(p.dv), p.dv.head,
+                                                    max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
+                                                    nullptr, 0.f, dw[1]);
   }
-  if (!p.partials) return;
+  if constexpr (kNorm) {
+    if (!p.partials) return;
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -277,13 +333,14 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_bwd_kernel(const RopePar
       float v = dw[t][i];
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (mine == 0) sums[warp][t][8 * sub + i] = v;
+      if (lane < kLanes) sums[warp][t][(i < 4 ? e0 : e1) + (i & 3)] = v;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {
     float v = 0.f;
     for (int w = 0; w < kRopeThreads / 32; ++w) v += (&sums[w][0][0])[i];
     p.partials[(long long)blockIdx.x * 2 * D + i] = v;
+  }
   }
 }
 

@@ -6,7 +6,8 @@
 
 namespace {
 
-constexpr int kRopeBwdCtas = 152 * 4;  // CTAs of the backward, each with a row of weight gradient sums
+constexpr int kRopeFwdCtas = 152 * fa::kRopeFwdPerSm;
+constexpr int kRopeBwdCtas = 152 * fa::kRopeBwdPerSm;  // CTAs of the backward, each with a row of weight gradient sums
 
 fa_status check_rows(const fa_rows& r) {
   if (!aligned16(r.ptr) || r.batch % 8 || r.token % 8 || r.head % 8) return FA_ERR_MISALIGNED;
@@ -61,15 +62,32 @@ fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
   return FA_OK;
 }
 
-// work units of a launch: groups of tokens (one pass of a CTA's warps) times
-// groups of heads
-void rope_units(fa::RopeParams& p, int d) {
-  const long long per_cta = (fa::kRopeThreads / 32) * (32 / (d / 8));
-  const long long groups = (p.tokens + per_cta - 1) / per_cta;
+// Warps' units of work: a warp's tokens times `head_step` heads.  All heads of a
+// token share its angles, so a unit takes as many as leave eight units for every
+// warp that the device holds at once (`warps`), whose number of turns is then
+// nearly even; a few tokens' heads are spread over the warps one by one.
+void rope_units(fa::RopeParams& p, int d, long long warps) {
+  const long long per_warp = 32 / (d / 8), groups = (p.tokens + per_warp - 1) / per_warp;
   const int heads = p.H + 2 * p.Hkv;
-  p.head_step = 8;
-  p.head_groups = (heads + p.head_step - 1) / p.head_step;
-  p.units = groups * p.head_groups;
+  const long long steps = std::max<long long>(1, std::min<long long>(heads, (8 * warps + groups - 1) / groups));
+  p.head_step = (int)((heads + steps - 1) / steps);
+  p.units = groups * ((heads + p.head_step - 1) / p.head_step);
+}
+
+template <int D, bool kNorm>
+void launch_rope_fwd(const fa::RopeParams& p, unsigned grid, int interleaved, cudaStream_t stream) {
+  if (interleaved)
+    fa::fa_rope_fwd_kernel<D, true, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  else
+    fa::fa_rope_fwd_kernel<D, false, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+}
+
+template <int D, bool kNorm>
+void launch_rope_bwd(const fa::RopeParams& p, unsigned grid, int interleaved, cudaStream_t stream) {
+  if (interleaved)
+    fa::fa_rope_bwd_kernel<D, true, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  else
+    fa::fa_rope_bwd_kernel<D, false, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -113,19 +131,12 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  rope_units(p, d);
-  const unsigned grid = (unsigned)std::min<long long>(p.units, 152LL * 8);
-  if (d == 128) {
-    if (interleaved)
-      fa::fa_rope_fwd_kernel<128, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-    else
-      fa::fa_rope_fwd_kernel<128, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved)
-      fa::fa_rope_fwd_kernel<64, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-    else
-      fa::fa_rope_fwd_kernel<64, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  }
+  rope_units(p, d, kRopeFwdCtas * 8LL);
+  const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeFwdCtas);
+  if (d == 128)
+    norm ? launch_rope_fwd<128, true>(p, grid, interleaved, stream) : launch_rope_fwd<128, false>(p, grid, interleaved, stream);
+  else
+    norm ? launch_rope_fwd<64, true>(p, grid, interleaved, stream) : launch_rope_fwd<64, false>(p, grid, interleaved, stream);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -187,19 +198,12 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  rope_units(p, d);
-  const unsigned grid = (unsigned)std::min<long long>(p.units, kRopeBwdCtas);
-  if (d == 128) {
-    if (interleaved)
-      fa::fa_rope_bwd_kernel<128, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-    else
-      fa::fa_rope_bwd_kernel<128, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved)
-      fa::fa_rope_bwd_kernel<64, true><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-    else
-      fa::fa_rope_bwd_kernel<64, false><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  }
+  rope_units(p, d, kRopeBwdCtas * 8LL);
+  const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeBwdCtas);
+  if (d == 128)
+    norm ? launch_rope_bwd<128, true>(p, grid, interleaved, stream) : launch_rope_bwd<128, false>(p, grid, interleaved, stream);
+  else
+    norm ? launch_rope_bwd<64, true>(p, grid, interleaved, stream) : launch_rope_bwd<64, false>(p, grid, interleaved, stream);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (weights) {
     fa::fa_rope_dw_kernel<<<2 * d / 8, 256, 0, stream>>>(p.partials, (int)grid, d, dq_weight, dk_weight);
