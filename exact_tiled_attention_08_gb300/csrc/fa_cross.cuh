@@ -13,6 +13,15 @@
 
 namespace fa {
 
+// Programmatic dependent launch: a kernel launched with it may start before the
+// kernel in front of it has ended.  grid_wait() returns once that one has
+// ended and its writes are visible (at once without such a launch): nothing in
+// global memory is read or written before it, and nothing that an earlier
+// kernel may have written is read through the read-only path (__ldg).  grid_trigger() lets the next
+// kernel start; all of a kernel's CTAs have to come by (or end) first.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // What the rows see.  Keys [0, len) of the request are visible to every row;
 // with drafts, key len + t is visible to the row of token n when t < drafts
 // and bit t of masks[b][n] is set (without masks: t <= n), and the rows of
@@ -27,14 +36,11 @@ struct CrossView {
   int R;                              // query rows per key/value head (G Nq)
   int Hkv;
   __device__ __forceinline__ int len(int b) const {
-    return lens ? min(max(__ldg(lens + b), 0), Nk) : (T ? max(Nk - T, 0) : Nk);
+    return lens ? min(max(lens[b], 0), Nk) : (T ? max(Nk - T, 0) : Nk);
   }
   // drafts of request b that have a key row
   __device__ __forceinline__ int drafted(int b, int len) const {
-    return T ? min(min(max(drafts ? __ldg(drafts + b) : T, 0), T), Nk - len) : 0;
-  }
-  __device__ __forceinline__ bool sees(int b, int n, int t) const {
-    return masks ? ((__ldg(masks + (long long)b * T + n) >> t) & 1) : t <= n;
+    return T ? min(min(max(drafts ? drafts[b] : T, 0), T), Nk - len) : 0;
   }
 };
 

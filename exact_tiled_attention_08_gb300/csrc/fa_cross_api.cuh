@@ -24,6 +24,26 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// Launch with programmatic stream serialization: the kernel may start while the
+// one in front of it ends (it calls grid_wait before it touches memory).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   fa::CrossView v{};
   v.Nk = Nk;
@@ -33,8 +53,8 @@ fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   return v;
 }
 
-// Grid and workspace of the forward: CTAs (at most one per SM, and one per key
-// block), and two parts per CTA where an item can be cut (more than one block).
+// Grid and workspace of the forward: CTAs (at most one per SM, and one per
+// place), and two parts per CTA where an item can be cut (more than one block).
 struct CrossFwdPlan {
   int row_tiles, part_rows, ctas;
   bool pair, cuts;
@@ -44,7 +64,7 @@ struct CrossFwdPlan {
     w.pair = R > 128;
     w.row_tiles = w.pair ? (R + 255) / 256 : 1;
     w.part_rows = w.pair ? 256 : R;
-    const long long blocks = (long long)B * Hkv * w.row_tiles * ((Nk + 127LL) / 128);
+    const long long blocks = (long long)B * Hkv * w.row_tiles * ((Nk + 127LL) / 128 + fa::kCrossStart);
     w.ctas = (int)std::min<long long>(blocks, fa::kCrossMaxCtas);
     w.cuts = Nk > 128;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -71,12 +91,13 @@ fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const C
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return FA_ERR_CUDA;
   const int grid = std::min(plan.ctas, sms);
-  kernel<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_early(kernel, dim3((unsigned)grid), C::kThreads, C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
+    return FA_ERR_CUDA;
   if (plan.cuts) {
-    const dim3 rows((unsigned)grid, (unsigned)((plan.part_rows + 7) / 8));
-    fa::fa_cross_combine_kernel<D, TREE, PAIR><<<rows, 256, 0, stream>>>(p, grid);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    const int per_block = PAIR ? 32 : 8;  // rows of a block
+    const dim3 rows((unsigned)grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
+    if (launch_early(fa::fa_cross_combine_kernel<D, TREE, PAIR>, rows, 256, 0, stream, p) != cudaSuccess)
+      return FA_ERR_CUDA;
   }
   return FA_OK;
 }
@@ -168,10 +189,10 @@ fa_status run_cross_bwd(const fa::CrossView& view, const void* q, const void* k,
     return FA_ERR_CUDA;
   const long long rows = (long long)BK * rpad, per_block = 256 / (D / 8);
   const long long prep = std::min((rows + per_block - 1) / per_block, 152LL * 16);
-  fa::fa_cross_bwd_prep_kernel<D><<<(unsigned)prep, 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, delta, lse2, dq_acc, R, rpad,
-      rows);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_early(fa::fa_cross_bwd_prep_kernel<D>, dim3((unsigned)prep), 256, 0, stream,
+                   static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, delta, lse2,
+                   dq_acc, R, rpad, rows) != cudaSuccess)
+    return FA_ERR_CUDA;
   fa::CrossBwdPostParams post{};
   fa::CrossBwdParams& p = post.p;
   p.view = view;
@@ -189,16 +210,18 @@ fa_status run_cross_bwd(const fa::CrossView& view, const void* q, const void* k,
   // one CTA per SM, and no more than there are query blocks to hand out
   const long long blocks = (long long)BK * ((view.Nk + 127LL) / 128) * std::min(nqb, fa::kCrossBwdMaxParts);
   const int grid = (int)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
-  kernel<<<(unsigned)grid, C::kThreads, fa::kCrossBwdSmemBytes<D>, stream>>>(mq, mk, mv, mdo, ml, mdel, mdq, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_early(kernel, dim3((unsigned)grid), C::kThreads, fa::kCrossBwdSmemBytes<D>, stream, mq, mk, mv, mdo, ml,
+                   mdel, mdq, p) != cudaSuccess)
+    return FA_ERR_CUDA;
   post.dq_acc = dq_acc;
   post.dq = static_cast<__nv_bfloat16*>(dq);
   post.n8 = (long long)BK * R * D / 8;
   post.ctas = grid;
   const long long convert = std::min((post.n8 + 255) / 256, 152LL * 16);
   const long long post_grid = 8LL * grid + (view.lens ? BK : 0) + convert;
-  fa::fa_cross_bwd_post_kernel<D><<<(unsigned)post_grid, 256, 0, stream>>>(post);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_early(fa::fa_cross_bwd_post_kernel<D>, dim3((unsigned)post_grid), 256, 0, stream, post) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 }  // namespace

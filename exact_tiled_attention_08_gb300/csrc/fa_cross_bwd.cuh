@@ -166,12 +166,12 @@ enum : int { kSiteCrossBwdClean = 60 };
 // for rows without keys, so that P = 0 there); the dQ accumulator is zeroed.
 template <int D>
 __global__ void __launch_bounds__(256)
-    fa_cross_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
-                             const float* __restrict__ lse, float* __restrict__ delta_pad,
-                             float* __restrict__ lse2_pad, float* __restrict__ dq_acc, int R, int Rpad,
-                             long long padded_rows) {
+    fa_cross_bwd_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, float* delta_pad,
+                             float* lse2_pad, float* dq_acc, int R, int Rpad, long long padded_rows) {
   constexpr int kThreadsPerRow = D / 8, kRows = 256 / kThreadsPerRow;
   const int sub = threadIdx.x % kThreadsPerRow;
+  grid_wait();
+  grid_trigger();
   for (long long prow = (long long)blockIdx.x * kRows + threadIdx.x / kThreadsPerRow;
        prow - threadIdx.x / kThreadsPerRow < padded_rows; prow += (long long)gridDim.x * kRows) {
     const long long bk = prow / Rpad;
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(256)
     const long long row = bk * R + n;
     float s = 0.f;
     if (valid) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(o + row * D) + sub);
-      const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + row * D) + sub);
+      const uint4 a = reinterpret_cast<const uint4*>(o + row * D)[sub];
+      const uint4 g = reinterpret_cast<const uint4*>(dout + row * D)[sub];
       const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
       const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
 #pragma unroll
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int off = kThreadsPerRow / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (in_range && sub == 0) {
-      const float l = valid ? __ldg(lse + row) : -CUDART_INF_F;
+      const float l = valid ? lse[row] : -CUDART_INF_F;
       delta_pad[prow] = valid ? s : 0.f;
       lse2_pad[prow] = l == -CUDART_INF_F ? CUDART_INF_F : l * 1.4426950408889634f;
     }
@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(512, 1)
     tma_prefetch_map(&map_delta);
     tma_prefetch_map(&map_dq);
   }
+  grid_wait();
   cross_bwd_plan<C::kThreads>(p, reinterpret_cast<int*>(sRing), &xbar->plan);
   fence_async_shared();  // the ring's first copies follow the plan's plain writes
   tc_fence_before();
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
+  grid_trigger();
   const CrossBwdPlan plan = xbar->plan;
   CrossBwdWalk at;  // every role walks the same segments
   CrossBwdSeg t;
@@ -708,6 +710,8 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_cross_bwd_post_kernel(const CrossBwdPostParams q) {
   const CrossBwdParams& p = q.p;
   const CrossView& v = p.view;
+  grid_wait();
+  grid_trigger();
   const int cut_blocks = 8 * q.ctas, zero_blocks = v.lens ? p.B * v.Hkv : 0;
   int x = blockIdx.x;
   if (x < cut_blocks) {
@@ -753,8 +757,8 @@ __global__ void __launch_bounds__(256) fa_cross_bwd_post_kernel(const CrossBwdPo
   x -= zero_blocks;
   for (long long i = (long long)x * 256 + threadIdx.x; i < q.n8;
        i += (long long)(gridDim.x - cut_blocks - zero_blocks) * 256) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(q.dq_acc) + 2 * i);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(q.dq_acc) + 2 * i + 1);
+    const float4 a = reinterpret_cast<const float4*>(q.dq_acc)[2 * i];
+    const float4 b = reinterpret_cast<const float4*>(q.dq_acc)[2 * i + 1];
     reinterpret_cast<uint4*>(q.dq)[i] =
         make_uint4(pack_bf16x2(a.x * p.scale, a.y * p.scale), pack_bf16x2(a.z * p.scale, a.w * p.scale),
                    pack_bf16x2(b.x * p.scale, b.y * p.scale), pack_bf16x2(b.z * p.scale, b.w * p.scale));

@@ -6,12 +6,13 @@
 // warpgroups hold a row of scores per thread.  What differs:
 //
 // Work.  The keys of every (request, key/value head, row tile) are cut into
-// blocks of 128, all of them form one sequence, and CTA c of G takes the
-// blocks [c Tot / G, (c + 1) Tot / G) of it: the CTAs' shares differ by one
-// block whatever the requests' lengths, and few rows over many keys use every
-// SM.  An item that lies within one CTA's share is written directly; one cut by
-// a share's end leaves a normalised fp32 O and a log-sum-exp per row and part
-// (at most two parts per CTA) that fa_cross_combine_kernel joins in CTA order.
+// blocks of 128; all items' blocks, each item's after a place or two for what a
+// segment costs at its ends, form one sequence, and CTA c of G takes the places
+// [c Tot / G, (c + 1) Tot / G) of it: the CTAs' shares are even whatever the
+// requests' lengths, and few rows over many keys use every SM.  An item that
+// lies within one CTA's share is written directly; one cut by a share's end
+// leaves a normalised fp32 O and a log-sum-exp per row and part (at most two
+// parts per CTA) that fa_cross_combine_kernel joins in CTA order.
 //
 // The two softmax warpgroups.  With more than 128 rows per key/value head
 // (PAIR) they take two row tiles that share each key block, as in
@@ -37,9 +38,8 @@ constexpr int kCrossMaxCtas = 152;  // the grid's bound: one CTA per SM
 struct CrossMeta {   // of each CTA, for the combine kernel
   int split;         // its last item goes on in the next CTA
   int b, it;         // that item
-  int n;             // its key blocks
-  long long first;   // its first block in the sequence
-  long long total;   // blocks of the sequence
+  long long last;    // the place behind the item's last block
+  long long total;   // places of the sequence
 };
 
 struct CrossFwdParams {
@@ -61,10 +61,14 @@ struct CrossFwdParams {
 // key blocks of a request: at least one, so that rows without keys are written
 __device__ __forceinline__ int cross_blocks(int keys) { return keys > 128 ? (keys + 127) >> 7 : 1; }
 
-// A CTA's place in the sequence of blocks.
+// What a segment costs beyond its blocks (queries, first scores, epilogue), in
+// blocks: each item takes kCrossStart places of the sequence before its blocks.
+constexpr int kCrossStart = 2;
+
+// A CTA's share of the sequence of all items' places.
 struct CrossPlace {
-  int b, it, j;    // request, item of it (head, row tile), key block
-  long long left;  // blocks of the CTA from there on
+  int b, it, j;    // request, item of it (head, row tile), place in the item
+  long long left;  // places of the CTA from there on
 };
 
 // A run of key blocks of one item.
@@ -78,70 +82,71 @@ struct CrossSeg {
 };
 
 __device__ __forceinline__ bool cross_next(const CrossView& v, int items, CrossPlace& at, CrossSeg& s) {
-  if (at.left <= 0) return false;
-  s.b = at.b;
-  s.it = at.it;
-  s.len = v.len(at.b);
-  s.keys = s.len + v.drafted(at.b, s.len);
-  s.n = cross_blocks(s.keys);
-  s.j0 = at.j;
-  s.j1 = (int)min((long long)s.n, at.j + at.left);
-  at.left -= s.j1 - s.j0;
-  at.j = s.j1;
-  if (at.j == s.n) {
-    at.j = 0;
-    if (++at.it == items) {
-      at.it = 0;
-      ++at.b;
-    }
-  }
-  return true;
-}
-
-// Where CTA `cta` of at most `ctas` starts, by all of the block's threads.
-// `scratch`: kThreads long longs of shared memory.  Returns the blocks of the
-// sequence; the CTAs past it (more CTAs than blocks) get nothing.
-template <int kThreads>
-__device__ __forceinline__ long long cross_schedule(const CrossView& v, int B, int items, int cta, int ctas,
-                                                    long long* scratch, CrossPlace* place) {
-  const int tid = threadIdx.x;
-  const int chunk = (B + kThreads - 1) / kThreads;
-  const int b0 = min(B, tid * chunk), b1 = min(B, b0 + chunk);
-  auto blocks = [&](int b) {
-    const int len = v.len(b);
-    return cross_blocks(len + v.drafted(b, len));
-  };
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += blocks(b);
-  scratch[tid] = mine;
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {  // inclusive scan
-    const long long add = tid >= o ? scratch[tid - o] : 0;
-    __syncthreads();
-    scratch[tid] += add;
-    __syncthreads();
-  }
-  const long long total = scratch[kThreads - 1] * items;
-  if (total < ctas) ctas = (int)total;
-  const long long start = cta < ctas ? cta * total / ctas : total;
-  const long long end = cta < ctas ? (cta + 1) * total / ctas : total;
-  if (cta >= ctas) {
-    if (tid == 0) *place = {0, 0, 0, 0};
-  } else {
-    long long at = (scratch[tid] - mine) * items;
-    if (start >= at && start < scratch[tid] * items) {
-      for (int b = b0; b < b1; ++b) {
-        const int n = blocks(b);
-        if (start < at + (long long)n * items) {
-          const long long off = start - at;
-          *place = {b, (int)(off / n), (int)(off % n), end - start};
-          break;
-        }
-        at += (long long)n * items;
+  while (at.left > 0) {
+    s.b = at.b;
+    s.it = at.it;
+    s.len = v.len(at.b);
+    s.keys = s.len + v.drafted(at.b, s.len);
+    s.n = cross_blocks(s.keys);
+    const int end = (int)min((long long)s.n + kCrossStart, at.j + at.left);
+    s.j0 = max(at.j - kCrossStart, 0);
+    s.j1 = end - kCrossStart;
+    at.left -= end - at.j;
+    at.j = end;
+    if (at.j == s.n + kCrossStart) {
+      at.j = 0;
+      if (++at.it == items) {
+        at.it = 0;
+        ++at.b;
       }
     }
+    if (s.j1 > 0) return true;  // (else only places before the item's blocks)
   }
-  return total;
+  return false;
+}
+
+// The share of CTA `cta` of at most `ctas`, by one warp; CTAs past the sequence's
+// places get none.
+__device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int items, int cta, int ctas,
+                                               CrossPlace* place, long long* all, long long* share_end) {
+  const int lane = threadIdx.x & 31;
+  const int chunk = (B + 31) / 32;
+  const int b0 = min(B, lane * chunk), b1 = min(B, b0 + chunk);
+  auto places = [&](int b) {
+    const int len = v.len(b);
+    return cross_blocks(len + v.drafted(b, len)) + kCrossStart;
+  };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += places(b);
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long add = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += add;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31) * items;
+  if (total < ctas) ctas = (int)total;
+  if (cta >= ctas) {
+    if (lane == 0) *place = {0, 0, 0, 0};
+    return;
+  }
+  const long long start = cta * total / ctas, end = (cta + 1) * total / ctas;
+  if (lane == 0) {
+    *all = total;
+    *share_end = end;
+  }
+  long long at = (upto - mine) * items;
+  if (start >= at && start < upto * items) {
+    for (int b = b0; b < b1; ++b) {
+      const int n = places(b);
+      if (start < at + (long long)n * items) {
+        const long long off = start - at;
+        *place = {b, (int)(off / n), (int)(off % n), end - start};
+        break;
+      }
+      at += (long long)n * items;
+    }
+  }
 }
 
 template <int D>
@@ -179,7 +184,6 @@ struct CrossCfg {
   static constexpr int kMergeBytes = 3 * 128 * 4;
   static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + kMergeBytes + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-  static_assert(kSlots * kTileBytes >= kThreads * 8, "the schedule's scan uses the ring");
 };
 
 struct CrossBarriers {
@@ -194,6 +198,7 @@ struct CrossBarriers {
   uint64_t drain[2];
   uint64_t never;
   CrossPlace place;
+  long long total, end;  // places of the sequence; end of the CTA's share
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -273,12 +278,13 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_map(&map_k);
     tma_prefetch_map(&map_v);
   }
-  const long long total = cross_schedule<C::kThreads>(v, p.B, items, blockIdx.x, gridDim.x,
-                                                      reinterpret_cast<long long*>(sKV), &bar->place);
-  fence_async_shared();  // the ring's first copies follow the scan's plain writes
+  grid_wait();
+  if (warp == 10)
+    cross_schedule(v, p.B, items, blockIdx.x, gridDim.x, &bar->place, &bar->total, &bar->end);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_trigger();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
   CrossPlace at = bar->place;  // every role walks the same segments
@@ -435,8 +441,7 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------------------------ warp 11: rows of V behind the keys
       int g = 0, cleaned = 0;
       bool ok = true;
-      CrossMeta meta{0, 0, 0, 0, 0, total};
-      long long place = (long long)blockIdx.x * total / min((long long)gridDim.x, total);
+      CrossMeta meta{};
       while (ok && cross_next(v, items, at, w)) {
         if (w.dirty(v)) {
           const int vs = C::template slot<PAIR>(1, g + w.j1 - 1 - w.j0);
@@ -453,8 +458,14 @@ __global__ void __launch_bounds__(384, 1)
           if (lane == 0) mbar_arrive(&bar->v_clean);
         }
         g += w.j1 - w.j0;
-        if (w.first() && !w.last()) meta = {1, w.b, w.it, w.n, place, total};
-        place += w.j1 - w.j0;
+        if (w.first() && !w.last()) {
+          // (the CTA's last segment: the item's other blocks follow its share)
+          meta.split = 1;
+          meta.b = w.b;
+          meta.it = w.it;
+          meta.last = bar->end + w.n - w.j1;
+          meta.total = bar->total;
+        }
       }
       if (!ok) meta.split = 0;
       if (lane == 0) p.meta[blockIdx.x] = meta;
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(384, 1)
       if constexpr (TREE) {
         const int tok = row % v.Nq;
         if (v.masks)
-          mask = __ldg(v.masks + (long long)w.b * v.T + tok) &
+          mask = v.masks[(long long)w.b * v.T + tok] &
                  (w.keys - w.len >= 64 ? ~0ull : (1ull << (w.keys - w.len)) - 1ull);
         else
           last_key = min(last_key, w.len + tok);
@@ -724,48 +735,108 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Joins the parts of the items that share ends cut: block x takes the item that
-// begins in CTA x's share and goes on behind it, one warp per row.  O = sum of
+// begins in CTA x's share and goes on behind it, kRows rows per warp.  O = sum of
 // the parts' O weighted by 2^(their LSE - the largest), in CTA order.
+template <int E>
+__device__ __forceinline__ void cross_join_load(const float* o, float (&x)[E]) {
+  if constexpr (E == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(o);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  } else {
+    const float2 a = *reinterpret_cast<const float2*>(o);
+    x[0] = a.x, x[1] = a.y;
+  }
+}
+
 template <int D, bool TREE, bool PAIR>
-__global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdParams p, int ctas) {
+__global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdParams p) {
+  constexpr int E = D / 32;
+  constexpr int kRows = PAIR ? 4 : 1;  // rows of a warp (cut PAIR items have mostly two parts)
+  grid_wait();
+  grid_trigger();
   const CrossMeta meta = p.meta[blockIdx.x];
   if (!meta.split) return;
   const CrossView& v = p.view;
-  const int lane = threadIdx.x & 31, local = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int parts = (int)((meta.last * min((long long)gridDim.x, meta.total) - 1) / meta.total) - (int)blockIdx.x + 1;
+  const int lane = threadIdx.x & 31, local0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
   const int kvh = meta.it / p.row_tiles;
-  const int row = (meta.it - kvh * p.row_tiles) * (PAIR ? 256 : 128) + local;
-  if (local >= p.part_rows || row >= v.R) return;
-  if (TREE) {
-    const int len = v.len(meta.b);
-    if (row % v.Nq >= v.drafted(meta.b, len)) return;
-  }
-  const long long g = min((long long)ctas, meta.total);
-  const int parts = (int)(((meta.first + meta.n) * g - 1) / meta.total) - (int)blockIdx.x + 1;
+  const int row0 = (meta.it - kvh * p.row_tiles) * (PAIR ? 256 : 128) + local0;
+  int drafted = v.Nq;
+  if (TREE) drafted = v.drafted(meta.b, v.len(meta.b));
+  const size_t grow0 = ((size_t)meta.b * v.Hkv + kvh) * v.R + row0;
   // part i: the last segment of CTA x, then the first of each CTA after it
-  auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local; };
-  float mx = -CUDART_INF_F;
-  for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_lse[part(i)]);
+  auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local0; };
+  auto there = [&](int r) {
+    return local0 + r < p.part_rows && row0 + r < v.R && (!TREE || (row0 + r) % v.Nq < drafted);
+  };
+  auto write = [&](int r, const float (&acc)[E], float sum, float ref) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + (grow0 + r) * D) + lane * (E / 2);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-  constexpr int E = D / 32;
-  float acc[E], sum = 0.f;
+    for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) p.lse[grow0 + r] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+  };
+  if (kRows > 1 && parts == 2) {
+    float l[2][kRows], o[2][kRows][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float wt = ex2_approx(p.part_lse[part(i)] - ref);
-    sum += wt;
-    const float* o = p.part_o + part(i) * D + lane * E;
+    for (int r = 0; r < kRows; ++r)
+      if (there(r))
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[e], acc[e]);
+        for (int i = 0; i < 2; ++i) {
+          l[i][r] = p.part_lse[part(i) + r];
+          cross_join_load<E>(p.part_o + (part(i) + r) * D + lane * E, o[i][r]);
+        }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (!there(r)) continue;
+      const float mx = fmaxf(l[0][r], l[1][r]), ref = mx == -CUDART_INF_F ? 0.f : mx;
+      const float w0 = ex2_approx(l[0][r] - ref), w1 = ex2_approx(l[1][r] - ref);
+      float acc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w1, o[1][r][e], w0 * o[0][r][e]);
+      write(r, acc, w0 + w1, ref);
+    }
+    return;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const size_t grow = ((size_t)meta.b * v.Hkv + kvh) * v.R + row;
-  uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
+  constexpr int kWeights = (kCrossMaxCtas + 31) / 32;
+  for (int r = 0; r < kRows; ++r) {
+    if (!there(r)) continue;
+    // lane i keeps the weights of parts i, i + 32, ...
+    float w[kWeights], mx = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+    for (int k = 0; k < kWeights; ++k) {
+      const int i = 32 * k + lane;
+      w[k] = i < parts ? p.part_lse[part(i) + r] : -CUDART_INF_F;
+      mx = fmaxf(mx, w[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) sum += w[k] = ex2_approx(w[k] - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) {
+      for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 8) {
+        float o[8][E];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (i0 + u < parts) cross_join_load<E>(p.part_o + (part(i0 + u) + r) * D + lane * E, o[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wt = __shfl_sync(0xffffffffu, w[k], (i0 + u) & 31);
+          if (i0 + u < parts)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[u][e], acc[e]);
+        }
+      }
+    }
+    write(r, acc, sum, ref);
+  }
 }
 
 }  // namespace fa

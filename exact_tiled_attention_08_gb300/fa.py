@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -34,13 +35,6 @@ _STATUS_NAMES = {
     FA_ERR_CUDA: "FA_ERR_CUDA",
     FA_ERR_TIMEOUT: "FA_ERR_TIMEOUT",
 }
-
-
-class FaRows(ctypes.Structure):
-    """``fa_rows`` of the C ABI: a token-major tensor's address and strides in elements."""
-
-    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong),
-                ("head", ctypes.c_longlong)]
 
 
 class FaError(RuntimeError):
@@ -90,7 +84,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fa_tree_fwd_workspace_bytes.restype = sz
     lib.fa_tree_fwd.argtypes = [vp] * 9 + [sz] + [i] * 6 + [f, vp]
     lib.fa_tree_fwd.restype = i
-    rows = ctypes.POINTER(FaRows)
+    rows = vp  # fa_rows: an address, or its 32 bytes
     lib.fa_rope_fwd.argtypes = [rows] * 3 + [vp] * 8 + [i] * 8 + [f, f, i, vp]
     lib.fa_rope_fwd.restype = i
     lib.fa_rope_bwd_workspace_bytes.argtypes = [i] * 5
@@ -312,12 +306,39 @@ def fa_bwd_static_scratch(q, k, v, o, dout, lse, dq, dk, dv, scale: float, causa
 # ---------------------------------------------------------------------------
 # cross attention, attention over a cache, head norm and rotation
 # ---------------------------------------------------------------------------
+# Single tokens are launched every few microseconds, so the checks below look at
+# each property once and leave the messages to _check; the library's device and
+# stream are taken without a context manager where they are current already.
+def _ptr(t, name: str, dtype, shape, device) -> int:
+    """Address of a tensor, checked."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
 def _given(t, name: str, dtype, shape, device) -> int:
     """Address of an optional tensor (0 for None), checked."""
-    if t is None:
-        return 0
-    _check(t, name, dtype, shape, device)
-    return t.data_ptr()
+    return 0 if t is None else _ptr(t, name, dtype, shape, device)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(entry, device: torch.device, stream, where: str, *args) -> None:
+    """entry(*args, stream) with the tensors' device current; raises on a status."""
+    if device.type != "cuda":
+        raise ValueError(f"{where} needs CUDA tensors, got {device}")
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = _stream_handle(stream, device)
+    if torch.cuda.current_device() == device.index:
+        st = entry(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = entry(*args, handle)
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
 def _workspace(workspace, device):
@@ -326,14 +347,12 @@ def _workspace(workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _cross_shapes(q, k, v):
-    B, H, Nq, d = _shape4(q, "q")
-    _, Hkv, Nk, _ = _shape4(k, "k")
-    dev = q.device
-    _check(q, "q", torch.bfloat16, (B, H, Nq, d), dev)
-    _check(k, "k", torch.bfloat16, (B, Hkv, Nk, d), dev)
-    _check(v, "v", torch.bfloat16, (B, Hkv, Nk, d), dev)
-    return B, H, Hkv, Nq, Nk, d, dev
+def _cross_sizes(q, k):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be [B, H, N, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    B, H, Nq, d = q.shape
+    _, Hkv, Nk, _ = k.shape
+    return B, H, Hkv, Nq, Nk, d
 
 
 def fa_cross_fwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -343,16 +362,13 @@ def fa_cross_fwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: 
 def fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale: float, stream=None) -> None:
     """Attention of q [B,H,Nq,d] to k, v [B,Hkv,Nk,d] of another length; key_lens
     int32 [B] (or None: all Nk); o like q, lse [B,H,Nq] fp32."""
-    B, H, Hkv, Nq, Nk, d, dev = _cross_shapes(q, k, v)
-    _check(o, "o", torch.bfloat16, (B, H, Nq, d), dev)
-    _check(lse, "lse", torch.float32, (B, H, Nq), dev)
-    lens = _given(key_lens, "key_lens", torch.int32, (B,), dev)
+    B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
+    dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    with _on_device(dev):
-        st = load_library().fa_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(), lse.data_ptr(),
-                                         ws, ws_bytes, B, H, Hkv, Nq, Nk, d, float(scale),
-                                         _stream_handle(stream, dev))
-    _raise(st, "fa_cross_fwd")
+    _call(load_library().fa_cross_fwd, dev, stream, "fa_cross_fwd", _ptr(q, "q", bf, rows, dev),
+          _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
+          _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
+          _ptr(lse, "lse", torch.float32, (B, H, Nq), dev), ws, ws_bytes, B, H, Hkv, Nq, Nk, d, scale)
 
 
 def fa_cross_bwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -361,20 +377,15 @@ def fa_cross_bwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: 
 
 def fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale: float, stream=None) -> None:
     """dQ, dK, dV of fa_cross_fwd by recomputation; dk, dv like k, v."""
-    B, H, Hkv, Nq, Nk, d, dev = _cross_shapes(q, k, v)
-    for t, name in ((o, "o"), (dout, "dout"), (dq, "dq")):
-        _check(t, name, torch.bfloat16, (B, H, Nq, d), dev)
-    for t, name in ((dk, "dk"), (dv, "dv")):
-        _check(t, name, torch.bfloat16, (B, Hkv, Nk, d), dev)
-    _check(lse, "lse", torch.float32, (B, H, Nq), dev)
-    lens = _given(key_lens, "key_lens", torch.int32, (B,), dev)
+    B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
+    dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    with _on_device(dev):
-        st = load_library().fa_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, o.data_ptr(),
-                                         dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                         ws, ws_bytes, B, H, Hkv, Nq, Nk, d, float(scale),
-                                         _stream_handle(stream, dev))
-    _raise(st, "fa_cross_bwd")
+    _call(load_library().fa_cross_bwd, dev, stream, "fa_cross_bwd", _ptr(q, "q", bf, rows, dev),
+          _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
+          _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
+          _ptr(dout, "dout", bf, rows, dev), _ptr(lse, "lse", torch.float32, (B, H, Nq), dev),
+          _ptr(dq, "dq", bf, rows, dev), _ptr(dk, "dk", bf, keys, dev), _ptr(dv, "dv", bf, keys, dev), ws, ws_bytes,
+          B, H, Hkv, Nq, Nk, d, scale)
 
 
 def fa_tree_fwd_workspace_bytes(B: int, H: int, Hkv: int, T: int, C: int, d: int) -> int:
@@ -387,18 +398,15 @@ def fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse
     cache_lens[b] tokens and then the new ones.  draft_lens int32 [B] (or
     None: T); draft_masks int64 [B,T], bit t of word n: token n sees token t
     (or None: each sees the ones before it and itself; see tree_masks)."""
-    B, H, Hkv, T, C, d, dev = _cross_shapes(q, k_cache, v_cache)
-    _check(o, "o", torch.bfloat16, (B, H, T, d), dev)
-    _check(lse, "lse", torch.float32, (B, H, T), dev)
-    _check(cache_lens, "cache_lens", torch.int32, (B,), dev)
-    drafts = _given(draft_lens, "draft_lens", torch.int32, (B,), dev)
-    masks = _given(draft_masks, "draft_masks", torch.int64, (B, T), dev)
+    B, H, Hkv, T, C, d = _cross_sizes(q, k_cache)
+    dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, T, d), (B, Hkv, C, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    with _on_device(dev):
-        st = load_library().fa_tree_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cache_lens.data_ptr(),
-                                        drafts, masks, o.data_ptr(), lse.data_ptr(), ws, ws_bytes, B, H, Hkv, T, C, d,
-                                        float(scale), _stream_handle(stream, dev))
-    _raise(st, "fa_tree_fwd")
+    _call(load_library().fa_tree_fwd, dev, stream, "fa_tree_fwd", _ptr(q, "q", bf, rows, dev),
+          _ptr(k_cache, "k_cache", bf, keys, dev), _ptr(v_cache, "v_cache", bf, keys, dev),
+          _ptr(cache_lens, "cache_lens", torch.int32, (B,), dev),
+          _given(draft_lens, "draft_lens", torch.int32, (B,), dev),
+          _given(draft_masks, "draft_masks", torch.int64, (B, T), dev), _ptr(o, "o", bf, rows, dev),
+          _ptr(lse, "lse", torch.float32, (B, H, T), dev), ws, ws_bytes, B, H, Hkv, T, C, d, scale)
 
 
 def tree_masks(parents: torch.Tensor) -> torch.Tensor:
@@ -453,34 +461,44 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return freq.to(device), factor
 
 
+_pack_rows = struct.Struct("Pqqq").pack
+
+
 def _rows(t, name: str, shape, device):
-    """``fa_rows`` of a [B, N, heads, d] tensor whose d values lie next to each other (None: no such rows)."""
+    """``fa_rows`` (as bytes) of a [B, N, heads, d] tensor whose d values lie next to
+    each other; None: no such rows."""
     if t is None:
         return None
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     sb, sn, sh, sd = t.stride()
-    if sd != 1 and shape[3] != 1:
+    if sd != 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     # (the stride of a dimension of one is any number: it is never used)
-    return FaRows(t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+    return _pack_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
 
 
 def _rope_sizes(q, k, v, names):
     """B, N, H, Hkv, d and device of the token-major tensors that are given."""
-    first = next((t for t in (q, k, v) if t is not None), None)
+    kv = k if k is not None else v
+    first = q if q is not None else kv
     if first is None:
         raise ValueError(f"one of {', '.join(names)} must be given")
-    for t, name in zip((q, k, v), names):
-        if t is not None and t.dim() != 4:
-            raise ValueError(f"{name} must be [B, N, heads, d], got {tuple(t.shape)}")
+    if first.dim() != 4 or (kv is not None and kv.dim() != 4):
+        raise ValueError(f"{', '.join(names)} must be [B, N, heads, d]")
     B, N, _, d = first.shape
-    kv = k if k is not None else v
     return B, N, (q.shape[2] if q is not None else 1), (kv.shape[2] if kv is not None else 1), d, first.device
+
+
+def _frequencies(inv_freq, device):
+    if inv_freq is None:
+        return 0, 0
+    n = inv_freq.numel()
+    return _ptr(inv_freq, "inv_freq", torch.float64, (n,), device), 2 * n
 
 
 def fa_rope_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, starts, q_out, k_out, v_out, *, eps=None,
@@ -492,23 +510,19 @@ def fa_rope_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, starts, q_out,
     fp32 [d] or None; inv_freq fp64 or None (no rotation); positions int32
     [B,N] or None (starts[b] + n); starts int32 [B] or None (0)."""
     B, N, H, Hkv, d, dev = _rope_sizes(q, k, v, ("q", "k", "v"))
-    rq, rk, rv = _rows(q, "q", (B, N, H, d), dev), _rows(k, "k", (B, N, Hkv, d), dev), _rows(v, "v", (B, N, Hkv, d), dev)
     if eps is None and (q_weight is not None or k_weight is not None):
         raise ValueError("weights need eps: without it there is no norm")
     cache = k_out if k_out is not None else v_out
-    C = _shape4(cache, "k_out")[2] if cache is not None else N
-    args = (_given(q_weight, "q_weight", torch.float32, (d,), dev), _given(k_weight, "k_weight", torch.float32, (d,), dev),
-            0 if inv_freq is None else _given(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev),
-            _given(positions, "positions", torch.int32, (B, N), dev), _given(starts, "starts", torch.int32, (B,), dev),
-            _given(q_out, "q_out", torch.bfloat16, (B, H, N, d), dev),
-            _given(k_out, "k_out", torch.bfloat16, (B, Hkv, C, d), dev),
-            _given(v_out, "v_out", torch.bfloat16, (B, Hkv, C, d), dev))
-    with _on_device(dev):
-        st = load_library().fa_rope_fwd(rq, rk, rv, *args, B, N, H, Hkv, C, d,
-                                        0 if inv_freq is None else 2 * inv_freq.numel(), int(eps is not None),
-                                        float(eps or 0.0), float(factor), int(bool(interleaved)),
-                                        _stream_handle(stream, dev))
-    _raise(st, "fa_rope_fwd")
+    C = N if cache is None else _shape4(cache, "k_out")[2]
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    freq, rot = _frequencies(inv_freq, dev)
+    _call(load_library().fa_rope_fwd, dev, stream, "fa_rope_fwd", _rows(q, "q", (B, N, H, d), dev),
+          _rows(k, "k", (B, N, Hkv, d), dev), _rows(v, "v", (B, N, Hkv, d), dev),
+          _given(q_weight, "q_weight", f32, (d,), dev), _given(k_weight, "k_weight", f32, (d,), dev), freq,
+          _given(positions, "positions", i32, (B, N), dev), _given(starts, "starts", i32, (B,), dev),
+          _given(q_out, "q_out", bf, (B, H, N, d), dev), _given(k_out, "k_out", bf, (B, Hkv, C, d), dev),
+          _given(v_out, "v_out", bf, (B, Hkv, C, d), dev), B, N, H, Hkv, C, d, rot, 0 if eps is None else 1,
+          eps or 0.0, factor, 1 if interleaved else 0)
 
 
 def fa_rope_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int) -> int:
@@ -523,27 +537,22 @@ def fa_rope_bwd(q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, d
     dk_weight [d] (or None).  q and k are read only with eps; any of the three
     gradients may be None with its output; workspace is needed for weights."""
     B, N, H, Hkv, d, dev = _rope_sizes(dq, dk, dv, ("dq", "dk", "dv"))
-    outs = (_rows(dq, "dq", (B, N, H, d), dev), _rows(dk, "dk", (B, N, Hkv, d), dev),
-            _rows(dv, "dv", (B, N, Hkv, d), dev))
     if eps is None and any(t is not None for t in (q_weight, k_weight, dq_weight, dk_weight)):
         raise ValueError("weights need eps: without it there is no norm")
-    rq = _rows(q, "q", (B, N, H, d), dev) if eps is not None and dq is not None else None
-    rk = _rows(k, "k", (B, N, Hkv, d), dev) if eps is not None and dk is not None else None
-    args = (_given(q_weight, "q_weight", torch.float32, (d,), dev), _given(k_weight, "k_weight", torch.float32, (d,), dev),
-            0 if inv_freq is None else _given(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev),
-            _given(positions, "positions", torch.int32, (B, N), dev),
-            _given(dq_out, "dq_out", torch.bfloat16, (B, H, N, d), dev),
-            _given(dk_out, "dk_out", torch.bfloat16, (B, Hkv, N, d), dev),
-            _given(dv_out, "dv_out", torch.bfloat16, (B, Hkv, N, d), dev))
-    grads = (_given(dq_weight, "dq_weight", torch.float32, (d,), dev),
-             _given(dk_weight, "dk_weight", torch.float32, (d,), dev))
+    norm = eps is not None
+    bf, f32 = torch.bfloat16, torch.float32
+    freq, rot = _frequencies(inv_freq, dev)
     ws, ws_bytes = (0, 0) if workspace is None else _workspace(workspace, dev)
-    with _on_device(dev):
-        st = load_library().fa_rope_bwd(rq, rk, *args, *outs, *grads, ws, ws_bytes, B, N, H, Hkv, d,
-                                        0 if inv_freq is None else 2 * inv_freq.numel(), int(eps is not None),
-                                        float(eps or 0.0), float(factor), int(bool(interleaved)),
-                                        _stream_handle(stream, dev))
-    _raise(st, "fa_rope_bwd")
+    _call(load_library().fa_rope_bwd, dev, stream, "fa_rope_bwd",
+          _rows(q, "q", (B, N, H, d), dev) if norm and dq is not None else None,
+          _rows(k, "k", (B, N, Hkv, d), dev) if norm and dk is not None else None,
+          _given(q_weight, "q_weight", f32, (d,), dev), _given(k_weight, "k_weight", f32, (d,), dev), freq,
+          _given(positions, "positions", torch.int32, (B, N), dev),
+          _given(dq_out, "dq_out", bf, (B, H, N, d), dev), _given(dk_out, "dk_out", bf, (B, Hkv, N, d), dev),
+          _given(dv_out, "dv_out", bf, (B, Hkv, N, d), dev), _rows(dq, "dq", (B, N, H, d), dev),
+          _rows(dk, "dk", (B, N, Hkv, d), dev), _rows(dv, "dv", (B, N, Hkv, d), dev),
+          _given(dq_weight, "dq_weight", f32, (d,), dev), _given(dk_weight, "dk_weight", f32, (d,), dev), ws, ws_bytes,
+          B, N, H, Hkv, d, rot, 1 if norm else 0, eps or 0.0, factor, 1 if interleaved else 0)
 
 
 # ---------------------------------------------------------------------------

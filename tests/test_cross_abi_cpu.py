@@ -2,6 +2,7 @@
 arguments are turned down before anything is enqueued."""
 
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -65,12 +66,15 @@ def test_tree_masks():
 
 
 def rows(ptr=P, batch=1024, token=1024, head=128):
-    return fa.FaRows(ptr, batch, token, head)
+    return struct.pack("Pqqq", ptr, batch, token, head)  # fa_rows
 
 
-def rope_fwd(lib, q="d", k="d", v="d", qo=P, ko=P, vo=P, freq=P, B=1, N=2, H=4, Hkv=2, C=2, d=128, rot=128, norm=1,
+DEFAULT = object()
+
+
+def rope_fwd(lib, q=DEFAULT, k=DEFAULT, v=DEFAULT, qo=P, ko=P, vo=P, freq=P, B=1, N=2, H=4, Hkv=2, C=2, d=128, rot=128, norm=1,
              eps=1e-6, factor=1.0, inter=0, weight=P, pos=P, starts=P):
-    r = [rows() if isinstance(x, str) else x for x in (q, k, v)]
+    r = [rows() if x is DEFAULT else x for x in (q, k, v)]
     return lib.fa_rope_fwd(*r, VP(weight), VP(weight), VP(freq), VP(pos), VP(starts), VP(qo), VP(ko), VP(vo), B, N, H,
                            Hkv, C, d, rot, norm, eps, factor, inter, None)
 
@@ -90,9 +94,9 @@ def test_rope_forward_refusals(lib):
     assert rope_fwd(lib, v=rows(head=4)) == odd and rope_fwd(lib, qo=P + 8) == odd and rope_fwd(lib, pos=P + 4) == odd
 
 
-def rope_bwd(lib, q="d", k="d", dq="d", dk="d", dv="d", gq=P, gk=P, gv=P, dqw=P, dkw=P, ws=P, ws_bytes=None, N=2, H=4,
+def rope_bwd(lib, q=DEFAULT, k=DEFAULT, dq=DEFAULT, dk=DEFAULT, dv=DEFAULT, gq=P, gk=P, gv=P, dqw=P, dkw=P, ws=P, ws_bytes=None, N=2, H=4,
              Hkv=2, norm=1, eps=1e-6):
-    r = [rows() if isinstance(x, str) else x for x in (q, k, dq, dk, dv)]
+    r = [rows() if x is DEFAULT else x for x in (q, k, dq, dk, dv)]
     need = lib.fa_rope_bwd_workspace_bytes(1, H, Hkv, N, 128)
     return lib.fa_rope_bwd(r[0], r[1], VP(P), VP(P), VP(P), VP(P), VP(gq), VP(gk), VP(gv), r[2], r[3], r[4], VP(dqw),
                            VP(dkw), VP(ws), need if ws_bytes is None else ws_bytes, 1, N, H, Hkv, 128, 128, norm, eps,
