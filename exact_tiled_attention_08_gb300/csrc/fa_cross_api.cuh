@@ -93,7 +93,14 @@ fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const C
   const int grid = std::min(plan.ctas, sms);
   if (launch_early(kernel, dim3((unsigned)grid), C::kThreads, C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (plan.cuts) {
+  // without lengths the host knows whether the CTAs cut items
+  bool cuts = plan.cuts;
+  if (cuts && !p.view.lens) {
+    const int most = (p.view.Nk + 127) / 128 + fa::kCrossStart;
+    const long long items = (long long)p.B * p.view.Hkv * p.row_tiles;
+    cuts = !fa::cross_whole(items, grid, most, items * most);
+  }
+  if (cuts) {
     const int per_block = PAIR ? 32 : 8;  // rows of a block
     const dim3 rows((unsigned)grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
     if (launch_early(fa::fa_cross_combine_kernel<D, TREE, PAIR>, rows, 256, 0, stream, p) != cudaSuccess)

@@ -710,8 +710,7 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_cross_bwd_post_kernel(const CrossBwdPostParams q) {
   const CrossBwdParams& p = q.p;
   const CrossView& v = p.view;
-  grid_wait();
-  grid_trigger();
+  grid_wait();  // (no grid_trigger: a next call's first blocks would take the place of this one's)
   const int cut_blocks = 8 * q.ctas, zero_blocks = v.lens ? p.B * v.Hkv : 0;
   int x = blockIdx.x;
   if (x < cut_blocks) {

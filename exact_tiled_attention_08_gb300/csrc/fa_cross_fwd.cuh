@@ -65,6 +65,15 @@ __device__ __forceinline__ int cross_blocks(int keys) { return keys > 128 ? (key
 // blocks: each item takes kCrossStart places of the sequence before its blocks.
 constexpr int kCrossStart = 2;
 
+// What cutting items costs at the end (parts written, read and joined), in places.
+constexpr int kCrossCut = 5;
+
+// Whether the CTAs take whole items, ceil(items / ctas) at most: where that
+// ends no later than even shares and the join of what they cut.
+__host__ __device__ __forceinline__ bool cross_whole(long long items, int ctas, int most, long long total) {
+  return (items + ctas - 1) / ctas * most <= total / ctas + kCrossCut;
+}
+
 // A CTA's share of the sequence of all items' places.
 struct CrossPlace {
   int b, it, j;    // request, item of it (head, row tile), place in the item
@@ -117,7 +126,12 @@ __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int it
     return cross_blocks(len + v.drafted(b, len)) + kCrossStart;
   };
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += places(b);
+  int most = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = places(b);
+    mine += n;
+    most = max(most, n);
+  }
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -125,6 +139,22 @@ __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int it
     if (lane >= o) upto += add;
   }
   const long long total = __shfl_sync(0xffffffffu, upto, 31) * items;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (cross_whole((long long)B * items, ctas, most, total)) {
+    if (lane == 0) {
+      long long at = cta * ((long long)B * items) / ctas, left = (cta + 1) * ((long long)B * items) / ctas - at;
+      CrossPlace x{(int)(at / items), (int)(at % items), 0, 0};
+      for (long long b = x.b, it = x.it; left > 0; ++b, it = 0) {  // the places of those items
+        const long long take = min(left, items - it);
+        x.left += take * places((int)b);
+        left -= take;
+      }
+      *place = x;
+      *all = *share_end = 1;  // (nothing is cut)
+    }
+    return;
+  }
   if (total < ctas) ctas = (int)total;
   if (cta >= ctas) {
     if (lane == 0) *place = {0, 0, 0, 0};
@@ -798,42 +828,39 @@ __global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdPar
     }
     return;
   }
-  constexpr int kWeights = (kCrossMaxCtas + 31) / 32;
+  constexpr int kBatch = 8;  // parts whose loads are in flight together
   for (int r = 0; r < kRows; ++r) {
     if (!there(r)) continue;
-    // lane i keeps the weights of parts i, i + 32, ...
-    float w[kWeights], mx = -CUDART_INF_F, sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWeights; ++k) {
-      const int i = 32 * k + lane;
-      w[k] = i < parts ? p.part_lse[part(i) + r] : -CUDART_INF_F;
-      mx = fmaxf(mx, w[k]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-#pragma unroll
-    for (int k = 0; k < kWeights; ++k) sum += w[k] = ex2_approx(w[k] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float acc[E];
+    float acc[E], sum = 0.f, ref = -CUDART_INF_F;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += kBatch) {
+      float l[kBatch], o[kBatch][E];
 #pragma unroll
-    for (int k = 0; k < kWeights; ++k) {
-      for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 8) {
-        float o[8][E];
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (i0 + u < parts) cross_join_load<E>(p.part_o + (part(i0 + u) + r) * D + lane * E, o[u]);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float wt = __shfl_sync(0xffffffffu, w[k], (i0 + u) & 31);
-          if (i0 + u < parts)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[u][e], acc[e]);
+      for (int u = 0; u < kBatch; ++u) {
+        l[u] = -CUDART_INF_F;
+        if (i0 + u < parts) {
+          l[u] = p.part_lse[part(i0 + u) + r];
+          cross_join_load<E>(p.part_o + (part(i0 + u) + r) * D + lane * E, o[u]);
         }
       }
+      float mx = ref;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, l[u]);
+      if (mx == -CUDART_INF_F) mx = 0.f;  // no key so far
+      const float alpha = ex2_approx(ref - mx);
+      ref = mx;
+      sum *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i0 + u < parts) {
+          const float wt = ex2_approx(l[u] - ref);
+          sum += wt;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[u][e], acc[e]);
+        }
     }
     write(r, acc, sum, ref);
   }

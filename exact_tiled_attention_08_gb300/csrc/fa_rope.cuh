@@ -25,6 +25,7 @@
 
 #include <cuda_bf16.h>
 
+#include "fa_cross.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
                                                     nullptr, 0.f, dw[1]);
   }
   if constexpr (kNorm) {
+    grid_trigger();  // the next kernel adds the CTAs' sums
     if (!p.partials) return;
 #pragma unroll
   for (int t = 0; t < 2; ++t)
@@ -344,19 +346,24 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
   }
 }
 
-// dw[t][i] = sum over the CTAs of partials[cta][t][i], in CTA order; one warp
-// per output value.
-__global__ void __launch_bounds__(256)
-    fa_rope_dw_kernel(const float* __restrict__ partials, int ctas, int d, float* __restrict__ dq_weight,
-                      float* __restrict__ dk_weight) {
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (i >= 2 * d) return;
+// dw[t][i] = sum over the CTAs of partials[cta][t][i]: a block per 32 values,
+// its warps over the CTAs, then over the warps in order.
+__global__ void __launch_bounds__(1024)
+    fa_rope_dw_kernel(const float* partials, int ctas, int d, float* dq_weight, float* dk_weight) {
+  __shared__ float sums[32][32];
+  grid_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int c = lane; c < ctas; c += 32) v += partials[(long long)c * 2 * d + i];
+#pragma unroll 4
+  for (int c = warp; c < ctas; c += 32) v += partials[(long long)c * 2 * d + i];
+  sums[warp][lane] = v;
+  __syncthreads();
+  if (warp) return;
+  v = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int w = 0; w < 32; ++w) v += sums[w][lane];
   float* out = i < d ? dq_weight : dk_weight;
-  if (lane == 0 && out) out[i < d ? i : i - d] = v;
+  if (out) out[i < d ? i : i - d] = v;
 }
 
 }  // namespace fa

@@ -206,8 +206,9 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
     norm ? launch_rope_bwd<64, true>(p, grid, interleaved, stream) : launch_rope_bwd<64, false>(p, grid, interleaved, stream);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (weights) {
-    fa::fa_rope_dw_kernel<<<2 * d / 8, 256, 0, stream>>>(p.partials, (int)grid, d, dq_weight, dk_weight);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (launch_early(fa::fa_rope_dw_kernel, dim3((unsigned)(2 * d / 32)), 1024, 0, stream, p.partials, (int)grid, d,
+                     dq_weight, dk_weight) != cudaSuccess)
+      return FA_ERR_CUDA;
   }
   return FA_OK;
 }
