@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 namespace {
 
@@ -44,6 +45,19 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int 
   return e;
 }
 
+// Whether `kernel` launches with `regs` registers per thread, asked once per
+// device.  (The warpgroups re-divide the block's registers with setmaxnreg,
+// which only works if the block really gets that many.)
+template <typename Kernel>
+bool has_launch_regs(Kernel kernel, int regs, int dev, std::atomic<unsigned long long>& known) {
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (known.load(std::memory_order_relaxed) & bit) return true;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != regs) return false;
+  known.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   fa::CrossView v{};
   v.Nk = Nk;
@@ -82,14 +96,12 @@ fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const C
   using C = fa::CrossCfg<D>;
   auto kernel = fa::fa_cross_fwd_kernel<D, TREE, PAIR>;
   if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
-  // the warpgroups re-divide the block's registers (setmaxnreg); that only
-  // works if the block really gets kLaunchRegs per thread
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != C::kLaunchRegs) return FA_ERR_CUDA;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return FA_ERR_CUDA;
+  static std::atomic<unsigned long long> known{0};
+  if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
   const int grid = std::min(plan.ctas, sms);
   if (launch_early(kernel, dim3((unsigned)grid), C::kThreads, C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
     return FA_ERR_CUDA;
@@ -188,12 +200,12 @@ fa_status run_cross_bwd(const fa::CrossView& view, const void* q, const void* k,
     return FA_ERR_CUDA;
   auto kernel = fa::fa_cross_bwd_kernel<D>;
   if (set_smem(kernel, fa::kCrossBwdSmemBytes<D>) != cudaSuccess) return FA_ERR_CUDA;
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != C::kLaunchRegs) return FA_ERR_CUDA;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return FA_ERR_CUDA;
+  static std::atomic<unsigned long long> known{0};
+  if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
   const long long rows = (long long)BK * rpad, per_block = 256 / (D / 8);
   const long long prep = std::min((rows + per_block - 1) / per_block, 152LL * 16);
   if (launch_early(fa::fa_cross_bwd_prep_kernel<D>, dim3((unsigned)prep), 256, 0, stream,
@@ -308,6 +320,24 @@ fa_status fa_tree_fwd(const void* q, const void* k_cache, const void* v_cache, c
   view.masks = draft_masks;
   view.T = T;
   return run_cross_fwd(view, q, k_cache, v_cache, o, lse, workspace, B, d, scale, stream);
+}
+
+fa_status fa_cross_fwd_packed(const fa_cross_fwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_cross_fwd(a->q, a->k, a->v, a->key_lens, a->o, a->lse, a->workspace, a->ws_bytes, a->B, a->H, a->Hkv, a->Nq,
+                      a->Nk, a->d, a->scale, a->stream);
+}
+
+fa_status fa_cross_bwd_packed(const fa_cross_bwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_cross_bwd(a->q, a->k, a->v, a->key_lens, a->o, a->dout, a->lse, a->dq, a->dk, a->dv, a->workspace,
+                      a->ws_bytes, a->B, a->H, a->Hkv, a->Nq, a->Nk, a->d, a->scale, a->stream);
+}
+
+fa_status fa_tree_fwd_packed(const fa_tree_fwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_tree_fwd(a->q, a->k_cache, a->v_cache, a->cache_lens, a->draft_lens, a->draft_masks, a->o, a->lse,
+                     a->workspace, a->ws_bytes, a->B, a->H, a->Hkv, a->T, a->C, a->d, a->scale, a->stream);
 }
 
 }  // extern "C"

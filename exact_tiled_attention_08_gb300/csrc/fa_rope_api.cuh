@@ -213,4 +213,18 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
   return FA_OK;
 }
 
+fa_status fa_rope_fwd_packed(const fa_rope_fwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_rope_fwd(&a->q, &a->k, &a->v, a->q_weight, a->k_weight, a->inv_freq, a->positions, a->starts, a->q_out,
+                     a->k_out, a->v_out, a->B, a->N, a->H, a->Hkv, a->C, a->d, a->rotary_dim, a->norm, a->eps,
+                     a->factor, a->interleaved, a->stream);
+}
+
+fa_status fa_rope_bwd_packed(const fa_rope_bwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_rope_bwd(&a->q, &a->k, a->q_weight, a->k_weight, a->inv_freq, a->positions, a->dq_out, a->dk_out, a->dv_out,
+                     &a->dq, &a->dk, &a->dv, a->dq_weight, a->dk_weight, a->workspace, a->ws_bytes, a->B, a->N, a->H,
+                     a->Hkv, a->d, a->rotary_dim, a->norm, a->eps, a->factor, a->interleaved, a->stream);
+}
+
 }  // extern "C"

@@ -43,6 +43,17 @@ class FaError(RuntimeError):
         super().__init__(f"{where}: {_STATUS_NAMES.get(status, status)}")
 
 
+# The argument structs of the *_packed entry points (fa_rows: Pqqq).  One struct
+# costs a call a fraction of what twenty ctypes arguments do.
+_PACKED = {
+    "fa_cross_fwd": struct.Struct("@7PN6ifP").pack,
+    "fa_cross_bwd": struct.Struct("@11PN6ifP").pack,
+    "fa_tree_fwd": struct.Struct("@9PN6ifP").pack,
+    "fa_rope_fwd": struct.Struct("@PqqqPqqqPqqq8P8i2fiP").pack,
+    "fa_rope_bwd": struct.Struct("@PqqqPqqq7PPqqqPqqqPqqq3PN7i2fiP").pack,
+}
+_entries = {}  # name -> (packed entry point, pack)
+
 _lib = None
 
 
@@ -85,6 +96,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fa_tree_fwd.argtypes = [vp] * 9 + [sz] + [i] * 6 + [f, vp]
     lib.fa_tree_fwd.restype = i
     rows = vp  # fa_rows: an address, or its 32 bytes
+    for entry in _PACKED:
+        getattr(lib, entry + "_packed").argtypes = [vp]
+        getattr(lib, entry + "_packed").restype = i
     lib.fa_rope_fwd.argtypes = [rows] * 3 + [vp] * 8 + [i] * 8 + [f, f, i, vp]
     lib.fa_rope_fwd.restype = i
     lib.fa_rope_bwd_workspace_bytes.argtypes = [i] * 5
@@ -324,21 +338,28 @@ def _given(t, name: str, dtype, shape, device) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(entry, device: torch.device, stream, where: str, *args) -> None:
-    """entry(*args, stream) with the tensors' device current; raises on a status."""
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """The entry point on (*args, stream) with the tensors' device current; raises on a status."""
     if device.type != "cuda":
-        raise ValueError(f"{where} needs CUDA tensors, got {device}")
+        raise ValueError(f"{name} needs CUDA tensors, got {device}")
     if stream is None and _raw_stream is not None:
         handle = _raw_stream(device.index)
     else:
         handle = _stream_handle(stream, device)
+    if name not in _entries:
+        _entries[name] = getattr(load_library(), name + "_packed"), _PACKED[name]
+    entry, pack = _entries[name]
+    try:
+        packed = pack(*args, handle)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise ValueError(f"{name}: {e}") from None  # a number that the C type does not hold
     if torch.cuda.current_device() == device.index:
-        st = entry(*args, handle)
+        st = entry(packed)
     else:
         with torch.cuda.device(device):
-            st = entry(*args, handle)
+            st = entry(packed)
     if st != FA_OK:
-        raise FaError(st, where)
+        raise FaError(st, name)
 
 
 def _workspace(workspace, device):
@@ -365,7 +386,7 @@ def fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale: float, stream=None
     B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    _call(load_library().fa_cross_fwd, dev, stream, "fa_cross_fwd", _ptr(q, "q", bf, rows, dev),
+    _call("fa_cross_fwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
           _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
           _ptr(lse, "lse", torch.float32, (B, H, Nq), dev), ws, ws_bytes, B, H, Hkv, Nq, Nk, d, scale)
@@ -380,7 +401,7 @@ def fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale: 
     B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    _call(load_library().fa_cross_bwd, dev, stream, "fa_cross_bwd", _ptr(q, "q", bf, rows, dev),
+    _call("fa_cross_bwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
           _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
           _ptr(dout, "dout", bf, rows, dev), _ptr(lse, "lse", torch.float32, (B, H, Nq), dev),
@@ -401,7 +422,7 @@ def fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse
     B, H, Hkv, T, C, d = _cross_sizes(q, k_cache)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, T, d), (B, Hkv, C, d)
     ws, ws_bytes = _workspace(workspace, dev)
-    _call(load_library().fa_tree_fwd, dev, stream, "fa_tree_fwd", _ptr(q, "q", bf, rows, dev),
+    _call("fa_tree_fwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k_cache, "k_cache", bf, keys, dev), _ptr(v_cache, "v_cache", bf, keys, dev),
           _ptr(cache_lens, "cache_lens", torch.int32, (B,), dev),
           _given(draft_lens, "draft_lens", torch.int32, (B,), dev),
@@ -461,14 +482,14 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return freq.to(device), factor
 
 
-_pack_rows = struct.Struct("Pqqq").pack
+_NO_ROWS = (0, 0, 0, 0)
 
 
 def _rows(t, name: str, shape, device):
-    """``fa_rows`` (as bytes) of a [B, N, heads, d] tensor whose d values lie next to
-    each other; None: no such rows."""
+    """``fa_rows`` (address and strides) of a [B, N, heads, d] tensor whose d values lie
+    next to each other; None: no such rows."""
     if t is None:
-        return None
+        return _NO_ROWS
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != shape:
@@ -479,7 +500,7 @@ def _rows(t, name: str, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     # (the stride of a dimension of one is any number: it is never used)
-    return _pack_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+    return t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0
 
 
 def _rope_sizes(q, k, v, names):
@@ -516,8 +537,8 @@ def fa_rope_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, starts, q_out,
     C = N if cache is None else _shape4(cache, "k_out")[2]
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     freq, rot = _frequencies(inv_freq, dev)
-    _call(load_library().fa_rope_fwd, dev, stream, "fa_rope_fwd", _rows(q, "q", (B, N, H, d), dev),
-          _rows(k, "k", (B, N, Hkv, d), dev), _rows(v, "v", (B, N, Hkv, d), dev),
+    _call("fa_rope_fwd", dev, stream, *_rows(q, "q", (B, N, H, d), dev),
+          *_rows(k, "k", (B, N, Hkv, d), dev), *_rows(v, "v", (B, N, Hkv, d), dev),
           _given(q_weight, "q_weight", f32, (d,), dev), _given(k_weight, "k_weight", f32, (d,), dev), freq,
           _given(positions, "positions", i32, (B, N), dev), _given(starts, "starts", i32, (B,), dev),
           _given(q_out, "q_out", bf, (B, H, N, d), dev), _given(k_out, "k_out", bf, (B, Hkv, C, d), dev),
@@ -543,14 +564,14 @@ def fa_rope_bwd(q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, d
     bf, f32 = torch.bfloat16, torch.float32
     freq, rot = _frequencies(inv_freq, dev)
     ws, ws_bytes = (0, 0) if workspace is None else _workspace(workspace, dev)
-    _call(load_library().fa_rope_bwd, dev, stream, "fa_rope_bwd",
-          _rows(q, "q", (B, N, H, d), dev) if norm and dq is not None else None,
-          _rows(k, "k", (B, N, Hkv, d), dev) if norm and dk is not None else None,
+    _call("fa_rope_bwd", dev, stream,
+          *(_rows(q, "q", (B, N, H, d), dev) if norm and dq is not None else _NO_ROWS),
+          *(_rows(k, "k", (B, N, Hkv, d), dev) if norm and dk is not None else _NO_ROWS),
           _given(q_weight, "q_weight", f32, (d,), dev), _given(k_weight, "k_weight", f32, (d,), dev), freq,
           _given(positions, "positions", torch.int32, (B, N), dev),
           _given(dq_out, "dq_out", bf, (B, H, N, d), dev), _given(dk_out, "dk_out", bf, (B, Hkv, N, d), dev),
-          _given(dv_out, "dv_out", bf, (B, Hkv, N, d), dev), _rows(dq, "dq", (B, N, H, d), dev),
-          _rows(dk, "dk", (B, N, Hkv, d), dev), _rows(dv, "dv", (B, N, Hkv, d), dev),
+          _given(dv_out, "dv_out", bf, (B, Hkv, N, d), dev), *_rows(dq, "dq", (B, N, H, d), dev),
+          *_rows(dk, "dk", (B, N, Hkv, d), dev), *_rows(dv, "dv", (B, N, Hkv, d), dev),
           _given(dq_weight, "dq_weight", f32, (d,), dev), _given(dk_weight, "dk_weight", f32, (d,), dev), ws, ws_bytes,
           B, N, H, Hkv, d, rot, 1 if norm else 0, eps or 0.0, factor, 1 if interleaved else 0)
 

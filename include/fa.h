@@ -365,6 +365,83 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
                       int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream);
 
 /*
+ * The entry points above from fa_cross_fwd on, with their arguments in one
+ * struct (in the same order and with the same meaning), for callers whose
+ * foreign function interface pays for every argument, as the Python binding's
+ * does.  A null struct gives FA_ERR_INVALID_ARG.
+ */
+typedef struct {
+  const void *q, *k, *v;
+  const int* key_lens;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, Nq, Nk, d;
+  float scale;
+  cudaStream_t stream;
+} fa_cross_fwd_args;
+
+typedef struct {
+  const void *q, *k, *v;
+  const int* key_lens;
+  const void *o, *dout;
+  const float* lse;
+  void *dq, *dk, *dv, *workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, Nq, Nk, d;
+  float scale;
+  cudaStream_t stream;
+} fa_cross_bwd_args;
+
+typedef struct {
+  const void *q, *k_cache, *v_cache;
+  const int *cache_lens, *draft_lens;
+  const unsigned long long* draft_masks;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, T, C, d;
+  float scale;
+  cudaStream_t stream;
+} fa_tree_fwd_args;
+
+typedef struct {
+  fa_rows q, k, v;
+  const float *q_weight, *k_weight;
+  const double* inv_freq;
+  const int *positions, *starts;
+  void *q_out, *k_out, *v_out;
+  int B, N, H, Hkv, C, d, rotary_dim, norm;
+  float eps, factor;
+  int interleaved;
+  cudaStream_t stream;
+} fa_rope_fwd_args;
+
+typedef struct {
+  fa_rows q, k;
+  const float *q_weight, *k_weight;
+  const double* inv_freq;
+  const int* positions;
+  const void *dq_out, *dk_out, *dv_out;
+  fa_rows dq, dk, dv;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  size_t ws_bytes;
+  int B, N, H, Hkv, d, rotary_dim, norm;
+  float eps, factor;
+  int interleaved;
+  cudaStream_t stream;
+} fa_rope_bwd_args;
+
+fa_status fa_cross_fwd_packed(const fa_cross_fwd_args* args);
+fa_status fa_cross_bwd_packed(const fa_cross_bwd_args* args);
+fa_status fa_tree_fwd_packed(const fa_tree_fwd_args* args);
+fa_status fa_rope_fwd_packed(const fa_rope_fwd_args* args);
+fa_status fa_rope_bwd_packed(const fa_rope_bwd_args* args);
+
+/*
  * Synchronizes `stream`, then returns and clears the current device's status
  * word: FA_OK, or FA_ERR_TIMEOUT if a kernel of this library gave up waiting
  * on one of its barriers since the last check (its outputs are then
