@@ -51,7 +51,11 @@ struct CrossBwdParams {
   float scale;
   uint64_t wait_limit_ns;
   int debug_stall;
-  int out_align32;
+  int out_align32;   // dk, dv (and dq, where it is written directly) are 32-byte aligned
+  // With at most one key block per request each query block meets one item:
+  // its dQ is written here (scaled, bf16) instead of being added to the
+  // accumulator.  nullptr: more key blocks.
+  __nv_bfloat16* dq;
 };
 
 // A CTA's unit of work: query blocks [i0, i1) of a key block.
@@ -63,6 +67,10 @@ struct CrossBwdSeg {
   int run;    // where its sums go, or -1: the item is whole
 };
 
+// key blocks of a request with `len` keys (direct dQ: one even without keys, so
+// that its rows are written)
+__device__ __forceinline__ int cross_bwd_blocks(int len, bool direct) { return direct ? 1 : (len + 127) >> 7; }
+
 // item -> request, key/value head and key block; the items are walked upwards
 // from the request that the last call stopped at
 struct CrossBwdWalk {
@@ -70,7 +78,8 @@ struct CrossBwdWalk {
   int b = 0, start = 0;  // a request and its first item
 };
 
-__device__ __forceinline__ void cross_bwd_item(const CrossView& v, int item, CrossBwdWalk& at, CrossBwdSeg& s) {
+__device__ __forceinline__ void cross_bwd_item(const CrossView& v, bool direct, int item, CrossBwdWalk& at,
+                                               CrossBwdSeg& s) {
   int nkb = (v.Nk + 127) >> 7, len = v.Nk;
   if (!v.lens) {
     at.b = item / (v.Hkv * nkb);
@@ -79,7 +88,7 @@ __device__ __forceinline__ void cross_bwd_item(const CrossView& v, int item, Cro
     if (item < at.start) at.b = at.start = 0;
     for (;;) {
       len = v.len(at.b);
-      nkb = (len + 127) >> 7;
+      nkb = cross_bwd_blocks(len, direct);
       if (item < at.start + v.Hkv * nkb) break;
       at.start += v.Hkv * nkb;
       ++at.b;
@@ -109,13 +118,26 @@ __device__ __forceinline__ bool cross_bwd_next(const CrossBwdParams& p, const Cr
     s.i1 = (int)((long long)(part + 1) * p.nqb / plan.parts);
     s.run = plan.parts > 1 ? u : -1;
   }
-  cross_bwd_item(p.view, item, at, s);
+  cross_bwd_item(p.view, p.dq != nullptr, item, at, s);
   return true;
 }
 
 // Rounds, and the number of runs that ends the last one soonest: parts runs of
 // an item take ceil(rest parts / G) turns of ceil(n / parts) query blocks each
 // and about two blocks' time to start and write.
+__host__ __device__ inline CrossBwdPlan cross_bwd_split(int items, int nqb, int G) {
+  CrossBwdPlan plan{items / G, items % G, 1};
+  int best = 0x7fffffff;
+  for (int parts = 1; parts <= kCrossBwdMaxParts && parts <= nqb && plan.rest * parts <= kCrossBwdSlots; ++parts) {
+    const int cost = ((plan.rest * parts + G - 1) / G) * ((nqb + parts - 1) / parts + 2);
+    if (cost < best) {
+      best = cost;
+      plan.parts = parts;
+    }
+  }
+  return plan;
+}
+
 template <int kThreads>
 __device__ __forceinline__ void cross_bwd_plan(const CrossBwdParams& p, int* scratch, CrossBwdPlan* out) {
   const CrossView& v = p.view;
@@ -123,7 +145,7 @@ __device__ __forceinline__ void cross_bwd_plan(const CrossBwdParams& p, int* scr
   if (!v.lens) {
     items = threadIdx.x == 0 ? p.B * ((v.Nk + 127) >> 7) : 0;
   } else {
-    for (int b = threadIdx.x; b < p.B; b += kThreads) items += (v.len(b) + 127) >> 7;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) items += cross_bwd_blocks(v.len(b), p.dq != nullptr);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
@@ -134,15 +156,7 @@ __device__ __forceinline__ void cross_bwd_plan(const CrossBwdParams& p, int* scr
     for (int w = 0; w < kThreads / 32; ++w) items += scratch[w];
     items *= v.Hkv;
     const int G = gridDim.x;
-    CrossBwdPlan plan{items / G, items % G, 1};
-    int best = 0x7fffffff;
-    for (int parts = 1; parts <= min(p.nqb, kCrossBwdMaxParts) && plan.rest * parts <= kCrossBwdSlots; ++parts) {
-      const int cost = ((plan.rest * parts + G - 1) / G) * ((p.nqb + parts - 1) / parts + 2);
-      if (cost < best) {
-        best = cost;
-        plan.parts = parts;
-      }
-    }
+    const CrossBwdPlan plan = cross_bwd_split(items, p.nqb, G);
     *out = plan;
     if (blockIdx.x == 0) *p.plan = plan;
   }
@@ -163,7 +177,8 @@ enum : int { kSiteCrossBwdClean = 60 };
 
 // Per row of each (request, key/value head), padded to whole 128-row blocks:
 // delta = sum dO O (0 behind the rows) and LSE log2(e) (+inf behind them, and
-// for rows without keys, so that P = 0 there); the dQ accumulator is zeroed.
+// for rows without keys, so that P = 0 there); the dQ accumulator, if there is
+// one, is zeroed.
 template <int D>
 __global__ void __launch_bounds__(256)
     fa_cross_bwd_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, float* delta_pad,
@@ -190,8 +205,10 @@ __global__ void __launch_bounds__(256)
         s = fmaf(x.x, y.x, s);
         s = fmaf(x.y, y.y, s);
       }
-      float4* z = reinterpret_cast<float4*>(dq_acc + row * D) + 2 * sub;
-      z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (dq_acc) {
+        float4* z = reinterpret_cast<float4*>(dq_acc + row * D) + 2 * sub;
+        z[0] = z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
 #pragma unroll
     for (int off = kThreadsPerRow / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -515,6 +532,29 @@ __global__ void __launch_bounds__(512, 1)
         // before a tile is refilled, the reduce issued from it two chunks ago
         // must have read it.
         const int qrow0 = (t.i0 + it) * 128 + 32 * q;
+        if (p.dq) {
+          __nv_bfloat16* row = p.dq + ((size_t)t.bk * p.view.R + qrow0 + lane) * D;
+          if (qrow0 + lane < p.view.R) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              uint32_t w16[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w16[e] = pack_bf16x2(__uint_as_float(dqv[c][2 * e]) * p.scale, __uint_as_float(dqv[c][2 * e + 1]) * p.scale);
+              if (p.out_align32) {
+                st_global_v8(row + 32 * c, w16);
+                st_global_v8(row + 32 * c + 16, w16 + 8);
+              } else {
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4)
+                  reinterpret_cast<uint4*>(row + 32 * c)[v4] =
+                      make_uint4(w16[4 * v4], w16[4 * v4 + 1], w16[4 * v4 + 2], w16[4 * v4 + 3]);
+              }
+            }
+          }
+          __syncwarp();  // the next tensor memory load is a whole warp's
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c, ++r) {
           uint8_t* tile = stage + (r & 1) * 4096;
@@ -697,7 +737,7 @@ __global__ void __launch_bounds__(512, 1)
 // After the main kernel: block x of the first 8 G writes a quarter (32 rows) of
 // dK or dV of a cut item, the sum of its runs in order; the next B Hkv blocks
 // zero dK and dV in the key blocks behind a request's keys; the others write
-// dQ = scale * accumulator in bf16.
+// dQ = scale * accumulator in bf16 (none where the main kernel wrote dQ).
 struct CrossBwdPostParams {
   CrossBwdParams p;
   const float* dq_acc;
@@ -711,7 +751,7 @@ __global__ void __launch_bounds__(256) fa_cross_bwd_post_kernel(const CrossBwdPo
   const CrossBwdParams& p = q.p;
   const CrossView& v = p.view;
   grid_wait();  // (no grid_trigger: a next call's first blocks would take the place of this one's)
-  const int cut_blocks = 8 * q.ctas, zero_blocks = v.lens ? p.B * v.Hkv : 0;
+  const int cut_blocks = 8 * q.ctas, zero_blocks = v.lens && !p.dq ? p.B * v.Hkv : 0;
   int x = blockIdx.x;
   if (x < cut_blocks) {
     const CrossBwdPlan plan = *p.plan;
@@ -719,7 +759,7 @@ __global__ void __launch_bounds__(256) fa_cross_bwd_post_kernel(const CrossBwdPo
     if (plan.parts == 1 || rest >= plan.rest) return;
     CrossBwdWalk at;
     CrossBwdSeg s;
-    cross_bwd_item(v, plan.rounds * q.ctas + rest, at, s);
+    cross_bwd_item(v, p.dq != nullptr, plan.rounds * q.ctas + rest, at, s);
     const float mul = grp ? 1.f : p.scale;
     __nv_bfloat16* out = (grp ? p.dv : p.dk) + ((size_t)s.bk * v.Nk + s.jb * 128) * D;
     for (int i = threadIdx.x; i < 32 * D / 4; i += 256) {

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -376,6 +377,7 @@ def _cross_sizes(q, k):
     return B, H, Hkv, Nq, Nk, d
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_cross_fwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
     return int(load_library().fa_cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d))
 
@@ -392,6 +394,7 @@ def fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale: float, stream=None
           _ptr(lse, "lse", torch.float32, (B, H, Nq), dev), ws, ws_bytes, B, H, Hkv, Nq, Nk, d, scale)
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_cross_bwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
     return int(load_library().fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d))
 
@@ -409,6 +412,7 @@ def fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale: 
           B, H, Hkv, Nq, Nk, d, scale)
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_tree_fwd_workspace_bytes(B: int, H: int, Hkv: int, T: int, C: int, d: int) -> int:
     return int(load_library().fa_tree_fwd_workspace_bytes(B, H, Hkv, T, C, d))
 
@@ -546,6 +550,7 @@ def fa_rope_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, starts, q_out,
           eps or 0.0, factor, 1 if interleaved else 0)
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_rope_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int) -> int:
     return int(load_library().fa_rope_bwd_workspace_bytes(B, H, Hkv, N, d))
 

@@ -138,7 +138,12 @@ def check_cross_bwd(q, k, v, o, do, lse, grads, scale, lens):
             assert (err <= bound).all(), (b, j, name, (err - bound).max(), err.max())
 
 
-CROSS_BWD = [c for c in CROSS if c[3] * c[4] < 1000000] + [(1, 1, 1, 3000, 40, None), (1, 2, 1, 900, 1100, [1000])]
+CROSS_BWD = [c for c in CROSS if c[3] * c[4] < 1000000] + [
+    (1, 1, 1, 3000, 40, None),           # one key block: dQ written directly, runs of query blocks
+    (3, 4, 2, 300, 128, [128, 0, 5]),
+    (2, 2, 2, 77, 100, [0, 0]),
+    (1, 2, 1, 900, 1100, [1000]),
+]
 
 
 @pytest.mark.parametrize("d", [64, 128])
