@@ -58,6 +58,13 @@ bool has_launch_regs(Kernel kernel, int regs, int dev, std::atomic<unsigned long
   return true;
 }
 
+// arrays of lengths, positions and masks: their element's alignment
+bool all_aligned(std::initializer_list<const void*> ptrs, unsigned bytes) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) return false;
+  return true;
+}
+
 fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   fa::CrossView v{};
   v.Nk = Nk;
@@ -267,7 +274,7 @@ fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* k
   if (st != FA_OK) return st;
   if ((st = check_scale(scale, 0)) != FA_OK) return st;
   if (ws_bytes < cross_fwd_workspace(B, H, Hkv, Nq, Nk, d)) return FA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k, v, key_lens, o, lse, workspace})) return FA_ERR_MISALIGNED;
+  if (!all_aligned16({q, k, v, o, lse, workspace}) || !all_aligned({key_lens}, 4)) return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, lse, workspace})) != FA_OK) return st;
   if (key_lens && (st = check_device_ptrs({key_lens})) != FA_OK) return st;
   fa::CrossView view = cross_view(H, Hkv, Nq, Nk);
@@ -291,7 +298,8 @@ fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* k
   if (st != FA_OK) return st;
   if ((st = check_scale(scale, 0)) != FA_OK) return st;
   if (ws_bytes < fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d)) return FA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace})) return FA_ERR_MISALIGNED;
+  if (!all_aligned16({q, k, v, o, dout, lse, dq, dk, dv, workspace}) || !all_aligned({key_lens}, 4))
+    return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, workspace})) != FA_OK) return st;
   if (key_lens && (st = check_device_ptrs({key_lens})) != FA_OK) return st;
   fa::CrossView view = cross_view(H, Hkv, Nq, Nk);
@@ -316,7 +324,8 @@ fa_status fa_tree_fwd(const void* q, const void* k_cache, const void* v_cache, c
   if (draft_masks && T > 64) return FA_ERR_UNSUPPORTED;
   if ((st = check_scale(scale, 0)) != FA_OK) return st;
   if (ws_bytes < cross_fwd_workspace(B, H, Hkv, T, C, d)) return FA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace}))
+  if (!all_aligned16({q, k_cache, v_cache, o, lse, workspace}) || !all_aligned({cache_lens, draft_lens}, 4) ||
+      !all_aligned({draft_masks}, 8))
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k_cache, v_cache, cache_lens, o, lse, workspace})) != FA_OK) return st;
   if (draft_lens && (st = check_device_ptrs({draft_lens})) != FA_OK) return st;

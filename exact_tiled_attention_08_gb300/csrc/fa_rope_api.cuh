@@ -106,7 +106,9 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   if (C < N) return FA_ERR_INVALID_ARG;
   for (const fa_rows* r : {q, k, v})
     if (present(r) && (st = check_rows(*r)) != FA_OK) return st;
-  if (!all_aligned16({q_weight, k_weight, inv_freq, positions, starts, q_out, k_out, v_out})) return FA_ERR_MISALIGNED;
+  if (!all_aligned16({q_weight, k_weight, q_out, k_out, v_out}) || !all_aligned({positions, starts}, 4) ||
+      !all_aligned({inv_freq}, 8))
+    return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs_given({q ? q->ptr : nullptr, k ? k->ptr : nullptr, v ? v->ptr : nullptr, q_weight,
                                      k_weight, inv_freq, positions, starts, q_out, k_out, v_out})) != FA_OK)
     return st;
@@ -167,8 +169,9 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
     if ((st = check_rows(*r)) != FA_OK) return st;
     if (!rows_disjoint(*r, B, N, r == dq ? H : Hkv, d)) return FA_ERR_INVALID_ARG;
   }
-  if (!all_aligned16({q_weight, k_weight, inv_freq, positions, dq_out, dk_out, dv_out, dq_weight, dk_weight,
-                      weights ? workspace : nullptr}))
+  if (!all_aligned16({q_weight, k_weight, dq_out, dk_out, dv_out, dq_weight, dk_weight,
+                      weights ? workspace : nullptr}) ||
+      !all_aligned({positions}, 4) || !all_aligned({inv_freq}, 8))
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs_given({need_q ? q->ptr : nullptr, need_k ? k->ptr : nullptr, q_weight, k_weight,
                                      inv_freq, positions, dq_out, dk_out, dv_out, dq ? dq->ptr : nullptr,

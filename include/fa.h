@@ -236,7 +236,9 @@ fa_status fa_bwd_static_scratch(const void* q, const void* k, const void* v, con
  *   key_lens in:  int32 [B] device array: request b has keys 0 .. key_lens[b]-1
  *                 (values outside [0, Nk] are taken as 0 and Nk), or null: Nk
  *                 for every request.  What K and V hold behind a request's
- *                 keys is never used, NaN and infinities included.
+ *                 keys is never used, NaN and infinities included.  (Arrays of
+ *                 lengths, positions, frequencies and masks, here and below,
+ *                 need only their element's alignment.)
  *   o        out: bf16 [B][H][Nq][d];  lse out: fp32 [B][H][Nq].
  *                 A row without keys (or whose scores are all -inf) gives
  *                 O = 0 and LSE = -inf.
@@ -291,6 +293,9 @@ fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* k
  *   T            any with draft_masks null; at most 64 with them
  *                (FA_ERR_UNSUPPORTED)
  *   workspace    as for fa_cross_fwd, of fa_tree_fwd_workspace_bytes()
+ * The values of a drafted token meet every row of its request (with weight 0
+ * where a mask hides it), so a drafted row of V with an infinity or NaN makes
+ * all of them NaN.
  * Limits: those of fa_cross_fwd with T for Nq and C for Nk.
  */
 size_t fa_tree_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d);

@@ -49,7 +49,31 @@ def test_attention_refusals(lib, entry):
     assert getattr(lib, entry + "_workspace_bytes")(1, 4, 2, 8, 100, 80) == 0
 
 
+def test_argument_structs(lib):
+    """The *_packed entry points check what their flat forms check; null is refused."""
+    for entry, pack in fa._PACKED.items():
+        assert getattr(lib, entry + "_packed")(None) == fa.FA_ERR_INVALID_ARG
+    need = lib.fa_cross_fwd_workspace_bytes(1, 4, 2, 8, 100, 128)
+
+    def call(q=P, ws_bytes=need, d=128, scale=0.1):
+        return lib.fa_cross_fwd_packed(fa._PACKED["fa_cross_fwd"](q, P, P, P, P, P, P, ws_bytes, 1, 4, 2, 8, 100, d,
+                                                                  scale, 0))
+
+    assert call(q=0) == fa.FA_ERR_INVALID_ARG and call(q=P + 8) == fa.FA_ERR_MISALIGNED
+    assert call(d=96) == fa.FA_ERR_UNSUPPORTED and call(scale=-1.0) == fa.FA_ERR_INVALID_ARG
+    assert call(ws_bytes=need - 1) == fa.FA_ERR_INVALID_ARG
+    row = (P, 1024, 1024, 128)
+    args = [*row, *row, *row, P, P, P, P, P, P, P, P, 1, 2, 4, 2, 2, 128, 128, 1, 1e-6, 1.0, 0, 0]
+    for at, wrong, status in ((0, P + 8, fa.FA_ERR_MISALIGNED), (25, 80, fa.FA_ERR_UNSUPPORTED),
+                              (24, 1, fa.FA_ERR_INVALID_ARG), (29, float("nan"), fa.FA_ERR_INVALID_ARG)):
+        bad = list(args)
+        bad[at] = wrong
+        assert lib.fa_rope_fwd_packed(fa._PACKED["fa_rope_fwd"](*bad)) == status, at
+
+
 def test_tree_refusals(lib):
+    assert cross(lib, "fa_tree_fwd", masks=P + 4) == fa.FA_ERR_MISALIGNED
+    assert cross(lib, "fa_tree_fwd", lens=P + 2) == fa.FA_ERR_MISALIGNED
     assert cross(lib, "fa_tree_fwd", lens=0) == fa.FA_ERR_INVALID_ARG
     assert cross(lib, "fa_tree_fwd", Nq=65) == fa.FA_ERR_UNSUPPORTED
 
@@ -91,7 +115,8 @@ def test_rope_forward_refusals(lib):
     assert rope_fwd(lib, eps=-1.0) == bad and rope_fwd(lib, eps=float("nan")) == bad
     assert rope_fwd(lib, factor=float("inf")) == bad
     assert rope_fwd(lib, q=rows(ptr=P + 8)) == odd and rope_fwd(lib, k=rows(token=1028)) == odd
-    assert rope_fwd(lib, v=rows(head=4)) == odd and rope_fwd(lib, qo=P + 8) == odd and rope_fwd(lib, pos=P + 4) == odd
+    assert rope_fwd(lib, v=rows(head=4)) == odd and rope_fwd(lib, qo=P + 8) == odd and rope_fwd(lib, pos=P + 2) == odd
+    assert rope_fwd(lib, freq=P + 4) == odd and rope_fwd(lib, weight=P + 4) == odd
 
 
 def rope_bwd(lib, q=DEFAULT, k=DEFAULT, dq=DEFAULT, dk=DEFAULT, dv=DEFAULT, gq=P, gk=P, gv=P, dqw=P, dkw=P, ws=P, ws_bytes=None, N=2, H=4,
