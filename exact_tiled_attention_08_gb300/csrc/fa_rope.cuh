@@ -17,10 +17,12 @@
 //
 // Both are bound by memory: a row is read once and written once.  A lane holds
 // 8 values of a row, D / 8 lanes a row; it holds whole pairs (in the half layout
-// 4 values of each half, two 8-byte accesses), so that the rotation needs no
-// other lane, and keeps 4 cosines and sines for the heads of its token.  The
-// rows of kRopeUnroll heads are loaded before the first is used.  Statistics
-// and rotation are fp32, rounded once.
+// 4 values of each half), so that the rotation needs no other lane, and keeps 4
+// cosines and sines for the heads of its token.  A warp has the rows of the
+// next kRopeStages - 1 heads on their way.  Statistics and rotation are fp32,
+// rounded once.  Measured, with the norm: 16384 tokens of 48 heads of 128 in 69 us
+// (5.8 TB/s), backward at 8004 tokens in 56 us (5.0 TB/s); a copy reaches
+// 6.8 TB/s.  What is left is the number of instructions per row.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -70,7 +72,9 @@ __device__ __forceinline__ void rope_angle(unsigned long long turns, int pos, fl
 // 8 values of a row: 4 from element e0 and 4 from e1
 struct RopeLane {
   float x[8];
-  __device__ __forceinline__ void unpack(const uint2& lo, const uint2& hi) {
+  // elements e0.. and e1.. of a row in shared memory
+  __device__ __forceinline__ void load(const uint8_t* row, int e0, int e1) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(row + 2 * e0), hi = *reinterpret_cast<const uint2*>(row + 2 * e1);
     const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -80,17 +84,21 @@ struct RopeLane {
   }
 };
 
-struct RopeRaw {
-  uint2 lo, hi;
-};
-__device__ __forceinline__ RopeRaw rope_load(const __nv_bfloat16* row, int e0, int e1, bool valid) {
-  RopeRaw r{make_uint2(0, 0), make_uint2(0, 0)};
-  if (valid) {
-    r.lo = __ldg(reinterpret_cast<const uint2*>(row + e0));
-    r.hi = __ldg(reinterpret_cast<const uint2*>(row + e1));
-  }
-  return r;
+// Rows on their way to a warp: a ring of kRopeStages in shared memory, one row of
+// each of the warp's tokens per stage (32 lanes x 16 bytes), filled with
+// cp.async, so that what is in flight takes no registers.
+constexpr int kRopeStages = 8;
+
+__device__ __forceinline__ void rope_copy(uint32_t smem, const void* row, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(row), "r"(valid ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void rope_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last kRopeStages - 1 groups of this warp have landed
+__device__ __forceinline__ void rope_landed() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kRopeStages - 1) : "memory");
+  __syncwarp();
+}
+
 __device__ __forceinline__ void rope_store(__nv_bfloat16* row, int e0, int e1, const RopeLane& v) {
   *reinterpret_cast<uint2*>(row + e0) = make_uint2(pack_bf16x2(v.x[0], v.x[1]), pack_bf16x2(v.x[2], v.x[3]));
   *reinterpret_cast<uint2*>(row + e1) = make_uint2(pack_bf16x2(v.x[4], v.x[5]), pack_bf16x2(v.x[6], v.x[7]));
@@ -137,10 +145,9 @@ __device__ __forceinline__ float rope_row_sum(float v) {
 }
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;
-// CTAs held by an SM.  (Measured, forward and backward with the norm, 16384 and
-// 8004 tokens of 48 heads: 3 and 2 take 78 and 71 us; 4 and 3, with their rows
-// spilled, 101 and 84 us.)
+// CTAs held by an SM.  More of them are slower, although they would fit: the
+// rows of more heads and tokens are then open in memory at once (forward with
+// 16384 tokens of 48 heads: 3 take 70 us, 4 74 us, 5 94 us).
 constexpr int kRopeFwdPerSm = 3, kRopeBwdPerSm = 2;
 
 // the weights of a lane's values (ones without a weight)
@@ -162,11 +169,15 @@ struct RopeToken {
 template <int D>
 __device__ __forceinline__ RopeToken rope_token(const RopeParams& p, long long unit) {
   constexpr int kLanes = D / 8, kTokens = 32 / kLanes;
-  const long long groups = (p.tokens + kTokens - 1) / kTokens;
+  // a CTA's warps take neighbouring tokens and the same heads, neighbouring CTAs
+  // the other heads of these tokens
+  constexpr int kWarps = kRopeThreads / 32;
+  const int steps = (p.H + 2 * p.Hkv + p.head_step - 1) / p.head_step;
   const int lane = threadIdx.x & 31;
+  const long long cta = unit / kWarps;
   RopeToken t;
-  const int step = (int)(unit / groups);
-  t.token = (unit - step * groups) * kTokens + lane / kLanes;
+  const int step = (int)(cta % steps);
+  t.token = (cta / steps * kWarps + unit % kWarps) * kTokens + lane / kLanes;
   t.sub = lane % kLanes;
   t.valid = t.token < p.tokens;
   t.b = t.valid ? (int)(t.token / p.N) : 0;
@@ -176,40 +187,63 @@ __device__ __forceinline__ RopeToken rope_token(const RopeParams& p, long long u
   return t;
 }
 
-// heads [h0, h1) of one of q, k, v: norm, rotation and store
+// Heads [h0, h1) of one of q, k, v: norm, rotation and store.  (Each of the three
+// has a loop of its own with running addresses: one loop over all heads that
+// looks up where a head's row is takes 86 instead of 70 us, its ring not
+// emptying in between notwithstanding.)
 template <int D, bool kInterleaved, bool kNorm, bool kTurn>
-__device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& turn, const __nv_bfloat16* in,
-                                               long long in_head, __nv_bfloat16* out, long long out_head, int h0,
-                                               int h1, int e0, int e1, bool valid, bool stored, const float* weight,
-                                               float eps) {
+__device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& turn, uint8_t* ring,
+                                               const __nv_bfloat16* in, long long in_head, __nv_bfloat16* out,
+                                               long long out_head, int h0, int h1, int e0, int e1, bool valid,
+                                               bool stored, const float* weight, float eps) {
+  constexpr int kLanes = D / 8;
+  if (h0 >= h1) return;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* mine = ring + (lane / kLanes) * (2 * D);  // this token's row of a stage
+  const uint32_t dst = smem_u32(ring) + lane * 16;
+  const __nv_bfloat16* src = in + 8 * (lane % kLanes) + h0 * in_head;
+  out += h0 * out_head;
   float w[8];
   if (kNorm) rope_weights(weight, e0, e1, w);
-  RopeRaw raw[kRopeUnroll];  // the next rows, on their way
+  int left = h1 - h0;  // rows to fetch
 #pragma unroll
-  for (int u = 0; u < kRopeUnroll; ++u) raw[u] = rope_load(in + (h0 + u) * in_head, e0, e1, valid && h0 + u < h1);
-  for (int h = h0; h < h1; h += kRopeUnroll) {
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      RopeLane v;
-      v.unpack(raw[u].lo, raw[u].hi);
-      raw[u] = rope_load(in + (h + u + kRopeUnroll) * in_head, e0, e1, valid && h + u + kRopeUnroll < h1);
-      if (kNorm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v.x[i], v.x[i], ss);
-        const float r = rsqrtf(rope_row_sum<D / 8>(ss) * (1.f / D) + eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v.x[i] *= r * w[i];
-      }
-      if (kTurn) turn.template apply<false>(v);
-      if (stored && h + u < h1) rope_store(out + (h + u) * out_head, e0, e1, v);
-    }
+  for (int i = 0; i < kRopeStages - 1; ++i) {
+    if (left > 0) rope_copy(dst + i * 512, src, valid);
+    rope_commit();
+    src += in_head;
+    --left;
   }
+  int stage = 0;
+  for (int n = h1 - h0; n > 0; --n) {
+    __syncwarp();  // the stage filled next has been read
+    if (left > 0) rope_copy(dst + ((stage + kRopeStages - 1) % kRopeStages) * 512, src, valid);
+    rope_commit();
+    src += in_head;
+    --left;
+    rope_landed();
+    RopeLane v;
+    v.load(mine + stage * 512, e0, e1);
+    stage = (stage + 1) % kRopeStages;
+    if (kNorm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v.x[i], v.x[i], ss);
+      const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.x[i] *= r * w[i];
+    }
+    if (kTurn) turn.template apply<false>(v);
+    if (stored) rope_store(out, e0, e1, v);
+    out += out_head;
+  }
+  __syncwarp();  // the ring has been read
 }
 
 template <int D, bool kInterleaved, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kernel(const RopeParams p) {
   __shared__ unsigned long long turns[64];
+  __shared__ __align__(16) uint8_t rings[kRopeThreads / 32][kRopeStages * 512];
+  uint8_t* ring = rings[threadIdx.x >> 5];
   for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = rope_turns(p.inv_freq[i]);
   __syncthreads();
   for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); unit < p.units;
@@ -225,16 +259,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     if (t.h0 < p.H + p.Hkv) turn.setup(turns, p.rot, t.sub, pos, p.factor);
     auto in = [&](const RopeRows& r) { return r.ptr + t.b * r.batch + t.n * r.token; };
     if (p.q.ptr && t.h0 < p.H)
-      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, in(p.q), p.q.head,
+      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.q), p.q.head,
                                                    p.q_out + ((long long)t.b * p.H * p.N + t.n) * D,
                                                    (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1, t.valid, t.valid,
                                                    p.q_weight, p.eps);
     const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D, next = (long long)p.C * D;
     if (p.k.ptr)
-      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, in(p.k), p.k.head, p.k_out + cache, next, max(t.h0 - p.H, 0),
+      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.k), p.k.head, p.k_out + cache, next, max(t.h0 - p.H, 0),
                                                    min(t.h1 - p.H, p.Hkv), e0, e1, t.valid, stored, p.k_weight, p.eps);
     if (p.v.ptr)
-      rope_fwd_heads<D, kInterleaved, false, false>(turn, in(p.v), p.v.head, p.v_out + cache, next,
+      rope_fwd_heads<D, kInterleaved, false, false>(turn, ring, in(p.v), p.v.head, p.v_out + cache, next,
                                                     max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
                                                     stored, nullptr, 0.f);
   }
@@ -242,51 +276,70 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
 
 // heads [h0, h1) of one of q, k, v, backwards: dw gathers g o x^ of its rows
 template <int D, bool kInterleaved, bool kNorm, bool kTurn>
-__device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& turn, const __nv_bfloat16* dy,
-                                               long long dy_head, const __nv_bfloat16* in, long long in_head,
-                                               __nv_bfloat16* out, long long out_head, int h0, int h1, int e0, int e1,
-                                               bool valid, const float* weight, float eps, float (&dw)[8]) {
-  constexpr int U = kNorm ? kRopeUnroll / 2 : kRopeUnroll;  // (two rows each with the norm)
+__device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& turn, uint8_t* ring,
+                                               const __nv_bfloat16* dy, long long dy_head, const __nv_bfloat16* in,
+                                               long long in_head, __nv_bfloat16* out, long long out_head, int h0,
+                                               int h1, int e0, int e1, bool valid, const float* weight, float eps,
+                                               float (&dw)[8]) {
+  constexpr int kLanes = D / 8;
+  if (h0 >= h1) return;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* mine = ring + (lane / kLanes) * (2 * D);
+  const uint32_t dst = smem_u32(ring) + lane * 16;
+  const __nv_bfloat16* src = dy + 8 * (lane % kLanes) + h0 * dy_head;
+  const __nv_bfloat16* xsrc = kNorm ? in + 8 * (lane % kLanes) + h0 * in_head : nullptr;
+  out += h0 * out_head;
+  int left = h1 - h0;  // rows to fetch
+  auto fetch = [&](int stage) {
+    if (left > 0) {
+      rope_copy(dst + stage * 512, src, valid);
+      if (kNorm) rope_copy(dst + (kRopeStages + stage) * 512, xsrc, valid);
+    }
+    rope_commit();
+    src += dy_head;
+    if (kNorm) xsrc += in_head;
+    --left;
+  };
   float w[8];
   if (kNorm) rope_weights(weight, e0, e1, w);
-  RopeRaw raw[U], xraw[U];  // the next rows, on their way
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    raw[u] = rope_load(dy + (h0 + u) * dy_head, e0, e1, valid && h0 + u < h1);
-    if (kNorm) xraw[u] = rope_load(in + (h0 + u) * in_head, e0, e1, valid && h0 + u < h1);
-  }
-  for (int h = h0; h < h1; h += U) {
+  for (int i = 0; i < kRopeStages - 1; ++i) fetch(i);
+  int stage = 0;
+  for (int n = h1 - h0; n > 0; --n) {
+    __syncwarp();  // the stage filled next has been read
+    fetch((stage + kRopeStages - 1) % kRopeStages);
+    rope_landed();
+    RopeLane g;
+    g.load(mine + stage * 512, e0, e1);
+    if (kTurn) turn.template apply<true>(g);
+    if (kNorm) {
+      RopeLane x;  // (of a token that is not there: zeros, which add nothing)
+      x.load(mine + (kRopeStages + stage) * 512, e0, e1);
+      float ss = 0.f, dot = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool more = valid && h + u + U < h1;
-      RopeLane g;
-      g.unpack(raw[u].lo, raw[u].hi);
-      raw[u] = rope_load(dy + (h + u + U) * dy_head, e0, e1, more);
-      if (kTurn) turn.template apply<true>(g);
-      if (kNorm) {
-        RopeLane x;
-        x.unpack(xraw[u].lo, xraw[u].hi);
-        xraw[u] = rope_load(in + (h + u + U) * in_head, e0, e1, more);
-        // rows that are not there were loaded as zeros: they add nothing
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x.x[i], x.x[i], ss);
-          dot = fmaf(g.x[i] * w[i], x.x[i], dot);
-        }
-        const float r = rsqrtf(rope_row_sum<D / 8>(ss) * (1.f / D) + eps);
-        dot = rope_row_sum<D / 8>(dot) * (1.f / D) * r;  // mean(w g x^)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x.x[i] = h + u < h1 && valid ? x.x[i] * r : 0.f;
-          dw[i] = fmaf(g.x[i], x.x[i], dw[i]);
-          g.x[i] = r * fmaf(-x.x[i], dot, g.x[i] * w[i]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(x.x[i], x.x[i], ss);
+        dot = fmaf(g.x[i] * w[i], x.x[i], dot);
       }
-      if (valid && h + u < h1) rope_store(out + (h + u) * out_head, e0, e1, g);
+      const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + eps);
+      dot = rope_row_sum<kLanes>(dot) * (1.f / D) * r;  // mean(w g x^)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x.x[i] = valid ? x.x[i] * r : 0.f;
+        dw[i] = fmaf(g.x[i], x.x[i], dw[i]);
+        g.x[i] = r * fmaf(-x.x[i], dot, g.x[i] * w[i]);
+      }
     }
+    stage = (stage + 1) % kRopeStages;
+    if (valid) rope_store(out, e0, e1, g);
+    out += out_head;
   }
+  __syncwarp();  // the ring has been read
 }
+
+template <bool kNorm>
+constexpr int kRopeBwdSmemBytes = kRopeThreads / 32 * (kNorm ? 2 : 1) * kRopeStages * 512;
+static_assert(kRopeBwdSmemBytes<true> >= kRopeThreads / 32 * 2 * 128 * 4, "the warps' sums take the rings' place");
 
 // Backward.  The weight gradients are summed in registers over a warp's rows,
 // over a CTA's warps in a fixed order, and over the CTAs by fa_rope_dw_kernel,
@@ -295,10 +348,11 @@ template <int D, bool kInterleaved, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8;
   __shared__ unsigned long long turns[64];
-  __shared__ float sums[kNorm ? kRopeThreads / 32 : 1][2][D];
+  extern __shared__ __align__(16) uint8_t rope_smem[];  // the warps' rings; at the end their sums [warp][2][D]
   for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = rope_turns(p.inv_freq[i]);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = rope_smem + warp * (kRopeBwdSmemBytes<kNorm> / (kRopeThreads / 32));
   float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
@@ -313,21 +367,23 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
     auto at = [&](const RopeRows& r) { return const_cast<__nv_bfloat16*>(r.ptr) + t.b * r.batch + t.n * r.token; };
     const long long next = (long long)p.N * D, kv = ((long long)t.b * p.Hkv * p.N + t.n) * D;
     if (p.dq.ptr && t.h0 < p.H)
-      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, p.q_out + ((long long)t.b * p.H * p.N + t.n) * D, next,
+      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, ring, p.q_out + ((long long)t.b * p.H * p.N + t.n) * D, next,
                                                    at(p.q), p.q.head, at(p.dq), p.dq.head, t.h0, min(t.h1, p.H), e0,
                                                    e1, t.valid, p.q_weight, p.eps, dw[0]);
     if (p.dk.ptr)
-      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, p.k_out + kv, next, at(p.k), p.k.head, at(p.dk), p.dk.head,
+      rope_bwd_heads<D, kInterleaved, kNorm, true>(turn, ring, p.k_out + kv, next, at(p.k), p.k.head, at(p.dk), p.dk.head,
                                                    max(t.h0 - p.H, 0), min(t.h1 - p.H, p.Hkv), e0, e1, t.valid,
                                                    p.k_weight, p.eps, dw[1]);
     if (p.dv.ptr)
-      rope_bwd_heads<D, kInterleaved, false, false>(turn, p.v_out + kv, next, nullptr, 0, at(p.dv), p.dv.head,
+      rope_bwd_heads<D, kInterleaved, false, false>(turn, ring, p.v_out + kv, next, nullptr, 0, at(p.dv), p.dv.head,
                                                     max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
                                                     nullptr, 0.f, dw[1]);
   }
   if constexpr (kNorm) {
     grid_trigger();  // the next kernel adds the CTAs' sums
     if (!p.partials) return;
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(rope_smem);
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -335,12 +391,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
       float v = dw[t][i];
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < kLanes) sums[warp][t][(i < 4 ? e0 : e1) + (i & 3)] = v;
+      if (lane < kLanes) sums[(warp * 2 + t) * D + (i < 4 ? e0 : e1) + (i & 3)] = v;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {
     float v = 0.f;
-    for (int w = 0; w < kRopeThreads / 32; ++w) v += (&sums[w][0][0])[i];
+    for (int w = 0; w < kRopeThreads / 32; ++w) v += sums[w * 2 * D + i];
     p.partials[(long long)blockIdx.x * 2 * D + i] = v;
   }
   }

@@ -63,15 +63,17 @@ fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
 }
 
 // Warps' units of work: a warp's tokens times `head_step` heads.  All heads of a
-// token share its angles, so a unit takes as many as leave eight units for every
-// warp that the device holds at once (`warps`), whose number of turns is then
-// nearly even; a few tokens' heads are spread over the warps one by one.
+// token share its angles and one start of the ring, so a unit takes as many as
+// leave four units for every warp that the device holds at once (`warps`); a
+// few tokens' heads are spread over the warps one by one.  (Measured, 8, 16, 24
+// and 48 heads: forward at 16384 tokens 82, 78, 70 and 74 us; backward at 8004
+// tokens 64, 59, 62 and 62 us.)
 void rope_units(fa::RopeParams& p, int d, long long warps) {
   const long long per_warp = 32 / (d / 8), groups = (p.tokens + per_warp - 1) / per_warp;
   const int heads = p.H + 2 * p.Hkv;
-  const long long steps = std::max<long long>(1, std::min<long long>(heads, (8 * warps + groups - 1) / groups));
+  const long long steps = std::max<long long>(1, std::min<long long>(heads, (4 * warps + groups - 1) / groups));
   p.head_step = (int)((heads + steps - 1) / steps);
-  p.units = groups * ((heads + p.head_step - 1) / p.head_step);
+  p.units = (groups + 7) / 8 * 8 * ((heads + p.head_step - 1) / p.head_step);
 }
 
 template <int D, bool kNorm>
@@ -84,10 +86,15 @@ void launch_rope_fwd(const fa::RopeParams& p, unsigned grid, int interleaved, cu
 
 template <int D, bool kNorm>
 void launch_rope_bwd(const fa::RopeParams& p, unsigned grid, int interleaved, cudaStream_t stream) {
-  if (interleaved)
-    fa::fa_rope_bwd_kernel<D, true, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  else
-    fa::fa_rope_bwd_kernel<D, false, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+  constexpr int smem = fa::kRopeBwdSmemBytes<kNorm>;
+  // (a failure to set the size shows in the launch)
+  if (interleaved) {
+    set_smem(fa::fa_rope_bwd_kernel<D, true, kNorm>, smem);
+    fa::fa_rope_bwd_kernel<D, true, kNorm><<<grid, fa::kRopeThreads, smem, stream>>>(p);
+  } else {
+    set_smem(fa::fa_rope_bwd_kernel<D, false, kNorm>, smem);
+    fa::fa_rope_bwd_kernel<D, false, kNorm><<<grid, fa::kRopeThreads, smem, stream>>>(p);
+  }
 }
 
 }  // namespace

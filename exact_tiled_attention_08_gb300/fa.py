@@ -326,8 +326,9 @@ def fa_bwd_static_scratch(q, k, v, o, dout, lse, dq, dk, dv, scale: float, causa
 # stream are taken without a context manager where they are current already.
 def _ptr(t, name: str, dtype, shape, device) -> int:
     """Address of a tensor, checked."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         _check(t, name, dtype, shape, device)
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
 
 
@@ -364,9 +365,9 @@ def _call(name: str, device: torch.device, stream, *args) -> None:
 
 
 def _workspace(workspace, device):
-    if workspace.device != device or not workspace.is_contiguous():
+    if workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _cross_sizes(q, k):
@@ -387,11 +388,10 @@ def fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale: float, stream=None
     int32 [B] (or None: all Nk); o like q, lse [B,H,Nq] fp32."""
     B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
-    ws, ws_bytes = _workspace(workspace, dev)
     _call("fa_cross_fwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
           _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
-          _ptr(lse, "lse", torch.float32, (B, H, Nq), dev), ws, ws_bytes, B, H, Hkv, Nq, Nk, d, scale)
+          _ptr(lse, "lse", torch.float32, (B, H, Nq), dev), *_workspace(workspace, dev), B, H, Hkv, Nq, Nk, d, scale)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -403,12 +403,11 @@ def fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale: 
     """dQ, dK, dV of fa_cross_fwd by recomputation; dk, dv like k, v."""
     B, H, Hkv, Nq, Nk, d = _cross_sizes(q, k)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, Nq, d), (B, Hkv, Nk, d)
-    ws, ws_bytes = _workspace(workspace, dev)
     _call("fa_cross_bwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k, "k", bf, keys, dev), _ptr(v, "v", bf, keys, dev),
           _given(key_lens, "key_lens", torch.int32, (B,), dev), _ptr(o, "o", bf, rows, dev),
           _ptr(dout, "dout", bf, rows, dev), _ptr(lse, "lse", torch.float32, (B, H, Nq), dev),
-          _ptr(dq, "dq", bf, rows, dev), _ptr(dk, "dk", bf, keys, dev), _ptr(dv, "dv", bf, keys, dev), ws, ws_bytes,
+          _ptr(dq, "dq", bf, rows, dev), _ptr(dk, "dk", bf, keys, dev), _ptr(dv, "dv", bf, keys, dev), *_workspace(workspace, dev),
           B, H, Hkv, Nq, Nk, d, scale)
 
 
@@ -425,13 +424,12 @@ def fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse
     (or None: each sees the ones before it and itself; see tree_masks)."""
     B, H, Hkv, T, C, d = _cross_sizes(q, k_cache)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, T, d), (B, Hkv, C, d)
-    ws, ws_bytes = _workspace(workspace, dev)
     _call("fa_tree_fwd", dev, stream, _ptr(q, "q", bf, rows, dev),
           _ptr(k_cache, "k_cache", bf, keys, dev), _ptr(v_cache, "v_cache", bf, keys, dev),
           _ptr(cache_lens, "cache_lens", torch.int32, (B,), dev),
           _given(draft_lens, "draft_lens", torch.int32, (B,), dev),
           _given(draft_masks, "draft_masks", torch.int64, (B, T), dev), _ptr(o, "o", bf, rows, dev),
-          _ptr(lse, "lse", torch.float32, (B, H, T), dev), ws, ws_bytes, B, H, Hkv, T, C, d, scale)
+          _ptr(lse, "lse", torch.float32, (B, H, T), dev), *_workspace(workspace, dev), B, H, Hkv, T, C, d, scale)
 
 
 def tree_masks(parents: torch.Tensor) -> torch.Tensor:
