@@ -38,6 +38,7 @@ constexpr int kCrossMaxCtas = 152;  // the grid's bound: one CTA per SM
 struct CrossMeta {   // of each CTA, for the combine kernel
   int split;         // its last item goes on in the next CTA
   int b, it;         // that item
+  int fresh;         // drafted tokens of the request (TREE)
   long long last;    // the place behind the item's last block
   long long total;   // places of the sequence
 };
@@ -118,6 +119,13 @@ __device__ __forceinline__ bool cross_next(const CrossView& v, int items, CrossP
   return false;
 }
 
+// a b / c, in 32 bits where they hold the product (64-bit divisions take a
+// quarter of a microsecond of the start)
+__device__ __forceinline__ long long cross_share(int a, long long b, int c) {
+  if (b < (1 << 23)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;  // a <= 152
+  return a * b / c;
+}
+
 // The share of CTA `cta` of at most `ctas`, by one warp; CTAs past the sequence's
 // places get none.
 __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int items, int cta, int ctas,
@@ -164,7 +172,7 @@ __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int it
     if (lane == 0) *place = {0, 0, 0, 0};
     return;
   }
-  const long long start = cta * total / ctas, end = (cta + 1) * total / ctas;
+  const long long start = cross_share(cta, total, ctas), end = cross_share(cta + 1, total, ctas);
   if (lane == 0) {
     *all = total;
     *share_end = end;
@@ -175,7 +183,8 @@ __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int it
       const int n = places(b);
       if (start < at + (long long)n * items) {
         const long long off = start - at;
-        *place = {b, (int)(off / n), (int)(off % n), end - start};
+        const int it = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)n) : (int)(off / n);
+        *place = {b, it, (int)(off - (long long)it * n), end - start};
         break;
       }
       at += (long long)n * items;
@@ -346,18 +355,24 @@ __global__ void __launch_bounds__(384, 1)
           const int kvh = w.it / p.row_tiles;
           const int row0 = (w.it - kvh * p.row_tiles) * (PAIR ? 256 : 128);
           const int bk = w.b * v.Hkv + kvh;
-          // the first key block needs only ring slots: it goes out before the
-          // queries, whose buffer an earlier segment may still be reading
+          const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+          const int tiles = PAIR && row0 + 128 < v.R ? 2 : 1;
+          auto load_q = [&] {
+            mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
+            for (int t = 0; t < tiles; ++t)
+              for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
+                            row0 + 128 * t, bk);
+          };
+          // a later segment's first key block needs only ring slots: it goes out
+          // before the queries, whose buffer an earlier segment may still be reading
+          if (nq == 0) load_q();
           ok = load_kv(w.j0, 0, bk) && load_kv(w.j0, 1, bk);
           if (!ok) break;
-          const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-          if (use > 0 && !(ok = wait_bounded_inl(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty))) break;
-          const int tiles = PAIR && row0 + 128 < v.R ? 2 : 1;
-          mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
-          for (int t = 0; t < tiles; ++t)
-            for (int a = 0; a < C::kAtoms; ++a)
-              tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
-                          row0 + 128 * t, bk);
+          if (nq > 0) {
+            if (use > 0 && !(ok = wait_bounded_inl(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty))) break;
+            load_q();
+          }
           ++nq;
           for (int j = w.j0 + 1; ok && j < w.j1; ++j) ok = load_kv(j, 0, bk) && load_kv(j, 1, bk);
         }
@@ -497,6 +512,7 @@ __global__ void __launch_bounds__(384, 1)
           meta.split = 1;
           meta.b = w.b;
           meta.it = w.it;
+          meta.fresh = w.keys - w.len;
           meta.last = bar->end + w.n - w.j1;
           meta.total = bar->total;
         }
@@ -795,8 +811,7 @@ __global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdPar
   const int lane = threadIdx.x & 31, local0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
   const int kvh = meta.it / p.row_tiles;
   const int row0 = (meta.it - kvh * p.row_tiles) * (PAIR ? 256 : 128) + local0;
-  int drafted = v.Nq;
-  if (TREE) drafted = v.drafted(meta.b, v.len(meta.b));
+  const int drafted = meta.fresh;
   const size_t grow0 = ((size_t)meta.b * v.Hkv + kvh) * v.R + row0;
   // part i: the last segment of CTA x, then the first of each CTA after it
   auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local0; };
