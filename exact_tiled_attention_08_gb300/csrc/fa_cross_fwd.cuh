@@ -225,7 +225,8 @@ struct CrossCfg {
   static constexpr uint32_t kSCol1 = kDualS ? kOCol1 + D : kSCol;
   static_assert((kDualS ? kSCol1 + 128 : kOCol1 + D) <= kTmemCols, "tensor memory budget");
   static constexpr int kMergeBytes = 3 * 128 * 4;
-  static constexpr int kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + kMergeBytes + 512;
+  // (declared 1024-byte aligned, which is checked at run time)
+  static constexpr int kSmemBytes = 2 * kTileBytes + kSlots * kTileBytes + kMergeBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -246,6 +247,13 @@ struct CrossBarriers {
   int abort_flag;
 };
 static_assert(sizeof(CrossBarriers) <= 512, "barriers overflow their shared-memory slot");
+
+// A softmax warp's place and segment, kept here while its registers hold scores.
+struct CrossWarp {
+  CrossPlace at;
+  CrossSeg w;
+};
+static_assert(sizeof(CrossWarp) <= 64, "512 bytes for eight warps");
 
 enum : int { kSiteCrossQEmpty = 40, kSiteCrossKvEmpty, kSiteCrossQ, kSiteCrossK, kSiteCrossSFree, kSiteCrossV,
              kSiteCrossClean, kSiteCrossP, kSiteCrossS, kSiteCrossPv, kSiteCrossMerge, kSiteCrossTail };
@@ -280,12 +288,21 @@ __global__ void __launch_bounds__(384, 1)
     fa_cross_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const CrossFwdParams p) {
   using C = CrossCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
+    if (threadIdx.x == 0) {
+      atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
+      p.meta[blockIdx.x].split = 0;
+    }
+    return;
+  }
+  uint8_t* smem = smem_raw;
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * C::kTileBytes;
   float* sMerge = reinterpret_cast<float*>(sKV + C::kSlots * C::kTileBytes);  // [3][128]
   CrossBarriers* bar = reinterpret_cast<CrossBarriers*>(reinterpret_cast<uint8_t*>(sMerge) + C::kMergeBytes);
+  uint8_t* sWarps = reinterpret_cast<uint8_t*>(bar) + 512;  // CrossWarp of each softmax warp, 64 bytes apart
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CrossView& v = p.view;
   const int items = v.Hkv * p.row_tiles;
@@ -533,27 +550,54 @@ __global__ void __launch_bounds__(384, 1)
     int uses = 0;   // blocks this tile has processed over all segments
     int merges = 0;  // ALT: segments whose two accumulators were joined
     bool alive = true;
-    while (alive && cross_next(v, items, at, w)) {
-      const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0);
-      if (PAIR ? (row0 >= v.R) : (t == 1 && w.j1 - w.j0 < 2)) continue;  // nothing for this tile
-      const int row = row0 + r;
-      // TREE: what the row's token sees of the drafts
-      unsigned long long mask = 0;
-      int last_key = w.keys - 1;
-      if constexpr (TREE) {
-        const int tok = row % v.Nq;
-        if (v.masks)
-          mask = v.masks[(long long)w.b * v.T + tok] &
-                 (w.keys - w.len >= 64 ? ~0ull : (1ull << (w.keys - w.len)) - 1ull);
-        else
-          last_key = min(last_key, w.len + tok);
+    // (volatile: read again after the segment's blocks, not kept in registers)
+    volatile CrossWarp* mine = reinterpret_cast<volatile CrossWarp*>(sWarps + 64 * warp);
+    auto store = [&] {
+      __syncwarp();
+      if (lane == 0) {
+        mine->at.b = at.b, mine->at.it = at.it, mine->at.j = at.j, mine->at.left = at.left;
+        mine->w.b = w.b, mine->w.it = w.it, mine->w.j0 = w.j0, mine->w.j1 = w.j1, mine->w.n = w.n;
+        mine->w.len = w.len, mine->w.keys = w.keys;
+      }
+      __syncwarp();
+    };
+    auto load_place = [&] {
+      at.b = mine->at.b, at.it = mine->at.it, at.j = mine->at.j, at.left = mine->at.left;
+    };
+    auto load_seg = [&] {
+      w.b = mine->w.b, w.it = mine->w.it, w.j0 = mine->w.j0, w.j1 = mine->w.j1, w.n = mine->w.n;
+      w.len = mine->w.len, w.keys = mine->w.keys;
+    };
+    store();
+    while (alive) {
+      load_place();
+      if (!cross_next(v, items, at, w)) break;
+      store();
+      int jfirst, j1, cut_from, last_key;
+      unsigned long long mask = 0;  // TREE: what the row's token sees of the drafts
+      {
+        const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0);
+        if (PAIR ? (row0 >= v.R) : (t == 1 && w.j1 - w.j0 < 2)) continue;  // nothing for this tile
+        jfirst = w.j0 + (PAIR ? 0 : t);
+        j1 = w.j1;
+        cut_from = (TREE ? w.len : w.keys) - 127;  // first key of a block that is not seen whole
+        last_key = w.keys - 1;
+        if constexpr (TREE) {
+          const int tok = (row0 + r) % v.Nq;
+          if (v.masks) {
+            mask = v.masks[(long long)w.b * v.T + tok] &
+                   (w.keys - w.len >= 64 ? ~0ull : (1ull << (w.keys - w.len)) - 1ull);
+            last_key = w.len;  // (the drafts' first key, from which the mask counts)
+          } else {
+            last_key = min(last_key, w.len + tok);
+          }
+        }
       }
       float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
       // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
       // block's largest one, so that l + lcorr normalises O (see fa_fwd_kernel)
       float l = 0.f, lcorr = 0.f;
-      const int jfirst = w.j0 + (PAIR ? 0 : t);
-      for (int j = jfirst; j < w.j1; j += PAIR ? 1 : 2, ++uses) {
+      for (int j = jfirst; j < j1; j += PAIR ? 1 : 2, ++uses) {
         if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
           alive = false;
           break;
@@ -585,12 +629,12 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&bar->s_free[C::kDualS ? t : 0]);
 
         const int kbase = j * 128;
-        const bool cut = kbase + 128 > (TREE ? w.len : w.keys);
+        const bool cut = kbase >= cut_from;
         if (cut) {
           if (TREE && v.masks) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t bits = cross_bits(mask, kbase + 32 * c - w.len);
+              const uint32_t bits = cross_bits(mask, kbase + 32 * c - last_key);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-CUDART_INF_F);
@@ -690,6 +734,8 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc_fence_after();
       // ---- end of the segment
+      load_seg();
+      const int row = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0) + r;
       const bool join = !PAIR && w.j1 - w.j0 >= 2;
       float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
       if (join) {
