@@ -15,6 +15,9 @@ fa_status check_cross_shape(int B, int H, int Hkv, int Nq, int Nk, int d, int* R
   if (rows > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   fa_status st = check_shape(B, Hkv, (int)rows, d);
   if (st == FA_OK) st = check_shape(B, Hkv, Nk, d);
+  // the forward counts the key blocks of all requests, with what each costs at
+  // its start, in 32 bits
+  if (st == FA_OK && ((Nk + 127LL) / 128 + fa::kCrossStart) * B * Hkv > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   *R = (int)rows;
   return st;
 }
@@ -117,7 +120,8 @@ fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const C
   if (cuts && !p.view.lens) {
     const int most = (p.view.Nk + 127) / 128 + fa::kCrossStart;
     const long long items = (long long)p.B * p.view.Hkv * p.row_tiles;
-    cuts = !fa::cross_whole(items, grid, most, items * most);
+    cuts = items >= grid ? fa::cross_tail((int)(items % grid), grid, most, PAIR) == fa::kCrossTailCut
+                         : !fa::cross_whole((int)items, grid, most, items * most);
   }
   if (cuts) {
     const int per_block = PAIR ? 32 : 8;  // rows of a block

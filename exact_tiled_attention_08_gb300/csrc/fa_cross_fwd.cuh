@@ -75,30 +75,56 @@ constexpr int kCrossCut = 9;
 
 // Whether the CTAs take whole items, ceil(items / ctas) at most: where that
 // ends no later than even shares and the join of what they cut.
-__host__ __device__ __forceinline__ bool cross_whole(long long items, int ctas, int most, long long total) {
-  return (items + ctas - 1) / ctas * most <= total / ctas + kCrossCut;
+__host__ __device__ __forceinline__ bool cross_whole(int items, int ctas, int most, long long total) {
+  const long long turns = ((unsigned)items + (unsigned)ctas - 1u) / (unsigned)ctas;
+  return (turns * most - kCrossCut) * ctas <= total;
 }
 
-// A CTA's share of the sequence of all items' places.
+// Where all items cost the same and there are enough of them, CTA c takes the
+// items c, c + G, ... of the full rounds: the CTAs of a round work on few heads
+// together, whose keys they share through L2.  (In contiguous shares every head
+// is read at the same time: B=2 H=32 Nq=Nk=4096 d=128 takes 390 instead of
+// 364 us.)  The `rest` items of the last round: as single row tiles
+// where these fit the CTAs, whole, or cut evenly.
+enum : int { kCrossTailWhole, kCrossTailSingle, kCrossTailCut };
+__host__ __device__ __forceinline__ int cross_tail(int rest, int ctas, int places, bool pair) {
+  if (pair && rest > 0 && 2 * rest <= ctas) return kCrossTailSingle;
+  return rest == 0 || (long long)(places - kCrossCut) * ctas <= (long long)rest * places ? kCrossTailWhole : kCrossTailCut;
+}
+
+// A CTA's work: places of the sequence of items' places, one item after another
+// or every step-th, and then, maybe, a second run of them.
 struct CrossPlace {
   int b, it, j;    // request, item of it (head, row tile), place in the item
-  long long left;  // places of the CTA from there on
+  int step;        // from one item to the next
+  int single;      // PAIR: one row tile (0 or 1) of each item; -1: both
+  int more;        // another run follows
+  long long left;  // places of this run from there on
 };
 
 // A run of key blocks of one item.
 struct CrossSeg {
   int b, it, j0, j1, n;
   int len, keys;  // the request's own keys; with its drafts
+  int single;     // as in CrossPlace
   __device__ __forceinline__ bool first() const { return j0 == 0; }
   __device__ __forceinline__ bool last() const { return j1 == n; }
   // the last block's rows of V behind the keys hold anything (past Nk the TMA fills zeros)
   __device__ __forceinline__ bool dirty(const CrossView& v) const { return last() && keys < (n << 7) && keys < v.Nk; }
 };
 
-__device__ __forceinline__ bool cross_next(const CrossView& v, int items, CrossPlace& at, CrossSeg& s) {
-  while (at.left > 0) {
+// The next segment of the CTA's work; `second`: the run after the first.
+__device__ __forceinline__ bool cross_next(const CrossView& v, int items, const CrossPlace* second, CrossPlace& at,
+                                           CrossSeg& s) {
+  for (;;) {
+    if (at.left <= 0) {
+      if (!at.more) return false;
+      at = *second;
+      if (at.left <= 0) return false;
+    }
     s.b = at.b;
     s.it = at.it;
+    s.single = at.single;
     s.len = v.len(at.b);
     s.keys = s.len + v.drafted(at.b, s.len);
     s.n = cross_blocks(s.keys);
@@ -109,14 +135,15 @@ __device__ __forceinline__ bool cross_next(const CrossView& v, int items, CrossP
     at.j = end;
     if (at.j == s.n + kCrossStart) {
       at.j = 0;
-      if (++at.it == items) {
-        at.it = 0;
-        ++at.b;
+      at.it += at.step;
+      if (at.it >= items) {
+        const int over = at.step == 1 ? 1 : at.it / items;
+        at.b += over;
+        at.it -= over * items;
       }
     }
     if (s.j1 > 0) return true;  // (else only places before the item's blocks)
   }
-  return false;
 }
 
 // a b / c, in 32 bits where they hold the product (64-bit divisions take a
@@ -126,70 +153,146 @@ __device__ __forceinline__ long long cross_share(int a, long long b, int c) {
   return a * b / c;
 }
 
-// The share of CTA `cta` of at most `ctas`, by one warp; CTAs past the sequence's
-// places get none.
+// The work of CTA `cta` of at most `ctas`, by one warp.  (The numbers of places
+// of all requests fit 32 bits, with the items' not: the shape checks bound them.)
+template <bool PAIR>
 __device__ __forceinline__ void cross_schedule(const CrossView& v, int B, int items, int cta, int ctas,
-                                               CrossPlace* place, long long* all, long long* share_end) {
+                                               CrossPlace* place, CrossPlace* second, long long* all,
+                                               long long* share_end) {
   const int lane = threadIdx.x & 31;
-  const int chunk = (B + 31) / 32;
-  const int b0 = min(B, lane * chunk), b1 = min(B, b0 + chunk);
+  const int count = B * items;
   auto places = [&](int b) {
     const int len = v.len(b);
     return cross_blocks(len + v.drafted(b, len)) + kCrossStart;
   };
-  long long mine = 0;
-  int most = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = places(b);
-    mine += n;
-    most = max(most, n);
-  }
-  long long upto = mine;
+  // places of this lane's requests, and of all before them
+  const int chunk = (B + 31) / 32, b0 = min(B, lane * chunk), b1 = min(B, b0 + chunk);
+  int mine = 0, upto = 0, sum, most, least;
+  const bool alike = B == 1 || !v.lens;
+  if (alike) {
+    most = least = places(0);
+    sum = B * most;
+  } else {
+    most = 0, least = 0x7fffffff;
+    for (int b = b0; b < b1; ++b) {
+      const int n = places(b);
+      mine += n;
+      most = max(most, n);
+      least = min(least, n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long add = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += add;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int add = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += add;
+    }
+    sum = __shfl_sync(0xffffffffu, upto, 31);
   }
-  const long long total = __shfl_sync(0xffffffffu, upto, 31) * items;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (cross_whole((long long)B * items, ctas, most, total)) {
+  const long long total = (long long)sum * items;
+  CrossPlace x{0, 0, 0, 1, -1, 0, 0};
+  // a share of `count` items from `item` on, all of `most` places
+  auto share = [&](int item, long long of) {
+    const int g = (int)min((long long)ctas, of);
+    if (cta < g) {
+      const long long start = cross_share(cta, of, g), end = cross_share(cta + 1, of, g);
+      const int skip = start < (1ll << 31) ? (int)((uint32_t)start / (uint32_t)most) : (int)(start / most);
+      item += skip;
+      x.j = (int)(start - (long long)skip * most);
+      x.left = end - start;
+      if (lane == 0) {
+        *all = of;
+        *share_end = end;
+      }
+    }
+    return item;
+  };
+  auto put = [&](CrossPlace* to, int item) {
+    x.b = item / items;
+    x.it = item - x.b * items;
+    if (lane == 0) *to = x;
+  };
+  if (most == least && count >= ctas) {
+    const int full = count / ctas, rest = count - full * ctas;
+    const int tail = cross_tail(rest, ctas, most, PAIR);
+    x.step = ctas;
+    x.left = (long long)(full + (tail == kCrossTailWhole && cta < rest ? 1 : 0)) * most;
+    x.more = tail != kCrossTailWhole;
+    put(place, cta);
+    if (tail == kCrossTailWhole) return;
+    int item = full * ctas;
+    x = {0, 0, 0, 1, -1, 0, 0};
+    if (tail == kCrossTailSingle) {
+      item += cta >> 1;
+      x.single = cta & 1;
+      const int row0 = (item % items % ((v.R + 255) / 256)) * 256 + 128 * x.single;
+      if (cta < 2 * rest && row0 < v.R) x.left = most;
+    } else {
+      item = share(item, (long long)rest * most);
+    }
+    put(second, item);
+    return;
+  }
+  if (alike) {
+    int item = cta;
+    if (cross_whole(count, ctas, most, total))
+      x.left = cta < count ? most : 0;
+    else
+      item = share(0, total);
+    put(place, item);
+    return;
+  }
+  if (cross_whole(count, ctas, most, total)) {
     if (lane == 0) {
-      long long at = cta * ((long long)B * items) / ctas, left = (cta + 1) * ((long long)B * items) / ctas - at;
-      CrossPlace x{(int)(at / items), (int)(at % items), 0, 0};
-      for (long long b = x.b, it = x.it; left > 0; ++b, it = 0) {  // the places of those items
-        const long long take = min(left, items - it);
-        x.left += take * places((int)b);
+      int at = (int)((long long)cta * count / ctas), left = (int)((cta + 1LL) * count / ctas) - at;
+      x.b = at / items;
+      x.it = at - x.b * items;
+      for (int b = x.b, it = x.it; left > 0; ++b, it = 0) {  // the places of those items
+        const int take = min(left, items - it);
+        x.left += (long long)take * places(b);
         left -= take;
       }
       *place = x;
-      *all = *share_end = 1;  // (nothing is cut)
     }
     return;
   }
-  if (total < ctas) ctas = (int)total;
-  if (cta >= ctas) {
-    if (lane == 0) *place = {0, 0, 0, 0};
+  const int g = (int)min((long long)ctas, total);
+  if (cta >= g) {
+    if (lane == 0) *place = x;
     return;
   }
-  const long long start = cross_share(cta, total, ctas), end = cross_share(cta + 1, total, ctas);
+  const long long start = cross_share(cta, total, g), end = cross_share(cta + 1, total, g);
   if (lane == 0) {
     *all = total;
     *share_end = end;
   }
-  long long at = (upto - mine) * items;
-  if (start >= at && start < upto * items) {
+  long long at = (long long)(upto - mine) * items;
+  if (start >= at && start < (long long)upto * items) {
     for (int b = b0; b < b1; ++b) {
       const int n = places(b);
       if (start < at + (long long)n * items) {
         const long long off = start - at;
-        const int it = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)n) : (int)(off / n);
-        *place = {b, it, (int)(off - (long long)it * n), end - start};
+        x.b = b;
+        x.it = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)n) : (int)(off / n);
+        x.j = (int)(off - (long long)x.it * n);
+        x.left = end - start;
+        *place = x;
         break;
       }
       at += (long long)n * items;
     }
   }
+}
+
+// A segment's first row, and (PAIR) whether it has a second row tile.
+template <bool PAIR>
+__device__ __forceinline__ int cross_row0(const CrossSeg& w, int row_tiles) {
+  return (w.it % row_tiles) * (PAIR ? 256 : 128) + (PAIR && w.single > 0 ? 128 : 0);
+}
+template <bool PAIR>
+__device__ __forceinline__ bool cross_two(const CrossSeg& w, int row0, int R) {
+  return PAIR && w.single < 0 && row0 + 128 < R;
 }
 
 template <int D>
@@ -241,7 +344,7 @@ struct CrossBarriers {
   uint64_t merge_ready, merge_free;    // ALT: warpgroup 1's sums are in place; O_1 has been read
   uint64_t drain[2];
   uint64_t never;
-  CrossPlace place;
+  CrossPlace place, second;
   long long total, end;  // places of the sequence; end of the CTA's share
   uint32_t tmem_base;
   int abort_flag;
@@ -340,7 +443,8 @@ __global__ void __launch_bounds__(384, 1)
   }
   grid_wait();
   if (warp == 10)
-    cross_schedule(v, p.B, items, blockIdx.x, gridDim.x, &bar->place, &bar->total, &bar->end);
+    cross_schedule<PAIR>(v, p.B, items, blockIdx.x, gridDim.x, &bar->place, &bar->second,
+                         &bar->total, &bar->end);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -368,12 +472,12 @@ __global__ void __launch_bounds__(384, 1)
           ++loads;
           return true;
         };
-        while (ok && cross_next(v, items, at, w)) {
+        while (ok && cross_next(v, items, &bar->second, at, w)) {
           const int kvh = w.it / p.row_tiles;
-          const int row0 = (w.it - kvh * p.row_tiles) * (PAIR ? 256 : 128);
+          const int row0 = cross_row0<PAIR>(w, p.row_tiles);
           const int bk = w.b * v.Hkv + kvh;
           const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-          const int tiles = PAIR && row0 + 128 < v.R ? 2 : 1;
+          const int tiles = cross_two<PAIR>(w, row0, v.R) ? 2 : 1;
           auto load_q = [&] {
             mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
             for (int t = 0; t < tiles; ++t)
@@ -415,12 +519,11 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;
         bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
-        while (ok && cross_next(v, items, at, w)) {
+        while (ok && cross_next(v, items, &bar->second, at, w)) {
           const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
           if (!wait_bounded_inl(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
           ++nq;
-          const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128);
-          const bool two = PAIR && row0 + 128 < v.R;
+          const bool two = cross_two<PAIR>(w, cross_row0<PAIR>(w, p.row_tiles), v.R);
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int ks = C::template slot<PAIR>(0, g);
             if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK))) break;
@@ -463,9 +566,8 @@ __global__ void __launch_bounds__(384, 1)
         int g = 0, cleaned = 0;
         int pv_uses[2] = {0, 0};
         bool ok = true;
-        while (ok && cross_next(v, items, at, w)) {
-          const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128);
-          const bool two = PAIR && row0 + 128 < v.R;
+        while (ok && cross_next(v, items, &bar->second, at, w)) {
+          const bool two = cross_two<PAIR>(w, cross_row0<PAIR>(w, p.row_tiles), v.R);
           const bool dirty = w.dirty(v);
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int vs = C::template slot<PAIR>(1, g);
@@ -508,7 +610,7 @@ __global__ void __launch_bounds__(384, 1)
       int g = 0, cleaned = 0;
       bool ok = true;
       CrossMeta meta{};
-      while (ok && cross_next(v, items, at, w)) {
+      while (ok && cross_next(v, items, &bar->second, at, w)) {
         if (w.dirty(v)) {
           const int vs = C::template slot<PAIR>(1, g + w.j1 - 1 - w.j0);
           ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
@@ -555,29 +657,32 @@ __global__ void __launch_bounds__(384, 1)
     auto store = [&] {
       __syncwarp();
       if (lane == 0) {
+        mine->at.step = at.step, mine->at.single = at.single, mine->at.more = at.more;
         mine->at.b = at.b, mine->at.it = at.it, mine->at.j = at.j, mine->at.left = at.left;
         mine->w.b = w.b, mine->w.it = w.it, mine->w.j0 = w.j0, mine->w.j1 = w.j1, mine->w.n = w.n;
-        mine->w.len = w.len, mine->w.keys = w.keys;
+        mine->w.len = w.len, mine->w.keys = w.keys, mine->w.single = w.single;
       }
       __syncwarp();
     };
     auto load_place = [&] {
+      at.step = mine->at.step, at.single = mine->at.single, at.more = mine->at.more;
       at.b = mine->at.b, at.it = mine->at.it, at.j = mine->at.j, at.left = mine->at.left;
     };
     auto load_seg = [&] {
       w.b = mine->w.b, w.it = mine->w.it, w.j0 = mine->w.j0, w.j1 = mine->w.j1, w.n = mine->w.n;
-      w.len = mine->w.len, w.keys = mine->w.keys;
+      w.len = mine->w.len, w.keys = mine->w.keys, w.single = mine->w.single;
     };
     store();
     while (alive) {
       load_place();
-      if (!cross_next(v, items, at, w)) break;
+      if (!cross_next(v, items, &bar->second, at, w)) break;
       store();
       int jfirst, j1, cut_from, last_key;
       unsigned long long mask = 0;  // TREE: what the row's token sees of the drafts
       {
-        const int row0 = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0);
-        if (PAIR ? (row0 >= v.R) : (t == 1 && w.j1 - w.j0 < 2)) continue;  // nothing for this tile
+        const int row0 = cross_row0<PAIR>(w, p.row_tiles) + (PAIR ? 128 * t : 0);
+        // nothing for this tile
+        if (PAIR ? (t == 1 && !cross_two<PAIR>(w, row0 - 128, v.R)) : (t == 1 && w.j1 - w.j0 < 2)) continue;
         jfirst = w.j0 + (PAIR ? 0 : t);
         j1 = w.j1;
         cut_from = (TREE ? w.len : w.keys) - 127;  // first key of a block that is not seen whole
@@ -667,7 +772,7 @@ __global__ void __launch_bounds__(384, 1)
             m = m_new;
           }
         }
-        const float ref = m == -CUDART_INF_F ? 0.f : m;  // a row without keys so far: every P is 2^-inf = 0
+        const float ref = fmaxf(m, -3.402823466e38f);  // (finite for a row without keys so far: every P is 2^-inf = 0)
         const float2 c2 = make_float2(cj, cj);
         const float2 mneg2 = make_float2(-ref, -ref);
         float2 acc[4];
@@ -735,7 +840,7 @@ __global__ void __launch_bounds__(384, 1)
       tc_fence_after();
       // ---- end of the segment
       load_seg();
-      const int row = (w.it % p.row_tiles) * (PAIR ? 256 : 128) + (PAIR ? 128 * t : 0) + r;
+      const int row = cross_row0<PAIR>(w, p.row_tiles) + (PAIR ? 128 * t : 0) + r;
       const bool join = !PAIR && w.j1 - w.j0 >= 2;
       float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
       if (join) {

@@ -246,7 +246,7 @@ fa_status fa_bwd_static_scratch(const void* q, const void* k, const void* v, con
  *                 16-byte aligned, contents on entry ignored; calls that may
  *                 overlap on the GPU need one each.
  * Limits: those of fa_fwd with B * Hkv for B * H and, for N, both
- * (H / Hkv) * Nq and Nk.  The results are the same from run to run.
+ * (H / Hkv) * Nq and Nk; and (ceil(Nk / 128) + 4) * B * Hkv < 2^31.  The results are the same from run to run.
  */
 size_t fa_cross_fwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
 fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* key_lens, void* o, float* lse,

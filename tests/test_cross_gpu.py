@@ -360,3 +360,30 @@ def test_replayed_graph_and_other_stream():
         assert fa.fa_check_device_status() == fa.FA_OK
         check_cross_fwd(q, k, v, o, lse, 0.1, n)
         check_cross_bwd(q, k, v, o, do, lse, g, 0.1, n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", [
+    (1, 160, 160, 200, 300, None),      # 160 row tile pairs: a full round, then pairs cut into single tiles
+    (1, 160, 160, 100, 500, None),      # the same with one row tile per head
+    (2, 130, 130, 300, 260, None),      # 520 pairs, a last round of many
+    (2, 20, 10, 1100, 200, [200, 190]),  # equal numbers of blocks of unequal lengths
+    (1, 250, 250, 129, 3000, None),     # a last round that is cut
+    (1, 153, 153, 256, 128, None),
+])
+def test_rounds_of_equal_items(case, d):
+    """More items than CTAs, all with the same number of key blocks."""
+    B, H, Hkv, Nq, Nk, lens = case
+    q, k, v, _ = (x.cuda() for x in cross_inputs(B, H, Hkv, Nq, Nk, d, 7))
+    scale = 1 / math.sqrt(d)
+    kl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = fa.cross_attention_forward(q, k, v, scale, kl)
+    # every head against fp32, the oracle's spread of twelve by its bounds
+    check_cross_fwd(q, k, v, o, lse, scale, lens)
+    G = H // Hkv
+    s = torch.matmul(q.float(), k.float().repeat_interleave(G, 1).transpose(-1, -2)) * scale
+    if lens is not None:
+        s = s.masked_fill(torch.arange(Nk, device="cuda") >= kl[:, None, None, None], -math.inf)
+    ref = torch.matmul(torch.softmax(s, -1), v.float().repeat_interleave(G, 1))
+    assert (o.float() - ref).abs().max() <= 4 * H2 * v.float().abs().max()
+    assert (lse - torch.logsumexp(s, -1)).abs().max() <= 1e-3  # (both sides fp32)
