@@ -114,8 +114,8 @@ __device__ __forceinline__ bool cross_bwd_next(const CrossBwdParams& p, const Cr
     if (u >= plan.rest * plan.parts) return false;
     const int part = u / plan.rest;
     item = plan.rounds * G + (u - part * plan.rest);
-    s.i0 = (int)((long long)part * p.nqb / plan.parts);
-    s.i1 = (int)((long long)(part + 1) * p.nqb / plan.parts);
+    s.i0 = part * p.nqb / plan.parts;  // (at most 16 * 2^24)
+    s.i1 = (part + 1) * p.nqb / plan.parts;
     s.run = plan.parts > 1 ? u : -1;
   }
   cross_bwd_item(p.view, p.dq != nullptr, item, at, s);

@@ -334,7 +334,17 @@ def _ptr(t, name: str, dtype, shape, device) -> int:
 
 def _given(t, name: str, dtype, shape, device) -> int:
     """Address of an optional tensor (0 for None), checked."""
-    return 0 if t is None else _ptr(t, name, dtype, shape, device)
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
+        return _ptr(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1)
+def _only_device() -> bool:
+    """Whether the process sees one GPU, which is then always the current one."""
+    return torch.cuda.device_count() == 1
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -355,7 +365,7 @@ def _call(name: str, device: torch.device, stream, *args) -> None:
         packed = pack(*args, handle)
     except (struct.error, OverflowError, TypeError) as e:
         raise ValueError(f"{name}: {e}") from None  # a number that the C type does not hold
-    if torch.cuda.current_device() == device.index:
+    if _only_device() or torch.cuda.current_device() == device.index:
         st = entry(packed)
     else:
         with torch.cuda.device(device):
