@@ -21,7 +21,11 @@ force, finite differences and the worked example that [datarekha] prints),
 and every function in ``fp8`` (the FP8 forward's rotation, E4M3 rounding and
 block quantisation) by ``tests/test_oracle_fp8.py`` (torch's float8 cast, the
 format's codes, closed forms, orthogonality, error bounds and the direction
-of the pages' error claim).  No function is "parity unpinned".
+of the pages' error claim).  ``cross`` (keys of another length, drafted trees
+over a cache, head norm and rotation) has no passage on the pages: it is
+written from the formulas in ``include/fa.h`` and pinned by
+``tests/test_oracle_cross.py`` (the square oracle, loops over the definitions,
+finite differences).  No function is "parity unpinned".
 """
 
 from .attention import (  # noqa: F401
