@@ -12,7 +12,8 @@ namespace {
 fa_status check_cross_shape(int B, int H, int Hkv, int Nq, int Nk, int d, int* R) {
   if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || d < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   const long long rows = (long long)(H / Hkv) * Nq;
-  if (rows > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  // (rounded up to whole row tile pairs and blocks they still fit an int)
+  if (rows > 0x7fffff00LL || Nk > 0x7fffff00) return FA_ERR_INVALID_ARG;
   fa_status st = check_shape(B, Hkv, (int)rows, d);
   if (st == FA_OK) st = check_shape(B, Hkv, Nk, d);
   // the forward counts the key blocks of all requests, with what each costs at

@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(512, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
+    grid_wait();
     if (threadIdx.x == 0) atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
     return;
   }

@@ -509,7 +509,7 @@ def _rows(t, name: str, shape, device):
     sb, sn, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     # (the stride of a dimension of one is any number: it is never used)
     return t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0, sh if shape[2] > 1 else 0

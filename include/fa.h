@@ -246,7 +246,8 @@ fa_status fa_bwd_static_scratch(const void* q, const void* k, const void* v, con
  *                 16-byte aligned, contents on entry ignored; calls that may
  *                 overlap on the GPU need one each.
  * Limits: those of fa_fwd with B * Hkv for B * H and, for N, both
- * (H / Hkv) * Nq and Nk; and (ceil(Nk / 128) + 4) * B * Hkv < 2^31.  The results are the same from run to run.
+ * (H / Hkv) * Nq and Nk, each at most 2^31 - 256; and
+ * (ceil(Nk / 128) + 4) * B * Hkv < 2^31.  The results are the same from run to run.
  */
 size_t fa_cross_fwd_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
 fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* key_lens, void* o, float* lse,
@@ -465,7 +466,8 @@ void fa_set_wait_limit_ns(unsigned long long limit_ns);
 
 /*
  * Test hook for the timeout path.  While `enable` is nonzero, every kernel
- * launched by fa_fwd / fa_bwd first makes its MMA-issuing thread wait on a
+ * launched by fa_fwd / fa_bwd (and the main kernels of fa_cross_fwd,
+ * fa_cross_bwd and fa_tree_fwd) first makes its MMA-issuing thread wait on a
  * barrier that nothing ever signals; that wait runs out after the wait limit
  * (fa_set_wait_limit_ns), the kernel reports FA_ERR_TIMEOUT, drains the copies
  * it started and returns without writing its outputs.  Process-wide; 0 (the

@@ -44,6 +44,7 @@ def test_attention_refusals(lib, entry):
     need = getattr(lib, entry + "_workspace_bytes")(1, 4, 2, 8, 100, 128)
     assert need > 0 and cross(lib, entry, ws_bytes=need - 1) == bad
     assert cross(lib, entry, H=1 << 20, Hkv=1, Nq=1 << 11) == bad  # 2^31 rows share a head
+    assert cross(lib, entry, H=1, Hkv=1, Nq=2 ** 31 - 1) == bad and cross(lib, entry, Nk=2 ** 31 - 1) == bad
     assert cross(lib, entry, B=1 << 16, H=1 << 15, Hkv=1 << 15) == bad
     assert getattr(lib, entry + "_workspace_bytes")(1, 4, 3, 8, 100, 128) == 0
     assert getattr(lib, entry + "_workspace_bytes")(1, 4, 2, 8, 100, 80) == 0
