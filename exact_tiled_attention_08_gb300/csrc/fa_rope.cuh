@@ -21,8 +21,9 @@
 // cosines and sines for the heads of its token.  A warp has the rows of the
 // next kRopeStages - 1 heads on their way.  Statistics and rotation are fp32,
 // rounded once.  Measured, with the norm: 16384 tokens of 48 heads of 128 in 69 us
-// (5.8 TB/s), backward at 8004 tokens in 56 us (5.0 TB/s); a copy reaches
-// 6.8 TB/s.  What is left is the number of instructions per row.
+// (5.8 TB/s), backward at 8004 tokens in 55 us (5.1 TB/s); a copy reaches
+// 6.8 TB/s.  (Packed arithmetic, a quarter fewer instructions, left the forward
+// as it was: what is left is how rows of many heads lie in memory.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,6 +38,17 @@ struct RopeRows {
   long long batch, token, head;  // strides in elements
 };
 
+// A token's heads, q, k and v counted on, in units that do not mix q with the
+// others: q_units of q_step heads, then k and v in one unit, or each in units
+// of kv_step.
+struct RopeSplit {
+  int steps;             // units per token group
+  int q_units, q_step;
+  int k_units, v_units;  // (0: left out, or both in one unit)
+  int kv_step;
+  int both;              // 1: one unit of all key and value heads
+};
+
 struct RopeParams {
   RopeRows q, k, v;               // token-major rows: forward inputs; backward: q, k inputs (v unused)
   RopeRows dq, dk, dv;            // backward: token-major gradients, written
@@ -48,8 +60,8 @@ struct RopeParams {
   float* partials;                       // backward: [gridDim.x][2][d] sums of the weight gradients
   int N, H, Hkv, C, rot;
   long long tokens;     // B * N
-  int head_step;        // heads (of H + Hkv + Hkv) that a warp takes for its tokens
-  long long units;      // warps' units of work: token groups * ceil(heads / head_step)
+  RopeSplit split;      // how a token's heads are divided into units of work
+  long long units;      // warps' units of work: token groups (rounded up to whole CTAs) * split.steps
   float eps, factor;
   int norm;
 };
@@ -69,18 +81,67 @@ __device__ __forceinline__ void rope_angle(unsigned long long turns, int pos, fl
   s *= f;
 }
 
-// 8 values of a row: 4 from element e0 and 4 from e1
+// A lane's 8 values of a row as four pairs to be turned, (a, b): those of the
+// halves, elements e0 + i and e1 + i, or neighbours.  Two pairs side by side, so
+// that the arithmetic is packed (two fp32 operations an instruction).
+template <bool kInterleaved>
 struct RopeLane {
-  float x[8];
-  // elements e0.. and e1.. of a row in shared memory
+  float2 a[2], b[2];
+
+  // element i (0 .. 7: e0 .. e0 + 3, e1 .. e1 + 3)
+  __device__ __forceinline__ float& at(int i) {
+    if (kInterleaved) {
+      float2& v = (i & 1) ? b[i >> 2] : a[i >> 2];
+      return (i >> 1) & 1 ? v.y : v.x;
+    }
+    float2& v = i < 4 ? a[(i >> 1) & 1] : b[(i >> 1) & 1];
+    return i & 1 ? v.y : v.x;
+  }
   __device__ __forceinline__ void load(const uint8_t* row, int e0, int e1) {
     const uint2 lo = *reinterpret_cast<const uint2*>(row + 2 * e0), hi = *reinterpret_cast<const uint2*>(row + 2 * e1);
     const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      at(2 * i) = __uint_as_float(w[i] << 16);
+      at(2 * i + 1) = __uint_as_float(w[i] & 0xffff0000u);
     }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* row, int e0, int e1) {
+    *reinterpret_cast<uint2*>(row + e0) = make_uint2(pack_bf16x2(at(0), at(1)), pack_bf16x2(at(2), at(3)));
+    *reinterpret_cast<uint2*>(row + e1) = make_uint2(pack_bf16x2(at(4), at(5)), pack_bf16x2(at(6), at(7)));
+  }
+  // the weights of these elements (ones without a weight)
+  __device__ __forceinline__ void weights(const float* w, int e0, int e1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at(i) = w ? __ldg(w + (i < 4 ? e0 : e1) + (i & 3)) : 1.f;
+  }
+  __device__ __forceinline__ void scale(const RopeLane& w) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a[i] = __fmul2_rn(a[i], w.a[i]), b[i] = __fmul2_rn(b[i], w.b[i]);
+  }
+  __device__ __forceinline__ void scale(float f) {
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a[i] = __fmul2_rn(a[i], f2), b[i] = __fmul2_rn(b[i], f2);
+  }
+  // this lane's part of sum x o y
+  __device__ __forceinline__ float dot(const RopeLane& y) const {
+    float2 s = __fmul2_rn(a[0], y.a[0]);
+    s = __ffma2_rn(a[1], y.a[1], s);
+    s = __ffma2_rn(b[0], y.b[0], s);
+    s = __ffma2_rn(b[1], y.b[1], s);
+    return s.x + s.y;
+  }
+  // this += x o y
+  __device__ __forceinline__ void add_product(const RopeLane& x, const RopeLane& y) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a[i] = __ffma2_rn(x.a[i], y.a[i], a[i]), b[i] = __ffma2_rn(x.b[i], y.b[i], b[i]);
+  }
+  // this += f x
+  __device__ __forceinline__ void add(float f, const RopeLane& x) {
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a[i] = __ffma2_rn(x.a[i], f2, a[i]), b[i] = __ffma2_rn(x.b[i], f2, b[i]);
   }
 };
 
@@ -99,16 +160,10 @@ __device__ __forceinline__ void rope_landed() {
   __syncwarp();
 }
 
-__device__ __forceinline__ void rope_store(__nv_bfloat16* row, int e0, int e1, const RopeLane& v) {
-  *reinterpret_cast<uint2*>(row + e0) = make_uint2(pack_bf16x2(v.x[0], v.x[1]), pack_bf16x2(v.x[2], v.x[3]));
-  *reinterpret_cast<uint2*>(row + e1) = make_uint2(pack_bf16x2(v.x[4], v.x[5]), pack_bf16x2(v.x[6], v.x[7]));
-}
-
-// The rotation of a lane's values for one token: pairs (x[i], x[4 + i]) of the
-// halves, or (x[2 i], x[2 i + 1]) interleaved.
+// The rotation of a lane's values for one token.
 template <bool kInterleaved>
 struct RopeTurn {
-  float c[4], s[4];
+  float2 c[2], s[2];
   bool active;  // the lane's values are in the rotated part
 
   // a lane's elements: e0 .. e0 + 3 and e1 .. e1 + 3
@@ -121,18 +176,20 @@ struct RopeTurn {
     active = 8 * sub < rot;
     if (!active) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rope_angle(turns[4 * sub + i], pos, f, c[i], s[i]);
+    for (int i = 0; i < 2; ++i) {
+      rope_angle(turns[4 * sub + 2 * i], pos, f, c[i].x, s[i].x);
+      rope_angle(turns[4 * sub + 2 * i + 1], pos, f, c[i].y, s[i].y);
+    }
   }
   template <bool kBack>
-  __device__ __forceinline__ void apply(RopeLane& v) const {
+  __device__ __forceinline__ void apply(RopeLane<kInterleaved>& v) const {
     if (!active) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      constexpr int kStep = kInterleaved ? 1 : 4;
-      float &a = v.x[kInterleaved ? 2 * i : i], &b = v.x[(kInterleaved ? 2 * i : i) + kStep];
-      const float sn = kBack ? -s[i] : s[i], a0 = a;
-      a = fmaf(a0, c[i], -b * sn);
-      b = fmaf(a0, sn, b * c[i]);
+    for (int i = 0; i < 2; ++i) {
+      const float2 n = make_float2(-s[i].x, -s[i].y);
+      const float2 a = __ffma2_rn(v.b[i], kBack ? s[i] : n, __fmul2_rn(v.a[i], c[i]));
+      v.b[i] = __ffma2_rn(v.a[i], kBack ? n : s[i], __fmul2_rn(v.b[i], c[i]));
+      v.a[i] = a;
     }
   }
 };
@@ -150,15 +207,6 @@ constexpr int kRopeThreads = 256;
 // 16384 tokens of 48 heads: 3 take 70 us, 4 74 us, 5 94 us).
 constexpr int kRopeFwdPerSm = 3, kRopeBwdPerSm = 2;
 
-// the weights of a lane's values (ones without a weight)
-__device__ __forceinline__ void rope_weights(const float* w, int e0, int e1, float (&out)[8]) {
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-  const float4 a = w ? __ldg(reinterpret_cast<const float4*>(w + e0)) : one;
-  const float4 b = w ? __ldg(reinterpret_cast<const float4*>(w + e1)) : one;
-  out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
-  out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
-}
-
 // A warp's tokens in a unit of work, one per D / 8 lanes.
 struct RopeToken {
   int b, n, sub;
@@ -172,18 +220,30 @@ __device__ __forceinline__ RopeToken rope_token(const RopeParams& p, long long u
   // a CTA's warps take neighbouring tokens and the same heads, neighbouring CTAs
   // the other heads of these tokens
   constexpr int kWarps = kRopeThreads / 32;
-  const int steps = (p.H + 2 * p.Hkv + p.head_step - 1) / p.head_step;
+  const int steps = p.split.steps;
   const int lane = threadIdx.x & 31;
   const long long cta = unit / kWarps;
   RopeToken t;
-  const int step = (int)(cta % steps);
+  int step = (int)(cta % steps);
   t.token = (cta / steps * kWarps + unit % kWarps) * kTokens + lane / kLanes;
   t.sub = lane % kLanes;
   t.valid = t.token < p.tokens;
   t.b = t.valid ? (int)(t.token / p.N) : 0;
   t.n = t.valid ? (int)(t.token - (long long)t.b * p.N) : 0;
-  t.h0 = step * p.head_step;
-  t.h1 = min(t.h0 + p.head_step, p.H + 2 * p.Hkv);
+  if (step < p.split.q_units) {
+    t.h0 = step * p.split.q_step;
+    t.h1 = min(t.h0 + p.split.q_step, p.H);
+  } else if (p.split.both) {
+    t.h0 = p.H;
+    t.h1 = p.H + 2 * p.Hkv;
+  } else {
+    step -= p.split.q_units;
+    const bool v = step >= p.split.k_units;
+    if (v) step -= p.split.k_units;
+    const int first = p.H + (v ? p.Hkv : 0);
+    t.h0 = first + step * p.split.kv_step;
+    t.h1 = min(t.h0 + p.split.kv_step, first + p.Hkv);
+  }
   return t;
 }
 
@@ -203,8 +263,8 @@ __device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& tur
   const uint32_t dst = smem_u32(ring) + lane * 16;
   const __nv_bfloat16* src = in + 8 * (lane % kLanes) + h0 * in_head;
   out += h0 * out_head;
-  float w[8];
-  if (kNorm) rope_weights(weight, e0, e1, w);
+  RopeLane<kInterleaved> w;
+  if (kNorm) w.weights(weight, e0, e1);
   int left = h1 - h0;  // rows to fetch
 #pragma unroll
   for (int i = 0; i < kRopeStages - 1; ++i) {
@@ -221,19 +281,16 @@ __device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& tur
     src += in_head;
     --left;
     rope_landed();
-    RopeLane v;
+    RopeLane<kInterleaved> v;
     v.load(mine + stage * 512, e0, e1);
     stage = (stage + 1) % kRopeStages;
     if (kNorm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v.x[i], v.x[i], ss);
-      const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v.x[i] *= r * w[i];
+      const float r = rsqrtf(rope_row_sum<kLanes>(v.dot(v)) * (1.f / D) + eps);
+      v.scale(w);
+      v.scale(r);
     }
     if (kTurn) turn.template apply<false>(v);
-    if (stored) rope_store(out, e0, e1, v);
+    if (stored) v.store(out, e0, e1);
     out += out_head;
   }
   __syncwarp();  // the ring has been read
@@ -280,7 +337,7 @@ __device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& tur
                                                const __nv_bfloat16* dy, long long dy_head, const __nv_bfloat16* in,
                                                long long in_head, __nv_bfloat16* out, long long out_head, int h0,
                                                int h1, int e0, int e1, bool valid, const float* weight, float eps,
-                                               float (&dw)[8]) {
+                                               RopeLane<kInterleaved>& dw) {
   constexpr int kLanes = D / 8;
   if (h0 >= h1) return;
   const int lane = threadIdx.x & 31;
@@ -300,8 +357,8 @@ __device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& tur
     if (kNorm) xsrc += in_head;
     --left;
   };
-  float w[8];
-  if (kNorm) rope_weights(weight, e0, e1, w);
+  RopeLane<kInterleaved> w;
+  if (kNorm) w.weights(weight, e0, e1);
 #pragma unroll
   for (int i = 0; i < kRopeStages - 1; ++i) fetch(i);
   int stage = 0;
@@ -309,29 +366,22 @@ __device__ __forceinline__ void rope_bwd_heads(const RopeTurn<kInterleaved>& tur
     __syncwarp();  // the stage filled next has been read
     fetch((stage + kRopeStages - 1) % kRopeStages);
     rope_landed();
-    RopeLane g;
+    RopeLane<kInterleaved> g;
     g.load(mine + stage * 512, e0, e1);
     if (kTurn) turn.template apply<true>(g);
     if (kNorm) {
-      RopeLane x;  // (of a token that is not there: zeros, which add nothing)
+      RopeLane<kInterleaved> x;  // (of a token that is not there: zeros, which add nothing)
       x.load(mine + (kRopeStages + stage) * 512, e0, e1);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(x.x[i], x.x[i], ss);
-        dot = fmaf(g.x[i] * w[i], x.x[i], dot);
-      }
-      const float r = rsqrtf(rope_row_sum<kLanes>(ss) * (1.f / D) + eps);
-      dot = rope_row_sum<kLanes>(dot) * (1.f / D) * r;  // mean(w g x^)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x.x[i] = valid ? x.x[i] * r : 0.f;
-        dw[i] = fmaf(g.x[i], x.x[i], dw[i]);
-        g.x[i] = r * fmaf(-x.x[i], dot, g.x[i] * w[i]);
-      }
+      const float r = rsqrtf(rope_row_sum<kLanes>(x.dot(x)) * (1.f / D) + eps);
+      x.scale(valid ? r : 0.f);  // x^
+      dw.add_product(g, x);
+      g.scale(w);
+      const float mean = rope_row_sum<kLanes>(g.dot(x)) * (1.f / D);  // of w g x^
+      g.add(-mean, x);
+      g.scale(r);
     }
     stage = (stage + 1) % kRopeStages;
-    if (valid) rope_store(out, e0, e1, g);
+    if (valid) g.store(out, e0, e1);
     out += out_head;
   }
   __syncwarp();  // the ring has been read
@@ -353,9 +403,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = rope_smem + warp * (kRopeBwdSmemBytes<kNorm> / (kRopeThreads / 32));
-  float dw[2][8];
+  RopeLane<kInterleaved> dw[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[0].at(i) = dw[1].at(i) = 0.f;
   int e0, e1;
   RopeTurn<kInterleaved>::place(p.rot, lane % kLanes, e0, e1);
   for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + warp; unit < p.units;
@@ -388,7 +438,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdPerSm) fa_rope_bwd_kerne
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v = dw[t][i];
+      float v = dw[t].at(i);
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane < kLanes) sums[(warp * 2 + t) * D + (i < 4 ? e0 : e1) + (i & 3)] = v;

@@ -62,18 +62,36 @@ fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
   return FA_OK;
 }
 
-// Warps' units of work: a warp's tokens times `head_step` heads.  All heads of a
-// token share its angles and one start of the ring, so a unit takes as many as
-// leave four units for every warp that the device holds at once (`warps`); a
-// few tokens' heads are spread over the warps one by one.  (Measured, 8, 16, 24
-// and 48 heads: forward at 16384 tokens 82, 78, 70 and 74 us; backward at 8004
-// tokens 64, 59, 62 and 62 us.)
-void rope_units(fa::RopeParams& p, int d, long long warps) {
-  const long long per_warp = 32 / (d / 8), groups = (p.tokens + per_warp - 1) / per_warp;
-  const int heads = p.H + 2 * p.Hkv;
-  const long long steps = std::max<long long>(1, std::min<long long>(heads, (4 * warps + groups - 1) / groups));
-  p.head_step = (int)((heads + steps - 1) / steps);
-  p.units = (groups + 7) / 8 * 8 * ((heads + p.head_step - 1) / p.head_step);
+// Warps' units of work: a warp's tokens times some heads.  The heads of a unit
+// share the token's angles and one start of the ring, about four rows' time; the
+// device holds `warps` warps at once, and the split that ends soonest is taken.
+// (Measured, heads per unit: forward at 16384 tokens of 32 + 8 + 8 heads 8: 82 us,
+// 16: 66 us, 24, with q and k in one unit: 71 us; backward at 8004 tokens 12, with q and k
+// in one unit: 62 us, 16: 51 us.)
+void rope_units(fa::RopeParams& p, int d, long long warps, bool q, bool k, bool v) {
+  const long long per_warp = 32 / (d / 8), groups = ((p.tokens + per_warp - 1) / per_warp + 7) / 8 * 8;
+  const int most = std::max(q ? p.H : 0, p.Hkv * ((k ? 1 : 0) + (v ? 1 : 0)));
+  double best = 0;
+  for (int step = 1; step <= most; ++step) {
+    fa::RopeSplit s{};
+    s.q_units = q ? (p.H + step - 1) / step : 0;
+    s.q_step = q ? (p.H + s.q_units - 1) / s.q_units : 0;
+    s.both = k && v && 2 * p.Hkv <= step;
+    const int n = (p.Hkv + step - 1) / step;
+    s.kv_step = (p.Hkv + n - 1) / n;
+    s.k_units = k && !s.both ? n : 0;
+    s.v_units = v && !s.both ? n : 0;
+    s.steps = s.q_units + s.k_units + s.v_units + s.both;
+    const long long units = groups * s.steps;
+    const double turns = (double)((units + warps - 1) / warps);
+    const double cost = turns * (std::max(s.q_step, s.both ? 2 * p.Hkv : s.kv_step) + 4);
+    if (step == 1 || cost < best) {
+      best = cost;
+      p.split = s;
+      p.units = units;
+    }
+    if (step >= 256) break;  // (more heads in a unit share nothing more worth having)
+  }
 }
 
 template <int D, bool kNorm>
@@ -140,7 +158,7 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  rope_units(p, d, kRopeFwdCtas * 8LL);
+  rope_units(p, d, kRopeFwdCtas * 8LL, q_out, k_out, v_out);
   const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeFwdCtas);
   if (d == 128)
     norm ? launch_rope_fwd<128, true>(p, grid, interleaved, stream) : launch_rope_fwd<128, false>(p, grid, interleaved, stream);
@@ -208,7 +226,7 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  rope_units(p, d, kRopeBwdCtas * 8LL);
+  rope_units(p, d, kRopeBwdCtas * 8LL, dq_out, dk_out, dv_out);
   const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeBwdCtas);
   if (d == 128)
     norm ? launch_rope_bwd<128, true>(p, grid, interleaved, stream) : launch_rope_bwd<128, false>(p, grid, interleaved, stream);

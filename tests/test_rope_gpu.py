@@ -54,6 +54,8 @@ CASES = [
     (1, 9, 2, 1, 64, 48, 1e-6, False, 3),
     (2, 17, 8, 2, 128, 0, 1e-6, False, 0),
     (1, 2000, 8, 2, 128, 32, None, False, 77),
+    (1, 9001, 11, 3, 64, 64, 1e-6, True, 10),   # units of several heads
+    (2, 6000, 3, 20, 128, 128, 1e-6, False, 0),
 ]
 
 
