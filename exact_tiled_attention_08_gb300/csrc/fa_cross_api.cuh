@@ -32,21 +32,30 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {
 // Launch with programmatic stream serialization: the kernel may start while the
 // one in front of it ends (it calls grid_wait before it touches memory).
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                         const Args&... args) {
+cudaError_t launch_early_clusters(void (*kernel)(Params...), dim3 grid, int cluster, int threads, int smem,
+                                  cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const Args&... args) {
+  return launch_early_clusters(kernel, grid, 1, threads, smem, stream, args...);
 }
 
 // Whether `kernel` launches with `regs` registers per thread, asked once per
@@ -101,11 +110,39 @@ struct CrossFwdPlan {
   }
 };
 
+// CTAs per item in a cluster (1: no clusters).  For few enough items that the
+// clusters of 8, 4 or 2 fit the device's SMs at once (two clusters of 8 and four
+// of 4 per GPC of 18 or more SMs), with few blocks each, or all alike (one request,
+// or no lengths) and enough CTAs to draw on most of the memory's bandwidth.
+// (Measured, without and with: B=4 H=16 Nq=1 Nk=1500 d=64 15.8 and 11.7 us; one token
+// of H=32/8 d=128 over 1.9k tokens 12.3 and 9.7 us; B=8 H=32/8 Nq=1 Nk=4096 d=128 44
+// and 40 us.)
+int cross_cluster(long long items, int blocks, bool alike) {
+  const int ctas = items <= 16 ? 8 : items <= 32 ? 4 : items <= 72 ? 2 : 1;
+  return blocks > 1 && (blocks <= 4 * ctas || (alike && items * ctas >= 64)) ? ctas : 1;
+}
+
+template <int D, bool TREE>
+fa_status launch_cross_clusters(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                const fa::CrossFwdParams& p, int items, cudaStream_t stream) {
+  using C = fa::CrossCfg<D>;
+  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, false, true>;
+  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  static std::atomic<unsigned long long> known{0};
+  if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
+  return launch_early_clusters(kernel, dim3((unsigned)(items * p.cluster)), p.cluster, C::kThreads, C::kSmemBytes, stream,
+                               mq, mk, mv, p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
 template <int D, bool TREE, bool PAIR>
 fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                            const fa::CrossFwdParams& p, const CrossFwdPlan& plan, cudaStream_t stream) {
   using C = fa::CrossCfg<D>;
-  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, PAIR>;
+  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, PAIR, false>;
   if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -156,6 +193,17 @@ fa_status run_cross_fwd(const fa::CrossView& view, const void* q, const void* k,
   p.debug_stall = g_debug_stall.load();
   p.o_align32 = aligned32(o);
   const bool tree = view.T > 0;
+  if (!plan.pair) {
+    const long long items = (long long)B * view.Hkv;
+    p.cluster = cross_cluster(items, (view.Nk + 127) / 128, B == 1 || !view.lens);
+    if (p.cluster > 1) {
+      if (d == 128)
+        return tree ? launch_cross_clusters<128, true>(mq, mk, mv, p, (int)items, stream)
+                    : launch_cross_clusters<128, false>(mq, mk, mv, p, (int)items, stream);
+      return tree ? launch_cross_clusters<64, true>(mq, mk, mv, p, (int)items, stream)
+                  : launch_cross_clusters<64, false>(mq, mk, mv, p, (int)items, stream);
+    }
+  }
   if (d == 128) {
     if (tree)
       return plan.pair ? launch_cross_fwd<128, true, true>(mq, mk, mv, p, plan, stream)

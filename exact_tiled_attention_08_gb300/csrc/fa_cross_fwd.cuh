@@ -20,6 +20,10 @@
 // its key blocks in turn, each with its own maximum, sum and accumulator; at
 // the end warpgroup 0 joins the two, reading O_1 from the same TMEM lanes.
 //
+// A few items (CLUSTER, with ALT): 2, 4 or 8 CTAs of a cluster share an item's
+// key blocks and join their parts through one another's shared memory, without
+// parts in global memory and without the second kernel.
+//
 // Keys behind a request's length.  Their scores become -inf; their rows of V
 // (which may hold anything, and 0 times NaN is NaN) are zeroed in shared
 // memory by warp 11 before the last block's P V.
@@ -53,6 +57,7 @@ struct CrossFwdParams {
   int part_rows;         // rows of a part: 256 (PAIR) or R (ALT)
   int B;
   int row_tiles;         // row tiles (PAIR: pairs of them) per key/value head
+  int cluster;           // CLUSTER: CTAs per item
   float scale_log2;
   uint64_t wait_limit_ns;
   int debug_stall;
@@ -331,6 +336,7 @@ struct CrossCfg {
   // (declared 1024-byte aligned, which is checked at run time)
   static constexpr int kSmemBytes = 2 * kTileBytes + kSlots * kTileBytes + kMergeBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(128 * (D + 4) * 4 <= kSlots * kTileBytes, "a cluster's parts take the ring's place");
 };
 
 struct CrossBarriers {
@@ -346,6 +352,7 @@ struct CrossBarriers {
   uint64_t never;
   CrossPlace place, second;
   long long total, end;  // places of the sequence; end of the CTA's share
+  int fresh;             // CLUSTER: drafted tokens of the item's request
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -385,19 +392,48 @@ __device__ __forceinline__ uint32_t cross_bits(unsigned long long mask, int rel)
   return rel < 64 ? (uint32_t)(mask >> rel) : 0u;
 }
 
+// The share of a cluster's item, by one lane.
+__device__ __forceinline__ void cross_cluster_share(const CrossView& v, int items, int ctas, CrossPlace* place,
+                                                    int* fresh) {
+  const int item = blockIdx.x / ctas, rank = blockIdx.x - item * ctas;
+  const int b = item / items, len = v.len(b), drafted = v.drafted(b, len);
+  const int n = cross_blocks(len + drafted), j0 = rank * n / ctas, j1 = (rank + 1) * n / ctas;
+  *place = {b, item - b * items, j0 + kCrossStart, 1, -1, 0, j1 - j0};
+  *fresh = drafted;
+}
+
+// fp32 values of shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ float cluster_load(const float* local, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(local), rank)));
+  return v;
+}
+template <int E>
+__device__ __forceinline__ void cluster_load(const float* local, uint32_t rank, float (&x)[E]) {
+  const uint32_t at = mapa_shared(smem_u32(local), rank);
+  if constexpr (E == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                 : "r"(at));
+  else
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(at));
+}
+
 // TREE: drafted tokens behind the request's own.  PAIR: two row tiles per item.
-template <int D, bool TREE, bool PAIR>
+// CLUSTER: a cluster of p.cluster CTAs per item (not with PAIR).
+template <int D, bool TREE, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(384, 1)
     fa_cross_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const CrossFwdParams p) {
   using C = CrossCfg<D>;
+  static_assert(!(PAIR && CLUSTER), "clusters take one row tile");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
     grid_wait();
     if (threadIdx.x == 0) {
       atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
-      p.meta[blockIdx.x].split = 0;
+      if (!CLUSTER) p.meta[blockIdx.x].split = 0;
     }
     return;
   }
@@ -443,7 +479,10 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_map(&map_v);
   }
   grid_wait();
-  if (warp == 10)
+  if (CLUSTER) {
+    if (tid < 128) sMerge[tid] = -CUDART_INF_F;  // no part so far
+    if (warp == 10 && lane == 0) cross_cluster_share(v, items, p.cluster, &bar->place, &bar->fresh);
+  } else if (warp == 10)
     cross_schedule<PAIR>(v, p.B, items, blockIdx.x, gridDim.x, &bar->place, &bar->second,
                          &bar->total, &bar->end);
   tc_fence_before();
@@ -638,7 +677,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (!ok) meta.split = 0;
-      if (lane == 0) p.meta[blockIdx.x] = meta;
+      if (!CLUSTER && lane == 0) p.meta[blockIdx.x] = meta;
     }
   } else {
     setmaxnreg_inc<C::kSoftRegs>();
@@ -674,6 +713,10 @@ __global__ void __launch_bounds__(384, 1)
       w.len = mine->w.len, w.keys = mine->w.keys, w.single = mine->w.single;
     };
     store();
+    // CLUSTER: this CTA's part of the item, in the ring's memory once the ring has
+    // been read: rows of D + 4 floats (so that a warp's rows spread over the banks);
+    // its log-sum-exps at sMerge
+    float* sPart = reinterpret_cast<float*>(sKV);
     while (alive) {
       load_place();
       if (!cross_next(v, items, &bar->second, at, w)) break;
@@ -897,7 +940,13 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive(&bar->merge_free);
         }
-        if (write && whole) {
+        if (CLUSTER) {
+          if (write)
+#pragma unroll
+            for (int v4 = 0; v4 < 8; ++v4)
+              reinterpret_cast<uint4*>(sPart + r * (D + 4) + 32 * c)[v4] =
+                  make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+        } else if (write && whole) {
           __nv_bfloat16* orow = p.o + grow * D + 32 * c;
           uint32_t w16[16];
 #pragma unroll
@@ -918,7 +967,9 @@ __global__ void __launch_bounds__(384, 1)
         }
         __syncwarp();  // the next tensor memory load is a whole warp's
       }
-      if (write) {
+      if (CLUSTER) {
+        sMerge[r] = write ? lse2 : -CUDART_INF_F;
+      } else if (write) {
         if (whole)
           p.lse[grow] = lse2 * 0.6931471805599453f;
         else
@@ -933,6 +984,45 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if constexpr (CLUSTER) {
+    // every CTA of the cluster writes every p.cluster-th row, a warp per row
+    cluster_sync();
+    constexpr int E = D / 32, kMost = 8;
+    const int ctas = p.cluster, item = blockIdx.x / ctas, fresh = bar->fresh;
+    const float* parts = reinterpret_cast<const float*>(sKV) + lane * E;
+    for (int row = (int)cluster_ctarank() + ctas * warp; row < v.R; row += ctas * (C::kThreads / 32)) {
+      if (TREE && row % v.Nq >= fresh) continue;
+      float l[kMost], o[kMost][E], mx = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas) {
+          l[i] = cluster_load(sMerge + row, i);
+          cluster_load<E>(parts + row * (D + 4), i, o[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas) mx = fmaxf(mx, l[i]);
+      const float ref = fmaxf(mx, -3.402823466e38f);
+      float sum = 0.f, acc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas && l[i] != -CUDART_INF_F) {  // (a part without keys was not written)
+          const float wt = ex2_approx(l[i] - ref);
+          sum += wt;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
+        }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t grow = (size_t)item * v.R + row;  // (one row tile per key/value head)
+      uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+    }
+    cluster_sync();  // the others have read this CTA's part
   }
 }
 

@@ -96,6 +96,14 @@ CROSS = [
     (2, 40, 40, 130, 384, [384, 130]),  # more items than SMs
     (4, 40, 40, 2, 1500, [1500, 700, 1499, 64]),  # many key blocks a CTA
     (2, 40, 20, 130, 1111, None),
+    # few items with equal lengths: CTAs of a cluster share an item
+    (1, 8, 8, 1, 1500, None),
+    (4, 16, 16, 2, 129, None),
+    (1, 40, 20, 60, 2000, None),
+    (2, 16, 8, 16, 700, None),
+    (1, 3, 1, 40, 900, [899]),
+    (1, 72, 72, 128, 1300, None),
+    (1, 2, 2, 5, 300, [0]),
 ]
 
 
@@ -258,6 +266,10 @@ TREE = [
     (1, 2, 1, 3, 30000, [29000], None, True),
     (2, 2, 2, 8, 64, [60, 64], None, False),     # drafts that do not fit are not there
     (40, 16, 8, 2, 300, list(range(0, 280, 7)), None, True),
+    (1, 32, 8, 1, 2048, [1907], None, False),
+    (1, 16, 16, 7, 900, [850], [5], True),
+    (1, 8, 4, 64, 300, [200], [64], True),
+    (1, 4, 2, 3, 1000, [0], [0], False),
     (20, 16, 8, 3, 4000, [3990 - 7 * i for i in range(20)], None, True),  # many key blocks a CTA
 ]
 
