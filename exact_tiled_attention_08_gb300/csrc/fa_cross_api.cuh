@@ -293,7 +293,7 @@ fa_status run_cross_bwd(const fa::CrossView& view, const void* q, const void* k,
   p.out_align32 = aligned32(dk) && aligned32(dv) && aligned32(dq);
   p.dq = direct ? static_cast<__nv_bfloat16*>(dq) : nullptr;
   // one CTA per SM, and no more than there are query blocks to hand out
-  const long long blocks = (long long)BK * ((view.Nk + 127LL) / 128) * std::min(nqb, fa::kCrossBwdMaxParts);
+  const long long blocks = (long long)BK * ((view.Nk + 127LL) / 128) * nqb;
   const int grid = (int)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
   if (launch_early(kernel, dim3((unsigned)grid), C::kThreads, fa::kCrossBwdSmemBytes<D>, stream, mq, mk, mv, mdo, ml,
                    mdel, mdq, p) != cudaSuccess)
