@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include "fa_fwd.cuh"  // (fa_bwd.cuh uses its limits)
 #include "fa_bwd.cuh"
 #include "fa_cross.cuh"
 
@@ -100,6 +101,13 @@ __device__ __forceinline__ void cross_bwd_item(const CrossView& v, bool direct, 
   s.valid = min(128, len - s.jb * 128);
 }
 
+// The first query block of run `part`: floor(part nqb / parts), in 32 bits (a long
+// item's 2^24 blocks times its hundreds of runs do not fit them).
+__host__ __device__ __forceinline__ int cross_bwd_cut(int part, int parts, int nqb) {
+  const int each = nqb / parts;
+  return part * each + part * (nqb - parts * each) / parts;
+}
+
 __device__ __forceinline__ bool cross_bwd_next(const CrossBwdParams& p, const CrossBwdPlan& plan, CrossBwdWalk& at,
                                                CrossBwdSeg& s) {
   const int k = at.k++, G = gridDim.x, c = blockIdx.x;
@@ -114,8 +122,8 @@ __device__ __forceinline__ bool cross_bwd_next(const CrossBwdParams& p, const Cr
     if (u >= plan.rest * plan.parts) return false;
     const int part = u / plan.rest;
     item = plan.rounds * G + (u - part * plan.rest);
-    s.i0 = part * p.nqb / plan.parts;  // (at most 16 * 2^24)
-    s.i1 = (part + 1) * p.nqb / plan.parts;
+    s.i0 = cross_bwd_cut(part, plan.parts, p.nqb);
+    s.i1 = cross_bwd_cut(part + 1, plan.parts, p.nqb);
     s.run = plan.parts > 1 ? u : -1;
   }
   cross_bwd_item(p.view, p.dq != nullptr, item, at, s);

@@ -357,7 +357,8 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
  *   dq_out, dk_out, dv_out  in: bf16 [B][H][N][d], [B][Hkv][N][d]: the gradients
  *                of its outputs, as the attention backward passes write them
  *   dq, dk, dv   out: bf16 rows like q, k, v; a null one leaves that tensor out
- *                (its gradient then null too).  The rows may not overlap.
+ *                (its gradient then null too).  The rows may overlap neither one
+                another nor an input.
  *   dq_weight, dk_weight  out: fp32 [d], summed over all rows; may be null
  *   workspace    device scratch of ws_bytes >= fa_rope_bwd_workspace_bytes(),
  *                16-byte aligned; may be null when no weight gradient is asked for

@@ -2,13 +2,15 @@
 arguments are turned down before anything is enqueued."""
 
 import ctypes
+import os
 import struct
+import subprocess
 
 import pytest
 import torch
 
 from exact_tiled_attention_08_gb300 import fa
-from exact_tiled_attention_08_gb300.build import build_library
+from exact_tiled_attention_08_gb300.build import ARCH_FLAGS, _nvcc, build_library
 
 P = 0x7F0000000000  # aligned, never dereferenced
 VP = ctypes.c_void_p
@@ -159,3 +161,29 @@ def test_binding_refusals(lib):
         fa.rope_frequencies(15)
     with pytest.raises(ValueError):
         fa.rope_frequencies(64, scaling="what")
+
+
+def test_runs_of_long_items(tmp_path):
+    """The backward's runs cover an item's query blocks without gaps, at the longest item too."""
+    package = os.path.dirname(os.path.abspath(fa.__file__))
+    source = tmp_path / "runs.cu"
+    source.write_text("""
+#include "fa_cross_bwd.cuh"
+#include <cstdio>
+int main() {
+  const int blocks[] = {1, 2, 77, 607, 608, 609, 1 << 20, (1 << 24) - 2, 1 << 24};
+  for (int nqb : blocks)
+    for (int items = 1; items < 304; ++items) {
+      const fa::CrossBwdPlan plan = fa::cross_bwd_split(items, nqb, 152);
+      if (plan.parts < 1 || plan.parts > nqb || plan.rest * plan.parts > fa::kCrossBwdSlots) return 1;
+      if (plan.rounds * 152 + plan.rest != items) return 2;
+      for (int part = 0; part <= plan.parts; ++part)
+        if (fa::cross_bwd_cut(part, plan.parts, nqb) != (long long)part * nqb / plan.parts) return 3;
+    }
+  return 0;
+}
+""")
+    program = tmp_path / "runs"
+    subprocess.run([_nvcc(), *ARCH_FLAGS, "-std=c++17", "-I", os.path.join(package, "csrc"), "-o", str(program),
+                    str(source)], check=True, capture_output=True)
+    assert subprocess.run([str(program)]).returncode == 0
