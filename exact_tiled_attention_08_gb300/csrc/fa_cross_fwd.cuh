@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(384, 1)
           const bool two = cross_two<PAIR>(w, cross_row0<PAIR>(w, p.row_tiles), v.R);
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int ks = C::template slot<PAIR>(0, g);
-            if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK))) break;
             const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
+            bool landed = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (PAIR ? (t == 0 || two) : (((j - w.j0) & 1) == t)) {
@@ -576,6 +576,12 @@ __global__ void __launch_bounds__(384, 1)
                   ok = false;
                   break;
                 }
+                // K_g's tile only now: with PAIR's ring of five its slot held V_(g-3), for
+                // which this thread never waits.  S(g-1) loaded says that product g-3 is
+                // done; asked before that, the parity of the phase before V's would pass.
+                if (!landed && !(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK)))
+                  break;
+                landed = true;
                 tc_fence_after();
                 const uint64_t qd = sdesc_sw128(sq + (PAIR ? t : qs) * C::kTileBytes, 16, 1024);
 #pragma unroll
