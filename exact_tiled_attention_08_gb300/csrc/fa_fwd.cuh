@@ -370,13 +370,20 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
       // K_j is ring fill 2g (g counts key blocks over all items); S(k) waits
-      // until the tile that used S before has loaded it
+      // until the tile that used S before has loaded it.
+      // K_g's wait.  With an odd number of slots its slot held V_(g-3), for which
+      // this thread never waits: while that is on its way, the parity of the
+      // phase before it would pass for K_g's.  S(g-1) loaded says that product
+      // g-3 is done, so K_g is asked for behind s_free; where block g-1 had two
+      // tiles, S_1(g-1) was issued behind the loads that say so, and K_g is asked
+      // for first (behind s_free in every block the forward loses 2 % at causal N = 32768).
       if (lane == 0) {
         const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
         const uint64_t qdesc0 = sdesc_sw128(sq, 16, 1024);
         const uint64_t qdesc1 = sdesc_sw128(sq + C::kTileBytes, 16, 1024);
         constexpr uint32_t id_s = FP8 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;  // S products issued into each score buffer
+        bool two_before = false;                // the last block had both tiles
         bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
         FwdItem w;
         for (int k = 0; ok && fwd_item<CAUSAL>(p, k, w); ++k) {
@@ -387,11 +394,13 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = 0; ok && j < nb_max; ++j, ++g) {
             const int f = 2 * g;
             const int ks = f % C::kSlots;
-            if (!wait_bounded_inl(&bar->kv_full[ks], (f / C::kSlots) & 1, ctx, kSiteFwdK)) {
+            const uint64_t kdesc = sdesc_sw128(skv + C::slot_offset(ks), 16, 1024);
+            bool landed = two_before;
+            if (two_before && !wait_bounded_inl(&bar->kv_full[ks], (f / C::kSlots) & 1, ctx, kSiteFwdK)) {
               ok = false;
               break;
             }
-            const uint64_t kdesc = sdesc_sw128(skv + C::slot_offset(ks), 16, 1024);
+            two_before = j < w.nb0 && j < w.nb1;
   #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (j < (t ? w.nb1 : w.nb0)) {
@@ -400,6 +409,11 @@ __global__ void __launch_bounds__(384, 1)
                   ok = false;
                   break;
                 }
+                if (!landed && !wait_bounded_inl(&bar->kv_full[ks], (f / C::kSlots) & 1, ctx, kSiteFwdK)) {
+                  ok = false;
+                  break;
+                }
+                landed = true;
                 tc_fence_after();
                 const uint64_t qd = t ? qdesc1 : qdesc0;
   #pragma unroll

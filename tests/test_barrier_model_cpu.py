@@ -48,9 +48,10 @@ def wait(barrier, use):
     assert barrier.phase == use + 1, ("a wait passed early", barrier.phase, use)
 
 
-def run(items, slots, free_first, dual, seed):
+def run(items, slots, waits, dual, seed):
     """`items`: key blocks of tile 0 and of tile 1 of each item (a pair of row
-    tiles, or one).  One ring of K and V tiles in turn; `dual`: a score buffer per tile."""
+    tiles, or one).  One ring of K and V tiles in turn; `waits`: what the S issuer
+    waits for, in its order; `dual`: a score buffer per tile."""
     rng = random.Random(seed)
     full, empty = [[Barrier() for _ in range(slots)] for _ in range(2)]
     s_full, s_free, p_full, pv_done = [[Barrier(), Barrier()] for _ in range(4)]
@@ -106,21 +107,25 @@ def run(items, slots, free_first, dual, seed):
         queue.append(done)
 
     def s_issuer():
-        q, uses = 0, [0, 0]
+        q, uses, two_before = 0, [0, 0], False
         for g, j, tiles, last in blocks():
             f = 2 * g
+            landed = False
             if j == 0:
                 yield from wait(q_full, q)
                 q += 1
-            for i, t in enumerate(tiles):
+            for t in tiles:
                 b = t if dual else 0
-                free = wait(s_free[b], uses[b] - 1) if uses[b] else ()
-                here = wait(full[f % slots], f // slots) if i == 0 else ()
-                for one in (free, here) if free_first else (here, free):
-                    yield from one
+                for what in waits:
+                    if what == "free" and uses[b]:
+                        yield from wait(s_free[b], uses[b] - 1)
+                    elif (what == "here" or what == "here after two" and two_before) and not landed:
+                        yield from wait(full[f % slots], f // slots)
+                        landed = True
                 product(products[0], f, s_full[t])
                 uses[b] += 1
                 yield
+            two_before = len(tiles) == 2
             release(products[0], f)
             if last:
                 products[0].append(q_empty.arrive)
@@ -161,7 +166,7 @@ def run(items, slots, free_first, dual, seed):
     steps = 0
     while roles or copies or products[0] or products[1]:
         steps += 1
-        assert steps < 200000, "no role can go on"
+        assert steps < 20000, "no role can go on"
         names = [*roles, *(["copies"] if copies else []), *(i for i in (0, 1) if products[i])]
         name = rng.choices(names, [speed[n] for n in names])[0]
         if name == "copies":
@@ -176,11 +181,16 @@ def run(items, slots, free_first, dual, seed):
 
 
 def ring(source, d):
-    """Slots of the K/V ring at head dimension d, and whether the S issuer waits for the score buffer first."""
+    """Slots of the K/V ring at head dimension d, and the S issuer's waits in their
+    order: for the score buffer ("free") and for K's tile ("here"; "here after
+    two" where the block before had two row tiles)."""
     text = open(os.path.join(build.CSRC_DIR, source)).read()
     slots = re.search(r"kSlots = .*?\(?D == 128\)? \? (\d+) : (\d+)", text)
     issuer = text[text.index("- S issuer"):text.index("- P V issuer")]
-    return int(slots.group(1 if d == 128 else 2)), issuer.index("&bar->s_free[") < issuer.index("&bar->kv_full[")
+    waits = []
+    for line in re.findall(r".*wait_bounded_inl\(&bar->(?:s_free|kv_full)\[.*", issuer):
+        waits.append("free" if "s_free" in line else "here after two" if "two_before" in line else "here")
+    return int(slots.group(1 if d == 128 else 2)), waits
 
 
 # items of two row tiles, of one, of both kinds (a last round, a head's last rows), causal ones
@@ -194,9 +204,9 @@ ITEMS = {
 
 @pytest.mark.parametrize("items", ITEMS)
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("source", ["fa_cross_fwd.cuh"])
+@pytest.mark.parametrize("source", ["fa_fwd.cuh", "fa_cross_fwd.cuh"])
 def test_no_wait_passes_early(source, d, items):
-    slots, free_first = ring(source, d)
-    for seed in range(400):
+    slots, waits = ring(source, d)
+    for seed in range(300):
         r = random.Random(seed)
-        run(ITEMS[items](r.choice([1, 2, 4, 9, 30]), r), slots, free_first, d == 64, seed)
+        run(ITEMS[items](r.choice([1, 2, 4, 9, 30]), r), slots, waits, d == 64, seed)
