@@ -553,11 +553,18 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
-      // g counts key blocks over all segments
+      // g counts key blocks over all segments.
+      // K_g's wait.  In PAIR's ring of five its slot held V_(g-3), for which this
+      // thread never waits: while that is on its way, the parity of the phase
+      // before it would pass for K_g's.  S(g-1) loaded says that product g-3 is
+      // done, so K_g is asked for behind s_free; where block g-1 had two tiles,
+      // S_1(g-1) was issued behind the loads that say so, and K_g is asked for first
+      // (as in fa_fwd_kernel, which loses 2 % without that).
       if (lane == 0) {
         const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;
+        bool two_before = false;  // the last block had two row tiles
         bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
         while (ok && cross_next(v, items, &bar->second, at, w)) {
           const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
@@ -567,7 +574,10 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int ks = C::template slot<PAIR>(0, g);
             const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
-            bool landed = false;
+            bool landed = two_before;
+            if (two_before && !(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK)))
+              break;
+            two_before = two;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (PAIR ? (t == 0 || two) : (((j - w.j0) & 1) == t)) {
@@ -576,9 +586,6 @@ __global__ void __launch_bounds__(384, 1)
                   ok = false;
                   break;
                 }
-                // K_g's tile only now: with PAIR's ring of five its slot held V_(g-3), for
-                // which this thread never waits.  S(g-1) loaded says that product g-3 is
-                // done; asked before that, the parity of the phase before V's would pass.
                 if (!landed && !(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK)))
                   break;
                 landed = true;
