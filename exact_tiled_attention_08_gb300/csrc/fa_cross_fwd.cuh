@@ -1121,8 +1121,10 @@ __global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdPar
       float mx = ref;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, l[u]);
-      if (mx == -CUDART_INF_F) mx = 0.f;  // no key so far
-      const float alpha = ex2_approx(ref - mx);
+      // finite where no part so far has a key; `ref` stays -inf there, so that parts
+      // of any low log-sum-exp count
+      const float safe = fmaxf(mx, -3.402823466e38f);
+      const float alpha = ex2_approx(ref - safe);
       ref = mx;
       sum *= alpha;
 #pragma unroll
@@ -1130,7 +1132,7 @@ __global__ void __launch_bounds__(256) fa_cross_combine_kernel(const CrossFwdPar
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (i0 + u < parts) {
-          const float wt = ex2_approx(l[u] - ref);
+          const float wt = ex2_approx(l[u] - safe);
           sum += wt;
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[u][e], acc[e]);

@@ -399,3 +399,22 @@ def test_rounds_of_equal_items(case, d):
     ref = torch.matmul(torch.softmax(s, -1), v.float().repeat_interleave(G, 1))
     assert (o.float() - ref).abs().max() <= 4 * H2 * v.float().abs().max()
     assert (lse - torch.logsumexp(s, -1)).abs().max() <= 1e-3  # (both sides fp32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 200])
+def test_parts_without_keys_before_low_scores(Nq, d):
+    """One head's keys in some forty parts; those of the first nine score -inf, the
+    others about e^-110 (2^-159, far below the least exponential in fp32)."""
+    Nk, dead = 5000, 1150
+    # scores (whole numbers) / 8, exact in fp32: what is left is c log2(e)'s rounding, 2^-24 of 112
+    q = torch.ones((1, 1, Nq, d), dtype=torch.bfloat16)
+    g = torch.Generator().manual_seed(d)
+    k = torch.full((1, 1, Nk, d), -896.0 / d)
+    k += torch.arange(d) < torch.randint(0, 17, (1, 1, Nk, 1), generator=g)
+    k[:, :, :dead] = -math.inf
+    q, k, v = q.cuda(), k.bfloat16().cuda(), randn(1, 1, 1, Nk, d).cuda()
+    o, lse = fa.cross_attention_forward(q, k, v, 0.125)
+    seen = np.ones((Nq, Nk - dead), bool)
+    ref = masked_attention_ref(host(q[0, 0]), host(k[0, 0, dead:]), host(v[0, 0, dead:]), 0.125, seen)
+    check_rows(host(o[0, 0]), host(lse[0, 0]), ref, Nq)
