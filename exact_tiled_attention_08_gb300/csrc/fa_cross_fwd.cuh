@@ -313,21 +313,12 @@ struct CrossCfg {
   static constexpr bool kDualS = D == 64;
   static constexpr int kSlots = D == 128 ? 5 : 12;
   // Ring slot and use of key block g's K (kv = 0) or V tile (g counts over the
-  // CTA's segments).  PAIR: one ring, K_g and V_g in turn.  ALT: K and V have
-  // slots of their own (3 and 2 at d = 128): there the S issuer may be several
-  // blocks ahead of the P V issuer, and a wait on the phase of a slot that K
-  // and V share could take the phase before last for its own.
-  static constexpr int kAltK = (kSlots + 1) / 2, kAltV = kSlots / 2;
-  template <bool PAIR>
-  static __device__ __forceinline__ int slot(int kv, int g) {
-    if (PAIR) return (2 * g + kv) % kSlots;
-    return kv ? kAltK + g % kAltV : g % kAltK;
-  }
-  template <bool PAIR>
-  static __device__ __forceinline__ int use(int kv, int g) {
-    if (PAIR) return (2 * g + kv) / kSlots;
-    return g / (kv ? kAltV : kAltK);
-  }
+  // CTA's segments).  K and V have slots of their own (3 and 2 at d = 128), so that
+  // each issuer waits for every tile that its slots take: a wait by parity cannot
+  // take the phase before last for its own.
+  static constexpr int kKSlots = (kSlots + 1) / 2, kVSlots = kSlots / 2;
+  static __device__ __forceinline__ int slot(int kv, int g) { return kv ? kKSlots + g % kVSlots : g % kKSlots; }
+  static __device__ __forceinline__ int use(int kv, int g) { return g / (kv ? kVSlots : kKSlots); }
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kSCol = 0, kPCol0 = 128, kPCol1 = 192, kOCol0 = 256, kOCol1 = 256 + D;
   static constexpr uint32_t kSCol1 = kDualS ? kOCol1 + D : kSCol;
@@ -502,9 +493,9 @@ __global__ void __launch_bounds__(384, 1)
         int loads = 0, nq = 0;  // K and V tiles, in turn
         bool ok = true;
         auto load_kv = [&](int j, int kv, int bk) -> bool {
-          const int g = loads >> 1, s = C::template slot<PAIR>(kv, g);
+          const int g = loads >> 1, s = C::slot(kv, g);
           const CUtensorMap* map = kv ? &map_v : &map_k;
-          if (!wait_bounded_inl(&bar->kv_empty[s], (C::template use<PAIR>(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty))
+          if (!wait_bounded_inl(&bar->kv_empty[s], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty))
             return false;
           mbar_arrive_expect_tx(&bar->kv_full[s], C::kTileBytes);
           for (int a = 0; a < C::kAtoms; ++a)
@@ -543,28 +534,20 @@ __global__ void __launch_bounds__(384, 1)
           if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
         }
         for (int s = 0; s < C::kSlots; ++s) {
-          // loads into slot s: of all in turn (PAIR), or of the K or V tiles
-          const bool vslot = !PAIR && s >= C::kAltK;
-          const int n = PAIR ? loads : (vslot ? loads >> 1 : (loads + 1) >> 1);
-          const int at0 = vslot ? s - C::kAltK : s, step = PAIR ? C::kSlots : (vslot ? C::kAltV : C::kAltK);
-          if (n > at0) wait_drain_inl(&bar->kv_full[s], ((n - 1 - at0) / step) & 1, kDrainLimitNs);
+          // loads into slot s
+          const bool vslot = s >= C::kKSlots;
+          const int n = vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
+          if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
         }
       }
       __syncwarp();
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
-      // g counts key blocks over all segments.
-      // K_g's wait.  In PAIR's ring of five its slot held V_(g-3), for which this
-      // thread never waits: while that is on its way, the parity of the phase
-      // before it would pass for K_g's.  S(g-1) loaded says that product g-3 is
-      // done, so K_g is asked for behind s_free; where block g-1 had two tiles,
-      // S_1(g-1) was issued behind the loads that say so, and K_g is asked for first
-      // (as in fa_fwd_kernel, which loses 2 % without that).
+      // g counts key blocks over all segments
       if (lane == 0) {
         const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;
-        bool two_before = false;  // the last block had two row tiles
         bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
         while (ok && cross_next(v, items, &bar->second, at, w)) {
           const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
@@ -572,12 +555,9 @@ __global__ void __launch_bounds__(384, 1)
           ++nq;
           const bool two = cross_two<PAIR>(w, cross_row0<PAIR>(w, p.row_tiles), v.R);
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
-            const int ks = C::template slot<PAIR>(0, g);
+            const int ks = C::slot(0, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::use(0, g) & 1, ctx, kSiteCrossK))) break;
             const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
-            bool landed = two_before;
-            if (two_before && !(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK)))
-              break;
-            two_before = two;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (PAIR ? (t == 0 || two) : (((j - w.j0) & 1) == t)) {
@@ -586,9 +566,6 @@ __global__ void __launch_bounds__(384, 1)
                   ok = false;
                   break;
                 }
-                if (!landed && !(ok = wait_bounded_inl(&bar->kv_full[ks], C::template use<PAIR>(0, g) & 1, ctx, kSiteCrossK)))
-                  break;
-                landed = true;
                 tc_fence_after();
                 const uint64_t qd = sdesc_sw128(sq + (PAIR ? t : qs) * C::kTileBytes, 16, 1024);
 #pragma unroll
@@ -623,8 +600,8 @@ __global__ void __launch_bounds__(384, 1)
           const bool two = cross_two<PAIR>(w, cross_row0<PAIR>(w, p.row_tiles), v.R);
           const bool dirty = w.dirty(v);
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
-            const int vs = C::template slot<PAIR>(1, g);
-            if (!(ok = wait_bounded_inl(&bar->kv_full[vs], C::template use<PAIR>(1, g) & 1, ctx, kSiteCrossV))) break;
+            const int vs = C::slot(1, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
             bool clean = !(dirty && j == w.n - 1);
             if (!clean) mbar_arrive(&bar->v_ask);
             const uint64_t vdesc = sdesc_sw128(skv + vs * C::kTileBytes, 16384, 1024);
@@ -665,7 +642,7 @@ __global__ void __launch_bounds__(384, 1)
       CrossMeta meta{};
       while (ok && cross_next(v, items, &bar->second, at, w)) {
         if (w.dirty(v)) {
-          const int vs = C::template slot<PAIR>(1, g + w.j1 - 1 - w.j0);
+          const int vs = C::slot(1, g + w.j1 - 1 - w.j0);
           ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
           if (!ok) break;
           ++cleaned;

@@ -129,10 +129,17 @@ struct FwdCfg {
   // next scores never wait for the other tile to load its own.  At d = 128
   // (and in FP8) the two tiles share one buffer and take turns on it.
   static constexpr bool kDualS = !FP8 && (D == 64);
-  // K_j is ring fill 2j, V_j fill 2j+1; with the ones tiles the slots come in
-  // pairs (K, V, ones), so the slot count is even
+  // Key block g's K and V tiles (g counts over the CTA's items) have ring slots of
+  // their own, taken in turn: slots 0, 2, .. and 1, 3, .. (with the ones tiles the
+  // slots come in pairs: K, V, ones).  The S issuer waits for every K and the P V issuer for every
+  // V, so a wait by parity cannot take the phase before last for its own.
+  // (d = 128 once kept all tiles in turn in its odd number of slots: behind an item's
+  // last block with one row tile the S issuer could pass a slot whose V was late.)
   static constexpr int kSlots = FP8 ? 10 : ((D == 128) ? 5 : 12);
   static_assert(!kSumByMma || kSlots % 2 == 0, "K/V slot pairs");
+  static constexpr int kKSlots = (kSlots + 1) / 2, kVSlots = kSlots / 2;
+  static __device__ __forceinline__ int kv_slot(int kv, int g) { return kv ? 2 * (g % kVSlots) + 1 : 2 * (g % kKSlots); }
+  static __device__ __forceinline__ int kv_use(int kv, int g) { return g / (kv ? kVSlots : kKSlots); }
   static constexpr int kStageBytes = 2 * kTileBytes + kOnesBytes;
   static constexpr int kRingBytes = kSumByMma ? (kSlots / 2) * kStageBytes : kSlots * kTileBytes;
   static __device__ __host__ constexpr int slot_offset(int s) {
@@ -312,14 +319,13 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_dec<C::kMiscRegs>();
     if (warp == 9) {
       // ------------------------------------------------------------------ TMA producer
-      // fill order = consumption order: K_0, V_0, K_1, V_1, ... of each item in turn
+      // K_0, V_0, K_1, V_1, ... of each item in turn
       if (lane == 0) {
-        int fill = 0, nq = 0;
+        int fill = 0, nq = 0;  // K and V tiles asked for
         bool ok = true;
         auto load_kv = [&](int j, int kv, int bh) -> bool {
-          const int s = fill % C::kSlots;
-          const uint32_t u = fill / C::kSlots;
-          if (!wait_bounded_inl(&bar->kv_empty[s], (u & 1) ^ 1, ctx, kSiteFwdProducer)) return false;
+          const int g = fill >> 1, s = C::kv_slot(kv, g);
+          if (!wait_bounded_inl(&bar->kv_empty[s], (C::kv_use(kv, g) & 1) ^ 1, ctx, kSiteFwdProducer)) return false;
           mbar_arrive_expect_tx(&bar->kv_full[s], C::kTileBytes);
           if (FP8 && kv) {
             // V^T of key block j: d rows of 128 keys, tile (bh, j) of the transposed layout
@@ -360,30 +366,22 @@ __global__ void __launch_bounds__(384, 1)
         // every copy this thread started must land before the CTA can exit
         if (nq > 0) wait_drain_inl(&bar->q_full, (nq - 1) & 1, kDrainLimitNs);
         for (int s = 0; s < C::kSlots; ++s) {
-          if (fill > s) {
-            const int uses = (fill - 1 - s) / C::kSlots + 1;
-            wait_drain_inl(&bar->kv_full[s], (uses - 1) & 1, kDrainLimitNs);
-          }
+          // tiles asked for of this slot's kind, and the first of them that it took
+          const int n = (s & 1) ? fill >> 1 : (fill + 1) >> 1, first = s >> 1;
+          if (n > first) wait_drain_inl(&bar->kv_full[s], C::kv_use(s & 1, n - 1 - first) & 1, kDrainLimitNs);
         }
       }
       __syncwarp();
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
-      // K_j is ring fill 2g (g counts key blocks over all items); S(k) waits
-      // until the tile that used S before has loaded it.
-      // K_g's wait.  With an odd number of slots its slot held V_(g-3), for which
-      // this thread never waits: while that is on its way, the parity of the
-      // phase before it would pass for K_g's.  S(g-1) loaded says that product
-      // g-3 is done, so K_g is asked for behind s_free; where block g-1 had two
-      // tiles, S_1(g-1) was issued behind the loads that say so, and K_g is asked
-      // for first (behind s_free in every block the forward loses 2 % at causal N = 32768).
+      // g counts key blocks over all items; S(k) waits until the tile that used S
+      // before has loaded it
       if (lane == 0) {
         const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
         const uint64_t qdesc0 = sdesc_sw128(sq, 16, 1024);
         const uint64_t qdesc1 = sdesc_sw128(sq + C::kTileBytes, 16, 1024);
         constexpr uint32_t id_s = FP8 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;  // S products issued into each score buffer
-        bool two_before = false;                // the last block had both tiles
         bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
         FwdItem w;
         for (int k = 0; ok && fwd_item<CAUSAL>(p, k, w); ++k) {
@@ -392,15 +390,12 @@ __global__ void __launch_bounds__(384, 1)
           if (!wait_bounded_inl(&bar->q_full, nq & 1, ctx, kSiteFwdQ)) break;
           ++nq;
           for (int j = 0; ok && j < nb_max; ++j, ++g) {
-            const int f = 2 * g;
-            const int ks = f % C::kSlots;
-            const uint64_t kdesc = sdesc_sw128(skv + C::slot_offset(ks), 16, 1024);
-            bool landed = two_before;
-            if (two_before && !wait_bounded_inl(&bar->kv_full[ks], (f / C::kSlots) & 1, ctx, kSiteFwdK)) {
+            const int ks = C::kv_slot(0, g);
+            if (!wait_bounded_inl(&bar->kv_full[ks], C::kv_use(0, g) & 1, ctx, kSiteFwdK)) {
               ok = false;
               break;
             }
-            two_before = j < w.nb0 && j < w.nb1;
+            const uint64_t kdesc = sdesc_sw128(skv + C::slot_offset(ks), 16, 1024);
   #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (j < (t ? w.nb1 : w.nb0)) {
@@ -409,11 +404,6 @@ __global__ void __launch_bounds__(384, 1)
                   ok = false;
                   break;
                 }
-                if (!landed && !wait_bounded_inl(&bar->kv_full[ks], (f / C::kSlots) & 1, ctx, kSiteFwdK)) {
-                  ok = false;
-                  break;
-                }
-                landed = true;
                 tc_fence_after();
                 const uint64_t qd = t ? qdesc1 : qdesc0;
   #pragma unroll
@@ -443,7 +433,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     } else if (warp == 10) {
       // ------------------------------------------------------------------ P V issuer
-      // V_j is ring fill 2g+1; O_t += P_t(j) V_j once the softmax of tile t wrote P_t(j)
+      // O_t += P_t(j) V_j once the softmax of tile t wrote P_t(j)
       if (lane == 0) {
         const uint32_t skv = smem_u32(sKV);
         // bf16: V read N-major; FP8: V^T read K-major (with the ones rows after it)
@@ -456,9 +446,8 @@ __global__ void __launch_bounds__(384, 1)
           const int nb_max = max(w.nb0, w.nb1);
           if (nb_max == 0) continue;
           for (int j = 0; ok && j < nb_max; ++j, ++g) {
-            const int f = 2 * g + 1;
-            const int vs = f % C::kSlots;
-            if (!wait_bounded_inl(&bar->kv_full[vs], (f / C::kSlots) & 1, ctx, kSiteFwdV)) {
+            const int vs = C::kv_slot(1, g);
+            if (!wait_bounded_inl(&bar->kv_full[vs], C::kv_use(1, g) & 1, ctx, kSiteFwdV)) {
               ok = false;
               break;
             }

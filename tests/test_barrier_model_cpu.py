@@ -5,8 +5,8 @@ when the phase before last is the completed one.  The model runs the roles of a
 CTA (producer, the two issuers, the two softmax warpgroups) in random
 interleavings, with copies that land in any order, and fails where a wait
 passes on another phase than the one it means, where a product reads a tile that is not
-there, or where a copy overwrites one that is still read.  The number of ring
-slots and the order of the S issuer's waits are read from the kernels' sources.
+there, or where a copy overwrites one that is still read.  The ring's slots are
+read from the kernels' sources.
 """
 
 import os
@@ -48,16 +48,23 @@ def wait(barrier, use):
     assert barrier.phase == use + 1, ("a wait passed early", barrier.phase, use)
 
 
-def run(items, slots, waits, dual, seed):
+def run(items, slots, dual, seed):
     """`items`: key blocks of tile 0 and of tile 1 of each item (a pair of row
-    tiles, or one).  One ring of K and V tiles in turn; `waits`: what the S issuer
-    waits for, in its order; `dual`: a score buffer per tile."""
+    tiles, or one).  `slots`: of K and of V tiles, or one number for a ring that
+    takes both in turn; `dual`: a score buffer per tile."""
     rng = random.Random(seed)
-    full, empty = [[Barrier() for _ in range(slots)] for _ in range(2)]
+    shared = isinstance(slots, int)
+    rings = [slots] * 2 if shared else slots
+    full, empty = [[Barrier() for _ in range(slots if shared else sum(slots))] for _ in range(2)]
     s_full, s_free, p_full, pv_done = [[Barrier(), Barrier()] for _ in range(4)]
     q_full, q_empty = Barrier(), Barrier()
     copies, products = [], ([], [])  # products complete in the order of their issue
-    tile, used = [None] * slots, [None] * slots
+    tile, used = [None] * len(full), [None] * len(full)
+
+    def place(kv, g):
+        """Slot and use of block g's K (kv = 0) or V tile."""
+        f = 2 * g + kv if shared else g
+        return (0 if shared else kv * rings[0]) + f % rings[kv], f // rings[kv]
 
     def blocks():
         g = 0
@@ -67,16 +74,16 @@ def run(items, slots, waits, dual, seed):
                 g += 1
 
     def producer():
-        def load(f):
-            s, u = f % slots, f // slots
+        def load(kv, g):
+            s, u = place(kv, g)
             if u:
                 yield from wait(empty[s], u - 1)
-            assert used[s] is None, ("a tile still in use is overwritten", f)
+            assert used[s] is None, ("a tile still in use is overwritten", kv, g)
             full[s].expect()
-            tile[s], used[s] = None, f
+            tile[s], used[s] = None, (kv, g)
 
             def land():
-                tile[s] = f
+                tile[s] = kv, g
                 full[s].land()
 
             copies.append(land)
@@ -84,8 +91,8 @@ def run(items, slots, waits, dual, seed):
 
         q = 0
         for g, j, _, _ in blocks():
-            yield from load(2 * g)
-            yield from load(2 * g + 1)
+            yield from load(0, g)
+            yield from load(1, g)
             if j == 0:
                 if q:
                     yield from wait(q_empty, q - 1)
@@ -93,40 +100,35 @@ def run(items, slots, waits, dual, seed):
                 copies.append(q_full.land)
                 q += 1
 
-    def product(queue, f, barrier):
+    def product(kv, g, barrier):
         def read():
-            assert tile[f % slots] == f, ("a product reads another tile", tile[f % slots], f)
+            assert tile[place(kv, g)[0]] == (kv, g), ("a product reads another tile", kv, g)
 
-        queue.extend([read, barrier.arrive])
+        products[kv].extend([read, barrier.arrive])
 
-    def release(queue, f):
+    def release(kv, g):
         def done():
-            used[f % slots] = None
-            empty[f % slots].arrive()
+            used[place(kv, g)[0]] = None
+            empty[place(kv, g)[0]].arrive()
 
-        queue.append(done)
+        products[kv].append(done)
 
     def s_issuer():
-        q, uses, two_before = 0, [0, 0], False
+        q, uses = 0, [0, 0]
         for g, j, tiles, last in blocks():
-            f = 2 * g
-            landed = False
             if j == 0:
                 yield from wait(q_full, q)
                 q += 1
+            s, u = place(0, g)
+            yield from wait(full[s], u)
             for t in tiles:
                 b = t if dual else 0
-                for what in waits:
-                    if what == "free" and uses[b]:
-                        yield from wait(s_free[b], uses[b] - 1)
-                    elif (what == "here" or what == "here after two" and two_before) and not landed:
-                        yield from wait(full[f % slots], f // slots)
-                        landed = True
-                product(products[0], f, s_full[t])
+                if uses[b]:
+                    yield from wait(s_free[b], uses[b] - 1)
+                product(0, g, s_full[t])
                 uses[b] += 1
                 yield
-            two_before = len(tiles) == 2
-            release(products[0], f)
+            release(0, g)
             if last:
                 products[0].append(q_empty.arrive)
             yield
@@ -134,14 +136,14 @@ def run(items, slots, waits, dual, seed):
     def pv_issuer():
         uses = [0, 0]
         for g, _, tiles, _ in blocks():
-            f = 2 * g + 1
-            yield from wait(full[f % slots], f // slots)
+            s, u = place(1, g)
+            yield from wait(full[s], u)
             for t in tiles:
                 yield from wait(p_full[t], uses[t])
-                product(products[1], f, pv_done[t])
+                product(1, g, pv_done[t])
                 uses[t] += 1
                 yield
-            release(products[1], f)
+            release(1, g)
             yield
 
     def softmax(t):
@@ -181,16 +183,11 @@ def run(items, slots, waits, dual, seed):
 
 
 def ring(source, d):
-    """Slots of the K/V ring at head dimension d, and the S issuer's waits in their
-    order: for the score buffer ("free") and for K's tile ("here"; "here after
-    two" where the block before had two row tiles)."""
+    """Slots of the K/V ring at head dimension d."""
     text = open(os.path.join(build.CSRC_DIR, source)).read()
     slots = re.search(r"kSlots = .*?\(?D == 128\)? \? (\d+) : (\d+)", text)
-    issuer = text[text.index("- S issuer"):text.index("- P V issuer")]
-    waits = []
-    for line in re.findall(r".*wait_bounded_inl\(&bar->(?:s_free|kv_full)\[.*", issuer):
-        waits.append("free" if "s_free" in line else "here after two" if "two_before" in line else "here")
-    return int(slots.group(1 if d == 128 else 2)), waits
+    slots = int(slots.group(1 if d == 128 else 2))
+    return ((slots + 1) // 2, slots // 2) if "kKSlots = (kSlots + 1) / 2, kVSlots = kSlots / 2" in text else slots
 
 
 # items of two row tiles, of one, of both kinds (a last round, a head's last rows), causal ones
@@ -206,7 +203,7 @@ ITEMS = {
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("source", ["fa_fwd.cuh", "fa_cross_fwd.cuh"])
 def test_no_wait_passes_early(source, d, items):
-    slots, waits = ring(source, d)
-    for seed in range(300):
+    slots = ring(source, d)
+    for seed in range(250):
         r = random.Random(seed)
-        run(ITEMS[items](r.choice([1, 2, 4, 9, 30]), r), slots, waits, d == 64, seed)
+        run(ITEMS[items](r.choice([1, 2, 4, 9, 30]), r), slots, d == 64, seed)
