@@ -594,8 +594,26 @@ def fa_rope_bwd(q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, d
 # With check_status (the default) they wait for the work and raise FaError if
 # a kernel reported a timeout, so what they return is known to be valid; pass
 # check_status=False to keep the call asynchronous and check later with
-# fa_check_device_status.
+# fa_check_device_status.  Outputs and workspaces are allocated (and filled) on
+# the call's stream, and outputs are marked as used on the current one too, so that
+# neither stream gets memory back that the other still works on.
 # ---------------------------------------------------------------------------
+@contextlib.contextmanager
+def _allocating(stream, device: torch.device):
+    """Makes ``stream`` current; yields a function that marks tensors made there as
+    used on the stream that was current before."""
+    if stream is None or device.type != "cuda":
+        yield lambda *tensors: None
+        return
+    handle = _stream_handle(stream, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (0 and 1 are both the legacy default stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    before = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        yield lambda *tensors: [t.record_stream(before) for t in tensors] if before != stream else None
+
+
 def _checked(stream, device, where: str):
     with _on_device(device):
         st = int(load_library().fa_check_device_status(_stream_handle(stream, device)))
@@ -604,9 +622,11 @@ def _checked(stream, device, where: str):
 
 def attention_forward(q, k, v, scale: float, causal: bool = False, stream=None, check_status: bool = True):
     B, H, N, d = _shape4(q, "q")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    fa_fwd(q, k, v, o, lse, scale, causal, stream)
+    with _allocating(stream, q.device) as used:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        used(o, lse)
+        fa_fwd(q, k, v, o, lse, scale, causal, stream)
     if check_status:
         _checked(stream, q.device, "attention_forward")
     return o, lse
@@ -615,11 +635,13 @@ def attention_forward(q, k, v, scale: float, causal: bool = False, stream=None, 
 def attention_forward_fp8(q, k, v, signs, scale: float, causal: bool = False, workspace=None, stream=None,
                           check_status: bool = True):
     B, H, N, d = _shape4(q, "q")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(fa_fwd_fp8_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=q.device)
-    fa_fwd_fp8(q, k, v, signs, o, lse, workspace, scale, causal, stream)
+    with _allocating(stream, q.device) as used:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        used(o, lse)
+        if workspace is None:
+            workspace = torch.empty(fa_fwd_fp8_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=q.device)
+        fa_fwd_fp8(q, k, v, signs, o, lse, workspace, scale, causal, stream)
     if check_status:
         _checked(stream, q.device, "attention_forward_fp8")
     return o, lse
@@ -628,11 +650,13 @@ def attention_forward_fp8(q, k, v, signs, scale: float, causal: bool = False, wo
 def attention_backward(q, k, v, o, dout, lse, scale: float, causal: bool = False, workspace=None, stream=None,
                        deterministic: bool = False, check_status: bool = True):
     B, H, N, d = _shape4(q, "q")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=q.device)
-    (fa_bwd_deterministic if deterministic else fa_bwd)(q, k, v, o, dout, lse, dq, dk, dv, workspace, scale, causal,
-                                                        stream)
+    with _allocating(stream, q.device) as used:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        used(dq, dk, dv)
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_bytes(B, H, N, d), dtype=torch.uint8, device=q.device)
+        (fa_bwd_deterministic if deterministic else fa_bwd)(q, k, v, o, dout, lse, dq, dk, dv, workspace, scale, causal,
+                                                            stream)
     if check_status:
         _checked(stream, q.device, "attention_backward")
     return dq, dk, dv
@@ -642,11 +666,13 @@ def cross_attention_forward(q, k, v, scale: float, key_lens=None, workspace=None
                             check_status: bool = True):
     B, H, Nq, d = _shape4(q, "q")
     _, Hkv, Nk, _ = _shape4(k, "k")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(fa_cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
-    fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale, stream)
+    with _allocating(stream, q.device) as used:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        used(o, lse)
+        if workspace is None:
+            workspace = torch.empty(fa_cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
+        fa_cross_fwd(q, k, v, key_lens, o, lse, workspace, scale, stream)
     if check_status:
         _checked(stream, q.device, "cross_attention_forward")
     return o, lse
@@ -656,10 +682,12 @@ def cross_attention_backward(q, k, v, o, dout, lse, scale: float, key_lens=None,
                              check_status: bool = True):
     B, H, Nq, d = _shape4(q, "q")
     _, Hkv, Nk, _ = _shape4(k, "k")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    if workspace is None:
-        workspace = torch.empty(fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
-    fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale, stream)
+    with _allocating(stream, q.device) as used:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        used(dq, dk, dv)
+        if workspace is None:
+            workspace = torch.empty(fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device=q.device)
+        fa_cross_bwd(q, k, v, key_lens, o, dout, lse, dq, dk, dv, workspace, scale, stream)
     if check_status:
         _checked(stream, q.device, "cross_attention_backward")
     return dq, dk, dv
@@ -670,11 +698,13 @@ def tree_attention_forward(q, k_cache, v_cache, cache_lens, scale: float, draft_
     """Rows of tokens that a request does not have come out as O = 0, LSE = -inf."""
     B, H, T, d = _shape4(q, "q")
     _, Hkv, C, _ = _shape4(k_cache, "k_cache")
-    o = torch.zeros_like(q)
-    lse = torch.full((B, H, T), -math.inf, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(fa_tree_fwd_workspace_bytes(B, H, Hkv, T, C, d), dtype=torch.uint8, device=q.device)
-    fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace, scale, stream)
+    with _allocating(stream, q.device) as used:
+        o = torch.zeros_like(q)
+        lse = torch.full((B, H, T), -math.inf, dtype=torch.float32, device=q.device)
+        used(o, lse)
+        if workspace is None:
+            workspace = torch.empty(fa_tree_fwd_workspace_bytes(B, H, Hkv, T, C, d), dtype=torch.uint8, device=q.device)
+        fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace, scale, stream)
     if check_status:
         _checked(stream, q.device, "tree_attention_forward")
     return o, lse
