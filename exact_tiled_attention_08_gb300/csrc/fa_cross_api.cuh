@@ -110,16 +110,42 @@ struct CrossFwdPlan {
   }
 };
 
-// CTAs per item in a cluster (1: no clusters).  For few enough items that the
-// clusters of 8, 4 or 2 fit the device's SMs at once (two clusters of 8 and four
-// of 4 per GPC of 18 or more SMs), with few blocks each, or all alike (one request,
-// or no lengths) and enough CTAs to draw on most of the memory's bandwidth.
-// (Measured, without and with: B=4 H=16 Nq=1 Nk=1500 d=64 15.8 and 11.7 us; one token
-// of H=32/8 d=128 over 1.9k tokens 12.3 and 9.7 us; B=8 H=32/8 Nq=1 Nk=4096 d=128 44
-// and 40 us.)
-int cross_cluster(long long items, int blocks, bool alike) {
-  const int ctas = items <= 16 ? 8 : items <= 32 ? 4 : items <= 72 ? 2 : 1;
-  return blocks > 1 && (blocks <= 4 * ctas || (alike && items * ctas >= 64)) ? ctas : 1;
+// Clusters of 8, 4 and 2 CTAs that the device holds at once (15, 36 and 76 on a
+// GB300 whose 152 SMs are free), asked once per device.
+template <int D, bool TREE>
+fa::CrossClusterFit cross_cluster_fit(int dev) {
+  static std::atomic<unsigned long long> known[64];  // by device: the three numbers and a bit that says so
+  fa::CrossClusterFit fit{};
+  const unsigned long long was = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (was) {
+    for (int i = 0; i < 3; ++i) fit.clusters[i] = (int)(was >> (16 * i) & 0xffff);
+    return fit;
+  }
+  using C = fa::CrossCfg<D>;
+  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, false, true>;
+  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return fit;
+  unsigned long long found = 1ull << 63;
+  for (int i = 0; i < 3; ++i) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 8u >> i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((8u >> i) * fa::kCrossMaxCtas, 1, 1);
+    cfg.blockDim = dim3((unsigned)C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)C::kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return fa::CrossClusterFit{};
+    }
+    fit.clusters[i] = std::min(n, 0xffff);
+    found |= (unsigned long long)fit.clusters[i] << (16 * i);
+  }
+  if (dev < 64) known[dev].store(found, std::memory_order_relaxed);
+  return fit;
 }
 
 template <int D, bool TREE>
@@ -195,7 +221,15 @@ fa_status run_cross_fwd(const fa::CrossView& view, const void* q, const void* k,
   const bool tree = view.T > 0;
   if (!plan.pair) {
     const long long items = (long long)B * view.Hkv;
-    p.cluster = cross_cluster(items, (view.Nk + 127) / 128, B == 1 || !view.lens);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      return FA_ERR_CUDA;
+    const fa::CrossClusterFit fit =
+        d == 128 ? (tree ? cross_cluster_fit<128, true>(dev) : cross_cluster_fit<128, false>(dev))
+                 : (tree ? cross_cluster_fit<64, true>(dev) : cross_cluster_fit<64, false>(dev));
+    p.cluster = fa::cross_cluster(items, (view.Nk + 127) / 128, view.R, B == 1 || !view.lens,
+                                  std::min(sms, fa::kCrossMaxCtas), fit);
     if (p.cluster > 1) {
       if (d == 128)
         return tree ? launch_cross_clusters<128, true>(mq, mk, mv, p, (int)items, stream)

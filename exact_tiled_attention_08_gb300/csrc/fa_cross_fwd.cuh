@@ -97,6 +97,33 @@ __host__ __device__ __forceinline__ int cross_tail(int rest, int ctas, int place
   return rest == 0 || (long long)(places - kCrossCut) * ctas <= (long long)rest * places ? kCrossTailWhole : kCrossTailCut;
 }
 
+// CTAs per item in a cluster (1: no clusters), for items of at most 128 rows: the
+// largest size whose clusters of all items the device holds at once, where that
+// ends no later than whole items or even shares and their join.  The join costs
+// a place and one for each 32 rows in a cluster, 15 places with its kernel.  Where
+// lengths may differ the host only knows that no item has more than `blocks`: clusters
+// for few of them.  (One request counts as long as its cache has rows.)
+// (Measured at 33 numbers of items from 1 to 76, 256 to 32k keys, 1 and 128 rows: 0.8 %
+// above the best of no clusters and of 2, 4 and 8 on average, 21 % at most.  Without
+// and with clusters, d = 128, one row: 8 items, 2048 keys 19 and 15 us, 16k 31 and
+// 31, 32k 44 and 50; 33 items, 2048 keys 24 and 19; 15 items, 8192 keys 29 and 25;
+// 16, one more than the device holds clusters of 8, 31 and 38.)
+struct CrossClusterFit {
+  int clusters[3];  // of 8, 4 and 2 CTAs
+};
+inline int cross_cluster(long long items, int blocks, int rows, bool alike, int sms, const CrossClusterFit& fit) {
+  for (int i = 0; i < 3; ++i) {
+    const int ctas = 8 >> i;
+    if (items > fit.clusters[i]) continue;
+    if (!alike) return blocks > 1 && blocks <= 4 * ctas ? ctas : 1;
+    const long long places = blocks + kCrossStart;
+    long long apart = items * places / sms + 15;
+    if (items <= sms && places < apart) apart = places;
+    return blocks > 1 && (blocks + ctas - 1) / ctas + kCrossStart + 1 + rows / 32 <= apart ? ctas : 1;
+  }
+  return 1;
+}
+
 // A CTA's work: places of the sequence of items' places, one item after another
 // or every step-th, and then, maybe, a second run of them.
 struct CrossPlace {

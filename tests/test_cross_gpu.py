@@ -418,3 +418,12 @@ def test_parts_without_keys_before_low_scores(Nq, d):
     seen = np.ones((Nq, Nk - dead), bool)
     ref = masked_attention_ref(host(q[0, 0]), host(k[0, 0, dead:]), host(v[0, 0, dead:]), 0.125, seen)
     check_rows(host(o[0, 0]), host(lse[0, 0]), ref, Nq)
+
+
+@pytest.mark.parametrize("Nk", [300, 700, 9000])
+@pytest.mark.parametrize("items", [7, 15, 16, 36, 37, 76, 77])
+def test_on_either_side_of_the_cluster_rule(items, Nk):
+    """One more item than the device holds clusters, and keys that are too many for clusters."""
+    q, k, v, _ = (x.cuda() for x in cross_inputs(1, items, items, 3, Nk, 64, items + Nk))
+    o, lse = fa.cross_attention_forward(q, k, v, 0.125)
+    check_cross_fwd(q, k, v, o, lse, 0.125, None)
