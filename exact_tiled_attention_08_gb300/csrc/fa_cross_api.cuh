@@ -270,8 +270,10 @@ struct CrossBwdWorkspace {
     w.delta_at = w.dq_at + (Nk > 128 ? up(bk * R * d * sizeof(float)) : 0);
     w.lse_at = w.delta_at + up(bk * rpad * sizeof(float));
     w.runs_at = w.lse_at + up(bk * rpad * sizeof(float));
-    // (an item of one query block is never cut)
-    w.total = w.runs_at + (R > 128 ? (size_t)fa::kCrossBwdSlots * 2 * 128 * d * sizeof(float) : 0) + 256;
+    // (an item of one query block is never cut, and none into more runs than it has of them)
+    const size_t blocks = bk * (((size_t)Nk + 127) / 128) * (rpad / 128);
+    const size_t runs = R > 128 ? std::min<size_t>(fa::kCrossBwdSlots, blocks) : 0;
+    w.total = w.runs_at + runs * 2 * 128 * d * sizeof(float) + 256;
     return w;
   }
 };

@@ -3,7 +3,9 @@
 import os
 import subprocess
 
-from exact_tiled_attention_08_gb300 import build
+import pytest
+
+from exact_tiled_attention_08_gb300 import build, fa
 
 
 def test_clusters_only_where_they_fit_and_pay(tmp_path):
@@ -34,3 +36,17 @@ int main() {
     subprocess.run([build._nvcc(), *build.ARCH_FLAGS, "-std=c++17", "-I", build.CSRC_DIR, "-o", str(program), str(source)],
                    check=True, capture_output=True)
     assert subprocess.run([str(program)]).returncode == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_workspace_has_room_for_the_runs_that_there_can_be(d):
+    """Runs of cut items: at most one for each query block of each key block, and 608 in all."""
+    build.build_library()
+    run = 2 * 128 * d * 4
+    for B, H, Hkv, Nq, Nk in [(1, 1, 1, 129, 1), (1, 2, 1, 64, 129), (1, 2, 1, 65, 129), (2, 8, 2, 300, 500), (4, 32, 8, 2000, 900)]:
+        R, heads = H // Hkv * Nq, B * Hkv
+        nqb, nkb = -(-R // 128), -(-Nk // 128)
+        runs = 0 if nqb == 1 else min(608, heads * nqb * nkb)
+        others = (heads * R * d * 4 if nkb > 1 else 0) + 2 * heads * nqb * 128 * 4
+        got = fa.fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d)
+        assert runs * run + others <= got <= runs * run + others + 2048, (B, H, Hkv, Nq, Nk)

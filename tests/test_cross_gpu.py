@@ -427,3 +427,17 @@ def test_on_either_side_of_the_cluster_rule(items, Nk):
     q, k, v, _ = (x.cuda() for x in cross_inputs(1, items, items, 3, Nk, 64, items + Nk))
     o, lse = fa.cross_attention_forward(q, k, v, 0.125)
     check_cross_fwd(q, k, v, o, lse, 0.125, None)
+
+
+@pytest.mark.parametrize("case", [(1, 1, 1, 129, 1), (1, 2, 1, 65, 129), (1, 1, 1, 3000, 40), (2, 4, 2, 300, 500),
+                                  (2, 4, 1, 700, 200)])
+def test_backward_stays_within_its_workspace(case):
+    """Runs of cut items in a workspace of exactly the bytes asked for."""
+    B, H, Hkv, Nq, Nk = case
+    q, k, v, do = (x.cuda() for x in cross_inputs(B, H, Hkv, Nq, Nk, 64, 11))
+    o, lse = fa.cross_attention_forward(q, k, v, 0.125)
+    n = fa.fa_cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, 64)
+    memory = torch.full((n + (1 << 20),), 90, dtype=torch.uint8, device="cuda")
+    grads = fa.cross_attention_backward(q, k, v, o, do, lse, 0.125, workspace=memory[:n])
+    check_cross_bwd(q, k, v, o, do, lse, grads, 0.125, None)
+    assert (memory[n:] == 90).all()
