@@ -247,7 +247,10 @@ __global__ void __launch_bounds__(512, 1)
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
     grid_wait();
-    if (threadIdx.x == 0) atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
+    if (threadIdx.x == 0) {
+      atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
+      if (blockIdx.x == 0) *p.plan = CrossBwdPlan{0, 0, 1};  // no runs for the post kernel to add
+    }
     return;
   }
   uint8_t* smem = smem_raw;
