@@ -11,9 +11,12 @@
 // Backward: g = f R^T dy, dw = sum g o x^, dx = (w o g - x^ mean(w o g o x^)) / rms.
 //
 // Angles.  A position may be far (millions), where pos * freq in fp32 has lost
-// its fraction.  freq / 2 pi is kept as a 64-bit binary fraction of a turn;
-// the 64-bit product with the position wraps by whole turns, so its upper
-// 32 bits are the angle to 2^-32 of a turn at any 32-bit position.
+// its fraction.  freq / 2 pi, an fp64 product, is kept as a 64-bit binary fraction
+// of a turn; the 64-bit product with the position wraps by whole turns, and its
+// upper 32 bits become the fp32 angle.  In radians an angle is off by at most
+// 2^-52 |pos freq| (freq / 2 pi: the product's and the constant's rounding) and
+// 2^-23 (the fp32 half-turns, up to 2^-26 of a turn, and the bits cut off): 2^-22 at two
+// million and freq = 1, 2^-20 at the last 32-bit position; bf16's half step is 2^-8.
 //
 // Both are bound by memory: a row is read once and written once.  A lane holds
 // 8 values of a row, D / 8 lanes a row; it holds whole pairs (in the half layout

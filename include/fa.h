@@ -325,8 +325,9 @@ typedef struct {
  * with pairs (i, i + rotary_dim / 2) (interleaved = 0) or (2 i, 2 i + 1)
  * (interleaved = 1); values from rotary_dim on stay as they are.  Rows go from
  * token-major tensors to head-major ones, as the attention entry points read
- * them; value rows are moved along unchanged.  Angles keep their precision at
- * any 32-bit position.  Arithmetic is fp32, rounded once.
+ * them; value rows are moved along unchanged.  Angles (modulo
+ * whole turns) are off by at most 2^-23 + 2^-52 |position * inv_freq| radians.
+ * Arithmetic is fp32, rounded once.
  *
  *   q, k, v      in:  bf16 rows, B requests of N tokens, H heads (q) and Hkv
  *                heads (k, v); a null q, k or v (ptr null, and its output null)

@@ -8,6 +8,7 @@ n / 600 + 700 additions a partial: (n / 600 + 700) 2^-24 of the sum of sizes.
 """
 
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -215,3 +216,31 @@ def test_replayed_graph():
     graph.replay()
     for b in range(B):
         close(host(outs[0][b]), rope_ref(host(q[b].transpose(0, 1)), *oracle_args(case, w[0], freq, pos, b, 1.0)), "q")
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("position", [0, 1, 4097, 2 ** 24 + 1, 2 ** 31 - 1, -1, -2 ** 31])
+def test_angles_at_far_positions(position, interleaved):
+    """cos and sin as the gradient of a weight sees them, in fp32: a row of ones, of
+    which the first of each pair has a gradient of 1, gives cos and -sin.
+    Bound: the angle's 2^-23 + 2^-52 |position freq|, and 2^-21 for sincospi (1 ulp), the norm's
+    reciprocal root (2 ulp) and four roundings."""
+    d = 128
+    freq, _ = fa.rope_frequencies(d)
+    q = torch.ones((1, 1, 1, d), dtype=torch.bfloat16, device="cuda")
+    first = torch.arange(d, device="cuda") % 2 == 0 if interleaved else torch.arange(d, device="cuda") < d // 2
+    dy = first.bfloat16().reshape(1, 1, 1, d).contiguous()
+    dq, dw = torch.empty_like(q), torch.empty((d,), device="cuda")
+    ws = torch.empty(fa.fa_rope_bwd_workspace_bytes(1, 1, 1, 1, d), dtype=torch.uint8, device="cuda")
+    pos = torch.tensor([[position]], dtype=torch.int32, device="cuda")
+    fa.fa_rope_bwd(q, None, None, None, freq, pos, dy, None, None, dq, None, None, dw, None, ws, eps=0.0,
+                   interleaved=interleaved)
+    got = dw.double().cpu()
+    a, b = (got[0::2], got[1::2]) if interleaved else (got[:d // 2], got[d // 2:])
+    for i, f in enumerate(freq.tolist()):
+        angle = float(2 * PI * (Fraction(f) * position / (2 * PI) % 1))
+        bound = 2.0 ** -23 + 2.0 ** -52 * abs(position) * f + 2.0 ** -21
+        assert abs(a[i] - math.cos(angle)) <= bound and abs(b[i] + math.sin(angle)) <= bound, (i, f)
