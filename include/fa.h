@@ -229,7 +229,9 @@ fa_status fa_bwd_static_scratch(const void* q, const void* k, const void* v, con
  * Cross attention: queries [B][H][Nq][d] over keys and values [B][Hkv][Nk][d]
  * of another length (an encoder's states), O = softmax(scale Q K^T) V.
  * Query head h uses key/value head h / (H / Hkv); H is a multiple of Hkv.
- * There is no causal mask.
+ * There is no causal mask.  Scores, probabilities, their sums and what is joined of
+ * an item cut among thread blocks are fp32; P is rounded to bf16 for P V, O once
+ * at the end.
  *
  *   q        in:  bf16 [B][H][Nq][d]
  *   k, v     in:  bf16 [B][Hkv][Nk][d]
@@ -258,6 +260,8 @@ fa_status fa_cross_fwd(const void* q, const void* k, const void* v, const int* k
  * Backward pass of fa_cross_fwd by recomputation: P = exp(S - LSE),
  * dV = P^T dO, dS = P o (dO V^T - rowsum(dO o O)), dQ = scale dS K,
  * dK = scale dS^T Q, dK and dV summed over the query heads that share them.
+ * P and dS are rounded to bf16 for the products, the gradients once at the end
+ * from fp32 sums.
  *
  *   q, o, dout, lse  in:  as for fa_cross_fwd; o and lse as it wrote them
  *   dq               out: bf16 [B][H][Nq][d]
@@ -293,6 +297,8 @@ fa_status fa_cross_bwd(const void* q, const void* k, const void* v, const int* k
  *                     number of drafted tokens are left as they were
  *   T            any with draft_masks null; at most 64 with them
  *                (FA_ERR_UNSUPPORTED)
+ *                (every row meets all drafted keys of its request, hidden ones
+ *                too: a prompt of T tokens costs T x T scores, not half of them)
  *   workspace    as for fa_cross_fwd, of fa_tree_fwd_workspace_bytes()
  * The values of a drafted token meet every row of its request (with weight 0
  * where a mask hides it), so a drafted row of V with an infinity or NaN makes
@@ -359,7 +365,7 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
  *                of its outputs, as the attention backward passes write them
  *   dq, dk, dv   out: bf16 rows like q, k, v; a null one leaves that tensor out
  *                (its gradient then null too).  The rows may overlap neither one
-                another nor an input.
+ *                another nor an input.
  *   dq_weight, dk_weight  out: fp32 [d], summed over all rows; may be null
  *   workspace    device scratch of ws_bytes >= fa_rope_bwd_workspace_bytes(),
  *                16-byte aligned; may be null when no weight gradient is asked for
@@ -472,8 +478,9 @@ void fa_set_wait_limit_ns(unsigned long long limit_ns);
  * fa_cross_bwd and fa_tree_fwd) first makes its MMA-issuing thread wait on a
  * barrier that nothing ever signals; that wait runs out after the wait limit
  * (fa_set_wait_limit_ns), the kernel reports FA_ERR_TIMEOUT, drains the copies
- * it started and returns without writing its outputs.  Process-wide; 0 (the
- * default) turns it off.  Nothing traps or hangs.
+ * it started and returns.  The outputs of the call are then undefined, as after
+ * any wait that runs out: kernels that join or finish a call's parts run on
+ * what is there.  Process-wide; 0 (the default) turns it off.  Nothing traps or hangs.
  */
 void fa_debug_stall(int enable);
 
