@@ -102,7 +102,7 @@ __host__ __device__ __forceinline__ int cross_tail(int rest, int ctas, int place
 // ends no later than whole items or even shares and their join.  The join costs
 // a place and one for each 32 rows in a cluster, 15 places with its kernel.  Where
 // lengths may differ the host only knows that no item has more than `blocks`: clusters
-// for few of them.  (One request counts as long as its cache has rows.)
+// for few of them.
 // (Measured at 33 numbers of items from 1 to 76, 256 to 32k keys, 1 and 128 rows: 0.8 %
 // above the best of no clusters and of 2, 4 and 8 on average, 21 % at most.  Without
 // and with clusters, d = 128, one row: 8 items, 2048 keys 19 and 15 us, 16k 31 and
