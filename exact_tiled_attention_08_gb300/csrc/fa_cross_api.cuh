@@ -78,6 +78,15 @@ bool all_aligned(std::initializer_list<const void*> ptrs, unsigned bytes) {
   return true;
 }
 
+fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (!p) continue;
+    const fa_status st = check_device_ptrs({p});
+    if (st != FA_OK) return st;
+  }
+  return FA_OK;
+}
+
 fa::CrossView cross_view(int H, int Hkv, int Nq, int Nk) {
   fa::CrossView v{};
   v.Nk = Nk;

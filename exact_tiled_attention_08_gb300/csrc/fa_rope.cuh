@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 
 #include "fa_cross.cuh"
+#include "fa_span.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -67,6 +68,11 @@ struct RopeParams {
   long long units;      // warps' units of work: token groups (rounded up to whole CTAs) * split.steps
   float eps, factor;
   int norm;
+  // pages (their tokens' first positions in starts, C = width pages; table nullptr:
+  // queries alone)
+  PageRows k_pages, v_pages;
+  const int *table, *chunks;  // [B][width]; [B] or nullptr: N new tokens
+  int width, page_shift, pages;
 };
 
 // freq / 2 pi as a binary fraction of a turn (whole turns dropped)
@@ -299,7 +305,9 @@ __device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& tur
   __syncwarp();  // the ring has been read
 }
 
-template <int D, bool kInterleaved, bool kNorm>
+// kPaged: keys and values go to the pages of a cache.  (A kernel of its own, so that
+// contiguous caches keep their addresses and registers.)
+template <int D, bool kInterleaved, bool kNorm, bool kPaged>
 __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kernel(const RopeParams p) {
   __shared__ unsigned long long turns[64];
   __shared__ __align__(16) uint8_t rings[kRopeThreads / 32][kRopeStages * 512];
@@ -309,10 +317,33 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
   for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); unit < p.units;
        unit += (long long)gridDim.x * (kRopeThreads / 32)) {
     const RopeToken t = rope_token<D>(p, unit);
-    const int start = p.starts ? __ldg(p.starts + t.b) : 0;
+    int start = p.starts ? __ldg(p.starts + t.b) : 0;
+    bool here = t.valid;  // a token of the chunk
+    if (kPaged) {
+      start = min(max(start, 0), p.C);
+      here = here && t.n < min(p.chunks ? __ldg(p.chunks + t.b) : p.N, p.C - start);
+    }
     const int pos = p.positions ? __ldg(p.positions + (t.valid ? t.token : 0)) : start + t.n;
     const long long row = (long long)start + t.n;  // row of this token in k_out and v_out
-    const bool stored = t.valid && row >= 0 && row < p.C;
+    bool stored = here && row >= 0 && row < p.C;
+    // where the row of the first key/value head goes, and how far the next one's is
+    __nv_bfloat16 *k_to, *v_to;
+    long long k_next = (long long)p.C * D, v_next = k_next;
+    if (kPaged) {
+      int page = 0;
+      if (stored && p.table) page = __ldg(p.table + (long long)t.b * p.width + (row >> p.page_shift));
+      stored = stored && page >= 0 && page < p.pages;
+      if (!stored) page = 0;
+      const long long in_page = row & ((1 << p.page_shift) - 1);
+      k_to = p.k_pages.ptr + page * p.k_pages.page + in_page * p.k_pages.token;
+      v_to = p.v_pages.ptr + page * p.v_pages.page + in_page * p.v_pages.token;
+      k_next = p.k_pages.head;
+      v_next = p.v_pages.head;
+    } else {
+      const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D;
+      k_to = p.k_out + cache;
+      v_to = p.v_out + cache;
+    }
     int e0, e1;
     RopeTurn<kInterleaved>::place(p.rot, t.sub, e0, e1);
     RopeTurn<kInterleaved> turn;
@@ -321,14 +352,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     if (p.q.ptr && t.h0 < p.H)
       rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.q), p.q.head,
                                                    p.q_out + ((long long)t.b * p.H * p.N + t.n) * D,
-                                                   (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1, t.valid, t.valid,
+                                                   (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1, t.valid, here,
                                                    p.q_weight, p.eps);
-    const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D, next = (long long)p.C * D;
     if (p.k.ptr)
-      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.k), p.k.head, p.k_out + cache, next, max(t.h0 - p.H, 0),
+      rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.k), p.k.head, k_to, k_next, max(t.h0 - p.H, 0),
                                                    min(t.h1 - p.H, p.Hkv), e0, e1, t.valid, stored, p.k_weight, p.eps);
     if (p.v.ptr)
-      rope_fwd_heads<D, kInterleaved, false, false>(turn, ring, in(p.v), p.v.head, p.v_out + cache, next,
+      rope_fwd_heads<D, kInterleaved, false, false>(turn, ring, in(p.v), p.v.head, v_to, v_next,
                                                     max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
                                                     stored, nullptr, 0.f);
   }

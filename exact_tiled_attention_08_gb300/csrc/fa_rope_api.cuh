@@ -53,15 +53,6 @@ fa_status check_rope(const double* inv_freq, int B, int N, int H, int Hkv, int d
   return FA_OK;
 }
 
-fa_status check_device_ptrs_given(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs) {
-    if (!p) continue;
-    const fa_status st = check_device_ptrs({p});
-    if (st != FA_OK) return st;
-  }
-  return FA_OK;
-}
-
 // Warps' units of work: a warp's tokens times some heads.  The heads of a unit
 // share the token's angles and one start of the ring, about four rows' time; the
 // device holds `warps` warps at once, and the split that ends soonest is taken.
@@ -94,12 +85,25 @@ void rope_units(fa::RopeParams& p, int d, long long warps, bool q, bool k, bool 
   }
 }
 
-template <int D, bool kNorm>
+template <int D, bool kNorm, bool kPaged>
 void launch_rope_fwd(const fa::RopeParams& p, unsigned grid, int interleaved, cudaStream_t stream) {
   if (interleaved)
-    fa::fa_rope_fwd_kernel<D, true, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    fa::fa_rope_fwd_kernel<D, true, kNorm, kPaged><<<grid, fa::kRopeThreads, 0, stream>>>(p);
   else
-    fa::fa_rope_fwd_kernel<D, false, kNorm><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    fa::fa_rope_fwd_kernel<D, false, kNorm, kPaged><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+}
+
+template <bool kPaged>
+fa_status run_rope_fwd(fa::RopeParams& p, int d, bool q, bool k, bool v, int interleaved, cudaStream_t stream) {
+  rope_units(p, d, kRopeFwdCtas * 8LL, q, k, v);
+  const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeFwdCtas);
+  if (d == 128)
+    p.norm ? launch_rope_fwd<128, true, kPaged>(p, grid, interleaved, stream)
+           : launch_rope_fwd<128, false, kPaged>(p, grid, interleaved, stream);
+  else
+    p.norm ? launch_rope_fwd<64, true, kPaged>(p, grid, interleaved, stream)
+           : launch_rope_fwd<64, false, kPaged>(p, grid, interleaved, stream);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, bool kNorm>
@@ -158,13 +162,69 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  rope_units(p, d, kRopeFwdCtas * 8LL, q_out, k_out, v_out);
-  const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeFwdCtas);
-  if (d == 128)
-    norm ? launch_rope_fwd<128, true>(p, grid, interleaved, stream) : launch_rope_fwd<128, false>(p, grid, interleaved, stream);
-  else
-    norm ? launch_rope_fwd<64, true>(p, grid, interleaved, stream) : launch_rope_fwd<64, false>(p, grid, interleaved, stream);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return run_rope_fwd<false>(p, d, q_out, k_out, v_out, interleaved, stream);
+}
+
+fa_status fa_rope_paged_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const float* q_weight,
+                            const float* k_weight, const double* inv_freq, const int* positions,
+                            const int* page_table, const int* cache_lens, const int* chunk_lens, void* q_out,
+                            const fa_pages* k_pages, const fa_pages* v_pages, int B, int N, int H, int Hkv, int d,
+                            int num_pages, int page_size, int table_width, int rotary_dim, int norm, float eps,
+                            float factor, int interleaved, cudaStream_t stream) {
+  const bool to_k = k_pages && k_pages->ptr, to_v = v_pages && v_pages->ptr;
+  if (present(q) != (q_out != nullptr) || present(k) != to_k || present(v) != to_v) return FA_ERR_INVALID_ARG;
+  if (!q_out && !to_k && !to_v) return FA_ERR_INVALID_ARG;
+  fa_status st = check_rope(inv_freq, B, N, H, Hkv, d, rotary_dim, norm, eps, factor, interleaved);
+  if (st != FA_OK) return st;
+  const PageShape pages{num_pages, page_size, table_width};
+  if (to_k || to_v) {
+    if (!page_table || !cache_lens) return FA_ERR_INVALID_ARG;
+    if ((st = pages.check()) != FA_OK) return st;
+  }
+  for (const fa_pages* r : {k_pages, v_pages}) {
+    if (!r || !r->ptr) continue;
+    if ((st = check_pages(r, pages, Hkv)) != FA_OK) return st;
+    if (!rows_disjoint({r->ptr, r->page, r->token, r->head}, num_pages, page_size, Hkv, d)) return FA_ERR_INVALID_ARG;
+  }
+  for (const fa_rows* r : {q, k, v})
+    if (present(r) && (st = check_rows(*r)) != FA_OK) return st;
+  if (!all_aligned16({q_weight, k_weight, q_out}) ||
+      !all_aligned({positions, page_table, cache_lens, chunk_lens}, 4) || !all_aligned({inv_freq}, 8))
+    return FA_ERR_MISALIGNED;
+  if ((st = check_device_ptrs_given({q ? q->ptr : nullptr, k ? k->ptr : nullptr, v ? v->ptr : nullptr, q_weight,
+                                     k_weight, inv_freq, positions, page_table, cache_lens, chunk_lens, q_out,
+                                     to_k ? k_pages->ptr : nullptr, to_v ? v_pages->ptr : nullptr})) != FA_OK)
+    return st;
+  fa::RopeParams p{};
+  p.q = rope_rows(q);
+  p.k = rope_rows(k);
+  p.v = rope_rows(v);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.starts = cache_lens;
+  p.N = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.C = 0x7fffffff;
+  p.rot = rotary_dim;
+  p.tokens = (long long)B * N;
+  p.eps = eps;
+  p.factor = factor;
+  p.norm = norm;
+  p.chunks = chunk_lens;
+  if (to_k || to_v) {
+    if (to_k) p.k_pages = page_rows(k_pages);
+    if (to_v) p.v_pages = page_rows(v_pages);
+    p.C = (int)pages.capacity();
+    p.table = page_table;
+    p.width = table_width;
+    p.page_shift = pages.shift();
+    p.pages = num_pages;
+  }
+  return run_rope_fwd<true>(p, d, q_out, to_k, to_v, interleaved, stream);
 }
 
 size_t fa_rope_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
@@ -246,6 +306,14 @@ fa_status fa_rope_fwd_packed(const fa_rope_fwd_args* a) {
   return fa_rope_fwd(&a->q, &a->k, &a->v, a->q_weight, a->k_weight, a->inv_freq, a->positions, a->starts, a->q_out,
                      a->k_out, a->v_out, a->B, a->N, a->H, a->Hkv, a->C, a->d, a->rotary_dim, a->norm, a->eps,
                      a->factor, a->interleaved, a->stream);
+}
+
+fa_status fa_rope_paged_fwd_packed(const fa_rope_paged_fwd_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_rope_paged_fwd(&a->q, &a->k, &a->v, a->q_weight, a->k_weight, a->inv_freq, a->positions, a->page_table,
+                           a->cache_lens, a->chunk_lens, a->q_out, &a->k_pages, &a->v_pages, a->B, a->N, a->H, a->Hkv,
+                           a->d, a->num_pages, a->page_size, a->table_width, a->rotary_dim, a->norm, a->eps, a->factor,
+                           a->interleaved, a->stream);
 }
 
 fa_status fa_rope_bwd_packed(const fa_rope_bwd_args* a) {

@@ -44,7 +44,7 @@ class FaError(RuntimeError):
         super().__init__(f"{where}: {_STATUS_NAMES.get(status, status)}")
 
 
-# The argument structs of the *_packed entry points (fa_rows: Pqqq).  One struct
+# The argument structs of the *_packed entry points (fa_rows and fa_pages: Pqqq).  One struct
 # costs a call a fraction of what twenty ctypes arguments do.
 _PACKED = {
     "fa_cross_fwd": struct.Struct("@7PN6ifP").pack,
@@ -52,6 +52,10 @@ _PACKED = {
     "fa_tree_fwd": struct.Struct("@9PN6ifP").pack,
     "fa_rope_fwd": struct.Struct("@PqqqPqqqPqqq8P8i2fiP").pack,
     "fa_rope_bwd": struct.Struct("@PqqqPqqq7PPqqqPqqqPqqq3PN7i2fiP").pack,
+    "fa_span_fwd": struct.Struct("@9PN5i2f2iP").pack,
+    "fa_span_bwd": struct.Struct("@13PN5i2f2iP").pack,
+    "fa_paged_fwd": struct.Struct("@PPqqqPqqq7PN8i2fiP").pack,
+    "fa_rope_paged_fwd": struct.Struct("@PqqqPqqqPqqq8PPqqqPqqq10i2fiP").pack,
 }
 _entries = {}  # name -> (packed entry point, pack)
 
@@ -106,6 +110,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fa_rope_bwd_workspace_bytes.restype = sz
     lib.fa_rope_bwd.argtypes = [rows] * 2 + [vp] * 7 + [rows] * 3 + [vp] * 3 + [sz] + [i] * 7 + [f, f, i, vp]
     lib.fa_rope_bwd.restype = i
+    lib.fa_span_fwd_workspace_bytes.argtypes = [i] * 5
+    lib.fa_span_fwd_workspace_bytes.restype = sz
+    lib.fa_span_fwd.argtypes = [vp] * 9 + [sz] + [i] * 5 + [f, f, i, i, vp]
+    lib.fa_span_fwd.restype = i
+    lib.fa_span_bwd_workspace_bytes.argtypes = [i] * 5
+    lib.fa_span_bwd_workspace_bytes.restype = sz
+    lib.fa_span_bwd.argtypes = [vp] * 13 + [sz] + [i] * 5 + [f, f, i, i, vp]
+    lib.fa_span_bwd.restype = i
+    pages = vp  # fa_pages: an address, or its 32 bytes
+    lib.fa_paged_fwd_workspace_bytes.argtypes = [i] * 6
+    lib.fa_paged_fwd_workspace_bytes.restype = sz
+    lib.fa_paged_fwd.argtypes = [vp] + [pages] * 2 + [vp] * 7 + [sz] + [i] * 8 + [f, f, i, vp]
+    lib.fa_paged_fwd.restype = i
+    lib.fa_rope_paged_fwd.argtypes = [rows] * 3 + [vp] * 8 + [pages] * 2 + [i] * 10 + [f, f, i, vp]
+    lib.fa_rope_paged_fwd.restype = i
     lib.fa_check_device_status.argtypes = [vp]
     lib.fa_check_device_status.restype = i
     lib.fa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
@@ -590,6 +609,133 @@ def fa_rope_bwd(q, k, q_weight, k_weight, inv_freq, positions, dq_out, dk_out, d
 
 
 # ---------------------------------------------------------------------------
+# attention to spans of keys, caches in pages
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def fa_span_fwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int) -> int:
+    return int(load_library().fa_span_fwd_workspace_bytes(B, H, Hkv, N, d))
+
+
+def _span_sizes(q, k):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be [B, H, N, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    B, H, N, d = q.shape
+    return B, H, k.shape[1], N, d
+
+
+def fa_span_fwd(q, k, v, key_begin, key_end, o, lse, workspace, scale: float, *, causal: bool = False, window: int = 0,
+                cap: float = 0.0, slopes=None, stream=None) -> None:
+    """Self-attention of q [B,H,N,d] over k, v [B,Hkv,N,d] in which query i sees the keys
+    key_begin[b,i] <= j < key_end[b,i] (int32 [B,N] or None: 0 and N), j <= i (causal)
+    and |i - j| < window (0: any); scores cap tanh(scale q.k / cap) (0: no cap) minus
+    slopes[h] |i - j| (fp32 [H] or None); o like q, lse [B,H,N] fp32."""
+    B, H, Hkv, N, d = _span_sizes(q, k)
+    dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, N, d), (B, Hkv, N, d)
+    _call("fa_span_fwd", dev, stream, _ptr(q, "q", bf, rows, dev), _ptr(k, "k", bf, keys, dev),
+          _ptr(v, "v", bf, keys, dev), _given(key_begin, "key_begin", torch.int32, (B, N), dev),
+          _given(key_end, "key_end", torch.int32, (B, N), dev), _given(slopes, "slopes", torch.float32, (H,), dev),
+          _ptr(o, "o", bf, rows, dev), _ptr(lse, "lse", torch.float32, (B, H, N), dev), *_workspace(workspace, dev),
+          B, H, Hkv, N, d, scale, cap, window, 1 if causal else 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def fa_span_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int) -> int:
+    return int(load_library().fa_span_bwd_workspace_bytes(B, H, Hkv, N, d))
+
+
+def fa_span_bwd(q, k, v, key_begin, key_end, o, dout, lse, dq, dk, dv, workspace, scale: float, *,
+                causal: bool = False, window: int = 0, cap: float = 0.0, slopes=None, stream=None) -> None:
+    """dQ, dK, dV of fa_span_fwd by recomputation; dk, dv like k, v.  The cap and the
+    slopes are constants."""
+    B, H, Hkv, N, d = _span_sizes(q, k)
+    dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, N, d), (B, Hkv, N, d)
+    _call("fa_span_bwd", dev, stream, _ptr(q, "q", bf, rows, dev), _ptr(k, "k", bf, keys, dev),
+          _ptr(v, "v", bf, keys, dev), _given(key_begin, "key_begin", torch.int32, (B, N), dev),
+          _given(key_end, "key_end", torch.int32, (B, N), dev), _given(slopes, "slopes", torch.float32, (H,), dev),
+          _ptr(o, "o", bf, rows, dev), _ptr(dout, "dout", bf, rows, dev),
+          _ptr(lse, "lse", torch.float32, (B, H, N), dev), _ptr(dq, "dq", bf, rows, dev),
+          _ptr(dk, "dk", bf, keys, dev), _ptr(dv, "dv", bf, keys, dev), *_workspace(workspace, dev), B, H, Hkv, N, d,
+          scale, cap, window, 1 if causal else 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def fa_paged_fwd_workspace_bytes(B: int, H: int, Hkv: int, T: int, C: int, d: int) -> int:
+    """C: the tokens that a request's pages hold, page_table.shape[1] * page_size."""
+    return int(load_library().fa_paged_fwd_workspace_bytes(B, H, Hkv, T, C, d))
+
+
+def _pages(t, name: str, shape, device):
+    """``fa_pages`` (address and strides of pages, heads and tokens) of a [pages, Hkv,
+    page_size, d] tensor whose d values lie next to each other; None: no such pages."""
+    if t is None:
+        return _NO_ROWS
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sp, sh, st, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have its last dimension contiguous")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr(), sp, sh, st
+
+
+def _page_table(page_table, B: int, device):
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [B, width], got {tuple(page_table.shape)}")
+    width = page_table.shape[1]
+    return _ptr(page_table, "page_table", torch.int32, (B, width), device), width
+
+
+def fa_paged_fwd(q, k_pages, v_pages, page_table, cache_lens, chunk_lens, o, lse, workspace, scale: float, *,
+                 window: int = 0, cap: float = 0.0, slopes=None, stream=None) -> None:
+    """Attention of up to T new tokens per request, q [B,H,T,d], over a cache in pages
+    k_pages, v_pages [pages,Hkv,page_size,d] (any strides with d contiguous) that holds
+    cache_lens[b] tokens and then the new ones; page_table int32 [B,width]; chunk_lens
+    int32 [B] (or None: T).  Token n sees the positions up to its own, cache_lens[b] +
+    n, and less than window back; cap and slopes as for fa_span_fwd."""
+    if q.dim() != 4 or k_pages.dim() != 4:
+        raise ValueError(f"q must be [B, H, T, d] and k_pages [pages, Hkv, page_size, d], got {tuple(q.shape)} and "
+                         f"{tuple(k_pages.shape)}")
+    B, H, T, d = q.shape
+    pages, Hkv, size, _ = k_pages.shape
+    dev, bf, rows, shape = q.device, torch.bfloat16, (B, H, T, d), (pages, Hkv, size, d)
+    table, width = _page_table(page_table, B, dev)
+    _call("fa_paged_fwd", dev, stream, _ptr(q, "q", bf, rows, dev), *_pages(k_pages, "k_pages", shape, dev),
+          *_pages(v_pages, "v_pages", shape, dev), table, _ptr(cache_lens, "cache_lens", torch.int32, (B,), dev),
+          _given(chunk_lens, "chunk_lens", torch.int32, (B,), dev),
+          _given(slopes, "slopes", torch.float32, (H,), dev), _ptr(o, "o", bf, rows, dev),
+          _ptr(lse, "lse", torch.float32, (B, H, T), dev), *_workspace(workspace, dev), B, H, Hkv, T, d, pages, size,
+          width, scale, cap, window)
+
+
+def fa_rope_paged_fwd(q, k, v, q_weight, k_weight, inv_freq, positions, page_table, cache_lens, chunk_lens, q_out,
+                      k_pages, v_pages, *, eps=None, factor: float = 1.0, interleaved: bool = False,
+                      stream=None) -> None:
+    """fa_rope_fwd into a cache in pages: keys and values of new token n of request b go
+    to position cache_lens[b] + n of its pages k_pages, v_pages [pages,Hkv,page_size,d]
+    (as fa_paged_fwd reads them), queries to q_out [B,H,N,d].  chunk_lens int32 [B] (or
+    None: N tokens each); positions None: cache_lens[b] + n; page_table and cache_lens
+    may be None without k and v."""
+    B, N, H, Hkv, d, dev = _rope_sizes(q, k, v, ("q", "k", "v"))
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights need eps: without it there is no norm")
+    cache = k_pages if k_pages is not None else v_pages
+    pages, _, size, _ = (0, 0, 0, 0) if cache is None else _shape4(cache, "k_pages")
+    table, width = (0, 0) if page_table is None else _page_table(page_table, B, dev)
+    bf, f32, i32, shape = torch.bfloat16, torch.float32, torch.int32, (pages, Hkv, size, d)
+    freq, rot = _frequencies(inv_freq, dev)
+    _call("fa_rope_paged_fwd", dev, stream, *_rows(q, "q", (B, N, H, d), dev), *_rows(k, "k", (B, N, Hkv, d), dev),
+          *_rows(v, "v", (B, N, Hkv, d), dev), _given(q_weight, "q_weight", f32, (d,), dev),
+          _given(k_weight, "k_weight", f32, (d,), dev), freq, _given(positions, "positions", i32, (B, N), dev), table,
+          _given(cache_lens, "cache_lens", i32, (B,), dev), _given(chunk_lens, "chunk_lens", i32, (B,), dev),
+          _given(q_out, "q_out", bf, (B, H, N, d), dev), *_pages(k_pages, "k_pages", shape, dev),
+          *_pages(v_pages, "v_pages", shape, dev), B, N, H, Hkv, d, pages, size, width, rot, 0 if eps is None else 1,
+          eps or 0.0, factor, 1 if interleaved else 0)
+
+
+# ---------------------------------------------------------------------------
 # conveniences that allocate the outputs with torch and call the entry points.
 # With check_status (the default) they wait for the work and raise FaError if
 # a kernel reported a timeout, so what they return is known to be valid; pass
@@ -707,4 +853,58 @@ def tree_attention_forward(q, k_cache, v_cache, cache_lens, scale: float, draft_
         fa_tree_fwd(q, k_cache, v_cache, cache_lens, draft_lens, draft_masks, o, lse, workspace, scale, stream)
     if check_status:
         _checked(stream, q.device, "tree_attention_forward")
+    return o, lse
+
+
+def span_attention_forward(q, k, v, scale: float, key_begin=None, key_end=None, causal: bool = False, window: int = 0,
+                           cap: float = 0.0, slopes=None, workspace=None, stream=None, check_status: bool = True):
+    B, H, N, d = _shape4(q, "q")
+    _, Hkv, _, _ = _shape4(k, "k")
+    with _allocating(stream, q.device) as used:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        used(o, lse)
+        if workspace is None:
+            workspace = torch.empty(fa_span_fwd_workspace_bytes(B, H, Hkv, N, d), dtype=torch.uint8, device=q.device)
+        fa_span_fwd(q, k, v, key_begin, key_end, o, lse, workspace, scale, causal=causal, window=window, cap=cap,
+                    slopes=slopes, stream=stream)
+    if check_status:
+        _checked(stream, q.device, "span_attention_forward")
+    return o, lse
+
+
+def span_attention_backward(q, k, v, o, dout, lse, scale: float, key_begin=None, key_end=None, causal: bool = False,
+                            window: int = 0, cap: float = 0.0, slopes=None, workspace=None, stream=None,
+                            check_status: bool = True):
+    B, H, N, d = _shape4(q, "q")
+    _, Hkv, _, _ = _shape4(k, "k")
+    with _allocating(stream, q.device) as used:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        used(dq, dk, dv)
+        if workspace is None:
+            workspace = torch.empty(fa_span_bwd_workspace_bytes(B, H, Hkv, N, d), dtype=torch.uint8, device=q.device)
+        fa_span_bwd(q, k, v, key_begin, key_end, o, dout, lse, dq, dk, dv, workspace, scale, causal=causal,
+                    window=window, cap=cap, slopes=slopes, stream=stream)
+    if check_status:
+        _checked(stream, q.device, "span_attention_backward")
+    return dq, dk, dv
+
+
+def paged_attention_forward(q, k_pages, v_pages, page_table, cache_lens, scale: float, chunk_lens=None,
+                            window: int = 0, cap: float = 0.0, slopes=None, workspace=None, stream=None,
+                            check_status: bool = True):
+    """Rows of tokens that a request does not have come out as O = 0, LSE = -inf."""
+    B, H, T, d = _shape4(q, "q")
+    _, Hkv, size, _ = _shape4(k_pages, "k_pages")
+    with _allocating(stream, q.device) as used:
+        o = torch.zeros_like(q)
+        lse = torch.full((B, H, T), -math.inf, dtype=torch.float32, device=q.device)
+        used(o, lse)
+        if workspace is None:
+            n = fa_paged_fwd_workspace_bytes(B, H, Hkv, T, page_table.shape[-1] * size, d)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        fa_paged_fwd(q, k_pages, v_pages, page_table, cache_lens, chunk_lens, o, lse, workspace, scale, window=window,
+                     cap=cap, slopes=slopes, stream=stream)
+    if check_status:
+        _checked(stream, q.device, "paged_attention_forward")
     return o, lse

@@ -379,6 +379,130 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
                       int rotary_dim, int norm, float eps, float factor, int interleaved, cudaStream_t stream);
 
 /*
+ * Self-attention in which every query sees the keys of one span:
+ *   O = softmax(s) V,  s_ij = cap tanh(scale q_i . k_j / cap) - slope_h |i - j|
+ * over the keys j with key_begin_i <= j < key_end_i, j <= i (causal = 1) and
+ * |i - j| < window (window > 0).  Without a cap (0) the first term is scale
+ * q_i . k_j, without slopes there is no second one.  Packed documents are the
+ * spans from a document's first token to behind its last one, with causal = 1;
+ * a prefix that is seen both ways is key_end_i = max(i + 1, prefix) with
+ * causal = 0; padding has empty spans.
+ * Query head h uses key/value head h / (H / Hkv); H is a multiple of Hkv.
+ * Scores (the tanh included), probabilities and their sums are fp32; P is
+ * rounded to bf16 for P V, O once at the end.
+ *
+ *   q, o, lse    as for fa_fwd;  k, v  in: bf16 [B][Hkv][N][d]
+ *   key_begin, key_end  in: int32 [B][N], or null: 0 and N.  (Values outside
+ *                [0, N] are taken as 0 and N.)
+ *   slopes       in:  fp32 [H], or null
+ *   o, lse       rows that see no key give O = 0 and LSE = -inf
+ *   cap          finite, >= 0 (2 scale / cap finite);  window >= 0
+ *   workspace    as for fa_cross_fwd, of fa_span_fwd_workspace_bytes()
+ * Scores of pairs outside the spans have no effect, whatever they are.  Rows of V
+ * meet the queries of their tile with weight 0 where they are not seen, so a row
+ * of V with an infinity or NaN may make any row of O of its request and head NaN.
+ * Blocks of 128 keys that no query of a tile of 128 sees are left out.
+ * Limits: those of fa_fwd for H and Hkv heads.  The results are the same from run
+ * to run.
+ */
+size_t fa_span_fwd_workspace_bytes(int B, int H, int Hkv, int N, int d);
+fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
+                      const float* slopes, void* o, float* lse, void* workspace, size_t ws_bytes, int B, int H, int Hkv,
+                      int N, int d, float scale, float cap, int window, int causal, cudaStream_t stream);
+
+/*
+ * Backward pass of fa_span_fwd by recomputation: P = exp(s - LSE), dV = P^T dO,
+ * dS = P o (dO V^T - rowsum(dO o O)) o (1 - tanh^2), dQ = scale dS K,
+ * dK = scale dS^T Q, dK and dV summed over the query heads that share them.  The
+ * cap and the slopes are constants: they have no gradients here.
+ *
+ *   q, o, dout, lse  in:  as for fa_span_fwd; o and lse as it wrote them
+ *   dq               out: bf16 [B][H][N][d];  dk, dv  out: bf16 [B][Hkv][N][d]
+ *   workspace        as for fa_span_fwd, of fa_span_bwd_workspace_bytes()
+ * Rows that see no key have no gradient, keys that no query sees gradients of 0.
+ * Q, K, V and dO meet products with weight 0 where a pair is not seen: an infinity
+ * or NaN in any row of them may make any gradient of its request NaN.
+ * dQ is summed with fp32 atomics, so it is not bitwise repeatable from run to
+ * run; dK and dV are.
+ */
+size_t fa_span_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d);
+fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
+                      const float* slopes, const void* o, const void* dout, const float* lse, void* dq, void* dk,
+                      void* dv, void* workspace, size_t ws_bytes, int B, int H, int Hkv, int N, int d, float scale,
+                      float cap, int window, int causal, cudaStream_t stream);
+
+/*
+ * Keys or values of a cache in pages of page_size tokens: the d values of token t
+ * of a page and head start at ptr + page page + head head + t token (elements;
+ * every stride positive and a multiple of 8, ptr on a 16-byte boundary; strides of
+ * dimensions of size 1 are not used).  Both [page][head][token][d] and
+ * [page][token][head][d] are such caches, and so is one half of a cache that keeps
+ * keys and values side by side.
+ */
+typedef struct {
+  void* ptr;
+  long long page, head, token;
+} fa_pages;
+
+/*
+ * Attention of a chunk of up to T new tokens per request (one token or thousands)
+ * over a cache in pages that already holds them.  Request b has cache_lens[b]
+ * tokens from before; new token n is at position p = cache_lens[b] + n and sees the
+ * positions j <= p, with a window > 0 those with p - j < window.  Position j of
+ * request b is row j % page_size of page page_table[b][j / page_size].  Scores as
+ * for fa_span_fwd: cap tanh(scale q . k / cap) - slope_h (p - j).
+ *
+ *   q            in:  bf16 [B][H][T][d]
+ *   k_pages, v_pages  in: num_pages pages of bf16 rows
+ *   page_table   in:  int32 [B][table_width]; entries of pages that hold no token
+ *                which a query sees are never used.  A page may be in many
+ *                requests.  Numbers outside [0, num_pages) are pages of zeros.
+ *   cache_lens   in:  int32 [B] (taken into [0, C], C = table_width * page_size)
+ *   chunk_lens   in:  int32 [B], or null: request b has chunk_lens[b] <= T new
+ *                tokens, else T; never more than fit in C
+ *   slopes       in:  fp32 [H], or null
+ *   o, lse       out: as for fa_cross_fwd; rows of tokens >= the request's number
+ *                of new ones are left as they were
+ *   page_size    a power of two, at least 16 (others: FA_ERR_UNSUPPORTED)
+ *   workspace    as for fa_cross_fwd, of fa_paged_fwd_workspace_bytes()
+ * What the pages hold behind a request's last new token is never used.  The values
+ * of a chunk's tokens meet the rows of the tokens before them with weight 0, so a
+ * row of V with an infinity or NaN may make any row of O of its request and head
+ * NaN.  The results are the same from run to run.
+ * Limits: those of fa_cross_fwd with T for Nq and C for Nk.
+ */
+size_t fa_paged_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d);
+fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v_pages, const int* page_table,
+                       const int* cache_lens, const int* chunk_lens, const float* slopes, void* o, float* lse,
+                       void* workspace, size_t ws_bytes, int B, int H, int Hkv, int T, int d, int num_pages,
+                       int page_size, int table_width, float scale, float cap, int window, cudaStream_t stream);
+
+/*
+ * fa_rope_fwd for a cache in pages: the rotated keys and the values of new token n
+ * of request b go to position cache_lens[b] + n of its pages (as fa_paged_fwd reads
+ * them), the rotated queries to q_out.
+ *
+ *   q, k, v, q_weight, k_weight, inv_freq, q_out, rotary_dim, norm, eps, factor,
+ *   interleaved  as for fa_rope_fwd
+ *   positions    in:  int32 [B][N], or null: cache_lens[b] + n
+ *   page_table, cache_lens, chunk_lens  as for fa_paged_fwd; page_table and
+ *                cache_lens may be null where k and v are left out (cache_lens
+ *                then counts as 0)
+ *   k_pages, v_pages  out: pages whose rows share no memory.  Rows of positions
+ *                outside [0, C) and of pages outside [0, num_pages) are not
+ *                written; rows of tokens >= the request's number of new ones are
+ *                left as they were, in q_out too.  Where two tokens go to the same
+ *                row, which of them it holds is not said.
+ * No input may overlap an output.
+ */
+fa_status fa_rope_paged_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const float* q_weight,
+                            const float* k_weight, const double* inv_freq, const int* positions,
+                            const int* page_table, const int* cache_lens, const int* chunk_lens, void* q_out,
+                            const fa_pages* k_pages, const fa_pages* v_pages, int B, int N, int H, int Hkv, int d,
+                            int num_pages, int page_size, int table_width, int rotary_dim, int norm, float eps,
+                            float factor, int interleaved, cudaStream_t stream);
+
+/*
  * The entry points above from fa_cross_fwd on, with their arguments in one
  * struct (in the same order and with the same meaning), for callers whose
  * foreign function interface pays for every argument, as the Python binding's
@@ -449,11 +573,71 @@ typedef struct {
   cudaStream_t stream;
 } fa_rope_bwd_args;
 
+typedef struct {
+  const void *q, *k, *v;
+  const int *key_begin, *key_end;
+  const float* slopes;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, N, d;
+  float scale, cap;
+  int window, causal;
+  cudaStream_t stream;
+} fa_span_fwd_args;
+
+typedef struct {
+  const void *q, *k, *v;
+  const int *key_begin, *key_end;
+  const float* slopes;
+  const void *o, *dout;
+  const float* lse;
+  void *dq, *dk, *dv, *workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, N, d;
+  float scale, cap;
+  int window, causal;
+  cudaStream_t stream;
+} fa_span_bwd_args;
+
+typedef struct {
+  const void* q;
+  fa_pages k_pages, v_pages;
+  const int *page_table, *cache_lens, *chunk_lens;
+  const float* slopes;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  int B, H, Hkv, T, d, num_pages, page_size, table_width;
+  float scale, cap;
+  int window;
+  cudaStream_t stream;
+} fa_paged_fwd_args;
+
+typedef struct {
+  fa_rows q, k, v;
+  const float *q_weight, *k_weight;
+  const double* inv_freq;
+  const int *positions, *page_table, *cache_lens, *chunk_lens;
+  void* q_out;
+  fa_pages k_pages, v_pages;
+  int B, N, H, Hkv, d, num_pages, page_size, table_width, rotary_dim, norm;
+  float eps, factor;
+  int interleaved;
+  cudaStream_t stream;
+} fa_rope_paged_fwd_args;
+
 fa_status fa_cross_fwd_packed(const fa_cross_fwd_args* args);
 fa_status fa_cross_bwd_packed(const fa_cross_bwd_args* args);
 fa_status fa_tree_fwd_packed(const fa_tree_fwd_args* args);
 fa_status fa_rope_fwd_packed(const fa_rope_fwd_args* args);
 fa_status fa_rope_bwd_packed(const fa_rope_bwd_args* args);
+fa_status fa_span_fwd_packed(const fa_span_fwd_args* args);
+fa_status fa_span_bwd_packed(const fa_span_bwd_args* args);
+fa_status fa_paged_fwd_packed(const fa_paged_fwd_args* args);
+fa_status fa_rope_paged_fwd_packed(const fa_rope_paged_fwd_args* args);
 
 /*
  * Synchronizes `stream`, then returns and clears the current device's status
@@ -475,7 +659,7 @@ void fa_set_wait_limit_ns(unsigned long long limit_ns);
 /*
  * Test hook for the timeout path.  While `enable` is nonzero, every kernel
  * launched by fa_fwd / fa_bwd (and the main kernels of fa_cross_fwd,
- * fa_cross_bwd and fa_tree_fwd) first makes its MMA-issuing thread wait on a
+ * fa_cross_bwd, fa_tree_fwd, fa_span_fwd, fa_span_bwd and fa_paged_fwd) first makes its MMA-issuing thread wait on a
  * barrier that nothing ever signals; that wait runs out after the wait limit
  * (fa_set_wait_limit_ns), the kernel reports FA_ERR_TIMEOUT, drains the copies
  * it started and returns.  The outputs of the call are then undefined, as after
