@@ -48,20 +48,125 @@ struct PageRows {
   long long page, head, token;  // strides in elements
 };
 
-// one pair's score in log2 units, and d score / d (scale q k)
-struct SpanScore {
-  float scale, cap, inv_cap;  // cap 0: none
-  const float* slopes;        // [H] or nullptr
-  __device__ __forceinline__ float operator()(float qk, float slope, int far, float* bent) const {
-    float s = qk * scale;
-    *bent = 1.f;
-    if (cap > 0.f) {
-      const float t = tanhf(s * inv_cap);
-      *bent = 1.f - t * t;
-      s = t * cap;
+// The keys that the rows of a tile of 128 see between them, [lo, hi), and where all of
+// its rows see all keys: blocks from lo_cut on that end at hi_cut at the latest.
+struct SpanTile {
+  int lo, hi, lo_cut, hi_cut;
+  __device__ __forceinline__ bool empty() const { return lo >= hi; }
+};
+
+// Query rows are numbered in units: a query head's N rows, or (pages) the G N rows of
+// the heads that share a key/value head.
+struct SpanRows {
+  SpanView view;
+  const int4* bounds;  // [B][tiles] SpanTile, or nullptr: the mask is a formula of the position
+  int R, tiles;        // rows of a unit, and tiles of 128 of them
+  int units, kv_div;   // units of a request; of a key/value head
+  __device__ __forceinline__ SpanTile tile(int b, int t) const {
+    if (bounds) {
+      const int4 x = bounds[(long long)b * tiles + t];
+      return {x.x, x.y, x.z, x.w};
     }
-    return s - slope * (float)far;
+    // the tokens of the tile: of one head, or of several
+    const int row0 = t * 128, row1 = min(row0 + 127, R - 1), N = view.N;
+    int t0 = row0, t1 = row1;
+    if (R != N) {
+      const int h0 = row0 / N, h1 = row1 / N;
+      t0 = h0 == h1 ? row0 - h0 * N : 0;
+      t1 = h0 == h1 ? row1 - h0 * N : N - 1;
+    }
+    const int len = view.len(b);
+    t1 = min(t1, view.rows(b, len) - 1);
+    if (t0 > t1) return {0, 0, 0x7fffffff, 0};
+    SpanTile s{0, view.C, 0, view.C};
+    view.clip(len + t0, len + t1, s.lo, s.hi);
+    int other = view.C;
+    view.clip(len + t1, len + t1, s.lo_cut, other);
+    other = 0;
+    view.clip(len + t0, len + t0, other, s.hi_cut);
+    return s;
   }
 };
+
+// Bounds of the tiles where the spans are given by row; block (t, b), a thread per row.
+__device__ __forceinline__ SpanTile span_tile_reduce(int lo, int hi, bool row, int4* scratch) {
+  const bool live = row && lo < hi;
+  SpanTile s{live ? lo : 0x7fffffff, live ? hi : 0, row ? (live ? lo : 0x7fffffff) : 0,
+             row ? (live ? hi : 0) : 0x7fffffff};
+  s.lo = __reduce_min_sync(0xffffffffu, s.lo);
+  s.hi = __reduce_max_sync(0xffffffffu, s.hi);
+  s.lo_cut = __reduce_max_sync(0xffffffffu, s.lo_cut);
+  s.hi_cut = __reduce_min_sync(0xffffffffu, s.hi_cut);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = make_int4(s.lo, s.hi, s.lo_cut, s.hi_cut);
+  __syncthreads();
+  for (int w = 0; w < 4; ++w) {
+    const int4 x = scratch[w];
+    s = {min(s.lo, x.x), max(s.hi, x.y), max(s.lo_cut, x.z), min(s.hi_cut, x.w)};
+  }
+  if (s.lo >= s.hi) s.lo = s.hi = 0;
+  return s;
+}
+
+__global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, int4* bounds) {
+  __shared__ int4 scratch[4];
+  grid_wait();
+  grid_trigger();
+  const int i = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
+  int lo = 0, hi = 0;
+  if (i < v.N) v.span(b, i, i, lo, hi);
+  const SpanTile s = span_tile_reduce(lo, hi, i < v.N, scratch);
+  if (threadIdx.x == 0) bounds[(long long)b * gridDim.x + blockIdx.x] = make_int4(s.lo, s.hi, s.lo_cut, s.hi_cut);
+}
+
+// The cap in log2 units, cap log2(e) tanh(y / 2) for y = 2 scale q k / cap.
+//
+// Within |y| < 2 it is y G(y^2) with the minimax polynomial of tanh(sqrt u) / sqrt u
+// on [0, 1] (Remez exchange on the relative error: 5e-8), scaled; beyond it
+// 1 - 2 / (1 + e^y), whose absolute error (2^-22) is what counts there.  Whether any
+// of a warp's y is 2 or more in magnitude is one bit of their OR: bit 30.
+struct SpanCap {
+  float mul;      // 2 scale / cap
+  float top;      // cap log2(e)
+  float c[7];     // y (c[0] + c[1] y^2 + ...)
+};
+
+__device__ __forceinline__ float span_cap_any(float y, float top) {
+  const float e = ex2_approx(y * 1.4426950408889634f);
+  return top - __fdividef(2.f * top, e + 1.f);
+}
+
+__device__ __forceinline__ float2 span_cap_near(float2 y, const SpanCap& c) {
+  const float2 u = __fmul2_rn(y, y);
+  float2 g = __ffma2_rn(u, make_float2(c.c[6], c.c[6]), make_float2(c.c[5], c.c[5]));
+#pragma unroll
+  for (int i = 4; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.c[i], c.c[i]));
+  return __fmul2_rn(y, g);
+}
+
+// 32 products of one row, in place
+__device__ __forceinline__ void span_cap32(uint32_t (&x)[32], const SpanCap& c, bool near) {
+  const float2 mul = make_float2(c.mul, c.mul);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), mul);
+    const float2 s = near ? span_cap_near(y, c) : make_float2(span_cap_any(y.x, c.top), span_cap_any(y.y, c.top));
+    x[2 * i] = __float_as_uint(s.x);
+    x[2 * i + 1] = __float_as_uint(s.y);
+  }
+}
+
+// whether all products of a warp's rows (those that count) stay in the polynomial's range (|y| < 2)
+template <int n>
+__device__ __forceinline__ bool span_cap_all_near(const uint32_t (&x)[n][32], float mul, bool counts) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < n; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), make_float2(mul, mul));
+      any |= __float_as_uint(y.x) | __float_as_uint(y.y);
+    }
+  return __all_sync(0xffffffffu, !counts || !(any & 0x40000000u));
+}
 
 }  // namespace fa

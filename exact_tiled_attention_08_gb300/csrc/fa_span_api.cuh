@@ -38,7 +38,7 @@ fa_status check_span_args(float scale, float cap, int window, int causal) {
   fa_status st = check_scale(scale, causal);
   if (st != FA_OK) return st;
   if (!std::isfinite(cap) || cap < 0.f || window < 0) return FA_ERR_INVALID_ARG;
-  if (cap > 0.f && !std::isfinite(2.f * scale / cap)) return FA_ERR_INVALID_ARG;
+  if (cap > 0.f && (!std::isnormal(2.f * scale / cap) || !std::isfinite(2.f * cap))) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -52,12 +52,163 @@ fa::PageRows page_rows(const fa_pages* r) {
   return {static_cast<__nv_bfloat16*>(r->ptr), r->page, r->head, r->token};
 }
 
+// keys or values as a 4-D tensor (d, tokens, heads, pages) for boxes of 64 x box_rows,
+// 128-byte swizzle; what lies outside reads as zero
+bool encode_pages(CUtensorMap* map, const fa::PageRows& r, int tokens, int heads, int pages, int box_rows, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)tokens, (cuuint64_t)heads, (cuuint64_t)pages};
+  // (the stride of a dimension of one is not used, but looked at)
+  auto bytes = [&](long long stride, int size) { return (cuuint64_t)(size > 1 ? stride : d) * 2; };
+  const cuuint64_t strides[3] = {bytes(r.token, tokens), bytes(r.head, heads), bytes(r.page, pages)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r.ptr, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// tanh(sqrt u) / sqrt u on [0, 1]: minimax polynomial of degree 6 (Remez exchange), relative error 5e-8
+constexpr double kTanhPoly[7] = {0.9999999502407381,   -0.3333283915308157, 0.13325204075948163,  -0.05345702957318134,
+                                 0.02028998043217086, -0.0062033791124837, 0.0010410226362182575};
+
+fa::SpanCap span_cap(float scale, float cap) {
+  fa::SpanCap c{};
+  if (cap == 0.f) return c;
+  c.mul = 2.f * scale / cap;
+  c.top = cap * 1.4426950408889634f;
+  double f = 0.5 * 1.4426950408889634 * cap;
+  for (int i = 0; i < 7; ++i, f *= 0.25) c.c[i] = (float)(f * kTanhPoly[i]);
+  return c;
+}
+
+// Grid and workspace of the forward, as CrossFwdPlan; with spans by row their tiles' bounds first.
+struct SpanFwdPlan {
+  int tiles, row_tiles, part_rows, ctas;
+  bool pair, cuts;
+  size_t meta_at, lse_at, o_at, total;
+  static SpanFwdPlan of(int B, int units, int R, int C, int d, bool bounds) {
+    SpanFwdPlan w;
+    w.tiles = (R + 127) / 128;
+    w.pair = R > 128;
+    w.row_tiles = w.pair ? (w.tiles + 1) / 2 : 1;
+    w.part_rows = w.pair ? 256 : R;
+    const long long blocks = (long long)B * units * w.row_tiles * ((C + 127LL) / 128 + fa::kCrossStart);
+    w.ctas = (int)std::min<long long>(blocks, fa::kCrossMaxCtas);
+    w.cuts = C > 128;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t rows = w.cuts ? (size_t)2 * w.ctas * w.part_rows : 0;
+    w.meta_at = bounds ? up((size_t)B * w.tiles * sizeof(int4)) : 0;
+    w.lse_at = w.meta_at + up(w.ctas * sizeof(fa::SpanMeta));
+    w.o_at = w.lse_at + up(rows * sizeof(float));
+    w.total = w.o_at + up(rows * d * sizeof(float)) + 256;  // (the base is brought to a 256-byte boundary)
+    return w;
+  }
+};
+
+template <int D, int MOD, bool PAIR, bool CLUSTER>
+fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams& p, unsigned grid, cudaStream_t stream) {
+  using C = fa::CrossCfg<D>;
+  auto kernel = fa::fa_span_fwd_kernel<D, MOD, PAIR, CLUSTER>;
+  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  static std::atomic<unsigned long long> known{0};
+  if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
+  return launch_early_clusters(kernel, dim3(grid), CLUSTER ? p.cluster : 1, C::kThreads, C::kSmemBytes, stream, maps[0],
+                               maps[1], maps[2], p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+template <int D, int MOD>
+fa_status launch_span_form(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
+                           cudaStream_t stream) {
+  if (p.cluster > 1) return launch_span_fwd<D, MOD, false, true>(maps, p, grid, stream);
+  return pair ? launch_span_fwd<D, MOD, true, false>(maps, p, grid, stream)
+              : launch_span_fwd<D, MOD, false, false>(maps, p, grid, stream);
+}
+
+template <int D>
+fa_status launch_span_mod(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
+                          cudaStream_t stream) {
+  if (p.cap.top > 0.f) return launch_span_form<D, 2>(maps, p, pair, grid, stream);
+  return p.slopes ? launch_span_form<D, 1>(maps, p, pair, grid, stream)
+                  : launch_span_form<D, 0>(maps, p, pair, grid, stream);
+}
+
+struct SpanCall {
+  fa::SpanRows rows;
+  const void* q;
+  fa::PageRows k, v;
+  int box_rows, tokens, pages;  // of the key and value tensors
+  void* o;
+  float* lse;
+  void* workspace;
+  int B, H, Hkv, d;
+  float scale, cap;
+  const float* slopes;
+  cudaStream_t stream;
+};
+
+fa_status run_span_fwd(const SpanCall& a) {
+  const fa::SpanView& view = a.rows.view;
+  const bool by_row = view.begin || view.end;
+  const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.rows.units, a.rows.R, view.C, a.d, !view.table);
+  CUtensorMap maps[3];
+  if (!encode_bhnd(&maps[0], a.q, a.B * a.rows.units, a.rows.R, a.d) ||
+      !encode_pages(&maps[1], a.k, a.tokens, a.Hkv, a.pages, a.box_rows, a.d) ||
+      !encode_pages(&maps[2], a.v, a.tokens, a.Hkv, a.pages, a.box_rows, a.d))
+    return FA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return FA_ERR_CUDA;
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
+  fa::SpanFwdParams p{};
+  p.rows = a.rows;
+  p.rows.tiles = plan.tiles;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.meta = reinterpret_cast<fa::SpanMeta*>(ws + plan.meta_at);
+  p.part_lse = reinterpret_cast<float*>(ws + plan.lse_at);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_at);
+  p.part_rows = plan.part_rows;
+  p.B = a.B;
+  p.H = a.H;
+  p.row_tiles = plan.row_tiles;
+  p.pages = a.pages;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.cap = span_cap(a.scale, a.cap);
+  p.slopes = a.slopes;
+  p.wait_limit_ns = wait_limit_ns();
+  p.debug_stall = g_debug_stall.load();
+  p.o_align32 = aligned32(a.o);
+  p.cluster = 1;
+  if (by_row) {
+    int4* bounds = reinterpret_cast<int4*>(ws);
+    p.rows.bounds = bounds;
+    if (launch_early(fa::fa_span_bounds_kernel, dim3((unsigned)plan.tiles, (unsigned)a.B), 128, 0, a.stream, view,
+                     bounds) != cudaSuccess)
+      return FA_ERR_CUDA;
+  }
+  const unsigned grid = (unsigned)std::min(plan.ctas, sms);
+  const fa_status st = a.d == 128 ? launch_span_mod<128>(maps, p, plan.pair, grid, a.stream)
+                                  : launch_span_mod<64>(maps, p, plan.pair, grid, a.stream);
+  if (st != FA_OK || !plan.cuts) return st;
+  const int per_block = plan.pair ? 32 : 8;  // rows of a block
+  const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
+  auto combine = a.d == 128 ? (plan.pair ? fa::fa_span_combine_kernel<128, true> : fa::fa_span_combine_kernel<128, false>)
+                            : (plan.pair ? fa::fa_span_combine_kernel<64, true> : fa::fa_span_combine_kernel<64, false>);
+  return launch_early(combine, parts, 256, 0, a.stream, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t fa_span_fwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
-  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? 256 : 0;
+  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanFwdPlan::of(B, H, N, N, d, true).total : 0;
 }
 
 fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
@@ -72,14 +223,18 @@ fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* ke
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, lse, workspace})) != FA_OK) return st;
   if ((st = check_device_ptrs_given({key_begin, key_end, slopes})) != FA_OK) return st;
-  fa::SpanRowsParams p{};
-  p.view = {key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
-  p.score = {scale, cap, cap > 0.f ? 1.f / cap : 0.f, slopes};
-  p.q = static_cast<const __nv_bfloat16*>(q), p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v), p.out = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse, p.B = B, p.H = H, p.Hkv = Hkv;
-  d == 128 ? fa::span_rows_fwd<128><<<152 * 8, 256, 0, stream>>>(p) : fa::span_rows_fwd<64><<<152 * 8, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  SpanCall a{};
+  a.rows.view = {key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
+  a.rows.R = N;
+  a.rows.units = H;
+  a.rows.kv_div = H / Hkv;
+  a.q = q;
+  a.k = {static_cast<__nv_bfloat16*>(const_cast<void*>(k)), (long long)Hkv * N * d, (long long)N * d, d};
+  a.v = {static_cast<__nv_bfloat16*>(const_cast<void*>(v)), (long long)Hkv * N * d, (long long)N * d, d};
+  a.box_rows = 128, a.tokens = N, a.pages = B;
+  a.o = o, a.lse = lse, a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.d = d, a.scale = scale, a.cap = cap, a.slopes = slopes, a.stream = stream;
+  return run_span_fwd(a);
 }
 
 size_t fa_span_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
@@ -113,7 +268,7 @@ fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* ke
 
 size_t fa_paged_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d) {
   int R;
-  return check_cross_shape(B, H, Hkv, T, C, d, &R) == FA_OK ? 256 : 0;
+  return check_cross_shape(B, H, Hkv, T, C, d, &R) == FA_OK ? SpanFwdPlan::of(B, Hkv, R, C, d, false).total : 0;
 }
 
 fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v_pages, const int* page_table,
@@ -135,15 +290,18 @@ fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v
   if ((st = check_device_ptrs({q, k_pages->ptr, v_pages->ptr, page_table, cache_lens, o, lse, workspace})) != FA_OK)
     return st;
   if ((st = check_device_ptrs_given({chunk_lens, slopes})) != FA_OK) return st;
-  fa::SpanRowsParams p{};
-  p.view = {nullptr, nullptr, cache_lens, chunk_lens, page_table, table_width, pages.shift(), T,
-            (int)pages.capacity(), 1, window};
-  p.score = {scale, cap, cap > 0.f ? 1.f / cap : 0.f, slopes};
-  p.q = static_cast<const __nv_bfloat16*>(q), p.out = static_cast<__nv_bfloat16*>(o);
-  p.kp = page_rows(k_pages), p.vp = page_rows(v_pages);
-  p.lse = lse, p.B = B, p.H = H, p.Hkv = Hkv, p.pages = num_pages;
-  d == 128 ? fa::span_rows_fwd<128><<<152 * 8, 256, 0, stream>>>(p) : fa::span_rows_fwd<64><<<152 * 8, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  SpanCall a{};
+  a.rows.view = {nullptr, nullptr, cache_lens, chunk_lens, page_table, table_width, pages.shift(), T,
+                 (int)pages.capacity(), 1, window};
+  a.rows.R = R;
+  a.rows.units = Hkv;
+  a.rows.kv_div = 1;
+  a.q = q;
+  a.k = page_rows(k_pages), a.v = page_rows(v_pages);
+  a.box_rows = std::min(page_size, 128), a.tokens = page_size, a.pages = num_pages;
+  a.o = o, a.lse = lse, a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.d = d, a.scale = scale, a.cap = cap, a.slopes = slopes, a.stream = stream;
+  return run_span_fwd(a);
 }
 
 fa_status fa_span_fwd_packed(const fa_span_fwd_args* a) {

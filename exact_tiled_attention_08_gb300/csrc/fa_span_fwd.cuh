@@ -1,0 +1,946 @@
+// Forward kernel of attention to spans of keys, over contiguous keys (fa_span_fwd) or
+// a cache in pages (fa_paged_fwd).
+//
+// The arithmetic, the roles and the pipeline are those of fa_cross_fwd_kernel (TMA
+// fills a ring of K and V tiles, one thread issues S = Q K^T, one O += P V, two softmax
+// warpgroups hold a row of scores per thread; two row tiles per item, PAIR, or one
+// whose key blocks go to the warpgroups in turn, ALT; clusters for a few items of
+// one tile).  What differs:
+//
+// Work.  An item is a tile (pair) of query rows of a unit (SpanRows) with the blocks of
+// 128 keys that any of its rows sees; items cost what they have of them.  Where enough of them
+// are there, CTA c takes the items c, c + G, ... whole, a request's last row tiles (with
+// a causal mask the longest) of all heads first; otherwise the CTAs take even shares of all
+// items' blocks, and fa_span_combine_kernel joins the items that shares cut.  Within an item
+// each row tile takes only the blocks that it sees something of.
+//
+// Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
+// (MOD 2) and the bias (MOD 1 and 2) change the scores in registers, before the maximum.
+//
+// Pages.  A tile of 128 keys is 128 / page_size boxes, one per lane of the loading
+// warp, from where the page table says; pages that no row sees, and those outside the
+// pool, are asked for at a coordinate outside the tensor, which the TMA fills with zeros
+// without reading.
+//
+// Keys of an item's first and last block that none of its rows sees may hold
+// anything: their scores become -inf and warp 11 zeroes their rows of V.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "fa_cross_fwd.cuh"
+#include "fa_span.cuh"
+
+namespace fa {
+
+struct SpanMeta {     // of each CTA, for the combine kernel
+  int split;          // its last item goes on in the next CTA
+  int b, u, row0;     // that item
+  long long last;     // the place behind the item's last block
+  long long total;    // places of the sequence
+};
+
+struct SpanFwdParams {
+  SpanRows rows;
+  __nv_bfloat16* o;
+  float* lse;
+  SpanMeta* meta;    // [grid]
+  float* part_lse;   // [2 grid][part_rows], base 2
+  float* part_o;     // [2 grid][part_rows][d]
+  int part_rows;     // rows of a part: 256 (PAIR) or R (ALT)
+  int B, H;
+  int row_tiles;     // row tiles (PAIR: pairs of them) per unit
+  int cluster;       // CLUSTER: CTAs per item
+  int pages;         // pages in the pool
+  float scale_log2;  // without a cap
+  SpanCap cap;
+  const float* slopes;  // [H] or nullptr
+  uint64_t wait_limit_ns;
+  int debug_stall;
+  int o_align32;
+};
+
+// A CTA's work: whole items k, k + G, ... or a run of places of the sequence of all items.
+struct SpanPlace {
+  int e, u;   // entry (request and row tile) and unit of it
+  int j;      // place in the item (shares)
+  int left;   // places (shares) or items (whole) from there on
+  int whole;  // items to the next one's number; 0: shares
+};
+
+// A run of key blocks of one item; blocks are counted from key 0.
+struct SpanSeg {
+  int b, u, row0;
+  bool two;            // PAIR: there is a second row tile
+  bool first, last;    // the item's first and last block are in it
+  int j0, j1, rest;    // blocks; the item's blocks behind them
+  int lo, hi;          // keys that the item's rows see
+  int a0[2], a1[2];    // PAIR: the blocks of each row tile
+};
+
+template <bool PAIR>
+struct SpanItem {
+  SpanTile t[PAIR ? 2 : 1];
+  int lo, hi, base, n;  // keys seen; first block and number of blocks (at least one, so that rows without keys are written)
+  __device__ __forceinline__ SpanItem(const SpanFwdParams& p, int e) {
+    const int b = e / p.row_tiles, rt = p.row_tiles - 1 - (e - b * p.row_tiles);
+    t[0] = p.rows.tile(b, PAIR ? 2 * rt : rt);
+    lo = t[0].lo, hi = t[0].hi;
+    if constexpr (PAIR) {
+      t[1] = 2 * rt + 1 < p.rows.tiles ? p.rows.tile(b, 2 * rt + 1) : SpanTile{0, 0, 0x7fffffff, 0};
+      if (t[0].empty()) lo = t[1].lo, hi = t[1].hi;
+      else if (!t[1].empty()) lo = min(lo, t[1].lo), hi = max(hi, t[1].hi);
+    }
+    base = lo >> 7;
+    n = max(((hi + 127) >> 7) - base, 1);
+  }
+};
+
+// Items and places beside an item's blocks as in fa_cross_fwd.cuh.
+template <bool PAIR>
+__device__ __forceinline__ bool span_next(const SpanFwdParams& p, SpanPlace& at, SpanSeg& s) {
+  while (at.left > 0) {
+    const SpanItem<PAIR> item(p, at.e);
+    s.b = at.e / p.row_tiles;
+    const int rt = p.row_tiles - 1 - (at.e - s.b * p.row_tiles);
+    s.row0 = rt * (PAIR ? 256 : 128);
+    s.two = PAIR && s.row0 + 128 < p.rows.R;
+    s.u = at.u;
+    s.lo = item.lo, s.hi = item.hi;
+    const int end_block = item.base + item.n;
+    if (at.whole) {
+      s.j0 = item.base, s.j1 = end_block;
+      --at.left;
+      const int k = at.e * p.rows.units + at.u + at.whole;
+      at.e = k / p.rows.units;
+      at.u = k - at.e * p.rows.units;
+    } else {
+      const int places = item.n + kCrossStart, end = min(places, at.j + min(at.left, places));
+      s.j0 = item.base + max(at.j - kCrossStart, 0);
+      s.j1 = item.base + end - kCrossStart;
+      at.left -= end - at.j;
+      at.j = end;
+      if (end == places) {
+        at.j = 0;
+        if (++at.u == p.rows.units) at.u = 0, ++at.e;
+      }
+      if (s.j1 <= item.base) continue;  // only places before the item's blocks
+    }
+    s.first = s.j0 == item.base;
+    s.last = s.j1 == end_block;
+    s.rest = end_block - s.j1;
+    if constexpr (PAIR) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s.a0[t] = max(s.j0, item.t[t].lo >> 7);
+        s.a1[t] = min(s.j1, (item.t[t].hi + 127) >> 7);
+        // a tile that sees nothing here takes one block, whose keys are all masked
+        if (s.a0[t] >= s.a1[t]) s.a0[t] = s.j0, s.a1[t] = s.j0 + 1;
+      }
+    }
+    return true;
+  }
+  return false;
+}
+
+// keys of a block that no row of the item sees: below `from`, from `to` on
+__device__ __forceinline__ bool span_dirty(const SpanFwdParams& p, const SpanSeg& s, int j, int& from, int& to) {
+  from = max(s.lo - j * 128, 0);
+  to = max(min(s.hi - j * 128, 128), 0);
+  // (past the keys of a contiguous tensor the TMA has filled zeros)
+  const int filled = p.rows.view.table ? 128 : min(p.rows.view.C - j * 128, 128);
+  return from > 0 || to < filled;
+}
+
+// How the CTAs divide the items, by all 384 threads.  `scratch`: 1 KB of shared memory.
+// Up to kSpanRounds items a CTA the slowest CTA's whole items are added up; more of
+// them even out.
+constexpr int kSpanRounds = 32;
+template <bool PAIR>
+__device__ __forceinline__ void span_schedule(const SpanFwdParams& p, float* scratch, SpanPlace* place, long long* all,
+                                              long long* share_end) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = 384;
+  const int E = p.B * p.row_tiles, U = p.rows.units, G = gridDim.x, c = blockIdx.x;
+  const long long count = (long long)E * U;
+  const int whole_items = c < count ? (int)((count - c + G - 1) / G) : 0;
+  if (count > (long long)kSpanRounds * G) {
+    if (tid == 0) *place = SpanPlace{c / U, c % U, 0, whole_items, G};
+    return;
+  }
+  auto cost = [&](int e) { return SpanItem<PAIR>(p, e).n + kCrossStart; };
+  int* sums = reinterpret_cast<int*>(scratch);  // [G] places of each CTA's whole items
+  long long* part = reinterpret_cast<long long*>(scratch + 160);
+  static_assert(kCrossMaxCtas <= 160, "a sum for each CTA");
+  if (tid < G) sums[tid] = 0;
+  if (tid == 0) *place = SpanPlace{0, 0, 0, 0, 0};
+  __syncthreads();
+  const int chunk = (E + T - 1) / T, e0 = min(E, tid * chunk), e1 = min(E, e0 + chunk);
+  long long mine = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int n = cost(e);
+    mine += n;
+    for (int k = e * U; k < e * U + U; ++k) atomicAdd(&sums[k % G], n);
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long add = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += add;
+  }
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  long long total = 0, before = 0;
+  for (int w = 0; w < 12; ++w) {
+    if (w == warp) before = total;
+    total += part[w];
+  }
+  total *= U;
+  int lead = 0;
+  for (int i = lane; i < G; i += 32) lead = max(lead, sums[i]);
+  lead = __reduce_max_sync(0xffffffffu, lead);
+  // Whole items where the slowest CTA ends no later than even shares and the join of
+  // what they cut.
+  if ((long long)(lead - kCrossCut) * G <= total) {
+    if (tid == 0) *place = SpanPlace{c / U, c % U, 0, whole_items, G};
+    return;
+  }
+  const long long g = min((long long)G, total);
+  if (c >= g) return;
+  const long long start = c * total / g, end = (c + 1) * total / g;
+  if (tid == 0) *all = total, *share_end = end;
+  long long at = (before + upto - mine) * U;
+  if (start < at || start >= (before + upto) * U) return;
+  for (int e = e0; e < e1; ++e) {
+    const int n = cost(e);
+    if (start < at + (long long)n * U) {
+      const long long off = start - at;
+      const int u = (int)(off / n);
+      *place = SpanPlace{e, u, (int)(off - (long long)u * n), (int)(end - start), 0};
+      return;
+    }
+    at += (long long)n * U;
+  }
+}
+
+// The share of a cluster's item, by one thread.
+__device__ __forceinline__ void span_cluster_share(const SpanFwdParams& p, SpanPlace* place) {
+  const int k = blockIdx.x / p.cluster, rank = blockIdx.x - k * p.cluster, e = k / p.rows.units;
+  const int n = SpanItem<false>(p, e).n, j0 = rank * n / p.cluster, j1 = (rank + 1) * n / p.cluster;
+  *place = SpanPlace{e, k - e * p.rows.units, j0 + kCrossStart, j1 - j0, 0};
+}
+
+// (as CrossBarriers)
+struct SpanBarriers {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[12], kv_empty[12];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t v_ask, v_clean;
+  uint64_t merge_ready, merge_free;
+  uint64_t drain[2];
+  uint64_t never;
+  SpanPlace place;
+  long long total, end;  // places of the sequence; end of the CTA's share
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(SpanBarriers) <= 512, "barriers overflow their shared-memory slot");
+
+// What a softmax warp needs behind its blocks, kept here while its registers hold scores.
+struct SpanWarp {
+  SpanPlace at;
+  int b, u, row0, j0, j1, flags;
+};
+static_assert(sizeof(SpanWarp) <= 64, "512 bytes for eight warps");
+
+// adds a bias of -slope2 |rel - c| to the scores of keys c of a block (log2 units),
+// after multiplying them with mul; rel: the row's position from the block's first key
+__device__ __forceinline__ void span_bias(uint32_t (&s)[4][32], float mul, float slope2, int rel) {
+  const float relf = (float)rel;
+  const float2 mul2 = make_float2(mul, mul);
+  if (__all_sync(0xffffffffu, rel >= 127 || rel <= 0)) {
+    // all keys on one side of the row: a line
+    const float g = rel > 0 ? slope2 : -slope2, base = -g * relf;
+    const float2 g2 = make_float2(g, g), base2 = make_float2(base, base);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float k = (float)(32 * c + 2 * i);
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), mul2,
+                                    __ffma2_rn(make_float2(k, k + 1.f), g2, base2));
+        s[c][2 * i] = __float_as_uint(x.x);
+        s[c][2 * i + 1] = __float_as_uint(x.y);
+      }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        s[c][i] = __float_as_uint(fmaf(-slope2, fabsf(relf - (float)(32 * c + i)), __uint_as_float(s[c][i]) * mul));
+  }
+}
+
+// PAIR: two row tiles per item.  CLUSTER: a cluster of p.cluster CTAs per item (not with
+// PAIR).  MOD: 0 plain scores, 1 with a bias, 2 capped (and with a bias where there are slopes).
+template <int D, int MOD, bool PAIR, bool CLUSTER>
+__global__ void __launch_bounds__(384, 1)
+    fa_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
+  using C = CrossCfg<D>;
+  static_assert(!(PAIR && CLUSTER), "clusters take one row tile");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
+    grid_wait();
+    if (threadIdx.x == 0) {
+      atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
+      if (!CLUSTER) p.meta[blockIdx.x].split = 0;
+    }
+    return;
+  }
+  uint8_t* smem = smem_raw;
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * C::kTileBytes;
+  float* sMerge = reinterpret_cast<float*>(sKV + C::kSlots * C::kTileBytes);  // [3][128]
+  SpanBarriers* bar = reinterpret_cast<SpanBarriers*>(reinterpret_cast<uint8_t*>(sMerge) + C::kMergeBytes);
+  uint8_t* sWarps = reinterpret_cast<uint8_t*>(bar) + 512;  // SpanWarp of each softmax warp, 64 bytes apart
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const SpanView& v = p.rows.view;
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar->q_full[t], 1);
+      mbar_init(&bar->q_empty[t], 1);
+      mbar_init(&bar->s_full[t], 1);
+      mbar_init(&bar->s_free[t], 128);
+      mbar_init(&bar->p_full[t], 128);
+      mbar_init(&bar->pv_done[t], 1);
+      mbar_init(&bar->drain[t], 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bar->kv_full[s], 1);
+      mbar_init(&bar->kv_empty[s], 1);
+    }
+    mbar_init(&bar->v_clean, 1);
+    mbar_init(&bar->v_ask, 1);
+    mbar_init(&bar->merge_ready, 128);
+    mbar_init(&bar->merge_free, 128);
+    mbar_init(&bar->never, 1);
+    bar->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&bar->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+  }
+  grid_wait();
+  if (CLUSTER) {
+    if (tid < 128) sMerge[tid] = -CUDART_INF_F;  // no part so far
+    if (warp == 10 && lane == 0) span_cluster_share(p, &bar->place);
+  } else {
+    span_schedule<PAIR>(p, sMerge, &bar->place, &bar->total, &bar->end);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_trigger();
+  const uint32_t tmem = bar->tmem_base;
+  const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
+  SpanPlace at = bar->place;  // every role walks the same segments
+  SpanSeg w;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<C::kMiscRegs>();
+    if (warp == 9) {
+      // ------------------------------------------------------------------ TMA producer (a lane per page)
+      const int shift = v.page_shift, box_rows = v.table ? min(1 << shift, 128) : 128;
+      const int boxes = 128 / box_rows;
+      int loads = 0, nq = 0;  // K and V tiles, in turn
+      bool ok = true;
+      // the page of this lane's part of block j, or -1: nothing there that a row sees
+      auto page_of = [&](int j) -> int {
+        if (lane >= boxes) return -1;
+        const int key = j * 128 + lane * box_rows, i = key >> shift;
+        if (key >= w.hi || key + box_rows <= w.lo) return -1;
+        const int page = v.table[(long long)w.b * v.width + i];
+        return page >= 0 && page < p.pages ? page : -1;
+      };
+      auto load_kv = [&](int j, int kv, int kvh, int page) -> bool {
+        const int g = loads >> 1, s = C::slot(kv, g);
+        const CUtensorMap* map = kv ? &map_v : &map_k;
+        if (!__all_sync(0xffffffffu,
+                        wait_bounded_inl(&bar->kv_empty[s], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty)))
+          return false;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[s], C::kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int row = v.table ? (j * 128) & ((1 << shift) - 1) : j * 128;
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_4d(sKV + s * C::kTileBytes + a * 16384 + lane * box_rows * 128, map, &bar->kv_full[s], a * 64,
+                        boxes > 1 ? 0 : row, kvh, v.table ? page : w.b);
+        }
+        ++loads;
+        return true;
+      };
+      while (ok && span_next<PAIR>(p, at, w)) {
+        const int kvh = w.u / p.rows.kv_div, bu = w.b * p.rows.units + w.u;
+        const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+        const int tiles = w.two ? 2 : 1;
+        auto load_q = [&] {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
+            for (int t = 0; t < tiles; ++t)
+              for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
+                            w.row0 + 128 * t, bu);
+          }
+          __syncwarp();
+        };
+        int page = v.table ? page_of(w.j0) : 0;
+        // a later segment's first key block needs only ring slots: it goes out
+        // before the queries, whose buffer an earlier segment may still be reading
+        if (nq == 0) load_q();
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+          const int next = v.table && j + 1 < w.j1 ? page_of(j + 1) : 0;  // (asked for a block ahead)
+          ok = load_kv(j, 0, kvh, page) && load_kv(j, 1, kvh, page);
+          if (ok && j == w.j0 && nq > 0) {
+            if (use > 0) ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->q_empty[qs], (use - 1) & 1, ctx,
+                                                                       kSiteCrossQEmpty));
+            if (ok) load_q();
+          }
+          page = next;
+        }
+        if (ok) ++nq;
+      }
+      // every copy this warp started must land before the CTA can exit
+      if (lane == 0) {
+        for (int s = 0; s < 2; ++s) {
+          const int uses = PAIR ? (s ? 0 : nq) : (nq + 1 - s) >> 1;
+          if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
+        }
+        for (int s = 0; s < C::kSlots; ++s) {
+          // loads into slot s
+          const bool vslot = s >= C::kKSlots;
+          const int n = vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
+          if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // ------------------------------------------------------------------ S issuer
+      // g counts key blocks over all segments
+      if (lane == 0) {
+        const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+        int s_uses[2] = {0, 0}, g = 0, nq = 0;
+        bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
+        while (ok && span_next<PAIR>(p, at, w)) {
+          const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+          if (!wait_bounded_inl(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
+          ++nq;
+          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+            const int ks = C::slot(0, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::use(0, g) & 1, ctx, kSiteCrossK))) break;
+            const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (PAIR ? ((t == 0 || w.two) && j >= w.a0[t] && j < w.a1[t]) : (((j - w.j0) & 1) == t)) {
+                const int sb = C::kDualS ? t : 0;
+                if (s_uses[sb] > 0 && !wait_bounded_inl(&bar->s_free[sb], (s_uses[sb] - 1) & 1, ctx, kSiteCrossSFree)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                const uint64_t qd = sdesc_sw128(sq + (PAIR ? t : qs) * C::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+                  mma_bf16_ss(tmem + (sb ? C::kSCol1 : C::kSCol), qd + off, kdesc + off, id_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&bar->s_full[t]);
+                ++s_uses[sb];
+              }
+            }
+            if (!ok) break;
+            mma_commit(&bar->kv_empty[ks]);
+          }
+          if (!ok) break;
+          mma_commit(&bar->q_empty[qs]);  // the segment's queries have been read
+        }
+        mma_commit(&bar->drain[0]);
+        wait_drain_inl(&bar->drain[0], 0, kDrainLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ------------------------------------------------------------------ P V issuer
+      // O_t += P_t(j) V_j once the softmax of tile t wrote P_t(j)
+      if (lane == 0) {
+        const uint32_t skv = smem_u32(sKV);
+        constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+        int g = 0, cleaned = 0;
+        int pv_uses[2] = {0, 0};
+        bool ok = true;
+        while (ok && span_next<PAIR>(p, at, w)) {
+          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+            const int vs = C::slot(1, g);
+            if (!(ok = wait_bounded_inl(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
+            int from, to;
+            bool clean = !span_dirty(p, w, j, from, to);
+            if (!clean) mbar_arrive(&bar->v_ask);
+            const uint64_t vdesc = sdesc_sw128(skv + vs * C::kTileBytes, 16384, 1024);
+            auto cleaned_now = [&] {
+              if (!clean) clean = wait_bounded_inl(&bar->v_clean, cleaned++ & 1, ctx, kSiteCrossClean);
+              return clean;
+            };
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (PAIR ? ((t == 0 || w.two) && j >= w.a0[t] && j < w.a1[t]) : (((j - w.j0) & 1) == t)) {
+                if (!wait_bounded_inl(&bar->p_full[t], pv_uses[t] & 1, ctx, kSiteCrossP) || !cleaned_now()) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                const bool add = j > (PAIR ? w.a0[t] : w.j0 + 1);  // not the tile's first block of the segment
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_bf16_ts(tmem + (t ? C::kOCol1 : C::kOCol0), tmem + (t ? C::kPCol1 : C::kPCol0) + kk * 8,
+                              vdesc + (uint32_t)((kk * 2048) >> 4), id_pv, (add || kk > 0) ? 1u : 0u);
+                mma_commit(&bar->pv_done[t]);
+                ++pv_uses[t];
+              }
+            }
+            ok = ok && cleaned_now();
+            if (!ok) break;
+            mma_commit(&bar->kv_empty[vs]);
+          }
+        }
+        mma_commit(&bar->drain[1]);
+        wait_drain_inl(&bar->drain[1], 0, kDrainLimitNs);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ warp 11: rows of V that nobody sees
+      int g = 0, cleaned = 0;
+      bool ok = true;
+      SpanMeta meta{};
+      while (ok && span_next<PAIR>(p, at, w)) {
+        for (int j = w.j0; ok && j < w.j1; j = j + 1 < w.j1 - 1 ? w.j1 - 1 : j + 1) {  // (its first and its last block)
+          int from, to;
+          if (!span_dirty(p, w, j, from, to)) continue;
+          ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
+          if (!ok) break;
+          ++cleaned;
+          uint8_t* tile = sKV + C::slot(1, g + j - w.j0) * C::kTileBytes;
+          for (int a = 0; a < C::kAtoms; ++a) {
+            for (int c = lane; c < from * 8; c += 32)
+              *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = max(from, to) * 8 + lane; c < 128 * 8; c += 32)
+              *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->v_clean);
+        }
+        g += w.j1 - w.j0;
+        if (w.first && !w.last) {
+          // (the CTA's last segment: the item's other blocks follow its share)
+          meta.split = 1;
+          meta.b = w.b;
+          meta.u = w.u;
+          meta.row0 = w.row0;
+          meta.last = bar->end + w.rest;
+          meta.total = bar->total;
+        }
+      }
+      if (!ok) meta.split = 0;
+      if (!CLUSTER && lane == 0) p.meta[blockIdx.x] = meta;
+    }
+  } else {
+    setmaxnreg_inc<C::kSoftRegs>();
+    // ------------------------------------------------------------------ softmax warpgroups
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + ((C::kDualS && t) ? C::kSCol1 : C::kSCol) + lane_off;
+    const uint32_t tP = tmem + (t ? C::kPCol1 : C::kPCol0) + lane_off;
+    const uint32_t tO = tmem + (t ? C::kOCol1 : C::kOCol0) + lane_off;
+    const float cj = MOD == 0 ? p.scale_log2 : 1.f;  // (with MOD the scores are in log2 units)
+    int uses = 0;    // blocks this tile has processed over all segments
+    int merges = 0;  // ALT: segments whose two accumulators were joined
+    bool alive = true;
+    // (volatile: read again after the segment's blocks, not kept in registers)
+    volatile SpanWarp* mine = reinterpret_cast<volatile SpanWarp*>(sWarps + 64 * warp);
+    auto store_place = [&] {
+      mine->at.e = at.e, mine->at.u = at.u, mine->at.j = at.j, mine->at.left = at.left, mine->at.whole = at.whole;
+    };
+    if (lane == 0) store_place();
+    __syncwarp();
+    // CLUSTER: this CTA's part of the item, in the ring's memory once the ring has
+    // been read: rows of D + 4 floats (so that a warp's rows spread over the banks);
+    // its log-sum-exps at sMerge
+    float* sPart = reinterpret_cast<float*>(sKV);
+    while (alive) {
+      at.e = mine->at.e, at.u = mine->at.u, at.j = mine->at.j, at.left = mine->at.left, at.whole = mine->at.whole;
+      if (!span_next<PAIR>(p, at, w)) break;
+      int jfirst, j1, row_lo, row_hi, pos;
+      int lo_cut = 0, hi_cut = 0;  // blocks that all rows of the tile see whole
+      float slope2 = 0.f;
+      bool there = true;  // the row is written
+      {
+        __syncwarp();
+        if (lane == 0) {
+          store_place();
+          mine->b = w.b, mine->u = w.u, mine->row0 = w.row0, mine->j0 = w.j0, mine->j1 = w.j1;
+          mine->flags = (w.first ? 1 : 0) | (w.last ? 2 : 0);
+        }
+        __syncwarp();
+        // nothing for this tile
+        if (PAIR ? (t == 1 && !w.two) : (t == 1 && w.j1 - w.j0 < 2)) continue;
+        jfirst = PAIR ? w.a0[t] : w.j0 + t;
+        j1 = PAIR ? w.a1[t] : w.j1;
+        const SpanTile tile = p.rows.tile(w.b, w.row0 / 128 + (PAIR ? t : 0));
+        lo_cut = tile.lo_cut, hi_cut = tile.hi_cut;
+        const int row = min(w.row0 + (PAIR ? 128 * t : 0) + r, p.rows.R - 1), head = row / v.N, tok = row - head * v.N;
+        pos = v.len(w.b) + tok;
+        v.span(w.b, tok, pos, row_lo, row_hi);
+        if (MOD == 2) there = tok < v.rows(w.b, v.len(w.b));
+        if (MOD > 0 && p.slopes) slope2 = p.slopes[w.u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
+      }
+      float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
+      // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
+      // block's largest one, so that l + lcorr normalises O (see fa_fwd_kernel)
+      float l = 0.f, lcorr = 0.f;
+      for (int j = jfirst; j < j1; j += PAIR ? 1 : 2, ++uses) {
+        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+        // the scores are in registers: the next scores may now overwrite S
+        tc_fence_before();
+        mbar_arrive(&bar->s_free[C::kDualS ? t : 0]);
+
+        const int kbase = j * 128;
+        const bool cut = kbase < lo_cut || kbase + 128 > hi_cut;
+        auto hide = [&](float value) {
+          const int from = row_lo - kbase, to = row_hi - kbase;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < from || c >= to) sr[c >> 5][c & 31] = __float_as_uint(value);
+        };
+        if constexpr (MOD == 2) {
+          if (cut) hide(0.f);  // (what is not seen has no say in how the others are capped)
+          const bool near = span_cap_all_near(sr, p.cap.mul, there);
+          if (near) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, true);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, false);
+          }
+          if (p.slopes) span_bias(sr, 1.f, slope2, pos - kbase);
+        }
+        if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase);
+        if (cut) hide(-CUDART_INF_F);
+        const float mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
+        const float m_new = fmaxf(m, mx * cj);
+        // conditional rescale: the reference moves only when the row maximum
+        // rose by more than the threshold (always from -inf: no key so far)
+        float alpha = 1.f;
+        bool rescale_warp = false;
+        if (j == jfirst) {
+          m = m_new;
+        } else {
+          const bool need = (m_new - m) > kRescaleThresholdLog2;
+          rescale_warp = __any_sync(0xffffffffu, need);
+          if (need) {
+            alpha = ex2_approx(m - m_new);
+            m = m_new;
+          }
+        }
+        const float ref = fmaxf(m, -3.402823466e38f);  // (finite for a row without keys so far: every P is 2^-inf = 0)
+        const float2 c2 = make_float2(cj, cj);
+        const float2 mneg2 = make_float2(-ref, -ref);
+        float2 acc[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
+        {
+          const float pbm = ex2_approx(fmaf(mx, cj, -ref));
+          const float pbm_r = __uint_as_float(pack_bf16x2(pbm, 0.f) << 16);
+          lcorr = lcorr * alpha + (pbm_r - pbm);
+        }
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 s2 = make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1]));
+            const float2 x = MOD == 0 ? __ffma2_rn(s2, c2, mneg2) : __fadd2_rn(s2, mneg2);
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            pk[c][i] = pack_bf16x2(p0, p1);
+            acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+          }
+        }
+        const float2 accs = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        l = l * alpha + (accs.x + accs.y);
+        // P_t and O_t are in use until the tile's previous product has completed
+        // (a segment's first block: its predecessor's epilogue has waited for
+        // it; ALT: O_1 also until warpgroup 0 has read it)
+        if (j > jfirst) {
+          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+        } else if (!PAIR && t == 1 && merges > 0) {
+          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_free, (merges - 1) & 1, ctx, kSiteCrossMerge))) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        if (rescale_warp) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + 32 * c, ov);
+            tmem_wait_ld();
+            reg_fence32(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(tO + 32 * c, ov);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(tP + 16 * c, pk[c]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[t]);
+      }
+      if (!alive) break;
+      if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      // ---- end of the segment
+      w.b = mine->b, w.u = mine->u, w.row0 = mine->row0, w.j0 = mine->j0, w.j1 = mine->j1;
+      const int flags = mine->flags;
+      const bool seg_first = flags & 1, whole = flags == 3;
+      const int row = w.row0 + (PAIR ? 128 * t : 0) + r;
+      const bool join = !PAIR && w.j1 - w.j0 >= 2;
+      float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
+      if (join) {
+        if (t == 1) {
+          sMerge[r] = m;
+          sMerge[128 + r] = l;
+          sMerge[256 + r] = lo;
+          tc_fence_before();
+          mbar_arrive(&bar->merge_ready);
+          ++merges;
+          continue;
+        }
+        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_ready, merges & 1, ctx, kSiteCrossMerge))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        ++merges;
+        const float m1 = sMerge[r], mm = fmaxf(m, m1), ref = mm == -CUDART_INF_F ? 0.f : mm;
+        a0 = ex2_approx(m - ref);
+        a1 = ex2_approx(m1 - ref);
+        l = l * a0 + sMerge[128 + r] * a1;
+        lo = lo * a0 + sMerge[256 + r] * a1;
+        m = mm;
+      }
+      const float inv = lo == 0.f ? 0.f : 1.f / lo;
+      a0 *= inv;
+      a1 *= inv;
+      const float lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+      const bool write = row < p.rows.R && row % v.N < v.rows(w.b, v.len(w.b));
+      const size_t grow = ((size_t)w.b * p.rows.units + w.u) * p.rows.R + row;
+      const size_t prow = ((size_t)2 * blockIdx.x + (seg_first ? 1 : 0)) * p.part_rows + (PAIR ? 128 * t : 0) + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32], ow[32];
+        tmem_ld32(tO + 32 * c, ov);
+        if (join) tmem_ld32(tmem + C::kOCol1 + lane_off + 32 * c, ow);
+        tmem_wait_ld();
+        reg_fence32(ov);
+        if (join) {
+          reg_fence32(ow);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = __float_as_uint(fmaf(__uint_as_float(ow[i]), a1, __uint_as_float(ov[i]) * a0));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a0);
+        }
+        if (join && c == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&bar->merge_free);
+        }
+        if (CLUSTER) {
+          if (write)
+#pragma unroll
+            for (int v4 = 0; v4 < 8; ++v4)
+              reinterpret_cast<uint4*>(sPart + r * (D + 4) + 32 * c)[v4] =
+                  make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+        } else if (write && whole) {
+          __nv_bfloat16* orow = p.o + grow * D + 32 * c;
+          uint32_t w16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w16[e] = pack_bf16x2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
+          if (p.o_align32) {
+            st_global_v8(orow, w16);
+            st_global_v8(orow + 16, w16 + 8);
+          } else {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4)
+              reinterpret_cast<uint4*>(orow)[v4] =
+                  make_uint4(w16[4 * v4], w16[4 * v4 + 1], w16[4 * v4 + 2], w16[4 * v4 + 3]);
+          }
+        } else if (write) {
+          float* prow_o = p.part_o + prow * D + 32 * c;
+#pragma unroll
+          for (int v8 = 0; v8 < 4; ++v8) st_global_v8(prow_o + 8 * v8, ov + 8 * v8);
+        }
+        __syncwarp();  // the next tensor memory load is a whole warp's
+      }
+      if (CLUSTER) {
+        sMerge[r] = write ? lse2 : -CUDART_INF_F;
+      } else if (write) {
+        if (whole)
+          p.lse[grow] = lse2 * 0.6931471805599453f;
+        else
+          p.part_lse[prow] = lse2;
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if constexpr (CLUSTER) {
+    // every CTA of the cluster writes every p.cluster-th row, a warp per row
+    cluster_sync();
+    constexpr int E = D / 32, kMost = 8;
+    const int ctas = p.cluster, item = blockIdx.x / ctas, b = item / p.rows.units;
+    const int fresh = v.rows(b, v.len(b));
+    const float* parts = reinterpret_cast<const float*>(sKV) + lane * E;
+    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.R; row += ctas * (C::kThreads / 32)) {
+      if (row % v.N >= fresh) continue;
+      float l[kMost], o[kMost][E], mx = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas) {
+          l[i] = cluster_load(sMerge + row, i);
+          cluster_load<E>(parts + row * (D + 4), i, o[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas) mx = fmaxf(mx, l[i]);
+      const float ref = fmaxf(mx, -3.402823466e38f);
+      float sum = 0.f, acc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i)
+        if (i < ctas && l[i] != -CUDART_INF_F) {  // (a part without keys was not written)
+          const float wt = ex2_approx(l[i] - ref);
+          sum += wt;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
+        }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t grow = (size_t)item * p.rows.R + row;  // (one row tile per unit)
+      uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+    }
+    cluster_sync();  // the others have read this CTA's part
+  }
+}
+
+// Joins the parts of the items that share ends cut: block x takes the item that
+// begins in CTA x's share and goes on behind it, kRows rows per warp.  O = sum of
+// the parts' O weighted by 2^(their LSE - the largest), in CTA order.
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_constant__ SpanFwdParams p) {
+  constexpr int E = D / 32;
+  constexpr int kRows = PAIR ? 4 : 1;  // rows of a warp
+  constexpr int kBatch = 8;            // parts whose loads are in flight together
+  grid_wait();
+  grid_trigger();
+  const SpanMeta meta = p.meta[blockIdx.x];
+  if (!meta.split) return;
+  const SpanView& v = p.rows.view;
+  const int parts = (int)((meta.last * min((long long)gridDim.x, meta.total) - 1) / meta.total) - (int)blockIdx.x + 1;
+  const int lane = threadIdx.x & 31, local0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
+  const int fresh = v.rows(meta.b, v.len(meta.b));
+  const size_t grow0 = ((size_t)meta.b * p.rows.units + meta.u) * p.rows.R + meta.row0 + local0;
+  // part i: the last segment of CTA x, then the first of each CTA after it
+  auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local0; };
+  for (int r = 0; r < kRows; ++r) {
+    const int row = meta.row0 + local0 + r;
+    if (local0 + r >= p.part_rows || row >= p.rows.R || row % v.N >= fresh) continue;
+    float acc[E], sum = 0.f, ref = -CUDART_INF_F;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += kBatch) {
+      float l[kBatch], o[kBatch][E];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        l[u] = -CUDART_INF_F;
+        if (i0 + u < parts) {
+          l[u] = p.part_lse[part(i0 + u) + r];
+          cross_join_load<E>(p.part_o + (part(i0 + u) + r) * D + lane * E, o[u]);
+        }
+      }
+      float mx = ref;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, l[u]);
+      // finite where no part so far has a key; `ref` stays -inf there, so that parts
+      // of any low log-sum-exp count
+      const float safe = fmaxf(mx, -3.402823466e38f);
+      const float alpha = ex2_approx(ref - safe);
+      ref = mx;
+      sum *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i0 + u < parts) {
+          const float wt = ex2_approx(l[u] - safe);
+          sum += wt;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[u][e], acc[e]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + (grow0 + r) * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) p.lse[grow0 + r] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace fa

@@ -8,6 +8,22 @@
 
 namespace fa {
 
+// one pair's score, and d score / d (scale q k)
+struct SpanScore {
+  float scale, cap, inv_cap;  // cap 0: none
+  const float* slopes;        // [H] or nullptr
+  __device__ __forceinline__ float operator()(float qk, float slope, int far, float* bent) const {
+    float s = qk * scale;
+    *bent = 1.f;
+    if (cap > 0.f) {
+      const float t = tanhf(s * inv_cap);
+      *bent = 1.f - t * t;
+      s = t * cap;
+    }
+    return s - slope * (float)far;
+  }
+};
+
 struct SpanRowsParams {
   SpanView view;
   SpanScore score;
