@@ -118,55 +118,79 @@ __global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, i
   if (threadIdx.x == 0) bounds[(long long)b * gridDim.x + blockIdx.x] = make_int4(s.lo, s.hi, s.lo_cut, s.hi_cut);
 }
 
-// The cap in log2 units, cap log2(e) tanh(y / 2) for y = 2 scale q k / cap.
+// The cap in log2 units: cap log2(e) tanh(x), x = scale q k / cap.
 //
-// Within |y| < 2 it is y G(y^2) with the minimax polynomial of tanh(sqrt u) / sqrt u
-// on [0, 1] (Remez exchange on the relative error: 5e-8), scaled; beyond it
-// 1 - 2 / (1 + e^y), whose absolute error (2^-22) is what counts there.  Whether any
-// of a warp's y is 2 or more in magnitude is one bit of their OR: bit 30.
+// Within |x| <= 3/4 it is x G(x^2) with the minimax polynomial of tanh(sqrt u) / sqrt u on
+// [0, 9/16] (degree 5, by Remez exchange on the relative error: 3e-8), scaled; beyond it
+// 1 - 2 / (1 + e^2x), whose absolute error (2^-22) is what counts there.  Within |x| <= 3/8 a
+// polynomial of degree 3 (1.3e-8) does, in the products themselves.  A warp takes
+// the cheapest that all of its products of the block allow.
 struct SpanCap {
-  float mul;      // 2 scale / cap
-  float top;      // cap log2(e)
-  float c[7];     // y (c[0] + c[1] y^2 + ...)
+  float mul;    // scale / cap
+  float small;  // products up to there take the short polynomial: 3/8 cap / scale
+  float near;   // the long one: 3/4 cap / scale
+  float top;    // cap log2(e)
+  float c[6];   // x (c[0] + c[1] x^2 + ...)
+  float d[4];   // q k (d[0] + d[1] (q k)^2 + ...)
 };
 
-__device__ __forceinline__ float span_cap_any(float y, float top) {
-  const float e = ex2_approx(y * 1.4426950408889634f);
-  return top - __fdividef(2.f * top, e + 1.f);
+// score / product of small products
+__device__ __forceinline__ float2 span_cap_small(float2 s, const SpanCap& c) {
+  const float2 u = __fmul2_rn(s, s);
+  float2 g = __ffma2_rn(u, make_float2(c.d[3], c.d[3]), make_float2(c.d[2], c.d[2]));
+#pragma unroll
+  for (int i = 1; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.d[i], c.d[i]));
+  return g;
 }
 
-__device__ __forceinline__ float2 span_cap_near(float2 y, const SpanCap& c) {
-  const float2 u = __fmul2_rn(y, y);
-  float2 g = __ffma2_rn(u, make_float2(c.c[6], c.c[6]), make_float2(c.c[5], c.c[5]));
+__device__ __forceinline__ float span_cap_any(float x, float top) {
+  const float e = ex2_approx(x * 2.8853900817779268f);
+  return top - __fdividef(2.f * top, e + 1.f);  // (a divisor beyond 2^126 gives 0)
+}
+
+__device__ __forceinline__ float2 span_cap_near(float2 x, const SpanCap& c) {
+  const float2 u = __fmul2_rn(x, x);
+  float2 g = __ffma2_rn(u, make_float2(c.c[5], c.c[5]), make_float2(c.c[4], c.c[4]));
 #pragma unroll
-  for (int i = 4; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.c[i], c.c[i]));
-  return __fmul2_rn(y, g);
+  for (int i = 3; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.c[i], c.c[i]));
+  return __fmul2_rn(x, g);
 }
 
 // 32 products of one row, in place
-__device__ __forceinline__ void span_cap32(uint32_t (&x)[32], const SpanCap& c, bool near) {
+__device__ __forceinline__ void span_cap32(uint32_t (&s)[32], const SpanCap& c, bool near) {
   const float2 mul = make_float2(c.mul, c.mul);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), mul);
-    const float2 s = near ? span_cap_near(y, c) : make_float2(span_cap_any(y.x, c.top), span_cap_any(y.y, c.top));
-    x[2 * i] = __float_as_uint(s.x);
-    x[2 * i + 1] = __float_as_uint(s.y);
+    const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul);
+    const float2 y = near ? span_cap_near(x, c) : make_float2(span_cap_any(x.x, c.top), span_cap_any(x.y, c.top));
+    s[2 * i] = __float_as_uint(y.x);
+    s[2 * i + 1] = __float_as_uint(y.y);
   }
 }
 
-// whether all products of a warp's rows (those that count) stay in the polynomial's range (|y| < 2)
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// the largest magnitude of 32 n products: eight running maxima
 template <int n>
-__device__ __forceinline__ bool span_cap_all_near(const uint32_t (&x)[n][32], float mul, bool counts) {
-  uint32_t any = 0;
+__device__ __forceinline__ float span_absmax(const uint32_t (&x)[n][32]) {
+  float m[8];
 #pragma unroll
-  for (int c = 0; c < n; ++c)
+  for (int a = 0; a < 8; ++a) m[a] = fabsf(__uint_as_float(x[0][a]));
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 y = __fmul2_rn(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), make_float2(mul, mul));
-      any |= __float_as_uint(y.x) | __float_as_uint(y.y);
+  for (int i = 8; i + 16 <= 32 * n; i += 16)
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      const int e = i + 2 * a;
+      m[a] = absmax3(m[a], __uint_as_float(x[e >> 5][e & 31]), __uint_as_float(x[(e + 1) >> 5][(e + 1) & 31]));
     }
-  return __all_sync(0xffffffffu, !counts || !(any & 0x40000000u));
+  // (8 mod 16: the last eight)
+#pragma unroll
+  for (int a = 0; a < 8; ++a) m[a] = fmaxf(m[a], fabsf(__uint_as_float(x[n - 1][24 + a])));
+  return fmaxf(max3(m[0], m[1], m[2]), max3(max3(m[3], m[4], m[5]), m[6], m[7]));
 }
 
 }  // namespace fa

@@ -38,7 +38,7 @@ fa_status check_span_args(float scale, float cap, int window, int causal) {
   fa_status st = check_scale(scale, causal);
   if (st != FA_OK) return st;
   if (!std::isfinite(cap) || cap < 0.f || window < 0) return FA_ERR_INVALID_ARG;
-  if (cap > 0.f && (!std::isnormal(2.f * scale / cap) || !std::isfinite(2.f * cap))) return FA_ERR_INVALID_ARG;
+  if (cap > 0.f && (!std::isnormal(scale / cap) || !std::isfinite(2.f * cap))) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -68,17 +68,25 @@ bool encode_pages(CUtensorMap* map, const fa::PageRows& r, int tokens, int heads
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// tanh(sqrt u) / sqrt u on [0, 1]: minimax polynomial of degree 6 (Remez exchange), relative error 5e-8
-constexpr double kTanhPoly[7] = {0.9999999502407381,   -0.3333283915308157, 0.13325204075948163,  -0.05345702957318134,
-                                 0.02028998043217086, -0.0062033791124837, 0.0010410226362182575};
+// tanh(sqrt u) / sqrt u on [0, 9/16]: minimax polynomial of degree 5 (Remez exchange), relative error 2.9e-8
+constexpr double kTanhPoly[6] = {0.9999999710138949,   -0.33332958879477204, 0.13325406017696445,
+                                 -0.05334443014377955, 0.019582908187949204, -0.004716257251378197};
+
+// the same on [0, 9/64], of degree 3: 5.9e-8
+constexpr double kTanhShort[4] = {0.9999999405367285, -0.3333197482128287, 0.13284502145788482, -0.048272262378324014};
 
 fa::SpanCap span_cap(float scale, float cap) {
   fa::SpanCap c{};
   if (cap == 0.f) return c;
-  c.mul = 2.f * scale / cap;
-  c.top = cap * 1.4426950408889634f;
-  double f = 0.5 * 1.4426950408889634 * cap;
-  for (int i = 0; i < 7; ++i, f *= 0.25) c.c[i] = (float)(f * kTanhPoly[i]);
+  const double x = (double)scale / cap, top = 1.4426950408889634 * cap;
+  c.mul = scale / cap;
+  c.near = 0.75f * cap / scale;
+  c.top = (float)top;
+  for (int i = 0; i < 6; ++i) c.c[i] = (float)(top * kTanhPoly[i]);
+  for (int i = 0; i < 4; ++i) c.d[i] = (float)(top * kTanhShort[i] * std::pow(x, 2 * i + 1));
+  // (where fp32 does not hold these no product is small)
+  const bool held = std::isnormal(c.d[3]) && std::isnormal(c.d[2]) && std::isnormal(c.d[1]) && std::isnormal(c.d[0]);
+  c.small = held ? 0.375f * cap / scale : -1.f;
   return c;
 }
 
@@ -132,7 +140,9 @@ fa_status launch_span_form(const CUtensorMap* maps, const fa::SpanFwdParams& p, 
 template <int D>
 fa_status launch_span_mod(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
                           cudaStream_t stream) {
-  if (p.cap.top > 0.f) return launch_span_form<D, 2>(maps, p, pair, grid, stream);
+  if (p.cap.top > 0.f)
+    return p.slopes ? launch_span_form<D, 3>(maps, p, pair, grid, stream)
+                    : launch_span_form<D, 2>(maps, p, pair, grid, stream);
   return p.slopes ? launch_span_form<D, 1>(maps, p, pair, grid, stream)
                   : launch_span_form<D, 0>(maps, p, pair, grid, stream);
 }

@@ -9,10 +9,9 @@
 //
 // Work.  An item is a tile (pair) of query rows of a unit (SpanRows) with the blocks of
 // 128 keys that any of its rows sees; items cost what they have of them.  Where enough of them
-// are there, CTA c takes the items c, c + G, ... whole, a request's last row tiles (with
-// a causal mask the longest) of all heads first; otherwise the CTAs take even shares of all
-// items' blocks, and fa_span_combine_kernel joins the items that shares cut.  Within an item
-// each row tile takes only the blocks that it sees something of.
+// are there, the CTAs take whole items (the longest first, or head by head); otherwise even
+// shares of all items' blocks, and fa_span_combine_kernel joins the items that shares cut.
+// Within an item each row tile takes only the blocks that it sees something of.
 //
 // Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
 // (MOD 2) and the bias (MOD 1 and 2) change the scores in registers, before the maximum.
@@ -28,6 +27,8 @@
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "fa_cross_fwd.cuh"
 #include "fa_span.cuh"
@@ -61,23 +62,35 @@ struct SpanFwdParams {
   int o_align32;
 };
 
-// A CTA's work: whole items k, k + G, ... or a run of places of the sequence of all items.
+// A CTA's work: whole items, one of each round of G ranks (rank k G + c in even rounds k, k G +
+// G - 1 - c in odd ones, so that what the first gets more of evens out), or a share of places.
+enum : int { kSpanShares, kSpanSorted, kSpanByHead, kSpanByEntry };
 struct SpanPlace {
-  int e, u;   // entry (request and row tile) and unit of it
-  int j;      // place in the item (shares)
-  int left;   // places (shares) or items (whole) from there on
-  int whole;  // items to the next one's number; 0: shares
+  int e, u;   // shares: entry (request and row tile) and unit of it; whole: e is the rank
+  int j;      // shares: place in the item; whole: the round
+  int left;   // places or items from there on
+  int mode;   // kSpanShares: places; how ranks are numbered otherwise
 };
+__device__ __forceinline__ long long span_rank(int round, int G, int c) {
+  return (long long)round * G + (round & 1 ? G - 1 - c : c);
+}
 
-// A run of key blocks of one item; blocks are counted from key 0.
+// A run of key blocks of one item; blocks are counted from key 0.  The loading warp works the
+// segments out and leaves them in shared memory, where the other warps read them.  (Each warp
+// working them out for itself takes 20 KB more of code, and the loops of the kernel no
+// longer fit the instruction cache.)
+enum : int { kSegFirst = 1, kSegLast = 2, kSegTwo = 4, kSegDirtyFront = 8, kSegDirtyBack = 16, kSegEnd = 32 };
 struct SpanSeg {
   int b, u, row0;
-  bool two;            // PAIR: there is a second row tile
-  bool first, last;    // the item's first and last block are in it
+  int flags;           // the item's first and last block are in it; PAIR: there is a second row tile;
+                       // rows of V in block j0 and j1 - 1 that nobody sees; no more segments
   int j0, j1, rest;    // blocks; the item's blocks behind them
   int lo, hi;          // keys that the item's rows see
   int a0[2], a1[2];    // PAIR: the blocks of each row tile
+  int lo_cut[2], hi_cut[2];  // of each row tile: see SpanTile
 };
+constexpr int kSpanSegs = 4;  // segments in shared memory
+enum : int { kSiteSpanSeg = 70, kSiteSpanSegFree };
 
 template <bool PAIR>
 struct SpanItem {
@@ -97,24 +110,34 @@ struct SpanItem {
   }
 };
 
-// Items and places beside an item's blocks as in fa_cross_fwd.cuh.
+// The next segment.  Ranks are numbered by entry (with `order`: entries by falling cost), all
+// units of one after another, or head by head (all row tiles of a unit one after another, whose
+// keys the CTAs of a round then share in L2).  Places beside an item's blocks as in fa_cross_fwd.cuh.
 template <bool PAIR>
-__device__ __forceinline__ bool span_next(const SpanFwdParams& p, SpanPlace& at, SpanSeg& s) {
+__device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t* order, SpanPlace& at, SpanSeg& s) {
+  const int U = p.rows.units;
   while (at.left > 0) {
-    const SpanItem<PAIR> item(p, at.e);
-    s.b = at.e / p.row_tiles;
-    const int rt = p.row_tiles - 1 - (at.e - s.b * p.row_tiles);
-    s.row0 = rt * (PAIR ? 256 : 128);
-    s.two = PAIR && s.row0 + 128 < p.rows.R;
+    int e = at.e;
     s.u = at.u;
+    if (at.mode == kSpanByHead) {
+      const int head = at.e / p.row_tiles, b = head / U;
+      s.u = head - b * U;
+      e = b * p.row_tiles + (at.e - head * p.row_tiles);
+    } else if (at.mode != kSpanShares) {
+      e = at.e / U;
+      s.u = at.e - e * U;
+      if (PAIR && at.mode == kSpanSorted) e = order[e];
+    }
+    const SpanItem<PAIR> item(p, e);
+    s.b = e / p.row_tiles;
+    const int rt = p.row_tiles - 1 - (e - s.b * p.row_tiles);
+    s.row0 = rt * (PAIR ? 256 : 128);
     s.lo = item.lo, s.hi = item.hi;
     const int end_block = item.base + item.n;
-    if (at.whole) {
+    if (at.mode != kSpanShares) {
       s.j0 = item.base, s.j1 = end_block;
       --at.left;
-      const int k = at.e * p.rows.units + at.u + at.whole;
-      at.e = k / p.rows.units;
-      at.u = k - at.e * p.rows.units;
+      at.e = (int)span_rank(++at.j, gridDim.x, blockIdx.x);
     } else {
       const int places = item.n + kCrossStart, end = min(places, at.j + min(at.left, places));
       s.j0 = item.base + max(at.j - kCrossStart, 0);
@@ -123,103 +146,158 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, SpanPlace& at,
       at.j = end;
       if (end == places) {
         at.j = 0;
-        if (++at.u == p.rows.units) at.u = 0, ++at.e;
+        if (++at.u == U) at.u = 0, ++at.e;
       }
       if (s.j1 <= item.base) continue;  // only places before the item's blocks
     }
-    s.first = s.j0 == item.base;
-    s.last = s.j1 == end_block;
     s.rest = end_block - s.j1;
-    if constexpr (PAIR) {
+    s.flags = (s.j0 == item.base ? kSegFirst : 0) | (s.rest == 0 ? kSegLast : 0) |
+              (PAIR && s.row0 + 128 < p.rows.R ? kSegTwo : 0);
+    // (past the keys of a contiguous tensor the TMA has filled zeros)
+    const int filled = p.rows.view.table ? s.j1 * 128 : min(p.rows.view.C, s.j1 * 128);
+    if (s.lo > s.j0 * 128 || (s.j1 == s.j0 + 1 && s.hi < filled)) s.flags |= kSegDirtyFront;
+    if (s.hi < filled || (s.j1 == s.j0 + 1 && s.lo > s.j0 * 128)) s.flags |= kSegDirtyBack;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s.a0[t] = max(s.j0, item.t[t].lo >> 7);
-        s.a1[t] = min(s.j1, (item.t[t].hi + 127) >> 7);
-        // a tile that sees nothing here takes one block, whose keys are all masked
-        if (s.a0[t] >= s.a1[t]) s.a0[t] = s.j0, s.a1[t] = s.j0 + 1;
-      }
+    for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
+      s.lo_cut[t] = item.t[t].lo_cut, s.hi_cut[t] = item.t[t].hi_cut;
+      s.a0[t] = max(s.j0, item.t[t].lo >> 7);
+      s.a1[t] = min(s.j1, (item.t[t].hi + 127) >> 7);
+      // a tile that sees nothing here takes one block, whose keys are all masked
+      if (s.a0[t] >= s.a1[t]) s.a0[t] = s.j0, s.a1[t] = s.j0 + 1;
     }
     return true;
   }
   return false;
 }
 
-// keys of a block that no row of the item sees: below `from`, from `to` on
-__device__ __forceinline__ bool span_dirty(const SpanFwdParams& p, const SpanSeg& s, int j, int& from, int& to) {
-  from = max(s.lo - j * 128, 0);
-  to = max(min(s.hi - j * 128, 128), 0);
-  // (past the keys of a contiguous tensor the TMA has filled zeros)
-  const int filled = p.rows.view.table ? 128 : min(p.rows.view.C - j * 128, 128);
-  return from > 0 || to < filled;
+// the row tiles (bits) that take block j
+template <bool PAIR>
+__device__ __forceinline__ int span_active(const SpanSeg& s, int j) {
+  if (!PAIR) return 1 << ((j - s.j0) & 1);
+  return (j >= s.a0[0] && j < s.a1[0] ? 1 : 0) | (s.flags & kSegTwo && j >= s.a0[1] && j < s.a1[1] ? 2 : 0);
 }
 
-// How the CTAs divide the items, by all 384 threads.  `scratch`: 1 KB of shared memory.
-// Up to kSpanRounds items a CTA the slowest CTA's whole items are added up; more of
-// them even out.
-constexpr int kSpanRounds = 32;
+// whether block j of the segment has rows of V that no row of the item sees
+__device__ __forceinline__ bool span_dirty(const SpanSeg& s, int j) {
+  return (s.flags & kSegDirtyFront && j == s.j0) || (s.flags & kSegDirtyBack && j == s.j1 - 1);
+}
+
+// How the CTAs divide the items, by all 384 threads.  `scratch` (kMergeBytes of shared memory)
+// keeps the order of the entries with PAIR.  More than kSpanRounds items a CTA even out: they
+// go whole, head by head but where a causal mask alone makes the last row tiles the longest.  Fewer: the slowest CTA's items are added up for each way of
+// numbering them, and the items go whole where that ends no later than even shares and the
+// join of what they cut.
+constexpr int kSpanRounds = 32, kSpanThreads = 384;
 template <bool PAIR>
-__device__ __forceinline__ void span_schedule(const SpanFwdParams& p, float* scratch, SpanPlace* place, long long* all,
+__device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scratch, SpanPlace* place, long long* all,
                                               long long* share_end) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = 384;
+  constexpr int T = kSpanThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.row_tiles, U = p.rows.units, G = gridDim.x, c = blockIdx.x;
   const long long count = (long long)E * U;
-  const int whole_items = c < count ? (int)((count - c + G - 1) / G) : 0;
+  auto whole = [&](int mode) {
+    const int rounds = (int)(count / G);
+    if (tid == 0) *place = SpanPlace{c, 0, 0, rounds + (span_rank(rounds, G, c) < count ? 1 : 0), mode};
+  };
   if (count > (long long)kSpanRounds * G) {
-    if (tid == 0) *place = SpanPlace{c / U, c % U, 0, whole_items, G};
+    const SpanView& v = p.rows.view;
+    whole(PAIR && (v.window || !v.causal || v.begin) ? kSpanByHead : kSpanByEntry);
     return;
   }
-  auto cost = [&](int e) { return SpanItem<PAIR>(p, e).n + kCrossStart; };
-  int* sums = reinterpret_cast<int*>(scratch);  // [G] places of each CTA's whole items
-  long long* part = reinterpret_cast<long long*>(scratch + 160);
-  static_assert(kCrossMaxCtas <= 160, "a sum for each CTA");
-  if (tid < G) sums[tid] = 0;
-  if (tid == 0) *place = SpanPlace{0, 0, 0, 0, 0};
-  __syncthreads();
+  uint16_t* order = static_cast<uint16_t*>(scratch);                   // [T]
+  int* sums = reinterpret_cast<int*>(order + T);                       // [160] places of each CTA's whole items
+  long long* part = reinterpret_cast<long long*>(sums + 160);          // [12]
+  static_assert(kCrossMaxCtas <= 160 && T * 2 + 160 * 4 + 12 * 8 <= CrossCfg<128>::kMergeBytes, "a sum for each CTA");
+  if (tid == 0) *place = SpanPlace{0, 0, 0, 0, kSpanShares};
   const int chunk = (E + T - 1) / T, e0 = min(E, tid * chunk), e1 = min(E, e0 + chunk);
-  long long mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int n = cost(e);
-    mine += n;
-    for (int k = e * U; k < e * U + U; ++k) atomicAdd(&sums[k % G], n);
-  }
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long add = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += add;
-  }
-  if (lane == 31) part[warp] = upto;
-  __syncthreads();
-  long long total = 0, before = 0;
-  for (int w = 0; w < 12; ++w) {
-    if (w == warp) before = total;
-    total += part[w];
-  }
-  total *= U;
-  int lead = 0;
-  for (int i = lane; i < G; i += 32) lead = max(lead, sums[i]);
-  lead = __reduce_max_sync(0xffffffffu, lead);
-  // Whole items where the slowest CTA ends no later than even shares and the join of
-  // what they cut.
-  if ((long long)(lead - kCrossCut) * G <= total) {
-    if (tid == 0) *place = SpanPlace{c / U, c % U, 0, whole_items, G};
-    return;
-  }
-  const long long g = min((long long)G, total);
-  if (c >= g) return;
-  const long long start = c * total / g, end = (c + 1) * total / g;
-  if (tid == 0) *all = total, *share_end = end;
-  long long at = (before + upto - mine) * U;
-  if (start < at || start >= (before + upto) * U) return;
-  for (int e = e0; e < e1; ++e) {
-    const int n = cost(e);
-    if (start < at + (long long)n * U) {
-      const long long off = start - at;
-      const int u = (int)(off / n);
-      *place = SpanPlace{e, u, (int)(off - (long long)u * n), (int)(end - start), 0};
-      return;
+  const bool sorted = PAIR && E <= T;  // a thread per entry
+  int one = 0, place_of = tid;         // (sorted) the entry's cost and its place in the order
+  long long mine = 0, upto = 0, total = 0, start = 0, end = 0;
+  int lead[2] = {0, 0};
+  // Passes over this thread's entries: their places; with whole items, the CTAs' places by
+  // entry (by falling cost) and head by head; with shares, where this CTA's begins.
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    if (pass == 1 || pass == 2) {
+      if (tid < 160) sums[tid] = 0;
+      __syncthreads();
     }
-    at += (long long)n * U;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const int n = sorted && pass > 0 ? one : SpanItem<PAIR>(p, e).n + kCrossStart;
+      if (pass == 0) {
+        mine += n;
+        one = n;
+      } else if (pass < 3) {
+        const int b = e / p.row_tiles, at = sorted ? place_of : e;
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const int k = pass == 2 ? (b * U + u) * p.row_tiles + (e - b * p.row_tiles) : at * U + u;
+          const int round = k / G, i = k - round * G;
+          atomicAdd(&sums[round & 1 ? G - 1 - i : i], n);
+        }
+      } else {
+        if (start < upto + (long long)n * U) {
+          const long long off = start - upto;
+          const int u = (int)(off / n);
+          *place = SpanPlace{e, u, (int)(off - (long long)u * n), (int)(end - start), kSpanShares};
+          break;
+        }
+        upto += (long long)n * U;
+      }
+    }
+    if (pass == 0) {
+      if (sorted) {
+        int* costs = static_cast<int*>(scratch);
+        if (tid < E) costs[tid] = one;
+        __syncthreads();
+        place_of = 0;
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          const int n = costs[e];
+          place_of += n > one || (n == one && e < tid) ? 1 : 0;
+        }
+        __syncthreads();
+        if (tid < E) order[place_of] = (uint16_t)tid;
+      }
+      upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long add = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += add;
+      }
+      if (lane == 31) part[warp] = upto;
+    } else if (pass < 3) {
+      __syncthreads();
+      int most = 0;
+      for (int i = lane; i < G; i += 32) most = max(most, sums[i]);
+      most = __reduce_max_sync(0xffffffffu, most);
+      __syncthreads();
+      lead[pass - 1] = most;
+      if (PAIR && pass == 1) continue;
+      long long before = 0;
+#pragma unroll 1
+      for (int w = 0; w < 12; ++w) {
+        if (w == warp) before = total;
+        total += part[w];
+      }
+      total *= U;
+      // (head by head where that is as even to 3 %)
+      const bool by_head = PAIR && lead[1] * 32LL <= lead[0] * 33LL;
+      const long long slowest = by_head ? lead[1] : lead[0];
+      if ((slowest - kCrossCut) * G <= total || slowest * G <= total + total / 16) {
+        whole(by_head ? kSpanByHead : sorted ? kSpanSorted : kSpanByEntry);
+        return;
+      }
+      const long long g = min((long long)G, total);
+      if (c >= g) return;
+      start = c * total / g, end = (c + 1) * total / g;
+      if (tid == 0) *all = total, *share_end = end;
+      const long long at = (before + upto - mine) * U;
+      if (start < at || start >= (before + upto) * U) return;
+      upto = at;
+      pass = 2;
+    }
   }
 }
 
@@ -227,10 +305,10 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, float* scr
 __device__ __forceinline__ void span_cluster_share(const SpanFwdParams& p, SpanPlace* place) {
   const int k = blockIdx.x / p.cluster, rank = blockIdx.x - k * p.cluster, e = k / p.rows.units;
   const int n = SpanItem<false>(p, e).n, j0 = rank * n / p.cluster, j1 = (rank + 1) * n / p.cluster;
-  *place = SpanPlace{e, k - e * p.rows.units, j0 + kCrossStart, j1 - j0, 0};
+  *place = SpanPlace{e, k - e * p.rows.units, j0 + kCrossStart, j1 - j0, kSpanShares};
 }
 
-// (as CrossBarriers)
+// (as CrossBarriers, and the segments)
 struct SpanBarriers {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[12], kv_empty[12];
@@ -239,39 +317,67 @@ struct SpanBarriers {
   uint64_t merge_ready, merge_free;
   uint64_t drain[2];
   uint64_t never;
+  uint64_t seg_full[kSpanSegs], seg_empty[kSpanSegs];  // (read by the issuers, warp 11 and eight softmax warps)
+  SpanSeg seg[kSpanSegs];
   SpanPlace place;
   long long total, end;  // places of the sequence; end of the CTA's share
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(SpanBarriers) <= 512, "barriers overflow their shared-memory slot");
+constexpr int kSpanSegReaders = 11;
+static_assert(sizeof(SpanBarriers) <= 1024, "barriers overflow their shared-memory slot");
 
-// What a softmax warp needs behind its blocks, kept here while its registers hold scores.
-struct SpanWarp {
-  SpanPlace at;
-  int b, u, row0, j0, j1, flags;
-};
-static_assert(sizeof(SpanWarp) <= 64, "512 bytes for eight warps");
+// wait_bounded_inl in a third of its code
+__device__ __forceinline__ bool span_wait(uint64_t* bar, uint32_t parity, const WaitCtx& ctx, int site) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (int n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (n & 31) continue;
+    if (*ctx.abort_flag) return false;
+    const uint64_t now = global_timer_ns();
+    if (since == 0) since = now;
+    if (now - since > ctx.limit_ns) {
+      atomicCAS(&g_fa_device_status, 0u, kStatusTimeout | ((unsigned)(site & 0xff) << 8));
+      *ctx.abort_flag = 1;
+      __threadfence_block();
+      return false;
+    }
+  }
+}
 
-// adds a bias of -slope2 |rel - c| to the scores of keys c of a block (log2 units),
-// after multiplying them with mul; rel: the row's position from the block's first key
+// The n-th segment; false: there are no more (or the wait ran out).
+__device__ __forceinline__ bool span_segment(SpanBarriers* bar, int n, const WaitCtx& ctx, const SpanSeg*& w) {
+  const int s = n % kSpanSegs;
+  if (!span_wait(&bar->seg_full[s], (n / kSpanSegs) & 1, ctx, kSiteSpanSeg)) return false;
+  w = &bar->seg[s];
+  return !(w->flags & kSegEnd);
+}
+
+// multiplies a block's scores with mul and adds a bias of -slope2 |rel - c| to that of key c
+// (log2 units); rel: the row's position from the block's first key
 __device__ __forceinline__ void span_bias(uint32_t (&s)[4][32], float mul, float slope2, int rel) {
   const float relf = (float)rel;
-  const float2 mul2 = make_float2(mul, mul);
   if (__all_sync(0xffffffffu, rel >= 127 || rel <= 0)) {
-    // all keys on one side of the row: a line
+    // all keys on one side of the row: a line g c - g rel, as a value for each eight keys and
+    // offsets within them
     const float g = rel > 0 ? slope2 : -slope2, base = -g * relf;
-    const float2 g2 = make_float2(g, g), base2 = make_float2(base, base);
+    const float2 mul2 = make_float2(mul, mul);
+    float2 off[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int i = 0; i < 4; ++i) off[i] = make_float2(g * (float)(2 * i), g * (float)(2 * i + 1));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float k = (float)(32 * c + 2 * i);
-        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), mul2,
-                                    __ffma2_rn(make_float2(k, k + 1.f), g2, base2));
-        s[c][2 * i] = __float_as_uint(x.x);
-        s[c][2 * i + 1] = __float_as_uint(x.y);
+    for (int c8 = 0; c8 < 16; ++c8) {
+      const float at = fmaf(g, (float)(8 * c8), base);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t* e = &s[c8 >> 2][8 * (c8 & 3) + 2 * i];
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(e[0]), __uint_as_float(e[1])), mul2,
+                                    __fadd2_rn(off[i], make_float2(at, at)));
+        e[0] = __float_as_uint(x.x);
+        e[1] = __float_as_uint(x.y);
       }
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -281,14 +387,25 @@ __device__ __forceinline__ void span_bias(uint32_t (&s)[4][32], float mul, float
   }
 }
 
+// 32 keys' bits of those in [from, to)
+__device__ __forceinline__ uint32_t span_bits(int from, int to) {
+  const uint32_t below = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
+  const uint32_t before = from >= 32 ? 0xffffffffu : from <= 0 ? 0u : (1u << from) - 1u;
+  return below & ~before;
+}
+
 // PAIR: two row tiles per item.  CLUSTER: a cluster of p.cluster CTAs per item (not with
-// PAIR).  MOD: 0 plain scores, 1 with a bias, 2 capped (and with a bias where there are slopes).
+// PAIR).  MOD: 0 plain scores, 1 with a bias, 2 capped, 3 both.
 template <int D, int MOD, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(384, 1)
     fa_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
   using C = CrossCfg<D>;
   static_assert(!(PAIR && CLUSTER), "clusters take one row tile");
+  // The issuing threads' loops over the two row tiles: one copy of the products at d = 128, where
+  // the kernel's loops together outgrow the instruction cache (H=32/8 N=8192, two requests, causal:
+  // 814 us, and 904 with two copies); at d = 64 the shorter products outrun a loop (76 and 78 us).
+  constexpr int kIssueUnroll = D == 64 ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
@@ -304,7 +421,6 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* sKV = smem + 2 * C::kTileBytes;
   float* sMerge = reinterpret_cast<float*>(sKV + C::kSlots * C::kTileBytes);  // [3][128]
   SpanBarriers* bar = reinterpret_cast<SpanBarriers*>(reinterpret_cast<uint8_t*>(sMerge) + C::kMergeBytes);
-  uint8_t* sWarps = reinterpret_cast<uint8_t*>(bar) + 512;  // SpanWarp of each softmax warp, 64 bytes apart
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const SpanView& v = p.rows.view;
 
@@ -318,9 +434,14 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bar->pv_done[t], 1);
       mbar_init(&bar->drain[t], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&bar->kv_full[s], 1);
       mbar_init(&bar->kv_empty[s], 1);
+    }
+    for (int s = 0; s < kSpanSegs; ++s) {
+      mbar_init(&bar->seg_full[s], 1);
+      mbar_init(&bar->seg_empty[s], kSpanSegReaders);
     }
     mbar_init(&bar->v_clean, 1);
     mbar_init(&bar->v_ask, 1);
@@ -352,13 +473,13 @@ __global__ void __launch_bounds__(384, 1)
   grid_trigger();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
-  SpanPlace at = bar->place;  // every role walks the same segments
-  SpanSeg w;
-
   if (warp >= 8) {
     setmaxnreg_dec<C::kMiscRegs>();
     if (warp == 9) {
       // ------------------------------------------------------------------ TMA producer (a lane per page)
+      const uint16_t* order = reinterpret_cast<const uint16_t*>(sMerge);
+      SpanPlace at = bar->place;
+      SpanSeg w{};
       const int shift = v.page_shift, box_rows = v.table ? min(1 << shift, 128) : 128;
       const int boxes = 128 / box_rows;
       int loads = 0, nq = 0;  // K and V tiles, in turn
@@ -371,59 +492,75 @@ __global__ void __launch_bounds__(384, 1)
         const int page = v.table[(long long)w.b * v.width + i];
         return page >= 0 && page < p.pages ? page : -1;
       };
-      auto load_kv = [&](int j, int kv, int kvh, int page) -> bool {
-        const int g = loads >> 1, s = C::slot(kv, g);
-        const CUtensorMap* map = kv ? &map_v : &map_k;
-        if (!__all_sync(0xffffffffu,
-                        wait_bounded_inl(&bar->kv_empty[s], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty)))
-          return false;
-        if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[s], C::kTileBytes);
-        __syncwarp();
-        if (lane < boxes) {
-          const int row = v.table ? (j * 128) & ((1 << shift) - 1) : j * 128;
-          for (int a = 0; a < C::kAtoms; ++a)
-            tma_load_4d(sKV + s * C::kTileBytes + a * 16384 + lane * box_rows * 128, map, &bar->kv_full[s], a * 64,
-                        boxes > 1 ? 0 : row, kvh, v.table ? page : w.b);
+      auto load_q = [&](int qs) {
+        if (lane == 0) {
+          const int tiles = w.flags & kSegTwo ? 2 : 1;
+          mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
+          for (int t = 0; t < tiles; ++t)
+            for (int a = 0; a < C::kAtoms; ++a)
+              tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
+                          w.row0 + 128 * t, w.b * p.rows.units + w.u);
         }
-        ++loads;
-        return true;
+        __syncwarp();
       };
-      while (ok && span_next<PAIR>(p, at, w)) {
-        const int kvh = w.u / p.rows.kv_div, bu = w.b * p.rows.units + w.u;
+#pragma unroll 1
+      while (ok) {
+        const bool more = span_next<PAIR>(p, order, at, w);
+        if (!more) w.flags = kSegEnd;
+        // the segment for the other warps, once they have done with the one in its place
+        const int s = nq % kSpanSegs;
+        ok = __all_sync(0xffffffffu, span_wait(&bar->seg_empty[s], ((nq / kSpanSegs) & 1) ^ 1, ctx, kSiteSpanSegFree));
+        if (!ok) break;
+        if (lane == 0) {
+          bar->seg[s] = w;
+          mbar_arrive(&bar->seg_full[s]);
+        }
+        __syncwarp();
+        if (!more) break;
+        const int kvh = w.u / p.rows.kv_div;
         const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-        const int tiles = w.two ? 2 : 1;
-        auto load_q = [&] {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
-            for (int t = 0; t < tiles; ++t)
-              for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
-                            w.row0 + 128 * t, bu);
-          }
-          __syncwarp();
-        };
         int page = v.table ? page_of(w.j0) : 0;
         // a later segment's first key block needs only ring slots: it goes out
         // before the queries, whose buffer an earlier segment may still be reading
-        if (nq == 0) load_q();
+        if (nq == 0) load_q(qs);
+        ++nq;
+#pragma unroll 1
         for (int j = w.j0; ok && j < w.j1; ++j) {
           const int next = v.table && j + 1 < w.j1 ? page_of(j + 1) : 0;  // (asked for a block ahead)
-          ok = load_kv(j, 0, kvh, page) && load_kv(j, 1, kvh, page);
-          if (ok && j == w.j0 && nq > 0) {
-            if (use > 0) ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->q_empty[qs], (use - 1) & 1, ctx,
-                                                                       kSiteCrossQEmpty));
-            if (ok) load_q();
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const int g = loads >> 1, slot = C::slot(kv, g);
+            ok = __all_sync(0xffffffffu,
+                            span_wait(&bar->kv_empty[slot], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+            __syncwarp();
+            if (lane < boxes) {
+              const int row = !v.table ? j * 128 : boxes > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
+              for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_4d(sKV + slot * C::kTileBytes + a * 16384 + lane * box_rows * 128, kv ? &map_v : &map_k,
+                            &bar->kv_full[slot], a * 64, row, kvh, v.table ? page : w.b);
+            }
+            ++loads;
+          }
+          if (ok && j == w.j0 && nq > 1) {
+            if (use > 0)
+              ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
+            if (ok)
+              load_q(qs);
+            else
+              --nq;  // (these queries were not asked for)
           }
           page = next;
         }
-        if (ok) ++nq;
       }
       // every copy this warp started must land before the CTA can exit
       if (lane == 0) {
-        for (int s = 0; s < 2; ++s) {
-          const int uses = PAIR ? (s ? 0 : nq) : (nq + 1 - s) >> 1;
+        for (int s = 0; s < (PAIR ? 1 : 2); ++s) {
+          const int uses = PAIR ? nq : (nq + 1 - s) >> 1;
           if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
         }
+#pragma unroll 1
         for (int s = 0; s < C::kSlots; ++s) {
           // loads into slot s
           const bool vslot = s >= C::kKSlots;
@@ -439,20 +576,27 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         int s_uses[2] = {0, 0}, g = 0, nq = 0;
-        bool ok = !(p.debug_stall && !wait_bounded_inl(&bar->never, 0, ctx, kSiteStall));
-        while (ok && span_next<PAIR>(p, at, w)) {
+        const SpanSeg* at;
+        bool ok = !(p.debug_stall && !span_wait(&bar->never, 0, ctx, kSiteStall));
+#pragma unroll 1
+        while (ok && span_segment(bar, nq, ctx, at)) {
+          const SpanSeg w = *at;
+          mbar_arrive(&bar->seg_empty[nq % kSpanSegs]);
           const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-          if (!wait_bounded_inl(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
+          if (!span_wait(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
           ++nq;
+#pragma unroll 1
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int ks = C::slot(0, g);
-            if (!(ok = wait_bounded_inl(&bar->kv_full[ks], C::use(0, g) & 1, ctx, kSiteCrossK))) break;
+            if (!(ok = span_wait(&bar->kv_full[ks], C::use(0, g) & 1, ctx, kSiteCrossK))) break;
             const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
-#pragma unroll
+            const int active = span_active<PAIR>(w, j);
+#pragma unroll kIssueUnroll
             for (int t = 0; t < 2; ++t) {
-              if (PAIR ? ((t == 0 || w.two) && j >= w.a0[t] && j < w.a1[t]) : (((j - w.j0) & 1) == t)) {
+              if (active >> t & 1) {
                 const int sb = C::kDualS ? t : 0;
-                if (s_uses[sb] > 0 && !wait_bounded_inl(&bar->s_free[sb], (s_uses[sb] - 1) & 1, ctx, kSiteCrossSFree)) {
+                int& uses = sb ? s_uses[1] : s_uses[0];
+                if (uses > 0 && !span_wait(&bar->s_free[sb], (uses - 1) & 1, ctx, kSiteCrossSFree)) {
                   ok = false;
                   break;
                 }
@@ -464,7 +608,7 @@ __global__ void __launch_bounds__(384, 1)
                   mma_bf16_ss(tmem + (sb ? C::kSCol1 : C::kSCol), qd + off, kdesc + off, id_s, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(&bar->s_full[t]);
-                ++s_uses[sb];
+                ++uses;
               }
             }
             if (!ok) break;
@@ -486,37 +630,44 @@ __global__ void __launch_bounds__(384, 1)
         int g = 0, cleaned = 0;
         int pv_uses[2] = {0, 0};
         bool ok = true;
-        while (ok && span_next<PAIR>(p, at, w)) {
+        const SpanSeg* at;
+#pragma unroll 1
+        for (int n = 0; ok && span_segment(bar, n, ctx, at); ++n) {
+          const SpanSeg w = *at;
+          mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
+#pragma unroll 1
           for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
             const int vs = C::slot(1, g);
-            if (!(ok = wait_bounded_inl(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
-            int from, to;
-            bool clean = !span_dirty(p, w, j, from, to);
-            if (!clean) mbar_arrive(&bar->v_ask);
+            if (!(ok = span_wait(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
+            // rows that nobody sees: warp 11 zeroes them while P is being formed
+            const bool dirty = span_dirty(w, j);
+            if (dirty) mbar_arrive(&bar->v_ask);
             const uint64_t vdesc = sdesc_sw128(skv + vs * C::kTileBytes, 16384, 1024);
-            auto cleaned_now = [&] {
-              if (!clean) clean = wait_bounded_inl(&bar->v_clean, cleaned++ & 1, ctx, kSiteCrossClean);
-              return clean;
-            };
-#pragma unroll
+            const int active = span_active<PAIR>(w, j);
+            bool clean = !dirty;
+#pragma unroll kIssueUnroll
             for (int t = 0; t < 2; ++t) {
-              if (PAIR ? ((t == 0 || w.two) && j >= w.a0[t] && j < w.a1[t]) : (((j - w.j0) & 1) == t)) {
-                if (!wait_bounded_inl(&bar->p_full[t], pv_uses[t] & 1, ctx, kSiteCrossP) || !cleaned_now()) {
+              if (active >> t & 1) {
+                int& uses = t ? pv_uses[1] : pv_uses[0];
+                if (!span_wait(&bar->p_full[t], uses & 1, ctx, kSiteCrossP) ||
+                    (!clean && !span_wait(&bar->v_clean, cleaned & 1, ctx, kSiteCrossClean))) {
                   ok = false;
                   break;
                 }
+                clean = true;
                 tc_fence_after();
-                const bool add = j > (PAIR ? w.a0[t] : w.j0 + 1);  // not the tile's first block of the segment
+                const bool add = j > (PAIR ? (t ? w.a0[1] : w.a0[0]) : w.j0 + 1);  // not the tile's first block
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_bf16_ts(tmem + (t ? C::kOCol1 : C::kOCol0), tmem + (t ? C::kPCol1 : C::kPCol0) + kk * 8,
                               vdesc + (uint32_t)((kk * 2048) >> 4), id_pv, (add || kk > 0) ? 1u : 0u);
                 mma_commit(&bar->pv_done[t]);
-                ++pv_uses[t];
+                ++uses;
               }
             }
-            ok = ok && cleaned_now();
+            if (ok && !clean) ok = span_wait(&bar->v_clean, cleaned & 1, ctx, kSiteCrossClean);
             if (!ok) break;
+            cleaned += dirty ? 1 : 0;
             mma_commit(&bar->kv_empty[vs]);
           }
         }
@@ -529,26 +680,35 @@ __global__ void __launch_bounds__(384, 1)
       int g = 0, cleaned = 0;
       bool ok = true;
       SpanMeta meta{};
-      while (ok && span_next<PAIR>(p, at, w)) {
+      const SpanSeg* at;
+#pragma unroll 1
+      for (int n = 0; ok; ++n) {
+        if (!__all_sync(0xffffffffu, span_segment(bar, n, ctx, at))) {
+          ok = !*ctx.abort_flag;
+          break;
+        }
+        const SpanSeg w = *at;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
+#pragma unroll 1
         for (int j = w.j0; ok && j < w.j1; j = j + 1 < w.j1 - 1 ? w.j1 - 1 : j + 1) {  // (its first and its last block)
-          int from, to;
-          if (!span_dirty(p, w, j, from, to)) continue;
-          ok = __all_sync(0xffffffffu, wait_bounded_inl(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
+          if (!span_dirty(w, j)) continue;
+          ok = __all_sync(0xffffffffu, span_wait(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
           if (!ok) break;
           ++cleaned;
+          const int from = max(w.lo - j * 128, 0), to = max(min(w.hi - j * 128, 128), from);  // seen
           uint8_t* tile = sKV + C::slot(1, g + j - w.j0) * C::kTileBytes;
-          for (int a = 0; a < C::kAtoms; ++a) {
-            for (int c = lane; c < from * 8; c += 32)
-              *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
-            for (int c = max(from, to) * 8 + lane; c < 128 * 8; c += 32)
-              *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+          const int unseen = (from + 128 - to) * 8;  // 16-byte chunks of an atom
+          for (int i = lane; i < C::kAtoms * unseen; i += 32) {
+            const int a = i >= unseen ? 1 : 0, k = i - a * unseen, c = k < from * 8 ? k : k - from * 8 + to * 8;
+            *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->v_clean);
         }
         g += w.j1 - w.j0;
-        if (w.first && !w.last) {
+        if ((w.flags & (kSegFirst | kSegLast)) == kSegFirst) {
           // (the CTA's last segment: the item's other blocks follow its share)
           meta.split = 1;
           meta.b = w.b;
@@ -574,50 +734,43 @@ __global__ void __launch_bounds__(384, 1)
     int uses = 0;    // blocks this tile has processed over all segments
     int merges = 0;  // ALT: segments whose two accumulators were joined
     bool alive = true;
-    // (volatile: read again after the segment's blocks, not kept in registers)
-    volatile SpanWarp* mine = reinterpret_cast<volatile SpanWarp*>(sWarps + 64 * warp);
-    auto store_place = [&] {
-      mine->at.e = at.e, mine->at.u = at.u, mine->at.j = at.j, mine->at.left = at.left, mine->at.whole = at.whole;
-    };
-    if (lane == 0) store_place();
-    __syncwarp();
     // CLUSTER: this CTA's part of the item, in the ring's memory once the ring has
     // been read: rows of D + 4 floats (so that a warp's rows spread over the banks);
     // its log-sum-exps at sMerge
     float* sPart = reinterpret_cast<float*>(sKV);
-    while (alive) {
-      at.e = mine->at.e, at.u = mine->at.u, at.j = mine->at.j, at.left = mine->at.left, at.whole = mine->at.whole;
-      if (!span_next<PAIR>(p, at, w)) break;
-      int jfirst, j1, row_lo, row_hi, pos;
-      int lo_cut = 0, hi_cut = 0;  // blocks that all rows of the tile see whole
+#pragma unroll 1
+    for (int n = 0; alive; ++n) {
+      const SpanSeg* seg;
+      if (!__all_sync(0xffffffffu, span_segment(bar, n, ctx, seg))) break;
+      const volatile SpanSeg& w = *seg;  // (read where it is needed, not kept in registers)
+      auto release = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
+      };
+      // nothing for this tile
+      if (PAIR ? (t == 1 && !(w.flags & kSegTwo)) : (t == 1 && w.j1 - w.j0 < 2)) {
+        release();
+        continue;
+      }
+      int row_lo, row_hi, pos;
       float slope2 = 0.f;
       bool there = true;  // the row is written
+      const int jfirst = PAIR ? w.a0[t] : w.j0 + t, j1 = PAIR ? w.a1[t] : w.j1;
+      const int lo_cut = w.lo_cut[PAIR ? t : 0], hi_cut = w.hi_cut[PAIR ? t : 0];  // blocks that all rows see whole
       {
-        __syncwarp();
-        if (lane == 0) {
-          store_place();
-          mine->b = w.b, mine->u = w.u, mine->row0 = w.row0, mine->j0 = w.j0, mine->j1 = w.j1;
-          mine->flags = (w.first ? 1 : 0) | (w.last ? 2 : 0);
-        }
-        __syncwarp();
-        // nothing for this tile
-        if (PAIR ? (t == 1 && !w.two) : (t == 1 && w.j1 - w.j0 < 2)) continue;
-        jfirst = PAIR ? w.a0[t] : w.j0 + t;
-        j1 = PAIR ? w.a1[t] : w.j1;
-        const SpanTile tile = p.rows.tile(w.b, w.row0 / 128 + (PAIR ? t : 0));
-        lo_cut = tile.lo_cut, hi_cut = tile.hi_cut;
-        const int row = min(w.row0 + (PAIR ? 128 * t : 0) + r, p.rows.R - 1), head = row / v.N, tok = row - head * v.N;
-        pos = v.len(w.b) + tok;
-        v.span(w.b, tok, pos, row_lo, row_hi);
-        if (MOD == 2) there = tok < v.rows(w.b, v.len(w.b));
-        if (MOD > 0 && p.slopes) slope2 = p.slopes[w.u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
+        const int b = w.b, row = min(w.row0 + (PAIR ? 128 * t : 0) + r, p.rows.R - 1), head = row / v.N;
+        const int tok = row - head * v.N, len = v.len(b);
+        pos = len + tok;
+        v.span(b, tok, pos, row_lo, row_hi);
+        if (MOD >= 2) there = tok < v.rows(b, len);
+        if (MOD & 1) slope2 = p.slopes[w.u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
       }
       float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
       // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
       // block's largest one, so that l + lcorr normalises O (see fa_fwd_kernel)
       float l = 0.f, lcorr = 0.f;
       for (int j = jfirst; j < j1; j += PAIR ? 1 : 2, ++uses) {
-        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
+        if (!__all_sync(0xffffffffu, span_wait(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
           alive = false;
           break;
         }
@@ -635,27 +788,36 @@ __global__ void __launch_bounds__(384, 1)
         const int kbase = j * 128;
         const bool cut = kbase < lo_cut || kbase + 128 > hi_cut;
         auto hide = [&](float value) {
-          const int from = row_lo - kbase, to = row_hi - kbase;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < from || c >= to) sr[c >> 5][c & 31] = __float_as_uint(value);
-        };
-        if constexpr (MOD == 2) {
-          if (cut) hide(0.f);  // (what is not seen has no say in how the others are capped)
-          const bool near = span_cap_all_near(sr, p.cap.mul, there);
-          if (near) {
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = span_bits(row_lo - kbase - 32 * c, row_hi - kbase - 32 * c);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, true);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, false);
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(value);
           }
-          if (p.slopes) span_bias(sr, 1.f, slope2, pos - kbase);
+        };
+        // MOD 2, a block that is seen whole with small products: the cap is part of the exponent's
+        // argument below; else it (and the bias) is applied in place
+        const bool fused = MOD == 2 && !cut && __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.small);
+        if constexpr (MOD >= 2) {
+          if (MOD == 2 ? __builtin_expect(!fused, 0) : true) {
+            if (__builtin_expect(cut, 0)) hide(0.f);  // (what is not seen has no say in how the others are capped)
+            const bool near = __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.near);
+            if (__builtin_expect(near, 1)) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, true);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, false);
+            }
+            if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase);
+          }
         }
         if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase);
-        if (cut) hide(-CUDART_INF_F);
+        if (__builtin_expect(cut, 0)) hide(-CUDART_INF_F);
         const float mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
-        const float m_new = fmaxf(m, mx * cj);
+        const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;  // mx cmx: its score
+        const float m_new = fmaxf(m, mx * cmx);
         // conditional rescale: the reference moves only when the row maximum
         // rose by more than the threshold (always from -inf: no key so far)
         float alpha = 1.f;
@@ -677,41 +839,49 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
         {
-          const float pbm = ex2_approx(fmaf(mx, cj, -ref));
+          const float pbm = ex2_approx(fmaf(mx, cmx, -ref));
           const float pbm_r = __uint_as_float(pack_bf16x2(pbm, 0.f) << 16);
           lcorr = lcorr * alpha + (pbm_r - pbm);
         }
         uint32_t pk[4][16];
+        auto exponentials = [&](auto capped) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; ++c) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 s2 = make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1]));
-            const float2 x = MOD == 0 ? __ffma2_rn(s2, c2, mneg2) : __fadd2_rn(s2, mneg2);
-            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-            pk[c][i] = pack_bf16x2(p0, p1);
-            acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+            for (int i = 0; i < 16; ++i) {
+              const float2 s2 = make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1]));
+              const float2 x = capped.value ? __ffma2_rn(s2, span_cap_small(s2, p.cap), mneg2)
+                               : MOD == 0   ? __ffma2_rn(s2, c2, mneg2)
+                                            : __fadd2_rn(s2, mneg2);
+              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+              pk[c][i] = pack_bf16x2(p0, p1);
+              acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+            }
           }
-        }
+        };
+        if (MOD == 2 && __builtin_expect(fused, 1))
+          exponentials(std::true_type{});
+        else
+          exponentials(std::false_type{});
         const float2 accs = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l = l * alpha + (accs.x + accs.y);
         // P_t and O_t are in use until the tile's previous product has completed
         // (a segment's first block: its predecessor's epilogue has waited for
         // it; ALT: O_1 also until warpgroup 0 has read it)
         if (j > jfirst) {
-          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+          if (!__all_sync(0xffffffffu, span_wait(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
             alive = false;
             break;
           }
           tc_fence_after();
         } else if (!PAIR && t == 1 && merges > 0) {
-          if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_free, (merges - 1) & 1, ctx, kSiteCrossMerge))) {
+          if (!__all_sync(0xffffffffu, span_wait(&bar->merge_free, (merges - 1) & 1, ctx, kSiteCrossMerge))) {
             alive = false;
             break;
           }
           tc_fence_after();
         }
-        if (rescale_warp) {
+        if (__builtin_expect(rescale_warp, 0)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -731,15 +901,14 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&bar->p_full[t]);
       }
       if (!alive) break;
-      if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
+      if (!__all_sync(0xffffffffu, span_wait(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
         alive = false;
         break;
       }
       tc_fence_after();
       // ---- end of the segment
-      w.b = mine->b, w.u = mine->u, w.row0 = mine->row0, w.j0 = mine->j0, w.j1 = mine->j1;
-      const int flags = mine->flags;
-      const bool seg_first = flags & 1, whole = flags == 3;
+      const int flags = w.flags;
+      const bool seg_first = flags & kSegFirst, whole = seg_first && (flags & kSegLast);
       const int row = w.row0 + (PAIR ? 128 * t : 0) + r;
       const bool join = !PAIR && w.j1 - w.j0 >= 2;
       float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
@@ -751,9 +920,10 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive(&bar->merge_ready);
           ++merges;
+          release();
           continue;
         }
-        if (!__all_sync(0xffffffffu, wait_bounded_inl(&bar->merge_ready, merges & 1, ctx, kSiteCrossMerge))) {
+        if (!__all_sync(0xffffffffu, span_wait(&bar->merge_ready, merges & 1, ctx, kSiteCrossMerge))) {
           alive = false;
           break;
         }
@@ -828,6 +998,7 @@ __global__ void __launch_bounds__(384, 1)
         else
           p.part_lse[prow] = lse2;
       }
+      release();
       tc_fence_before();
     }
   }
