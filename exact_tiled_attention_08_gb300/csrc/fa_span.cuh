@@ -120,51 +120,41 @@ __global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, i
 
 // The cap in log2 units: cap log2(e) tanh(x), x = scale q k / cap.
 //
-// Within |x| <= 3/4 it is x G(x^2) with the minimax polynomial of tanh(sqrt u) / sqrt u on
-// [0, 9/16] (degree 5, by Remez exchange on the relative error: 3e-8), scaled; beyond it
-// 1 - 2 / (1 + e^2x), whose absolute error (2^-22) is what counts there.  Within |x| <= 3/8 a
-// polynomial of degree 3 (1.3e-8) does, in the products themselves.  A warp takes
-// the cheapest that all of its products of the block allow.
+// Within |x| <= 0.6 it is x G(x^2) with the minimax polynomial of tanh(sqrt u) / sqrt u on
+// [0, 0.36] (degree 4, by Remez exchange on the relative error: 7.3e-8), in powers of the product q k
+// itself; beyond it 1 - 2 / (1 + e^2x), whose absolute error (2^-22) is what counts there.
+// A warp takes the polynomial where all of its products of a block allow it.
 struct SpanCap {
-  float mul;    // scale / cap
-  float small;  // products up to there take the short polynomial: 3/8 cap / scale
-  float near;   // the long one: 3/4 cap / scale
+  float mul;    // 2 log2(e) scale / cap
+  float small;  // products up to there take the polynomial: 0.6 cap / scale
   float top;    // cap log2(e)
-  float c[6];   // x (c[0] + c[1] x^2 + ...)
-  float d[4];   // q k (d[0] + d[1] (q k)^2 + ...)
+  float d[5];   // q k (d[0] + d[1] (q k)^2 + ...)
 };
 
 // score / product of small products
 __device__ __forceinline__ float2 span_cap_small(float2 s, const SpanCap& c) {
   const float2 u = __fmul2_rn(s, s);
-  float2 g = __ffma2_rn(u, make_float2(c.d[3], c.d[3]), make_float2(c.d[2], c.d[2]));
+  float2 g = __ffma2_rn(u, make_float2(c.d[4], c.d[4]), make_float2(c.d[3], c.d[3]));
 #pragma unroll
-  for (int i = 1; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.d[i], c.d[i]));
+  for (int i = 2; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.d[i], c.d[i]));
   return g;
 }
 
-__device__ __forceinline__ float span_cap_any(float x, float top) {
-  const float e = ex2_approx(x * 2.8853900817779268f);
-  return top - __fdividef(2.f * top, e + 1.f);  // (a divisor beyond 2^126 gives 0)
-}
-
-__device__ __forceinline__ float2 span_cap_near(float2 x, const SpanCap& c) {
-  const float2 u = __fmul2_rn(x, x);
-  float2 g = __ffma2_rn(u, make_float2(c.c[5], c.c[5]), make_float2(c.c[4], c.c[4]));
-#pragma unroll
-  for (int i = 3; i >= 0; --i) g = __ffma2_rn(u, g, make_float2(c.c[i], c.c[i]));
-  return __fmul2_rn(x, g);
-}
-
 // 32 products of one row, in place
-__device__ __forceinline__ void span_cap32(uint32_t (&s)[32], const SpanCap& c, bool near) {
-  const float2 mul = make_float2(c.mul, c.mul);
+__device__ __forceinline__ void span_cap32_small(uint32_t (&s)[32], const SpanCap& c) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul);
-    const float2 y = near ? span_cap_near(x, c) : make_float2(span_cap_any(x.x, c.top), span_cap_any(x.y, c.top));
+    const float2 x = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    const float2 y = __fmul2_rn(x, span_cap_small(x, c));
     s[2 * i] = __float_as_uint(y.x);
     s[2 * i + 1] = __float_as_uint(y.y);
+  }
+}
+__device__ __forceinline__ void span_cap32(uint32_t (&s)[32], const SpanCap& c) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float e = ex2_approx(__uint_as_float(s[i]) * c.mul);
+    s[i] = __float_as_uint(fmaf(-2.f * c.top, rcp_approx(e + 1.f), c.top));
   }
 }
 

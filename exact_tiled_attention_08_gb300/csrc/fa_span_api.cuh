@@ -38,7 +38,7 @@ fa_status check_span_args(float scale, float cap, int window, int causal) {
   fa_status st = check_scale(scale, causal);
   if (st != FA_OK) return st;
   if (!std::isfinite(cap) || cap < 0.f || window < 0) return FA_ERR_INVALID_ARG;
-  if (cap > 0.f && (!std::isnormal(scale / cap) || !std::isfinite(2.f * cap))) return FA_ERR_INVALID_ARG;
+  if (cap > 0.f && (!std::isnormal(scale / cap) || !std::isfinite(4.f * scale / cap) || !std::isfinite(4.f * cap))) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -68,25 +68,22 @@ bool encode_pages(CUtensorMap* map, const fa::PageRows& r, int tokens, int heads
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// tanh(sqrt u) / sqrt u on [0, 9/16]: minimax polynomial of degree 5 (Remez exchange), relative error 2.9e-8
-constexpr double kTanhPoly[6] = {0.9999999710138949,   -0.33332958879477204, 0.13325406017696445,
-                                 -0.05334443014377955, 0.019582908187949204, -0.004716257251378197};
-
-// the same on [0, 9/64], of degree 3: 5.9e-8
-constexpr double kTanhShort[4] = {0.9999999405367285, -0.3333197482128287, 0.13284502145788482, -0.048272262378324014};
+// tanh(sqrt u) / sqrt u on [0, 0.36]: minimax polynomial of degree 4 (Remez exchange), relative error 7.3e-8
+constexpr double kTanhPoly[5] = {0.9999999268689591, -0.3333230997439495, 0.13310173657879062, -0.05210148011192052,
+                                 0.015475427482730527};
 
 fa::SpanCap span_cap(float scale, float cap) {
   fa::SpanCap c{};
   if (cap == 0.f) return c;
   const double x = (double)scale / cap, top = 1.4426950408889634 * cap;
-  c.mul = scale / cap;
-  c.near = 0.75f * cap / scale;
+  c.mul = (float)(2 * 1.4426950408889634 * x);
   c.top = (float)top;
-  for (int i = 0; i < 6; ++i) c.c[i] = (float)(top * kTanhPoly[i]);
-  for (int i = 0; i < 4; ++i) c.d[i] = (float)(top * kTanhShort[i] * std::pow(x, 2 * i + 1));
-  // (where fp32 does not hold these no product is small)
-  const bool held = std::isnormal(c.d[3]) && std::isnormal(c.d[2]) && std::isnormal(c.d[1]) && std::isnormal(c.d[0]);
-  c.small = held ? 0.375f * cap / scale : -1.f;
+  bool held = true;  // (where fp32 does not hold the coefficients no product is small)
+  for (int i = 0; i < 5; ++i) {
+    c.d[i] = (float)(top * kTanhPoly[i] * std::pow(x, 2 * i + 1));
+    held = held && std::isnormal(c.d[i]);
+  }
+  c.small = held ? 0.6f * cap / scale : -1.f;
   return c;
 }
 

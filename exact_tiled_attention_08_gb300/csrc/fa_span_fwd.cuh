@@ -776,46 +776,63 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_fence_after();
         uint32_t sr[4][32];
+        float mx_a = 0.f;
+        if constexpr (C::kDualS && MOD == 0) {  // two halves: the first's maximum is taken while the second loads
+          tmem_ld32(tS, sr[0]);
+          tmem_ld32(tS + 32, sr[1]);
+          tmem_wait_ld();
+          reg_fence32(sr[0]);
+          reg_fence32(sr[1]);
+          tmem_ld32(tS + 64, sr[2]);
+          tmem_ld32(tS + 96, sr[3]);
+          mx_a = cross_max64(sr[0], sr[1]);
+          tmem_wait_ld();
+          reg_fence32(sr[2]);
+          reg_fence32(sr[3]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
-        tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+          for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+        }
         // the scores are in registers: the next scores may now overwrite S
         tc_fence_before();
         mbar_arrive(&bar->s_free[C::kDualS ? t : 0]);
 
         const int kbase = j * 128;
         const bool cut = kbase < lo_cut || kbase + 128 > hi_cut;
-        auto hide = [&](float value) {
+        auto hide = [&] {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t bits = span_bits(row_lo - kbase - 32 * c, row_hi - kbase - 32 * c);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(value);
+              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-CUDART_INF_F);
           }
         };
-        // MOD 2, a block that is seen whole with small products: the cap is part of the exponent's
-        // argument below; else it (and the bias) is applied in place
-        const bool fused = MOD == 2 && !cut && __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.small);
+        // Small products are capped by the polynomial, in MOD 2 inside the exponent's argument
+        // below; others, and blocks seen in part (where what is not seen has no say in it), in place.
+        bool fused = false;
         if constexpr (MOD >= 2) {
-          if (MOD == 2 ? __builtin_expect(!fused, 0) : true) {
-            if (__builtin_expect(cut, 0)) hide(0.f);  // (what is not seen has no say in how the others are capped)
-            const bool near = __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.near);
-            if (__builtin_expect(near, 1)) {
+          const bool small = !cut && __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.small);
+          fused = MOD == 2 && small;
+          if (MOD == 3 && __builtin_expect(small, 1)) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, true);
-            } else {
+            for (int c = 0; c < 4; ++c) span_cap32_small(sr[c], p.cap);
+          } else if (!small) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap, false);
-            }
-            if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase);
+            for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap);
           }
+          if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase);
         }
         if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase);
-        if (__builtin_expect(cut, 0)) hide(-CUDART_INF_F);
-        const float mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
+        if (__builtin_expect(cut, 0)) hide();
+        float mx;
+        if constexpr (C::kDualS && MOD == 0)
+          mx = fmaxf(cut ? cross_max64(sr[0], sr[1]) : mx_a, cross_max64(sr[2], sr[3]));
+        else
+          mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
         const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;  // mx cmx: its score
         const float m_new = fmaxf(m, mx * cmx);
         // conditional rescale: the reference moves only when the row maximum
