@@ -210,6 +210,116 @@ fa_status run_span_fwd(const SpanCall& a) {
   return launch_early(combine, parts, 256, 0, a.stream, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// workspace of the backward: the plan, the spans and their tiles' bounds, the dQ accumulator (more than
+// one key block), delta and LSE log2(e) padded to whole blocks, runs of cut items
+struct SpanBwdWorkspace {
+  size_t first_at, runs_at, cuts_at, lo_at, hi_at, bounds_at, dq_at, delta_at, lse_at, sums_at, total;
+  static SpanBwdWorkspace of(int B, int H, int Hkv, int N, int d) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t nb = ((size_t)N + 127) / 128, npad = nb * 128, entries = (size_t)B * nb;
+    SpanBwdWorkspace w;
+    w.first_at = up(sizeof(fa::SpanBwdPlan));
+    w.runs_at = w.first_at + up(((size_t)B + 1) * sizeof(int));
+    w.cuts_at = w.runs_at + up((entries + fa::kSpanBwdSlots) * sizeof(fa::SpanRun));
+    w.lo_at = w.cuts_at + up(fa::kSpanBwdSlots / 2 * sizeof(int4));
+    w.hi_at = w.lo_at + up(B * npad * sizeof(int));
+    w.bounds_at = w.hi_at + up(B * npad * sizeof(int));
+    w.dq_at = w.bounds_at + up(entries * sizeof(int4));
+    w.delta_at = w.dq_at + (nb > 1 ? up((size_t)B * H * N * d * sizeof(float)) : 0);
+    w.lse_at = w.delta_at + up((size_t)B * H * npad * sizeof(float));
+    w.sums_at = w.lse_at + up((size_t)B * H * npad * sizeof(float));
+    // (no run is shorter than a block, and an item of one is never cut)
+    const size_t blocks = (size_t)B * H * nb * nb, runs = H / Hkv * nb > 1 ? std::min<size_t>(fa::kSpanBwdSlots, blocks) : 0;
+    w.total = w.sums_at + runs * 2 * 128 * d * sizeof(float) + 256;
+    return w;
+  }
+};
+
+template <int D, int MOD>
+fa_status launch_span_bwd(const CUtensorMap* maps, const fa::SpanBwdParams& p, unsigned grid, cudaStream_t stream) {
+  using C = fa::BwdCfg<D, true>;
+  auto kernel = fa::fa_span_bwd_kernel<D, MOD>;
+  if (set_smem(kernel, fa::kSpanBwdSmemBytes<D>) != cudaSuccess) return FA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  static std::atomic<unsigned long long> known{0};
+  if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
+  return launch_early(kernel, dim3(grid), C::kThreads, fa::kSpanBwdSmemBytes<D>, stream, maps[0], maps[1], maps[2],
+                      maps[3], maps[4], maps[5], maps[6], p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+template <int D>
+fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void* q, const void* k, const void* v,
+                       const void* o, const void* dout, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                       int B, int H, int Hkv, float scale, float cap, cudaStream_t stream) {
+  const int N = view.N, nb = (N + 127) / 128, npad = nb * 128;
+  const SpanBwdWorkspace w = SpanBwdWorkspace::of(B, H, Hkv, N, D);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+  float* dq_acc = reinterpret_cast<float*>(ws + w.dq_at);
+  float* delta = reinterpret_cast<float*>(ws + w.delta_at);
+  float* lse2 = reinterpret_cast<float*>(ws + w.lse_at);
+  CUtensorMap maps[7];
+  if (!encode_bhnd(&maps[0], q, B * H, N, D) || !encode_bhnd(&maps[1], k, B * Hkv, N, D) ||
+      !encode_bhnd(&maps[2], v, B * Hkv, N, D) || !encode_bhnd(&maps[3], dout, B * H, N, D) ||
+      !encode_f32_rows(&maps[4], lse2, B * H, npad, 128) || !encode_f32_rows(&maps[5], delta, B * H, npad, 128) ||
+      !encode_dq_acc(&maps[6], dq_acc, B * H, N, D))
+    return FA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return FA_ERR_CUDA;
+  // with one key block each query block meets one item: its dQ is written where it is formed
+  const bool direct = nb == 1;
+  fa::SpanBwdParams p{};
+  p.rows.view = view;
+  p.rows.bounds = reinterpret_cast<int4*>(ws + w.bounds_at);
+  p.rows.R = N, p.rows.tiles = nb, p.rows.units = H, p.rows.kv_div = H / Hkv;
+  p.lo = reinterpret_cast<int*>(ws + w.lo_at);
+  p.hi = reinterpret_cast<int*>(ws + w.hi_at);
+  p.plan = reinterpret_cast<fa::SpanBwdPlan*>(ws);
+  p.runs = reinterpret_cast<fa::SpanRun*>(ws + w.runs_at);
+  p.first = reinterpret_cast<int*>(ws + w.first_at);
+  p.cuts = reinterpret_cast<int4*>(ws + w.cuts_at);
+  p.sums = reinterpret_cast<float*>(ws + w.sums_at);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.dq = direct ? static_cast<__nv_bfloat16*>(dq) : nullptr;
+  p.B = B, p.H = H, p.Hkv = Hkv, p.N = N, p.nb = nb;
+  // heads handed out together: enough for four times the CTAs' number of items, so that the longest
+  // ones are handed out well before the last (see causal_group_heads)
+  p.group_heads = (int)std::min<long long>(Hkv, (4LL * sms + nb) / (nb + 1));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = scale;
+  p.cap = span_cap(scale, cap);
+  p.inv_top = cap > 0.f ? 1.f / p.cap.top : 0.f;
+  p.slopes = slopes;
+  p.wait_limit_ns = wait_limit_ns();
+  p.debug_stall = g_debug_stall.load();
+  p.out_align32 = aligned32(dk) && aligned32(dv) && aligned32(dq);
+  const long long blocks = (long long)B * H * nb * nb;  // (at most: what a mask leaves out is not known here)
+  p.ctas = (int)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
+  const long long rows = (long long)B * H * npad, per_block = 256 / (D / 8);
+  const long long prep = std::min((rows + per_block - 1) / per_block, 152LL * 16) + ((long long)B * nb + 1) / 2;
+  if (launch_early(fa::fa_span_bwd_prep_kernel<D>, dim3((unsigned)prep), 256, 0, stream,
+                   static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, delta, lse2,
+                   direct ? static_cast<float*>(nullptr) : dq_acc, view, const_cast<int*>(p.lo), const_cast<int*>(p.hi),
+                   const_cast<int4*>(p.rows.bounds), B, npad, rows) != cudaSuccess)
+    return FA_ERR_CUDA;
+  if (launch_early(fa::fa_span_plan_kernel, dim3(1), 1024, 0, stream, p) != cudaSuccess) return FA_ERR_CUDA;
+  const unsigned grid = (unsigned)p.ctas;
+  const fa_status st = cap > 0.f ? (slopes ? launch_span_bwd<D, 3>(maps, p, grid, stream) : launch_span_bwd<D, 2>(maps, p, grid, stream))
+                                 : (slopes ? launch_span_bwd<D, 1>(maps, p, grid, stream) : launch_span_bwd<D, 0>(maps, p, grid, stream));
+  if (st != FA_OK) return st;
+  const long long n8 = direct ? 0 : (long long)B * H * N * D / 8;
+  const long long post = 4LL * fa::kSpanBwdSlots + std::min((n8 + 255) / 256, 152LL * 16);
+  return launch_early(fa::fa_span_bwd_post_kernel<D>, dim3((unsigned)post), 256, 0, stream, p, dq_acc,
+                      static_cast<__nv_bfloat16*>(dq), n8) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -245,7 +355,7 @@ fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* ke
 }
 
 size_t fa_span_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
-  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? 256 : 0;
+  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanBwdWorkspace::of(B, H, Hkv, N, d).total : 0;
 }
 
 fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
@@ -261,16 +371,9 @@ fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* ke
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, workspace})) != FA_OK) return st;
   if ((st = check_device_ptrs_given({key_begin, key_end, slopes})) != FA_OK) return st;
-  fa::SpanRowsParams p{};
-  p.view = {key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
-  p.score = {scale, cap, cap > 0.f ? 1.f / cap : 0.f, slopes};
-  p.q = static_cast<const __nv_bfloat16*>(q), p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v), p.o = static_cast<const __nv_bfloat16*>(o);
-  p.dout = static_cast<const __nv_bfloat16*>(dout), p.lse = const_cast<float*>(lse);
-  p.dq = static_cast<__nv_bfloat16*>(dq), p.dk = static_cast<__nv_bfloat16*>(dk), p.dv = static_cast<__nv_bfloat16*>(dv);
-  p.B = B, p.H = H, p.Hkv = Hkv;
-  d == 128 ? fa::span_rows_bwd<128><<<152 * 8, 256, 0, stream>>>(p) : fa::span_rows_bwd<64><<<152 * 8, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const fa::SpanView view{key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
+  return (d == 128 ? run_span_bwd<128> : run_span_bwd<64>)(view, slopes, q, k, v, o, dout, lse, dq, dk, dv, workspace, B, H,
+                                                           Hkv, scale, cap, stream);
 }
 
 size_t fa_paged_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d) {
