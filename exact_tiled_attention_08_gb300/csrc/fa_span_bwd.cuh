@@ -12,9 +12,9 @@
 // everything into runs, whose sums fa_span_bwd_post_kernel adds in order; the CTAs draw runs by
 // a ticket when they are about to need one.
 //
-// Masks.  A block that all of the query block's rows see whole takes none.  In others each
-// thread (one key) compares its key with the spans of its 64 queries; P and so dS are zero
-// outside them.
+// Masks.  A block that all of the query block's rows see whole takes none.  In others a lane
+// takes one query's span as bits of the warp's 32 keys, and the warp transposes them to
+// a thread's (one key's) bits of 32 queries; P and so dS are zero outside them.
 //
 // Scores as in the forward: P = 2^(s log2e - LSE log2e) with the capped and biased score
 // s, and dS = P o (dP - delta) o (1 - tanh^2); P (1 - tanh^2) is what is kept
@@ -322,6 +322,17 @@ __device__ __forceinline__ bool span_bwd_segment(SpanBwdBarriers* bar, int n, co
   if (!span_wait(&bar->seg_full[s], (n / kSpanBwdSegs) & 1, ctx, kSiteSpanBwdSeg)) return false;
   t = bar->seg[s];
   return !t.end;
+}
+
+// bit q of lane k's result: bit k of lane q's value
+__device__ __forceinline__ uint32_t span_transpose(uint32_t v, int lane) {
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint32_t m = j == 16 ? 0x0000ffffu : j == 8 ? 0x00ff00ffu : j == 4 ? 0x0f0f0f0fu : j == 2 ? 0x33333333u : 0x55555555u;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, v, j);
+    v = lane & j ? (v & ~m) | ((y >> j) & m) : (v & m) | ((y << j) & ~m);
+  }
+  return v;
 }
 
 // the block after (head, i)
@@ -724,20 +735,33 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
       for (int it = 0; alive && it < t.n; ++it, ++g) {
         const float* stat = reinterpret_cast<const float*>(sStat + (g % C::kStatEntries) * C::kStatBytes);
+        const int q0 = i * 128 + 64 * grp;
+        [[maybe_unused]] float slope2 = 0.f;
+        if constexpr (MOD & 1) slope2 = p.slopes[t.kvh * G + head] * 1.4426950408889634f;
+        span_bwd_step(t, head, i);
+        // the pairs that are seen, of this thread's key (a bit per query), while the scores are
+        // formed (the cut flag is a plain store before the Q tile's arrival)
+        if (!__all_sync(0xffffffffu, span_wait(&bar->ring_full[g % C::kQSlots], (g / C::kQSlots) & 1, ctx, kSiteBwdS))) {
+          alive = false;
+          break;
+        }
+        const bool cut = xbar->cut[g % C::kStatEntries];
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        if (__builtin_expect(cut, 0)) {
+          // a lane's query's bits of the warp's keys, transposed
+          const long long at = (long long)t.b * p.nb * 128 + q0 + lane;
+          const int key0 = key - lane;
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+            seen[ch] = span_transpose(span_bits(p.lo[at + 32 * ch] - key0, p.hi[at + 32 * ch] - key0), lane);
+        }
         // ---- phase 1: P^T = 2^(S^T c - L log2e) into TMEM, the fp32 values kept
         // in registers; issuer B starts dV as soon as all of P^T is written
-        // (the Q tile's barrier, long complete: the cut flag is a plain store before its arrival)
-        if (!__all_sync(0xffffffffu, span_wait(&bar->s_full, g & 1, ctx, kSiteBwdS) &&
-                                         span_wait(&bar->ring_full[g % C::kQSlots], (g / C::kQSlots) & 1, ctx, kSiteBwdS))) {
+        if (!__all_sync(0xffffffffu, span_wait(&bar->s_full, g & 1, ctx, kSiteBwdS))) {
           alive = false;
           break;
         }
         tc_fence_after();
-        const bool cut = xbar->cut[g % C::kStatEntries];
-        const int q0 = i * 128 + 64 * grp;
-        float slope2 = 0.f;
-        if (MOD & 1) slope2 = p.slopes[t.kvh * G + head] * 1.4426950408889634f;
-        span_bwd_step(t, head, i);
         float2 pf[2][16];
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
@@ -746,25 +770,25 @@ __global__ void __launch_bounds__(512, 1)
           tmem_ld32(tS + qc, sv[0]);
           tmem_wait_ld();
           reg_fence32(sv[0]);
-          // the pairs that are seen
-          uint32_t seen = 0xffffffffu;
-          if (__builtin_expect(cut, 0)) {
-            const int4* lo = reinterpret_cast<const int4*>(p.lo + (long long)t.b * p.nb * 128 + q0 + 32 * ch);
-            const int4* hi = reinterpret_cast<const int4*>(p.hi + (long long)t.b * p.nb * 128 + q0 + 32 * ch);
-            seen = 0;
+          [[maybe_unused]] bool small = true;
+          if constexpr (MOD >= 2) {
+            if (__builtin_expect(cut, 0)) {  // (what is not seen has no say in how the others are capped)
 #pragma unroll
-            for (int e4 = 0; e4 < 8; ++e4) {
-              const int4 a = lo[e4], z = hi[e4];
-              seen |= (key >= a.x && key < z.x ? 1u << (4 * e4) : 0u) | (key >= a.y && key < z.y ? 2u << (4 * e4) : 0u) |
-                      (key >= a.z && key < z.z ? 4u << (4 * e4) : 0u) | (key >= a.w && key < z.w ? 8u << (4 * e4) : 0u);
+              for (int e = 0; e < 32; ++e)
+                if (!((seen[ch] >> e) & 1u)) sv[0][e] = 0u;
             }
+            small = __all_sync(0xffffffffu, span_absmax(sv) <= p.cap.small);
           }
-          bool small = true;
-          if constexpr (MOD >= 2) small = !cut && __all_sync(0xffffffffu, span_absmax(sv) <= p.cap.small);
-          // the bias -slope2 |rel + e| of query e of the chunk
-          const int rel = q0 + 32 * ch - key;
-          const bool line = MOD & 1 ? __all_sync(0xffffffffu, rel >= 0 || rel <= -31) : true;
-          const float gl = rel >= 0 ? -slope2 : slope2, base = gl * (float)rel;
+          // the bias -slope2 |rel + e| of query e of the chunk: a line where all pairs (or, with a
+          // causal mask, all that are seen) lie on one side
+          [[maybe_unused]] const int rel = q0 + 32 * ch - key;
+          [[maybe_unused]] bool line = true;
+          [[maybe_unused]] float gl = 0.f, base = 0.f;
+          if constexpr (MOD & 1) {
+            line = p.rows.view.causal || __all_sync(0xffffffffu, rel >= 0 || rel <= -31);
+            gl = p.rows.view.causal || rel >= 0 ? -slope2 : slope2;
+            base = gl * (float)rel;
+          }
           uint32_t pk[16];
           auto scores = [&](auto near) {
 #pragma unroll
@@ -801,26 +825,25 @@ __global__ void __launch_bounds__(512, 1)
                   wt = __ffma2_rn(make_float2(-tn.x, -tn.y), tn, make_float2(1.f, 1.f));
                 }
                 float2 pe = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
-                if (!near.value) {  // (blocks seen in part)
-                  if (!((seen >> e) & 1u)) pe.x = 0.f;
-                  if (!((seen >> (e + 1)) & 1u)) pe.y = 0.f;
-                }
                 pk[2 * e4 + h] = pack_bf16x2(pe.x, pe.y);
-                if constexpr (MOD >= 2) {
-                  pe = __fmul2_rn(pe, wt);
-                  if (!near.value) {  // (a hidden score that is NaN)
-                    if (!((seen >> e) & 1u)) pe.x = 0.f;
-                    if (!((seen >> (e + 1)) & 1u)) pe.y = 0.f;
-                  }
-                }
+                if constexpr (MOD >= 2) pe = __fmul2_rn(pe, wt);
                 pf[ch][e / 2] = pe;
               }
             }
           };
-          if (__builtin_expect(small && line && !cut, 1))
+          if (MOD == 0 || __builtin_expect(small && line, 1))
             scores(std::true_type{});
           else
             scores(std::false_type{});
+          if (__builtin_expect(cut, 0)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const bool x = (seen[ch] >> (2 * e)) & 1u, y = (seen[ch] >> (2 * e + 1)) & 1u;
+              pf[ch][e] = make_float2(x ? pf[ch][e].x : 0.f, y ? pf[ch][e].y : 0.f);
+              pk[e] = MOD < 2 ? pack_bf16x2(pf[ch][e].x, pf[ch][e].y)
+                              : (x ? pk[e] & 0xffffu : 0u) | (y ? pk[e] & 0xffff0000u : 0u);
+            }
+          }
           // P^T of query groups qc/16 and qc/16 + 1 over the first 8 of their own columns
           tmem_st8(tS + qc, pk);
           tmem_st8(tS + qc + 16, pk + 8);

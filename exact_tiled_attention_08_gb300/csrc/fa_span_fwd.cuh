@@ -356,12 +356,12 @@ __device__ __forceinline__ bool span_segment(SpanBarriers* bar, int n, const Wai
 
 // multiplies a block's scores with mul and adds a bias of -slope2 |rel - c| to that of key c
 // (log2 units); rel: the row's position from the block's first key
-__device__ __forceinline__ void span_bias(uint32_t (&s)[4][32], float mul, float slope2, int rel) {
+__device__ __forceinline__ void span_bias(uint32_t (&s)[4][32], float mul, float slope2, int rel, bool causal) {
   const float relf = (float)rel;
-  if (__all_sync(0xffffffffu, rel >= 127 || rel <= 0)) {
-    // all keys on one side of the row: a line g c - g rel, as a value for each eight keys and
-    // offsets within them
-    const float g = rel > 0 ? slope2 : -slope2, base = -g * relf;
+  if (causal || __all_sync(0xffffffffu, rel >= 127 || rel <= 0)) {
+    // all keys (with a causal mask: all that are seen) on one side of the row: a line
+    // g c - g rel, as a value for each eight keys and offsets within them
+    const float g = causal || rel > 0 ? slope2 : -slope2, base = -g * relf;
     const float2 mul2 = make_float2(mul, mul);
     float2 off[4];
 #pragma unroll
@@ -824,9 +824,9 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap);
           }
-          if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase);
+          if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase, v.causal);
         }
-        if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase);
+        if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase, v.causal);
         if (__builtin_expect(cut, 0)) hide();
         float mx;
         if constexpr (C::kDualS && MOD == 0)
