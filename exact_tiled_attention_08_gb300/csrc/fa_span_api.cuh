@@ -293,7 +293,6 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   p.scale_log2 = scale * 1.4426950408889634f;
   p.scale = scale;
   p.cap = span_cap(scale, cap);
-  p.inv_top = cap > 0.f ? 1.f / p.cap.top : 0.f;
   p.slopes = slopes;
   p.wait_limit_ns = wait_limit_ns();
   p.debug_stall = g_debug_stall.load();

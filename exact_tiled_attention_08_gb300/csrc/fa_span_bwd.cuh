@@ -64,16 +64,16 @@ struct SpanBwdParams {
   float scale_log2;        // scale * log2(e)
   float scale;
   SpanCap cap;
-  float inv_top;           // 1 / (cap log2(e))
   const float* slopes;
   uint64_t wait_limit_ns;
   int debug_stall;
   int out_align32;
 };
 
-// Per row of each request and query head, padded to whole 128-row blocks: delta = sum dO O
-// (0 behind the rows) and LSE log2(e) (+inf behind them, and for rows without keys, so that
-// P = 0 there); the dQ accumulator, if there is one, is zeroed.  The blocks behind
+// Per row of each request and query head, padded to whole 128-row blocks: -delta, delta = sum dO O
+// (0 behind the rows) and -LSE log2(e) (-inf behind them, and for rows without keys, so that
+// P = 0 there; negated here, not 128 times in the main kernel's loop); the dQ accumulator, if
+// there is one, is zeroed.  The blocks behind
 // these write the queries' spans and their tiles' bounds (128 rows a block).
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(256)
     for (int off = kThreadsPerRow / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (in_range && sub == 0) {
       const float l = valid ? lse[row] : -CUDART_INF_F;
-      delta_pad[prow] = valid ? s : 0.f;
-      lse2_pad[prow] = l == -CUDART_INF_F ? CUDART_INF_F : l * 1.4426950408889634f;
+      delta_pad[prow] = valid ? -s : 0.f;
+      lse2_pad[prow] = l == -CUDART_INF_F ? -CUDART_INF_F : l * -1.4426950408889634f;
     }
   }
 }
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(512, 1)
   uint8_t* sRing = smem + 2 * C::kTileBytes;
   uint8_t* sDS = sRing + C::kSlots * C::kTileBytes;
   uint8_t* sStage = sDS + C::kDsBytes;
-  // query block g: entry g % kStatEntries = LSE*log2e [128], delta [128]
+  // query block g: entry g % kStatEntries = -LSE*log2e [128], -delta [128]
   uint8_t* sStat = sStage + C::kStageBytes;
   SpanBwdBarriers* xbar = reinterpret_cast<SpanBwdBarriers*>(sStat + C::kStatEntries * C::kStatBytes);
   BwdBarriers* bar = &xbar->b;
@@ -763,91 +763,63 @@ __global__ void __launch_bounds__(512, 1)
         }
         tc_fence_after();
         float2 pf[2][16];
+        auto probabilities = [&](auto masked) {
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          const int qc = 64 * grp + 32 * ch;  // first query column of this chunk
-          uint32_t sv[1][32];
-          tmem_ld32(tS + qc, sv[0]);
-          tmem_wait_ld();
-          reg_fence32(sv[0]);
-          [[maybe_unused]] bool small = true;
-          if constexpr (MOD >= 2) {
-            if (__builtin_expect(cut, 0)) {  // (what is not seen has no say in how the others are capped)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((seen[ch] >> e) & 1u)) sv[0][e] = 0u;
-            }
-            small = __all_sync(0xffffffffu, span_absmax(sv) <= p.cap.small);
-          }
-          // the bias -slope2 |rel + e| of query e of the chunk: a line where all pairs (or, with a
-          // causal mask, all that are seen) lie on one side
-          [[maybe_unused]] const int rel = q0 + 32 * ch - key;
-          [[maybe_unused]] bool line = true;
-          [[maybe_unused]] float gl = 0.f, base = 0.f;
-          if constexpr (MOD & 1) {
-            line = p.rows.view.causal || __all_sync(0xffffffffu, rel >= 0 || rel <= -31);
-            gl = p.rows.view.causal || rel >= 0 ? -slope2 : slope2;
-            base = gl * (float)rel;
-          }
-          uint32_t pk[16];
-          auto scores = [&](auto near) {
+          for (int ch = 0; ch < 2; ++ch) {
+            const int qc = 64 * grp + 32 * ch;  // first query column of this chunk
+            uint32_t sv[32];
+            tmem_ld32(tS + qc, sv);
+            tmem_wait_ld();
+            reg_fence32(sv);
+            [[maybe_unused]] const float rel = (float)(q0 + 32 * ch - key);  // of the chunk's first query
+            uint32_t pk[16];
 #pragma unroll
             for (int e4 = 0; e4 < 8; ++e4) {
-              // four queries' L*log2e (the same for every thread: a broadcast read)
+              // four queries' -L*log2e (the same for every thread: a broadcast read)
               const float4 l4 = *reinterpret_cast<const float4*>(stat + qc + 4 * e4);
-              [[maybe_unused]] const float at = MOD & 1 ? fmaf(gl, (float)(4 * e4), base) : 0.f;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int e = 4 * e4 + 2 * h;  // two queries at a time (packed fp32x2 arithmetic)
-                float2 nl = h ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
-                const float2 s2 = make_float2(__uint_as_float(sv[0][e]), __uint_as_float(sv[0][e + 1]));
-                if constexpr (MOD & 1) {
-                  if (near.value || line)
-                    nl = __fadd2_rn(nl, __fadd2_rn(make_float2(at, at), make_float2((2 * h) * gl, (2 * h + 1) * gl)));
-                  else
-                    nl = make_float2(fmaf(-slope2, fabsf((float)(rel + e)), nl.x), fmaf(-slope2, fabsf((float)(rel + e + 1)), nl.y));
-                }
+                float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                const float2 s2 = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                if constexpr (MOD & 1)
+                  nl = make_float2(fmaf(-slope2, fabsf(rel + (float)e), nl.x), fmaf(-slope2, fabsf(rel + (float)(e + 1)), nl.y));
                 float2 xs;
                 [[maybe_unused]] float2 wt;
                 if constexpr (MOD < 2) {
                   xs = __ffma2_rn(s2, make_float2(p.scale_log2, p.scale_log2), nl);
                 } else {
-                  float2 tn;  // the tanh
-                  if constexpr (near.value) {
-                    const float2 y = __fmul2_rn(s2, span_cap_small(s2, p.cap));
-                    xs = __fadd2_rn(y, nl);
-                    tn = __fmul2_rn(y, make_float2(p.inv_top, p.inv_top));
-                  } else {
-                    tn = make_float2(fmaf(-2.f, rcp_approx(ex2_approx(s2.x * p.cap.mul) + 1.f), 1.f),
-                                     fmaf(-2.f, rcp_approx(ex2_approx(s2.y * p.cap.mul) + 1.f), 1.f));
-                    xs = __ffma2_rn(tn, make_float2(p.cap.top, p.cap.top), nl);
-                  }
+                  // (the special-function unit is idle enough here: the forward's polynomial, with its
+                  // test and its other path, takes as many instructions)
+                  const float2 x = __fmul2_rn(s2, make_float2(p.cap.mul, p.cap.mul));
+                  const float2 d = __fadd2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.f, 1.f));
+                  const float2 tn = __ffma2_rn(make_float2(rcp_approx(d.x), rcp_approx(d.y)), make_float2(-2.f, -2.f),
+                                               make_float2(1.f, 1.f));  // the tanh
+                  xs = __ffma2_rn(tn, make_float2(p.cap.top, p.cap.top), nl);
                   wt = __ffma2_rn(make_float2(-tn.x, -tn.y), tn, make_float2(1.f, 1.f));
                 }
                 float2 pe = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
+                if constexpr (masked.value)
+                  pe = make_float2((seen[ch] >> e) & 1u ? pe.x : 0.f, (seen[ch] >> (e + 1)) & 1u ? pe.y : 0.f);
                 pk[2 * e4 + h] = pack_bf16x2(pe.x, pe.y);
-                if constexpr (MOD >= 2) pe = __fmul2_rn(pe, wt);
+                if constexpr (MOD >= 2) {
+                  pe = __fmul2_rn(pe, wt);
+                  if constexpr (masked.value)  // (a hidden product may be NaN)
+                    pe = make_float2((seen[ch] >> e) & 1u ? pe.x : 0.f, (seen[ch] >> (e + 1)) & 1u ? pe.y : 0.f);
+                }
                 pf[ch][e / 2] = pe;
               }
             }
-          };
-          if (MOD == 0 || __builtin_expect(small && line, 1))
-            scores(std::true_type{});
-          else
-            scores(std::false_type{});
-          if (__builtin_expect(cut, 0)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const bool x = (seen[ch] >> (2 * e)) & 1u, y = (seen[ch] >> (2 * e + 1)) & 1u;
-              pf[ch][e] = make_float2(x ? pf[ch][e].x : 0.f, y ? pf[ch][e].y : 0.f);
-              pk[e] = MOD < 2 ? pack_bf16x2(pf[ch][e].x, pf[ch][e].y)
-                              : (x ? pk[e] & 0xffffu : 0u) | (y ? pk[e] & 0xffff0000u : 0u);
-            }
+            // P^T of query groups qc/16 and qc/16 + 1 over the first 8 of their own columns
+            tmem_st8(tS + qc, pk);
+            tmem_st8(tS + qc + 16, pk + 8);
           }
-          // P^T of query groups qc/16 and qc/16 + 1 over the first 8 of their own columns
-          tmem_st8(tS + qc, pk);
-          tmem_st8(tS + qc + 16, pk + 8);
-        }
+        };
+        // (two copies: with the masks in one the loop is 9 % slower also where nothing is masked)
+        if (__builtin_expect(cut, 0))
+          probabilities(std::true_type{});
+        else
+          probabilities(std::false_type{});
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar->p_done);
@@ -877,7 +849,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int e = 4 * e4 + 2 * h;
-              const float2 nd = h ? make_float2(-d4.z, -d4.w) : make_float2(-d4.x, -d4.y);
+              const float2 nd = h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
               const float2 dpd = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd);
               const float2 dse = __fmul2_rn(pf[ch][e / 2], dpd);
               dk[2 * e4 + h] = pack_bf16x2(dse.x, dse.y);
