@@ -124,11 +124,19 @@ __global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, i
 // [0, 0.36] (degree 4, by Remez exchange on the relative error: 7.3e-8), in powers of the product q k
 // itself; beyond it 1 - 2 / (1 + e^2x), whose absolute error (2^-22) is what counts there.
 // A warp takes the polynomial where all of its products of a block allow it.
+//
+// With caps of 30 and more it asks for less: no product above 0.6, and a row's largest not below
+// -0.2.  Products below -0.6, where the polynomial goes its own way downwards (to the
+// ninth power), then weigh less than e^-(0.53 - 0.2) 30 = 5e-5 in their row, and their weights'
+// errors, e^-(tanh|x| - 0.2) 30 times 30 |x G(x^2) - tanh x|, are below 1e-8 everywhere.  And a product of
+// -10 gives a weight of 0, so that it stands for a key that is not seen.
 struct SpanCap {
-  float mul;    // 2 log2(e) scale / cap
-  float small;  // products up to there take the polynomial: 0.6 cap / scale
-  float top;    // cap log2(e)
-  float d[5];   // q k (d[0] + d[1] (q k)^2 + ...)
+  float mul;     // 2 log2(e) scale / cap
+  float small;   // products up to there take the polynomial: 0.6 cap / scale
+  float low;     // the lowest largest one: -0.2 cap / scale
+  float hidden;  // -10 cap / scale; 0: a cap below 30, or coefficients that fp32 does not hold
+  float top;     // cap log2(e)
+  float d[5];    // q k (d[0] + d[1] (q k)^2 + ...)
 };
 
 // score / product of small products

@@ -84,6 +84,8 @@ fa::SpanCap span_cap(float scale, float cap) {
     held = held && std::isnormal(c.d[i]);
   }
   c.small = held ? 0.6f * cap / scale : -1.f;
+  c.low = -0.2f * cap / scale;
+  c.hidden = held && cap >= 30.f && std::isfinite(10.f * cap / scale) ? -10.f * cap / scale : 0.f;
   return c;
 }
 

@@ -802,38 +802,56 @@ __global__ void __launch_bounds__(384, 1)
 
         const int kbase = j * 128;
         const bool cut = kbase < lo_cut || kbase + 128 > hi_cut;
-        auto hide = [&] {
+        auto hide = [&](float value) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t bits = span_bits(row_lo - kbase - 32 * c, row_hi - kbase - 32 * c);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-CUDART_INF_F);
+              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(value);
           }
         };
-        // Small products are capped by the polynomial, in MOD 2 inside the exponent's argument
-        // below; others, and blocks seen in part (where what is not seen has no say in it), in place.
+        auto row_max = [&] { return fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3])); };
+        // MOD 2 and 3: small products are capped by the polynomial, in MOD 2 inside the exponent's
+        // argument below; others in place.  What is not seen has no say in it.
         bool fused = false;
+        float mx = 0.f;
         if constexpr (MOD >= 2) {
-          const bool small = !cut && __all_sync(0xffffffffu, !there || span_absmax(sr) <= p.cap.small);
+          bool small;
+          if (MOD == 2 && p.cap.hidden < 0.f) {
+            if (__builtin_expect(cut, 0)) hide(p.cap.hidden);
+            mx = row_max();
+            small = mx <= p.cap.small && (mx >= p.cap.low || mx <= p.cap.hidden);
+          } else {
+            mx = row_max();
+            small = !cut && span_absmax(sr) <= p.cap.small;
+          }
+          small = __all_sync(0xffffffffu, !there || small);
           fused = MOD == 2 && small;
           if (MOD == 3 && __builtin_expect(small, 1)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) span_cap32_small(sr[c], p.cap);
-          } else if (!small) {
+          } else if (__builtin_expect(!small, 0)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) span_cap32(sr[c], p.cap);
+            if (cut) hide(-CUDART_INF_F);
+            mx = row_max();
           }
-          if (MOD == 3) span_bias(sr, 1.f, slope2, pos - kbase, v.causal);
+          if constexpr (MOD == 3) {
+            span_bias(sr, 1.f, slope2, pos - kbase, v.causal);
+            mx = row_max();
+          }
+        } else {
+          if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase, v.causal);
+          if (__builtin_expect(cut, 0)) hide(-CUDART_INF_F);
+          if constexpr (C::kDualS && MOD == 0)
+            mx = fmaxf(cut ? cross_max64(sr[0], sr[1]) : mx_a, cross_max64(sr[2], sr[3]));
+          else
+            mx = row_max();
         }
-        if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase, v.causal);
-        if (__builtin_expect(cut, 0)) hide();
-        float mx;
-        if constexpr (C::kDualS && MOD == 0)
-          mx = fmaxf(cut ? cross_max64(sr[0], sr[1]) : mx_a, cross_max64(sr[2], sr[3]));
-        else
-          mx = fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3]));
-        const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;  // mx cmx: its score
+        // mx cmx: the largest score; a row that sees nothing of the block has none
+        const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;
+        if (MOD == 2 && fused && mx <= p.cap.hidden) mx = -CUDART_INF_F;
         const float m_new = fmaxf(m, mx * cmx);
         // conditional rescale: the reference moves only when the row maximum
         // rose by more than the threshold (always from -inf: no key so far)
@@ -849,7 +867,8 @@ __global__ void __launch_bounds__(384, 1)
             m = m_new;
           }
         }
-        const float ref = fmaxf(m, -3.402823466e38f);  // (finite for a row without keys so far: every P is 2^-inf = 0)
+        // (finite for a row without keys so far, whose every P is 2^-inf, or of hidden products, = 0)
+        const float ref = MOD == 2 ? (m == -CUDART_INF_F ? 0.f : m) : fmaxf(m, -3.402823466e38f);
         const float2 c2 = make_float2(cj, cj);
         const float2 mneg2 = make_float2(-ref, -ref);
         float2 acc[4];
