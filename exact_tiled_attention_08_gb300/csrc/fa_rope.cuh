@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     if (kPaged) {
       start = min(max(start, 0), p.C);
       here = here && t.n < min(p.chunks ? __ldg(p.chunks + t.b) : p.N, p.C - start);
+      if (!__any_sync(0xffffffffu, here)) continue;  // (padding is not read)
     }
     const int pos = p.positions ? __ldg(p.positions + (t.valid ? t.token : 0)) : start + t.n;
     const long long row = (long long)start + t.n;  // row of this token in k_out and v_out
@@ -352,15 +353,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     if (p.q.ptr && t.h0 < p.H)
       rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.q), p.q.head,
                                                    p.q_out + ((long long)t.b * p.H * p.N + t.n) * D,
-                                                   (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1, t.valid, here,
-                                                   p.q_weight, p.eps);
+                                                   (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1,
+                                                   kPaged ? here : t.valid, here, p.q_weight, p.eps);
     if (p.k.ptr)
       rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.k), p.k.head, k_to, k_next, max(t.h0 - p.H, 0),
-                                                   min(t.h1 - p.H, p.Hkv), e0, e1, t.valid, stored, p.k_weight, p.eps);
+                                                   min(t.h1 - p.H, p.Hkv), e0, e1, kPaged ? here : t.valid, stored,
+                                                   p.k_weight, p.eps);
     if (p.v.ptr)
       rope_fwd_heads<D, kInterleaved, false, false>(turn, ring, in(p.v), p.v.head, v_to, v_next,
-                                                    max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1, t.valid,
-                                                    stored, nullptr, 0.f);
+                                                    max(t.h0 - p.H - p.Hkv, 0), t.h1 - p.H - p.Hkv, e0, e1,
+                                                    kPaged ? here : t.valid, stored, nullptr, 0.f);
   }
 }
 
