@@ -119,20 +119,17 @@ struct CrossFwdPlan {
   }
 };
 
-// Clusters of 8, 4 and 2 CTAs that the device holds at once (15, 36 and 76 on a
-// GB300 whose 152 SMs are free), asked once per device.
-template <int D, bool TREE>
-fa::CrossClusterFit cross_cluster_fit(int dev) {
-  static std::atomic<unsigned long long> known[64];  // by device: the three numbers and a bit that says so
+// Clusters of 8, 4 and 2 CTAs of a kernel that the device holds at once (15, 36 and 76 on a
+// GB300 whose 152 SMs are free, at a CTA per SM), asked once per device.
+template <typename Kernel>
+fa::CrossClusterFit cluster_fit(Kernel kernel, int threads, int smem, int dev, std::atomic<unsigned long long>* known) {
   fa::CrossClusterFit fit{};
   const unsigned long long was = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
   if (was) {
     for (int i = 0; i < 3; ++i) fit.clusters[i] = (int)(was >> (16 * i) & 0xffff);
     return fit;
   }
-  using C = fa::CrossCfg<D>;
-  auto kernel = fa::fa_cross_fwd_kernel<D, TREE, false, true>;
-  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return fit;
+  if (set_smem(kernel, smem) != cudaSuccess) return fit;
   unsigned long long found = 1ull << 63;
   for (int i = 0; i < 3; ++i) {
     cudaLaunchAttribute attr[1];
@@ -141,8 +138,8 @@ fa::CrossClusterFit cross_cluster_fit(int dev) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((8u >> i) * fa::kCrossMaxCtas, 1, 1);
-    cfg.blockDim = dim3((unsigned)C::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)C::kSmemBytes;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
@@ -155,6 +152,12 @@ fa::CrossClusterFit cross_cluster_fit(int dev) {
   }
   if (dev < 64) known[dev].store(found, std::memory_order_relaxed);
   return fit;
+}
+template <int D, bool TREE>
+fa::CrossClusterFit cross_cluster_fit(int dev) {
+  using C = fa::CrossCfg<D>;
+  static std::atomic<unsigned long long> known[64];  // by device: the three numbers and a bit that says so
+  return cluster_fit(fa::fa_cross_fwd_kernel<D, TREE, false, true>, C::kThreads, C::kSmemBytes, dev, known);
 }
 
 template <int D, bool TREE>

@@ -9,6 +9,7 @@
 #include "fa_cross_bwd.cuh"
 #include "fa_span.cuh"
 #include "fa_span_fwd.cuh"
+#include "fa_span_few.cuh"
 #include "fa_span_bwd.cuh"
 #include "fa_rope.cuh"
 #include "fa_cross_api.cuh"

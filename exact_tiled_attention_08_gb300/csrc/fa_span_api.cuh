@@ -113,17 +113,16 @@ struct SpanFwdPlan {
   }
 };
 
-template <int D, int MOD, bool PAIR, bool CLUSTER>
+template <int D, int MOD, bool PAIR>
 fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams& p, unsigned grid, cudaStream_t stream) {
   using C = fa::CrossCfg<D>;
-  auto kernel = fa::fa_span_fwd_kernel<D, MOD, PAIR, CLUSTER>;
+  auto kernel = fa::fa_span_fwd_kernel<D, MOD, PAIR>;
   if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   static std::atomic<unsigned long long> known{0};
   if (!has_launch_regs(kernel, C::kLaunchRegs, dev, known)) return FA_ERR_CUDA;
-  return launch_early_clusters(kernel, dim3(grid), CLUSTER ? p.cluster : 1, C::kThreads, C::kSmemBytes, stream, maps[0],
-                               maps[1], maps[2], p) == cudaSuccess
+  return launch_early(kernel, dim3(grid), C::kThreads, C::kSmemBytes, stream, maps[0], maps[1], maps[2], p) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -131,9 +130,43 @@ fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams& p, u
 template <int D, int MOD>
 fa_status launch_span_form(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
                            cudaStream_t stream) {
-  if (p.cluster > 1) return launch_span_fwd<D, MOD, false, true>(maps, p, grid, stream);
-  return pair ? launch_span_fwd<D, MOD, true, false>(maps, p, grid, stream)
-              : launch_span_fwd<D, MOD, false, false>(maps, p, grid, stream);
+  return pair ? launch_span_fwd<D, MOD, true>(maps, p, grid, stream) : launch_span_fwd<D, MOD, false>(maps, p, grid, stream);
+}
+
+// Clusters of 8, 4 and 2 CTAs of the kernel for few rows that the device holds at once, asked once per device.
+template <int D, int R>
+fa::CrossClusterFit few_cluster_fit(int dev) {
+  using C = fa::FewCfg<D, R>;
+  static std::atomic<unsigned long long> known[64];  // by device: the three numbers and a bit that says so
+  return cluster_fit(fa::fa_span_few_kernel<D, R, true>, C::kThreads, C::kSmemBytes, dev, known);
+}
+
+template <int D, int R>
+fa_status launch_span_few(const CUtensorMap* maps, fa::SpanFwdParams& p, unsigned grid, int sms, cudaStream_t stream) {
+  using C = fa::FewCfg<D, R>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  // One request of a length that only the device knows counts as half of what its pages hold, as
+  // in the cross forward.
+  const bool paged = p.rows.view.table != nullptr;
+  const long long items = (long long)p.B * p.rows.units;
+  int blocks = (p.rows.view.C + 127) / 128;
+  if (p.B == 1 && paged && blocks > 2) blocks = (blocks + 1) / 2;
+  p.cluster = fa::cross_cluster(items, blocks, p.rows.R, p.B == 1 || !paged, std::min(sms, fa::kCrossMaxCtas),
+                                few_cluster_fit<D, R>(dev));
+  if (p.cluster > 1) {
+    auto kernel = fa::fa_span_few_kernel<D, R, true>;
+    if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
+    return launch_early_clusters(kernel, dim3((unsigned)(items * p.cluster)), p.cluster, C::kThreads, C::kSmemBytes, stream,
+                                 maps[0], maps[1], maps[2], p) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+  }
+  auto kernel = fa::fa_span_few_kernel<D, R, false>;
+  if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
+  return launch_early(kernel, dim3(grid), C::kThreads, C::kSmemBytes, stream, maps[0], maps[1], maps[2], p) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 template <int D>
@@ -164,8 +197,10 @@ fa_status run_span_fwd(const SpanCall& a) {
   const fa::SpanView& view = a.rows.view;
   const bool by_row = view.begin || view.end;
   const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.rows.units, a.rows.R, view.C, a.d, !view.table);
+  // (up to 32 rows per unit: the kernel that has the keys on the tensor memory's lanes)
+  const int few = a.rows.R <= 16 ? 16 : a.rows.R <= 32 ? 32 : 0;
   CUtensorMap maps[3];
-  if (!encode_bhnd(&maps[0], a.q, a.B * a.rows.units, a.rows.R, a.d) ||
+  if (!encode_bhnd(&maps[0], a.q, a.B * a.rows.units, a.rows.R, a.d, few ? few : 128) ||
       !encode_pages(&maps[1], a.k, a.tokens, a.Hkv, a.pages, a.box_rows, a.d) ||
       !encode_pages(&maps[2], a.v, a.tokens, a.Hkv, a.pages, a.box_rows, a.d))
     return FA_ERR_CUDA;
@@ -202,9 +237,16 @@ fa_status run_span_fwd(const SpanCall& a) {
       return FA_ERR_CUDA;
   }
   const unsigned grid = (unsigned)std::min(plan.ctas, sms);
-  const fa_status st = a.d == 128 ? launch_span_mod<128>(maps, p, plan.pair, grid, a.stream)
-                                  : launch_span_mod<64>(maps, p, plan.pair, grid, a.stream);
-  if (st != FA_OK || !plan.cuts) return st;
+  fa_status st;
+  if (few)
+    st = a.d == 128 ? (few == 16 ? launch_span_few<128, 16>(maps, p, grid, sms, a.stream)
+                                 : launch_span_few<128, 32>(maps, p, grid, sms, a.stream))
+                    : (few == 16 ? launch_span_few<64, 16>(maps, p, grid, sms, a.stream)
+                                 : launch_span_few<64, 32>(maps, p, grid, sms, a.stream));
+  else
+    st = a.d == 128 ? launch_span_mod<128>(maps, p, plan.pair, grid, a.stream)
+                    : launch_span_mod<64>(maps, p, plan.pair, grid, a.stream);
+  if (st != FA_OK || !plan.cuts || p.cluster > 1) return st;
   const int per_block = plan.pair ? 32 : 8;  // rows of a block
   const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
   auto combine = a.d == 128 ? (plan.pair ? fa::fa_span_combine_kernel<128, true> : fa::fa_span_combine_kernel<128, false>)

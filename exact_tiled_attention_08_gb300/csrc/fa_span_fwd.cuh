@@ -4,8 +4,8 @@
 // The arithmetic, the roles and the pipeline are those of fa_cross_fwd_kernel (TMA
 // fills a ring of K and V tiles, one thread issues S = Q K^T, one O += P V, two softmax
 // warpgroups hold a row of scores per thread; two row tiles per item, PAIR, or one
-// whose key blocks go to the warpgroups in turn, ALT; clusters for a few items of
-// one tile).  What differs:
+// whose key blocks go to the warpgroups in turn, ALT).  Up to 32 rows per unit go to
+// fa_span_few_kernel.  What differs:
 //
 // Work.  An item is a tile (pair) of query rows of a unit (SpanRows) with the blocks of
 // 128 keys that any of its rows sees; items cost what they have of them.  Where enough of them
@@ -52,7 +52,7 @@ struct SpanFwdParams {
   int part_rows;     // rows of a part: 256 (PAIR) or R (ALT)
   int B, H;
   int row_tiles;     // row tiles (PAIR: pairs of them) per unit
-  int cluster;       // CLUSTER: CTAs per item
+  int cluster;       // fa_span_few_kernel: CTAs per item, joined in a cluster (1: none)
   int pages;         // pages in the pool
   float scale_log2;  // without a cap
   SpanCap cap;
@@ -182,16 +182,15 @@ __device__ __forceinline__ bool span_dirty(const SpanSeg& s, int j) {
   return (s.flags & kSegDirtyFront && j == s.j0) || (s.flags & kSegDirtyBack && j == s.j1 - 1);
 }
 
-// How the CTAs divide the items, by all 384 threads.  `scratch` (kMergeBytes of shared memory)
+// How the CTAs divide the items, by all T threads.  `scratch` (kMergeBytes of shared memory)
 // keeps the order of the entries with PAIR.  More than kSpanRounds items a CTA even out: they
 // go whole, head by head but where a causal mask alone makes the last row tiles the longest.  Fewer: the slowest CTA's items are added up for each way of
 // numbering them, and the items go whole where that ends no later than even shares and the
 // join of what they cut.
-constexpr int kSpanRounds = 32, kSpanThreads = 384;
-template <bool PAIR>
+constexpr int kSpanRounds = 32;
+template <bool PAIR, int T>
 __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scratch, SpanPlace* place, long long* all,
                                               long long* share_end) {
-  constexpr int T = kSpanThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.row_tiles, U = p.rows.units, G = gridDim.x, c = blockIdx.x;
   const long long count = (long long)E * U;
@@ -206,8 +205,8 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
   }
   uint16_t* order = static_cast<uint16_t*>(scratch);                   // [T]
   int* sums = reinterpret_cast<int*>(order + T);                       // [160] places of each CTA's whole items
-  long long* part = reinterpret_cast<long long*>(sums + 160);          // [12]
-  static_assert(kCrossMaxCtas <= 160 && T * 2 + 160 * 4 + 12 * 8 <= CrossCfg<128>::kMergeBytes, "a sum for each CTA");
+  long long* part = reinterpret_cast<long long*>(sums + 160);          // [T / 32]
+  static_assert(kCrossMaxCtas <= 160 && T >= 160 && T % 64 == 0 && T * 2 + 160 * 4 + T / 4 <= CrossCfg<128>::kMergeBytes, "a sum for each CTA");
   if (tid == 0) *place = SpanPlace{0, 0, 0, 0, kSpanShares};
   const int chunk = (E + T - 1) / T, e0 = min(E, tid * chunk), e1 = min(E, e0 + chunk);
   const bool sorted = PAIR && E <= T;  // a thread per entry
@@ -277,7 +276,7 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
       if (PAIR && pass == 1) continue;
       long long before = 0;
 #pragma unroll 1
-      for (int w = 0; w < 12; ++w) {
+      for (int w = 0; w < T / 32; ++w) {
         if (w == warp) before = total;
         total += part[w];
       }
@@ -299,13 +298,6 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
       pass = 2;
     }
   }
-}
-
-// The share of a cluster's item, by one thread.
-__device__ __forceinline__ void span_cluster_share(const SpanFwdParams& p, SpanPlace* place) {
-  const int k = blockIdx.x / p.cluster, rank = blockIdx.x - k * p.cluster, e = k / p.rows.units;
-  const int n = SpanItem<false>(p, e).n, j0 = rank * n / p.cluster, j1 = (rank + 1) * n / p.cluster;
-  *place = SpanPlace{e, k - e * p.rows.units, j0 + kCrossStart, j1 - j0, kSpanShares};
 }
 
 // (as CrossBarriers, and the segments)
@@ -347,11 +339,112 @@ __device__ __forceinline__ bool span_wait(uint64_t* bar, uint32_t parity, const 
 }
 
 // The n-th segment; false: there are no more (or the wait ran out).
-__device__ __forceinline__ bool span_segment(SpanBarriers* bar, int n, const WaitCtx& ctx, const SpanSeg*& w) {
+template <class Bar>
+__device__ __forceinline__ bool span_segment(Bar* bar, int n, const WaitCtx& ctx, const SpanSeg*& w) {
   const int s = n % kSpanSegs;
   if (!span_wait(&bar->seg_full[s], (n / kSpanSegs) & 1, ctx, kSiteSpanSeg)) return false;
   w = &bar->seg[s];
   return !(w->flags & kSegEnd);
+}
+
+// The loading warp: works out the segments, publishes them, and fills Q's two buffers (QBYTES
+// each, atoms of 64 columns QATOM bytes apart) and the ring of K and V tiles, a lane per page.
+template <class C, bool PAIR, int QBYTES, int QATOM, class Bar>
+__device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUtensorMap* map_q, const CUtensorMap* map_k,
+                                                 const CUtensorMap* map_v, Bar* bar, const uint16_t* order, uint8_t* sQ,
+                                           uint8_t* sKV, const WaitCtx& ctx) {
+  const SpanView& v = p.rows.view;
+  const int lane = threadIdx.x & 31;
+  SpanPlace at = bar->place;
+  SpanSeg w{};
+  const int shift = v.page_shift, box_rows = v.table ? min(1 << shift, 128) : 128;
+  const int boxes = 128 / box_rows;
+  int loads = 0, nq = 0;  // K and V tiles, in turn
+  bool ok = true;
+  // the page of this lane's part of block j, or -1: nothing there that a row sees
+  auto page_of = [&](int j) -> int {
+    if (lane >= boxes) return -1;
+    const int key = j * 128 + lane * box_rows, i = key >> shift;
+    if (key >= w.hi || key + box_rows <= w.lo) return -1;
+    const int page = v.table[(long long)w.b * v.width + i];
+    return page >= 0 && page < p.pages ? page : -1;
+  };
+  auto load_q = [&](int qs) {
+    if (lane == 0) {
+      const int tiles = w.flags & kSegTwo ? 2 : 1;
+      mbar_arrive_expect_tx(&bar->q_full[qs], tiles * QBYTES);
+      for (int t = 0; t < tiles; ++t)
+        for (int a = 0; a < C::kAtoms; ++a)
+          tma_load_3d(sQ + (PAIR ? t : qs) * QBYTES + a * QATOM, map_q, &bar->q_full[qs], a * 64,
+                      w.row0 + 128 * t, w.b * p.rows.units + w.u);
+    }
+    __syncwarp();
+  };
+#pragma unroll 1
+  while (ok) {
+    const bool more = span_next<PAIR>(p, order, at, w);
+    if (!more) w.flags = kSegEnd;
+    // the segment for the other warps, once they have done with the one in its place
+    const int s = nq % kSpanSegs;
+    ok = __all_sync(0xffffffffu, span_wait(&bar->seg_empty[s], ((nq / kSpanSegs) & 1) ^ 1, ctx, kSiteSpanSegFree));
+    if (!ok) break;
+    if (lane == 0) {
+      bar->seg[s] = w;
+      mbar_arrive(&bar->seg_full[s]);
+    }
+    __syncwarp();
+    if (!more) break;
+    const int kvh = w.u / p.rows.kv_div;
+    const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
+    int page = v.table ? page_of(w.j0) : 0;
+    // a later segment's first key block needs only ring slots: it goes out
+    // before the queries, whose buffer an earlier segment may still be reading
+    if (nq == 0) load_q(qs);
+    ++nq;
+#pragma unroll 1
+    for (int j = w.j0; ok && j < w.j1; ++j) {
+      const int next = v.table && j + 1 < w.j1 ? page_of(j + 1) : 0;  // (asked for a block ahead)
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int g = loads >> 1, slot = C::slot(kv, g);
+        ok = __all_sync(0xffffffffu,
+                        span_wait(&bar->kv_empty[slot], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int row = !v.table ? j * 128 : boxes > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_4d(sKV + slot * C::kTileBytes + a * 16384 + lane * box_rows * 128, kv ? map_v : map_k,
+                        &bar->kv_full[slot], a * 64, row, kvh, v.table ? page : w.b);
+        }
+        ++loads;
+      }
+      if (ok && j == w.j0 && nq > 1) {
+        if (use > 0)
+          ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
+        if (ok)
+          load_q(qs);
+        else
+          --nq;  // (these queries were not asked for)
+      }
+      page = next;
+    }
+  }
+  // every copy this warp started must land before the CTA can exit
+  if (lane == 0) {
+    for (int s = 0; s < (PAIR ? 1 : 2); ++s) {
+      const int uses = PAIR ? nq : (nq + 1 - s) >> 1;
+      if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
+    }
+#pragma unroll 1
+    for (int s = 0; s < C::kSlots; ++s) {
+      // loads into slot s
+      const bool vslot = s >= C::kKSlots;
+      const int n = vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
+      if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
+    }
+  }
 }
 
 // multiplies a block's scores with mul and adds a bias of -slope2 |rel - c| to that of key c
@@ -394,14 +487,12 @@ __device__ __forceinline__ uint32_t span_bits(int from, int to) {
   return below & ~before;
 }
 
-// PAIR: two row tiles per item.  CLUSTER: a cluster of p.cluster CTAs per item (not with
-// PAIR).  MOD: 0 plain scores, 1 with a bias, 2 capped, 3 both.
-template <int D, int MOD, bool PAIR, bool CLUSTER>
+// PAIR: two row tiles per item.  MOD: 0 plain scores, 1 with a bias, 2 capped, 3 both.
+template <int D, int MOD, bool PAIR>
 __global__ void __launch_bounds__(384, 1)
     fa_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
   using C = CrossCfg<D>;
-  static_assert(!(PAIR && CLUSTER), "clusters take one row tile");
   // The issuing threads' loops over the two row tiles: one copy of the products at d = 128, where
   // the kernel's loops together outgrow the instruction cache (H=32/8 N=8192, two requests, causal:
   // 814 us, and 904 with two copies); at d = 64 the shorter products outrun a loop (76 and 78 us).
@@ -412,7 +503,7 @@ __global__ void __launch_bounds__(384, 1)
     grid_wait();
     if (threadIdx.x == 0) {
       atomicCAS(&g_fa_device_status, 0u, kStatusBadSmem);
-      if (!CLUSTER) p.meta[blockIdx.x].split = 0;
+      p.meta[blockIdx.x].split = 0;
     }
     return;
   }
@@ -461,12 +552,7 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_map(&map_v);
   }
   grid_wait();
-  if (CLUSTER) {
-    if (tid < 128) sMerge[tid] = -CUDART_INF_F;  // no part so far
-    if (warp == 10 && lane == 0) span_cluster_share(p, &bar->place);
-  } else {
-    span_schedule<PAIR>(p, sMerge, &bar->place, &bar->total, &bar->end);
-  }
+  span_schedule<PAIR, C::kThreads>(p, sMerge, &bar->place, &bar->total, &bar->end);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -476,98 +562,9 @@ __global__ void __launch_bounds__(384, 1)
   if (warp >= 8) {
     setmaxnreg_dec<C::kMiscRegs>();
     if (warp == 9) {
-      // ------------------------------------------------------------------ TMA producer (a lane per page)
-      const uint16_t* order = reinterpret_cast<const uint16_t*>(sMerge);
-      SpanPlace at = bar->place;
-      SpanSeg w{};
-      const int shift = v.page_shift, box_rows = v.table ? min(1 << shift, 128) : 128;
-      const int boxes = 128 / box_rows;
-      int loads = 0, nq = 0;  // K and V tiles, in turn
-      bool ok = true;
-      // the page of this lane's part of block j, or -1: nothing there that a row sees
-      auto page_of = [&](int j) -> int {
-        if (lane >= boxes) return -1;
-        const int key = j * 128 + lane * box_rows, i = key >> shift;
-        if (key >= w.hi || key + box_rows <= w.lo) return -1;
-        const int page = v.table[(long long)w.b * v.width + i];
-        return page >= 0 && page < p.pages ? page : -1;
-      };
-      auto load_q = [&](int qs) {
-        if (lane == 0) {
-          const int tiles = w.flags & kSegTwo ? 2 : 1;
-          mbar_arrive_expect_tx(&bar->q_full[qs], tiles * C::kTileBytes);
-          for (int t = 0; t < tiles; ++t)
-            for (int a = 0; a < C::kAtoms; ++a)
-              tma_load_3d(sQ + (PAIR ? t : qs) * C::kTileBytes + a * 16384, &map_q, &bar->q_full[qs], a * 64,
-                          w.row0 + 128 * t, w.b * p.rows.units + w.u);
-        }
-        __syncwarp();
-      };
-#pragma unroll 1
-      while (ok) {
-        const bool more = span_next<PAIR>(p, order, at, w);
-        if (!more) w.flags = kSegEnd;
-        // the segment for the other warps, once they have done with the one in its place
-        const int s = nq % kSpanSegs;
-        ok = __all_sync(0xffffffffu, span_wait(&bar->seg_empty[s], ((nq / kSpanSegs) & 1) ^ 1, ctx, kSiteSpanSegFree));
-        if (!ok) break;
-        if (lane == 0) {
-          bar->seg[s] = w;
-          mbar_arrive(&bar->seg_full[s]);
-        }
-        __syncwarp();
-        if (!more) break;
-        const int kvh = w.u / p.rows.kv_div;
-        const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-        int page = v.table ? page_of(w.j0) : 0;
-        // a later segment's first key block needs only ring slots: it goes out
-        // before the queries, whose buffer an earlier segment may still be reading
-        if (nq == 0) load_q(qs);
-        ++nq;
-#pragma unroll 1
-        for (int j = w.j0; ok && j < w.j1; ++j) {
-          const int next = v.table && j + 1 < w.j1 ? page_of(j + 1) : 0;  // (asked for a block ahead)
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const int g = loads >> 1, slot = C::slot(kv, g);
-            ok = __all_sync(0xffffffffu,
-                            span_wait(&bar->kv_empty[slot], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty));
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
-            __syncwarp();
-            if (lane < boxes) {
-              const int row = !v.table ? j * 128 : boxes > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
-              for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_4d(sKV + slot * C::kTileBytes + a * 16384 + lane * box_rows * 128, kv ? &map_v : &map_k,
-                            &bar->kv_full[slot], a * 64, row, kvh, v.table ? page : w.b);
-            }
-            ++loads;
-          }
-          if (ok && j == w.j0 && nq > 1) {
-            if (use > 0)
-              ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
-            if (ok)
-              load_q(qs);
-            else
-              --nq;  // (these queries were not asked for)
-          }
-          page = next;
-        }
-      }
-      // every copy this warp started must land before the CTA can exit
-      if (lane == 0) {
-        for (int s = 0; s < (PAIR ? 1 : 2); ++s) {
-          const int uses = PAIR ? nq : (nq + 1 - s) >> 1;
-          if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
-        }
-#pragma unroll 1
-        for (int s = 0; s < C::kSlots; ++s) {
-          // loads into slot s
-          const bool vslot = s >= C::kKSlots;
-          const int n = vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
-          if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
-        }
-      }
+      // ------------------------------------------------------------------ segments and TMA
+      span_load_warp<C, PAIR, C::kTileBytes, 16384>(p, &map_q, &map_k, &map_v, bar,
+                                                    reinterpret_cast<const uint16_t*>(sMerge), sQ, sKV, ctx);
       __syncwarp();
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
@@ -719,7 +716,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (!ok) meta.split = 0;
-      if (!CLUSTER && lane == 0) p.meta[blockIdx.x] = meta;
+      if (lane == 0) p.meta[blockIdx.x] = meta;
     }
   } else {
     setmaxnreg_inc<C::kSoftRegs>();
@@ -734,10 +731,6 @@ __global__ void __launch_bounds__(384, 1)
     int uses = 0;    // blocks this tile has processed over all segments
     int merges = 0;  // ALT: segments whose two accumulators were joined
     bool alive = true;
-    // CLUSTER: this CTA's part of the item, in the ring's memory once the ring has
-    // been read: rows of D + 4 floats (so that a warp's rows spread over the banks);
-    // its log-sum-exps at sMerge
-    float* sPart = reinterpret_cast<float*>(sKV);
 #pragma unroll 1
     for (int n = 0; alive; ++n) {
       const SpanSeg* seg;
@@ -999,13 +992,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_before();
           mbar_arrive(&bar->merge_free);
         }
-        if (CLUSTER) {
-          if (write)
-#pragma unroll
-            for (int v4 = 0; v4 < 8; ++v4)
-              reinterpret_cast<uint4*>(sPart + r * (D + 4) + 32 * c)[v4] =
-                  make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
-        } else if (write && whole) {
+        if (write && whole) {
           __nv_bfloat16* orow = p.o + grow * D + 32 * c;
           uint32_t w16[16];
 #pragma unroll
@@ -1026,9 +1013,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         __syncwarp();  // the next tensor memory load is a whole warp's
       }
-      if (CLUSTER) {
-        sMerge[r] = write ? lse2 : -CUDART_INF_F;
-      } else if (write) {
+      if (write) {
         if (whole)
           p.lse[grow] = lse2 * 0.6931471805599453f;
         else
@@ -1044,46 +1029,6 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
-  }
-  if constexpr (CLUSTER) {
-    // every CTA of the cluster writes every p.cluster-th row, a warp per row
-    cluster_sync();
-    constexpr int E = D / 32, kMost = 8;
-    const int ctas = p.cluster, item = blockIdx.x / ctas, b = item / p.rows.units;
-    const int fresh = v.rows(b, v.len(b));
-    const float* parts = reinterpret_cast<const float*>(sKV) + lane * E;
-    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.R; row += ctas * (C::kThreads / 32)) {
-      if (row % v.N >= fresh) continue;
-      float l[kMost], o[kMost][E], mx = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < kMost; ++i)
-        if (i < ctas) {
-          l[i] = cluster_load(sMerge + row, i);
-          cluster_load<E>(parts + row * (D + 4), i, o[i]);
-        }
-#pragma unroll
-      for (int i = 0; i < kMost; ++i)
-        if (i < ctas) mx = fmaxf(mx, l[i]);
-      const float ref = fmaxf(mx, -3.402823466e38f);
-      float sum = 0.f, acc[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kMost; ++i)
-        if (i < ctas && l[i] != -CUDART_INF_F) {  // (a part without keys was not written)
-          const float wt = ex2_approx(l[i] - ref);
-          sum += wt;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
-        }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t grow = (size_t)item * p.rows.R + row;  // (one row tile per unit)
-      uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
-    }
-    cluster_sync();  // the others have read this CTA's part
   }
 }
 
