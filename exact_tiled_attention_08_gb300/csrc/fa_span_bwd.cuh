@@ -54,6 +54,7 @@ struct SpanBwdParams {
   SpanBwdPlan* plan;
   SpanRun* runs;           // [entries + kSpanBwdSlots], request by request
   int* first;              // [B + 1] a request's first run
+  int2* hulls;             // [entries]
   int4* cuts;              // [kSpanBwdSlots / 2] entries that are cut: request, key block, slot, parts
   float* sums;             // [slot][dK, dV][128][d], fp32, unscaled
   __nv_bfloat16 *dk, *dv;
@@ -152,11 +153,12 @@ __global__ void __launch_bounds__(256)
 }
 
 // The query blocks of a key block: from the first to the last that sees one of its keys
-// (none: the first, whose pairs are all masked, so that zeros are written).
+// (none: the first, whose pairs are all masked, so that zeros are written).  By one warp.
 __device__ __forceinline__ int2 span_bwd_hull(const SpanBwdParams& p, int b, int jb) {
   const SpanView& v = p.rows.view;
-  int i0 = 0, i1 = p.nb;
+  const int lane = threadIdx.x & 31;
   if (!v.begin && !v.end) {
+    int i0 = 0, i1 = p.nb;
     if (v.causal) i0 = jb;
     if (v.window) {
       i1 = (int)min((long long)p.nb, ((long long)jb * 128 + 127 + v.window - 1) / 128 + 1);
@@ -166,14 +168,16 @@ __device__ __forceinline__ int2 span_bwd_hull(const SpanBwdParams& p, int b, int
   }
   const int4* bounds = p.rows.bounds + (long long)b * p.nb;
   int first = p.nb, last = -1;
-#pragma unroll 4
-  for (int i = 0; i < p.nb; ++i) {
+#pragma unroll 2
+  for (int i = lane; i < p.nb; i += 32) {
     const int4 x = bounds[i];
     if (x.x < (jb + 1) * 128 && x.y > jb * 128) {
       first = min(first, i);
       last = i;
     }
   }
+  first = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, last);
   return last < 0 ? make_int2(0, 1) : make_int2(first, last + 1);
 }
 
@@ -184,76 +188,67 @@ constexpr int kSpanBwdRun = 4;
 
 // One CTA: hulls and costs, the cut length, and the runs in the order of the entries.
 __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constant__ SpanBwdParams p) {
-  __shared__ long long parts_of[32];
-  __shared__ int warp_a[32], warp_b[32];
+  __shared__ long long work_of[32];
+  __shared__ int most_of[32], runs_of[32], cut_of[32], slots_of[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.nb, G = p.H / p.Hkv, chunk = (E + 1023) / 1024, e0 = min(E, tid * chunk), e1 = min(E, e0 + chunk);
   grid_wait();
+  for (int e = warp; e < E; e += 32) {
+    const int b = e / p.nb;
+    const int2 h = span_bwd_hull(p, b, e - b * p.nb);
+    if (lane == 0) p.hulls[e] = h;
+  }
+  __syncthreads();
   long long work = 0;
   int most = 0;
-  int2 one = make_int2(0, 0);  // (chunk = 1: the entry's hull)
   for (int e = e0; e < e1; ++e) {
-    const int b = e / p.nb;
-    one = span_bwd_hull(p, b, e - b * p.nb);
-    work += one.y - one.x;
-    most = max(most, one.y - one.x);
+    const int2 h = p.hulls[e];
+    work += h.y - h.x;
+    most = max(most, h.y - h.x);
   }
-  auto all_sum = [&](long long x) {
+  auto sum = [&](long long x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (lane == 0) parts_of[warp] = x;
-    __syncthreads();
-    long long s = 0;
-    for (int w = 0; w < 32; ++w) s += parts_of[w];
-    return s;
+    return x;
   };
-  work = all_sum(work) * G * p.Hkv;
+  auto upto = [&](int x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int add = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += add;
+    }
+    return x;
+  };
+  work = sum(work);
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) warp_a[warp] = most;
+  if (lane == 0) work_of[warp] = work, most_of[warp] = most;
   __syncthreads();
-  most = __reduce_max_sync(0xffffffffu, warp_a[lane]);
+  work = sum(work_of[lane]) * G * p.Hkv;
+  most = __reduce_max_sync(0xffffffffu, most_of[lane]);
   const long long share = (work + p.ctas - 1) / p.ctas;
   const bool cuts = (long long)most * G > share;
   const int length = (int)min((long long)0x7fffffff, max((long long)kSpanBwdRun, (2 * work + kSpanBwdSlots - 1) / kSpanBwdSlots));
   auto parts = [&](int cost) { return cuts && cost > length ? (cost + length - 1) / length : 1; };
-  // exclusive sums of the runs, and of the cut entries and their runs
-  int runs = 0, cut = 0, cut_runs = 0;
-  auto hull = [&](int e) {
-    const int b = e / p.nb;
-    return chunk == 1 ? one : span_bwd_hull(p, b, e - b * p.nb);
-  };
+  // this thread's runs, cut entries and their runs, and those of all before it
+  int runs = 0, cut = 0, slots = 0;
   for (int e = e0; e < e1; ++e) {
-    const int2 h = hull(e);
+    const int2 h = p.hulls[e];
     const int n = parts((h.y - h.x) * G);
     runs += n;
-    if (n > 1) ++cut, cut_runs += n;
+    if (n > 1) ++cut, slots += n;
   }
+  int at = upto(runs) - runs, cut_at = upto(cut) - cut, slot = upto(slots) - slots;
+  if (lane == 31) runs_of[warp] = at + runs, cut_of[warp] = cut_at + cut, slots_of[warp] = slot + slots;
   __syncthreads();
-  auto before = [&](int x, int* scratch, int* total) {
-    int upto = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int add = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += add;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = upto;
-    __syncthreads();
-    int base = 0, sum = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w == warp) base = sum;
-      sum += scratch[w];
-    }
-    *total = sum;
-    return base + upto - x;
-  };
-  int all_runs, all_cut, all_cut_runs;
-  int at = before(runs, warp_a, &all_runs), cut_at = before(cut, warp_b, &all_cut);
-  int slot = before(cut_runs, warp_a, &all_cut_runs);
+  const int all_runs = upto(runs_of[lane]), all_cut = upto(cut_of[lane]), all_slots = upto(slots_of[lane]);
+  if (warp > 0) {
+    at += __shfl_sync(0xffffffffu, all_runs, warp - 1);
+    cut_at += __shfl_sync(0xffffffffu, all_cut, warp - 1);
+    slot += __shfl_sync(0xffffffffu, all_slots, warp - 1);
+  }
   for (int e = e0; e < e1; ++e) {
     const int b = e / p.nb, jb = e - b * p.nb;
-    const int2 h = hull(e);
+    const int2 h = p.hulls[e];
     const int cost = (h.y - h.x) * G, n = parts(cost);
     if (jb == 0) p.first[b] = at;
     for (int i = 0; i < n; ++i)
@@ -265,7 +260,7 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
       slot += n;
     }
   }
-  if (tid == 0) {
+  if (tid == 31) {
     p.first[p.B] = all_runs;
     *p.plan = SpanBwdPlan{0, all_runs * p.Hkv, all_cut, 0};
   }
@@ -333,6 +328,46 @@ __device__ __forceinline__ uint32_t span_transpose(uint32_t v, int lane) {
     v = lane & j ? (v & ~m) | ((y >> j) & m) : (v & m) | ((y << j) & ~m);
   }
   return v;
+}
+
+// Blocks seen in part, by one warp, 32 queries at a time: hidden products become -inf in tensor
+// memory (with a cap their tanh is -1, its derivative 0), and with a cap hidden
+// probabilities 0 behind that.  (Small code away from the loop: masks unrolled into it
+// cost a block that is seen in part more than twice another's time.)
+__device__ __forceinline__ void span_bwd_hide_s(uint32_t at, const uint32_t (&seen)[2]) {
+#pragma unroll 1
+  for (int ch = 0; ch < 2; ++ch) {
+    const uint32_t bits = ch ? seen[1] : seen[0];
+    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+    uint32_t x[32];
+    tmem_ld32(at + 32 * ch, x);
+    tmem_wait_ld();
+    reg_fence32(x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((bits >> e) & 1u)) x[e] = __float_as_uint(-CUDART_INF_F);
+    tmem_st32(at + 32 * ch, x);
+  }
+  tmem_wait_st();
+}
+// (P of query groups 2 ch and 2 ch + 1: over the first 8 of their 16 columns)
+__device__ __forceinline__ void span_bwd_hide_p(uint32_t at, const uint32_t (&seen)[2]) {
+  tmem_wait_st();
+#pragma unroll 1
+  for (int ch = 0; ch < 2; ++ch) {
+    const uint32_t bits = ch ? seen[1] : seen[0];
+    uint32_t x[32];
+    tmem_ld32(at + 32 * ch, x);
+    tmem_wait_ld();
+    reg_fence32(x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      uint32_t& pair = x[(e >> 3) * 16 + (e & 7)];
+      pair &= ((bits >> (2 * e)) & 1u ? 0x0000ffffu : 0u) | ((bits >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+    }
+    tmem_st8(at + 32 * ch, x);
+    tmem_st8(at + 32 * ch + 16, x + 16);
+  }
 }
 
 // the block after (head, i)
@@ -762,8 +797,9 @@ __global__ void __launch_bounds__(512, 1)
           break;
         }
         tc_fence_after();
+        if (__builtin_expect(cut, 0)) span_bwd_hide_s(tS + 64 * grp, seen);
         float2 pf[2][16];
-        auto probabilities = [&](auto masked) {
+        {
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             const int qc = 64 * grp + 32 * ch;  // first query column of this chunk
@@ -799,14 +835,8 @@ __global__ void __launch_bounds__(512, 1)
                   wt = __ffma2_rn(make_float2(-tn.x, -tn.y), tn, make_float2(1.f, 1.f));
                 }
                 float2 pe = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
-                if constexpr (masked.value)
-                  pe = make_float2((seen[ch] >> e) & 1u ? pe.x : 0.f, (seen[ch] >> (e + 1)) & 1u ? pe.y : 0.f);
                 pk[2 * e4 + h] = pack_bf16x2(pe.x, pe.y);
-                if constexpr (MOD >= 2) {
-                  pe = __fmul2_rn(pe, wt);
-                  if constexpr (masked.value)  // (a hidden product may be NaN)
-                    pe = make_float2((seen[ch] >> e) & 1u ? pe.x : 0.f, (seen[ch] >> (e + 1)) & 1u ? pe.y : 0.f);
-                }
+                if constexpr (MOD >= 2) pe = __fmul2_rn(pe, wt);
                 pf[ch][e / 2] = pe;
               }
             }
@@ -814,12 +844,8 @@ __global__ void __launch_bounds__(512, 1)
             tmem_st8(tS + qc, pk);
             tmem_st8(tS + qc + 16, pk + 8);
           }
-        };
-        // (two copies: with the masks in one the loop is 9 % slower also where nothing is masked)
-        if (__builtin_expect(cut, 0))
-          probabilities(std::true_type{});
-        else
-          probabilities(std::false_type{});
+        }
+        if (MOD >= 2 && __builtin_expect(cut, 0)) span_bwd_hide_p(tS + 64 * grp, seen);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar->p_done);
