@@ -257,7 +257,7 @@ fa_status run_span_fwd(const SpanCall& a) {
 // workspace of the backward: the plan, the spans and their tiles' bounds, the dQ accumulator (more than
 // one key block), delta and LSE log2(e) padded to whole blocks, runs of cut items
 struct SpanBwdWorkspace {
-  size_t first_at, runs_at, cuts_at, hulls_at, lo_at, hi_at, bounds_at, dq_at, delta_at, lse_at, sums_at, total;
+  size_t first_at, runs_at, cuts_at, hulls_at, order_at, lo_at, hi_at, bounds_at, dq_at, delta_at, lse_at, sums_at, total;
   static SpanBwdWorkspace of(int B, int H, int Hkv, int N, int d) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t nb = ((size_t)N + 127) / 128, npad = nb * 128, entries = (size_t)B * nb;
@@ -266,7 +266,8 @@ struct SpanBwdWorkspace {
     w.runs_at = w.first_at + up(((size_t)B + 1) * sizeof(int));
     w.cuts_at = w.runs_at + up((entries + fa::kSpanBwdSlots) * sizeof(fa::SpanRun));
     w.hulls_at = w.cuts_at + up(fa::kSpanBwdSlots / 2 * sizeof(int4));
-    w.lo_at = w.hulls_at + up(entries * sizeof(int2));
+    w.order_at = w.hulls_at + up(entries * sizeof(int2));
+    w.lo_at = w.order_at + up(entries * sizeof(int));
     w.hi_at = w.lo_at + up(B * npad * sizeof(int));
     w.bounds_at = w.hi_at + up(B * npad * sizeof(int));
     w.dq_at = w.bounds_at + up(entries * sizeof(int4));
@@ -328,6 +329,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   p.first = reinterpret_cast<int*>(ws + w.first_at);
   p.cuts = reinterpret_cast<int4*>(ws + w.cuts_at);
   p.hulls = reinterpret_cast<int2*>(ws + w.hulls_at);
+  p.order = reinterpret_cast<int*>(ws + w.order_at);
   p.sums = reinterpret_cast<float*>(ws + w.sums_at);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);

@@ -8,7 +8,7 @@
 // G query heads that share the head, the query blocks from the first to the last that has
 // a row which sees one of its keys, so dK and dV are summed over the group in tensor memory.
 // Items cost what they have of them (a causal mask: from 1 to all).  fa_span_plan_kernel lists them, the
-// longest of a causal mask first, and cuts those that are longer than a CTA's share of
+// longest of a request first, and cuts those that are longer than a CTA's share of
 // everything into runs, whose sums fa_span_bwd_post_kernel adds in order; the CTAs draw runs by
 // a ticket when they are about to need one.
 //
@@ -55,6 +55,7 @@ struct SpanBwdParams {
   SpanRun* runs;           // [entries + kSpanBwdSlots], request by request
   int* first;              // [B + 1] a request's first run
   int2* hulls;             // [entries]
+  int* order;              // [entries] a request's key blocks, the longest first
   int4* cuts;              // [kSpanBwdSlots / 2] entries that are cut: request, key block, slot, parts
   float* sums;             // [slot][dK, dV][128][d], fp32, unscaled
   __nv_bfloat16 *dk, *dv;
@@ -199,6 +200,21 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
     if (lane == 0) p.hulls[e] = h;
   }
   __syncthreads();
+  // each request's key blocks by falling cost (a formula's fall with the key block already)
+  const bool sorted = p.rows.view.begin || p.rows.view.end;
+  for (int e = sorted ? tid : E; e < E; e += 1024) {
+    const int b = e / p.nb, jb = e - b * p.nb;
+    const int2 mine = p.hulls[e], *all = p.hulls + (long long)b * p.nb;
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < p.nb; ++i) {
+      const int more = (all[i].y - all[i].x) - (mine.y - mine.x);
+      rank += more > 0 || (more == 0 && i < jb) ? 1 : 0;
+    }
+    p.order[(long long)b * p.nb + rank] = jb;
+  }
+  __syncthreads();
+  auto block_of = [&](int e, int b) { return sorted ? p.order[e] : e - b * p.nb; };
   long long work = 0;
   int most = 0;
   for (int e = e0; e < e1; ++e) {
@@ -232,7 +248,8 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
   // this thread's runs, cut entries and their runs, and those of all before it
   int runs = 0, cut = 0, slots = 0;
   for (int e = e0; e < e1; ++e) {
-    const int2 h = p.hulls[e];
+    const int b = e / p.nb;
+    const int2 h = p.hulls[(long long)b * p.nb + block_of(e, b)];
     const int n = parts((h.y - h.x) * G);
     runs += n;
     if (n > 1) ++cut, slots += n;
@@ -247,10 +264,10 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
     slot += __shfl_sync(0xffffffffu, all_slots, warp - 1);
   }
   for (int e = e0; e < e1; ++e) {
-    const int b = e / p.nb, jb = e - b * p.nb;
-    const int2 h = p.hulls[e];
+    const int b = e / p.nb, jb = block_of(e, b);
+    const int2 h = p.hulls[(long long)b * p.nb + jb];
     const int cost = (h.y - h.x) * G, n = parts(cost);
-    if (jb == 0) p.first[b] = at;
+    if (e == b * p.nb) p.first[b] = at;
     for (int i = 0; i < n; ++i)
       p.runs[at + i] = SpanRun{jb, h.x, h.y - h.x, cross_bwd_cut(i, n, cost), cross_bwd_cut(i + 1, n, cost), i,
                                n > 1 ? slot * p.Hkv : -1, 0};
