@@ -88,34 +88,33 @@ struct SpanRows {
   }
 };
 
-// Bounds of the tiles where the spans are given by row; block (t, b), a thread per row.
-__device__ __forceinline__ SpanTile span_tile_reduce(int lo, int hi, bool row, int4* scratch) {
+// The bounds of one tile from its rows' spans, by 128 threads (row: there is one).
+__device__ __forceinline__ int4 span_tile_reduce(int lo, int hi, bool row, int4* scratch) {
   const bool live = row && lo < hi;
-  SpanTile s{live ? lo : 0x7fffffff, live ? hi : 0, row ? (live ? lo : 0x7fffffff) : 0,
-             row ? (live ? hi : 0) : 0x7fffffff};
-  s.lo = __reduce_min_sync(0xffffffffu, s.lo);
-  s.hi = __reduce_max_sync(0xffffffffu, s.hi);
-  s.lo_cut = __reduce_max_sync(0xffffffffu, s.lo_cut);
-  s.hi_cut = __reduce_min_sync(0xffffffffu, s.hi_cut);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = make_int4(s.lo, s.hi, s.lo_cut, s.hi_cut);
+  const int4 x = make_int4(__reduce_min_sync(0xffffffffu, live ? lo : 0x7fffffff), __reduce_max_sync(0xffffffffu, live ? hi : 0),
+                           __reduce_max_sync(0xffffffffu, row ? (live ? lo : 0x7fffffff) : 0),
+                           __reduce_min_sync(0xffffffffu, row ? (live ? hi : 0) : 0x7fffffff));
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
   __syncthreads();
-  for (int w = 0; w < 4; ++w) {
-    const int4 x = scratch[w];
-    s = {min(s.lo, x.x), max(s.hi, x.y), max(s.lo_cut, x.z), min(s.hi_cut, x.w)};
+  int4 s = scratch[0];
+  for (int w = 1; w < 4; ++w) {
+    const int4 y = scratch[w];
+    s = make_int4(min(s.x, y.x), max(s.y, y.y), max(s.z, y.z), min(s.w, y.w));
   }
-  if (s.lo >= s.hi) s.lo = s.hi = 0;
+  if (s.x >= s.y) s.x = s.y = 0;
   return s;
 }
 
-__global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, int4* bounds) {
+// Bounds of all tiles where the spans are given by row: a block of 128 threads per tile.
+__global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, int tiles, int4* bounds) {
   __shared__ int4 scratch[4];
   grid_wait();
   grid_trigger();
-  const int i = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
+  const int b = blockIdx.x / tiles, i = (blockIdx.x - b * tiles) * 128 + threadIdx.x;
   int lo = 0, hi = 0;
   if (i < v.N) v.span(b, i, i, lo, hi);
-  const SpanTile s = span_tile_reduce(lo, hi, i < v.N, scratch);
-  if (threadIdx.x == 0) bounds[(long long)b * gridDim.x + blockIdx.x] = make_int4(s.lo, s.hi, s.lo_cut, s.hi_cut);
+  const int4 s = span_tile_reduce(lo, hi, i < v.N, scratch);
+  if (threadIdx.x == 0) bounds[blockIdx.x] = s;
 }
 
 // The cap in log2 units: cap log2(e) tanh(x), x = scale q k / cap.

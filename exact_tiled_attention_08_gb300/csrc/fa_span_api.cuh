@@ -232,8 +232,8 @@ fa_status run_span_fwd(const SpanCall& a) {
   if (by_row) {
     int4* bounds = reinterpret_cast<int4*>(ws);
     p.rows.bounds = bounds;
-    if (launch_early(fa::fa_span_bounds_kernel, dim3((unsigned)plan.tiles, (unsigned)a.B), 128, 0, a.stream, view,
-                     bounds) != cudaSuccess)
+    if (launch_early(fa::fa_span_bounds_kernel, dim3((unsigned)plan.tiles * (unsigned)a.B), 128, 0, a.stream, view,
+                     plan.tiles, bounds) != cudaSuccess)
       return FA_ERR_CUDA;
   }
   const unsigned grid = (unsigned)std::min(plan.ctas, sms);

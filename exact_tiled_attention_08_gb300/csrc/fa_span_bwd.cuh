@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256)
                             float* lse2_pad, float* dq_acc, const SpanView v, int* lo_pad, int* hi_pad, int4* bounds,
                             int B, int npad, long long padded_rows) {
   constexpr int kThreadsPerRow = D / 8, kRows = 256 / kThreadsPerRow;
-  __shared__ int4 scratch[4];
+  __shared__ int4 scratch[8];  // (of the first four warps, and what the others leave)
   const int sub = threadIdx.x % kThreadsPerRow;
   const int N = v.N, tiles = npad / 128, row_blocks = gridDim.x - (B * tiles + 1) / 2;
   grid_wait();
@@ -93,29 +93,15 @@ __global__ void __launch_bounds__(256)
     for (int half = 0; half < 2; ++half) {
       const int k = 2 * (blockIdx.x - row_blocks) + half;
       if (k >= B * tiles) return;
-      const int b = k / tiles, t = k - b * tiles, i = t * 128 + (int)threadIdx.x;
+      const int b = k / tiles, i = (k - b * tiles) * 128 + (int)threadIdx.x;
+      int lo = 0, hi = 0;
       if (threadIdx.x < 128) {
-        int lo = 0, hi = 0;
         if (i < N) v.span(b, i, i, lo, hi);
         lo_pad[(long long)b * npad + i] = lo;
         hi_pad[(long long)b * npad + i] = hi;
-        const bool live = lo < hi, row = i < N;
-        const int4 x = make_int4(__reduce_min_sync(0xffffffffu, live ? lo : 0x7fffffff),
-                                 __reduce_max_sync(0xffffffffu, live ? hi : 0),
-                                 __reduce_max_sync(0xffffffffu, row ? (live ? lo : 0x7fffffff) : 0),
-                                 __reduce_min_sync(0xffffffffu, row ? (live ? hi : 0) : 0x7fffffff));
-        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
       }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int4 s = scratch[0];
-        for (int w = 1; w < 4; ++w) {
-          const int4 x = scratch[w];
-          s = make_int4(min(s.x, x.x), max(s.y, x.y), max(s.z, x.z), min(s.w, x.w));
-        }
-        if (s.x >= s.y) s.x = s.y = 0;
-        bounds[k] = s;
-      }
+      const int4 s = span_tile_reduce(lo, hi, threadIdx.x < 128 && i < N, scratch);
+      if (threadIdx.x == 0) bounds[k] = s;
       __syncthreads();
     }
     return;
