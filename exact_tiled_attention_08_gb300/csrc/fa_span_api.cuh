@@ -247,6 +247,9 @@ fa_status run_span_fwd(const SpanCall& a) {
     st = a.d == 128 ? launch_span_mod<128>(maps, p, plan.pair, grid, a.stream)
                     : launch_span_mod<64>(maps, p, plan.pair, grid, a.stream);
   if (st != FA_OK || !plan.cuts || p.cluster > 1) return st;
+  // Nothing is cut where whole items cannot take longer than what cutting costs (span_schedule's rule).
+  const long long items = (long long)a.B * a.rows.units * plan.row_tiles;
+  if ((items + grid - 1) / grid * ((view.C + 127LL) / 128 + fa::kCrossStart) <= fa::kCrossCut) return FA_OK;
   const int per_block = plan.pair ? 32 : 8;  // rows of a block
   const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
   auto combine = a.d == 128 ? (plan.pair ? fa::fa_span_combine_kernel<128, true> : fa::fa_span_combine_kernel<128, false>)

@@ -30,7 +30,7 @@ template <int D, int R>
 struct FewCfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kAtoms = D / 64;
-  static constexpr int kThreads = 192;  // four softmax warps, the loading and the issuing one
+  static constexpr int kThreads = 256;  // four softmax warps, one that loads K, the issuing one, one that loads V
   static constexpr int kKSlots = D == 128 ? 3 : 6, kVSlots = D == 128 && R == 32 ? 2 : kKSlots, kSlots = kKSlots + kVSlots;
   static __device__ __forceinline__ int slot(int kv, int g) { return kv ? kKSlots + g % kVSlots : g % kKSlots; }
   static __device__ __forceinline__ int use(int kv, int g) { return g / (kv ? kVSlots : kKSlots); }
@@ -62,18 +62,19 @@ struct FewBarriers {
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr int kFewSegReaders = 5;  // the issuer and the softmax warps
+constexpr int kFewSegReaders = 6;  // the issuer, the warp that loads V and the softmax warps
 static_assert(sizeof(FewBarriers) <= 1024, "barriers overflow their shared-memory slot");
 
 // Of the segment's rows, in shared memory.
 struct FewRows {
-  int lo[32], hi[32], pos[32];
+  int lo[32], hi[32];
   float slope2[32];
+  float rel[2][32];       // positions from the first key of a block and of the next one
   float ref[32];          // the reference (log2 units), -inf: no key so far
   float part[4][32];      // of each warp: maxima, sums
   float lse[32];          // CLUSTER: this CTA's part
 };
-static_assert(sizeof(FewRows) <= 2048, "statistics overflow their shared-memory slot");
+static_assert(sizeof(FewRows) <= 2048 && offsetof(FewRows, ref) % 16 == 0, "statistics overflow their shared-memory slot");
 
 // the four softmax warps: a barrier, and one that says whether any thread of them has x
 __device__ __forceinline__ void few_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
@@ -124,7 +125,7 @@ __device__ __forceinline__ void span_cluster_share(const SpanFwdParams& p, SpanP
 }
 
 template <int D, int R, bool CLUSTER>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(256, 1)
     fa_span_few_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
   using C = FewCfg<D, R>;
@@ -195,7 +196,34 @@ __global__ void __launch_bounds__(192, 1)
 
   if (warp == 4) {
     // ------------------------------------------------------------------ segments and TMA
-    span_load_warp<C, false, C::kQBytes, C::kQAtom>(p, &map_q, &map_k, &map_v, bar, nullptr, sQ, sKV, ctx);
+    span_load_warp<C, false, true, C::kQBytes, C::kQAtom>(p, &map_q, &map_k, &map_v, bar, nullptr, sQ, sKV, ctx);
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------ TMA of the V tiles
+    // (A box costs the warp that asks for it some 50 cycles: with pages of 16 tokens one
+    // warp for K and V takes longer over a block than memory does.)
+    const SpanBoxes boxes(p, sKV);
+    const SpanSeg* at;
+    int g = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok && __all_sync(0xffffffffu, span_segment(bar, n, ctx, at)); ++n) {
+      const SpanSeg w = *at;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
+      const int kvh = w.u / p.rows.kv_div;
+      int page = boxes.page(p, w, w.j0);
+#pragma unroll 1
+      for (int j = w.j0; j < w.j1; ++j, ++g) {
+        const int next = j + 1 < w.j1 ? boxes.page(p, w, j + 1) : 0;  // (asked for a block ahead)
+        if (!(ok = boxes.load<C>(&map_v, bar, 1, g, w, j, kvh, page, ctx))) break;
+        page = next;
+      }
+    }
+    if (lane == 0)
+#pragma unroll 1
+      for (int s = 0; s < C::kVSlots; ++s)
+        if (g > s) wait_drain_inl(&bar->kv_full[C::kKSlots + s], C::use(1, g - 1 - s) & 1, kDrainLimitNs);
     __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------------ issuer: S^T of a block ahead of its neighbour's O^T
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(192, 1)
       wait_drain_inl(&bar->drain, 0, kDrainLimitNs);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ softmax (thread: a key; a channel of O)
     // (The warps meet at barriers of their own: a wait that ran out is carried to the next one,
     // where all of them leave.)
@@ -277,8 +305,9 @@ __global__ void __launch_bounds__(192, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
       const int len = v.len(b), fresh = v.rows(b, len);
+      int pos = 0;  // of row `tid`
       if (tid < 32) {
-        int lo = 0, hi = 0, pos = 0;
+        int lo = 0, hi = 0;
         float slope2 = 0.f;
         if (tid < p.rows.R) {
           const int head = tid / v.N, tok = tid - head * v.N;
@@ -286,7 +315,8 @@ __global__ void __launch_bounds__(192, 1)
           if (tok < fresh) v.span(b, tok, pos, lo, hi);
           if (p.slopes) slope2 = p.slopes[u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
         }
-        rows->lo[tid] = lo, rows->hi[tid] = hi, rows->pos[tid] = pos, rows->slope2[tid] = slope2;
+        rows->lo[tid] = lo, rows->hi[tid] = hi, rows->slope2[tid] = slope2;
+        rows->rel[g & 1][tid] = (float)(pos - j0 * 128);
         rows->ref[tid] = -CUDART_INF_F;
       }
       float l[R];
@@ -313,10 +343,16 @@ __global__ void __launch_bounds__(192, 1)
           for (int q = 0; q < R; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * p.scale_log2);
         }
         if (p.slopes) {
+          if (tid < 32) rows->rel[buf ^ 1][tid] = (float)(pos - j * 128 - 128);  // (a barrier before it is read)
 #pragma unroll
-          for (int q = 0; q < R; ++q)
-            x[q] = __float_as_uint(
-                fmaf(-rows->slope2[q], fabsf((float)(rows->pos[q] - key)), __uint_as_float(x[q])));
+          for (int q4 = 0; q4 < R; q4 += 4) {
+            const float4 rel = *reinterpret_cast<const float4*>(rows->rel[buf] + q4);
+            const float4 slope2 = *reinterpret_cast<const float4*>(rows->slope2 + q4);
+            x[q4] = __float_as_uint(fmaf(-slope2.x, fabsf(rel.x - (float)tid), __uint_as_float(x[q4])));
+            x[q4 + 1] = __float_as_uint(fmaf(-slope2.y, fabsf(rel.y - (float)tid), __uint_as_float(x[q4 + 1])));
+            x[q4 + 2] = __float_as_uint(fmaf(-slope2.z, fabsf(rel.z - (float)tid), __uint_as_float(x[q4 + 2])));
+            x[q4 + 3] = __float_as_uint(fmaf(-slope2.w, fabsf(rel.w - (float)tid), __uint_as_float(x[q4 + 3])));
+          }
         }
         if (j * 128 < lo_cut || j * 128 + 128 > hi_cut) {
 #pragma unroll

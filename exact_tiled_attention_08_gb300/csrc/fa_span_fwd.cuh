@@ -347,28 +347,59 @@ __device__ __forceinline__ bool span_segment(Bar* bar, int n, const WaitCtx& ctx
   return !(w->flags & kSegEnd);
 }
 
+// A tile of 128 keys as TMA boxes, a lane per page.
+struct SpanBoxes {
+  int lane, shift, rows, count;
+  bool paged;
+  uint8_t* ring;
+  __device__ __forceinline__ SpanBoxes(const SpanFwdParams& p, uint8_t* sKV) {
+    const SpanView& v = p.rows.view;
+    lane = threadIdx.x & 31;
+    paged = v.table != nullptr;
+    shift = v.page_shift;
+    rows = paged ? min(1 << shift, 128) : 128;
+    count = 128 / rows;
+    ring = sKV;
+  }
+  // the page of this lane's part of block j, or -1: nothing there that a row sees
+  __device__ __forceinline__ int page(const SpanFwdParams& p, const SpanSeg& w, int j) const {
+    if (!paged) return w.b;
+    if (lane >= count) return -1;
+    const int key = j * 128 + lane * rows;
+    if (key >= w.hi || key + rows <= w.lo) return -1;
+    const int page = p.rows.view.table[(long long)w.b * p.rows.view.width + (key >> shift)];
+    return page >= 0 && page < p.pages ? page : -1;
+  }
+  // block j's K (kv = 0) or V tile as the g-th of its kind; false: the wait for its slot ran out
+  template <class C, class Bar>
+  __device__ __forceinline__ bool load(const CUtensorMap* map, Bar* bar, int kv, int g, const SpanSeg& w, int j, int kvh,
+                                       int page, const WaitCtx& ctx) const {
+    const int slot = C::slot(kv, g);
+    if (!__all_sync(0xffffffffu, span_wait(&bar->kv_empty[slot], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty)))
+      return false;
+    if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+    __syncwarp();
+    if (lane < count) {
+      const int row = !paged ? j * 128 : count > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
+      for (int a = 0; a < C::kAtoms; ++a)
+        tma_load_4d(ring + slot * C::kTileBytes + a * 16384 + lane * rows * 128, map, &bar->kv_full[slot], a * 64, row, kvh, page);
+    }
+    return true;
+  }
+};
+
 // The loading warp: works out the segments, publishes them, and fills Q's two buffers (QBYTES
-// each, atoms of 64 columns QATOM bytes apart) and the ring of K and V tiles, a lane per page.
-template <class C, bool PAIR, int QBYTES, int QATOM, class Bar>
+// each, atoms of 64 columns QATOM bytes apart) and the ring of K and V tiles (SPLIT: of K tiles).
+template <class C, bool PAIR, bool SPLIT, int QBYTES, int QATOM, class Bar>
 __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUtensorMap* map_q, const CUtensorMap* map_k,
                                                  const CUtensorMap* map_v, Bar* bar, const uint16_t* order, uint8_t* sQ,
                                            uint8_t* sKV, const WaitCtx& ctx) {
-  const SpanView& v = p.rows.view;
   const int lane = threadIdx.x & 31;
   SpanPlace at = bar->place;
   SpanSeg w{};
-  const int shift = v.page_shift, box_rows = v.table ? min(1 << shift, 128) : 128;
-  const int boxes = 128 / box_rows;
-  int loads = 0, nq = 0;  // K and V tiles, in turn
+  const SpanBoxes boxes(p, sKV);
+  int loads = 0, nq = 0;  // K and V tiles, in turn (SPLIT: K tiles)
   bool ok = true;
-  // the page of this lane's part of block j, or -1: nothing there that a row sees
-  auto page_of = [&](int j) -> int {
-    if (lane >= boxes) return -1;
-    const int key = j * 128 + lane * box_rows, i = key >> shift;
-    if (key >= w.hi || key + box_rows <= w.lo) return -1;
-    const int page = v.table[(long long)w.b * v.width + i];
-    return page >= 0 && page < p.pages ? page : -1;
-  };
   auto load_q = [&](int qs) {
     if (lane == 0) {
       const int tiles = w.flags & kSegTwo ? 2 : 1;
@@ -396,28 +427,18 @@ __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUt
     if (!more) break;
     const int kvh = w.u / p.rows.kv_div;
     const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-    int page = v.table ? page_of(w.j0) : 0;
+    int page = boxes.page(p, w, w.j0);
     // a later segment's first key block needs only ring slots: it goes out
     // before the queries, whose buffer an earlier segment may still be reading
     if (nq == 0) load_q(qs);
     ++nq;
 #pragma unroll 1
     for (int j = w.j0; ok && j < w.j1; ++j) {
-      const int next = v.table && j + 1 < w.j1 ? page_of(j + 1) : 0;  // (asked for a block ahead)
+      const int next = j + 1 < w.j1 ? boxes.page(p, w, j + 1) : 0;  // (asked for a block ahead)
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const int g = loads >> 1, slot = C::slot(kv, g);
-        ok = __all_sync(0xffffffffu,
-                        span_wait(&bar->kv_empty[slot], (C::use(kv, g) & 1) ^ 1, ctx, kSiteCrossKvEmpty));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
-        __syncwarp();
-        if (lane < boxes) {
-          const int row = !v.table ? j * 128 : boxes > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
-          for (int a = 0; a < C::kAtoms; ++a)
-            tma_load_4d(sKV + slot * C::kTileBytes + a * 16384 + lane * box_rows * 128, kv ? map_v : map_k,
-                        &bar->kv_full[slot], a * 64, row, kvh, v.table ? page : w.b);
-        }
+      for (int kv = 0; kv < (SPLIT ? 1 : 2); ++kv) {
+        const int g = SPLIT ? loads : loads >> 1;
+        if (!(ok = boxes.load<C>(kv ? map_v : map_k, bar, kv, g, w, j, kvh, page, ctx))) break;
         ++loads;
       }
       if (ok && j == w.j0 && nq > 1) {
@@ -441,7 +462,7 @@ __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUt
     for (int s = 0; s < C::kSlots; ++s) {
       // loads into slot s
       const bool vslot = s >= C::kKSlots;
-      const int n = vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
+      const int n = SPLIT ? (vslot ? 0 : loads) : vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
       if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
     }
   }
@@ -563,7 +584,7 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_dec<C::kMiscRegs>();
     if (warp == 9) {
       // ------------------------------------------------------------------ segments and TMA
-      span_load_warp<C, PAIR, C::kTileBytes, 16384>(p, &map_q, &map_k, &map_v, bar,
+      span_load_warp<C, PAIR, false, C::kTileBytes, 16384>(p, &map_q, &map_k, &map_v, bar,
                                                     reinterpret_cast<const uint16_t*>(sMerge), sQ, sKV, ctx);
       __syncwarp();
     } else if (warp == 8) {
