@@ -69,7 +69,7 @@ static_assert(sizeof(FewBarriers) <= 1024, "barriers overflow their shared-memor
 struct FewRows {
   int lo[32], hi[32];
   float slope2[32];
-  float rel[2][32];       // positions from the first key of a block and of the next one
+  float rel[2][32];       // positions from the first key of a block and of the one that follows
   float ref[32];          // the reference (log2 units), -inf: no key so far
   float part[4][32];      // of each warp: maxima, sums
   float lse[32];          // CLUSTER: this CTA's part
@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(256, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
       const int kvh = w.u / p.rows.kv_div;
-      int page = boxes.page(p, w, w.j0);
+      int page = boxes.page(p, w, w.j1 - 1);
 #pragma unroll 1
-      for (int j = w.j0; j < w.j1; ++j, ++g) {
-        const int next = j + 1 < w.j1 ? boxes.page(p, w, j + 1) : 0;  // (asked for a block ahead)
+      for (int j = w.j1 - 1; j >= w.j0; --j, ++g) {
+        const int next = j > w.j0 ? boxes.page(p, w, j - 1) : 0;  // (asked for a block ahead)
         if (!(ok = boxes.load<C>(&map_v, bar, 1, g, w, j, kvh, page, ctx))) break;
         page = next;
       }
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(256, 1)
           if (p.slopes) slope2 = p.slopes[u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
         }
         rows->lo[tid] = lo, rows->hi[tid] = hi, rows->slope2[tid] = slope2;
-        rows->rel[g & 1][tid] = (float)(pos - j0 * 128);
+        rows->rel[g & 1][tid] = (float)(pos - (j1 - 1) * 128);
         rows->ref[tid] = -CUDART_INF_F;
       }
       float l[R];
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256, 1)
       for (int q = 0; q < R; ++q) l[q] = 0.f;
       few_sync();
 #pragma unroll 1
-      for (int j = j0; j < j1; ++j, ++g) {
+      for (int j = j1 - 1; j >= j0; --j, ++g) {
         const int buf = g & 1, key = j * 128 + tid;
         bad = bad || !__all_sync(0xffffffffu, span_wait(&bar->s_full[buf], (g >> 1) & 1, ctx, kSiteCrossS));
         tc_fence_after();
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256, 1)
           for (int q = 0; q < R; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * p.scale_log2);
         }
         if (p.slopes) {
-          if (tid < 32) rows->rel[buf ^ 1][tid] = (float)(pos - j * 128 - 128);  // (a barrier before it is read)
+          if (tid < 32) rows->rel[buf ^ 1][tid] = (float)(pos - j * 128 + 128);  // (a barrier before it is read)
 #pragma unroll
           for (int q4 = 0; q4 < R; q4 += 4) {
             const float4 rel = *reinterpret_cast<const float4*>(rows->rel[buf] + q4);
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(256, 1)
             if (lane == q) rows->part[warp][q] = few_order(most);
           }
           few_sync();
-          const bool again = j > j0;
+          const bool again = j < j1 - 1;
           if (again) bad = !__all_sync(0xffffffffu, span_wait(&bar->pv_done[buf ^ 1], ((g - 1) >> 1) & 1, ctx, kSiteCrossPv));
           tc_fence_after();
           uint32_t o[R];

@@ -11,7 +11,10 @@
 // 128 keys that any of its rows sees; items cost what they have of them.  Where enough of them
 // are there, the CTAs take whole items (the longest first, or head by head); otherwise even
 // shares of all items' blocks, and fa_span_combine_kernel joins the items that shares cut.
-// Within an item each row tile takes only the blocks that it sees something of.
+// Within an item each row tile takes only the blocks that it sees something of, from the last
+// to the first: where a bias grows with the distance the largest scores come first, and the
+// running maximum stays (from the first to the last it rises in every block: H=16 N=2048
+// d=64, four requests, causal, with slopes, 84 us).
 //
 // Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
 // (MOD 2) and the bias (MOD 1 and 2) change the scores in registers, before the maximum.
@@ -173,7 +176,7 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t
 // the row tiles (bits) that take block j
 template <bool PAIR>
 __device__ __forceinline__ int span_active(const SpanSeg& s, int j) {
-  if (!PAIR) return 1 << ((j - s.j0) & 1);
+  if (!PAIR) return 1 << ((s.j1 - 1 - j) & 1);
   return (j >= s.a0[0] && j < s.a1[0] ? 1 : 0) | (s.flags & kSegTwo && j >= s.a0[1] && j < s.a1[1] ? 2 : 0);
 }
 
@@ -427,21 +430,21 @@ __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUt
     if (!more) break;
     const int kvh = w.u / p.rows.kv_div;
     const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
-    int page = boxes.page(p, w, w.j0);
+    int page = boxes.page(p, w, w.j1 - 1);
     // a later segment's first key block needs only ring slots: it goes out
     // before the queries, whose buffer an earlier segment may still be reading
     if (nq == 0) load_q(qs);
     ++nq;
 #pragma unroll 1
-    for (int j = w.j0; ok && j < w.j1; ++j) {
-      const int next = j + 1 < w.j1 ? boxes.page(p, w, j + 1) : 0;  // (asked for a block ahead)
+    for (int j = w.j1 - 1; ok && j >= w.j0; --j) {
+      const int next = j > w.j0 ? boxes.page(p, w, j - 1) : 0;  // (asked for a block ahead)
 #pragma unroll 1
       for (int kv = 0; kv < (SPLIT ? 1 : 2); ++kv) {
         const int g = SPLIT ? loads : loads >> 1;
         if (!(ok = boxes.load<C>(kv ? map_v : map_k, bar, kv, g, w, j, kvh, page, ctx))) break;
         ++loads;
       }
-      if (ok && j == w.j0 && nq > 1) {
+      if (ok && j == w.j1 - 1 && nq > 1) {
         if (use > 0)
           ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
         if (ok)
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(384, 1)
           if (!span_wait(&bar->q_full[qs], use & 1, ctx, kSiteCrossQ)) break;
           ++nq;
 #pragma unroll 1
-          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+          for (int j = w.j1 - 1; ok && j >= w.j0; --j, ++g) {
             const int ks = C::slot(0, g);
             if (!(ok = span_wait(&bar->kv_full[ks], C::use(0, g) & 1, ctx, kSiteCrossK))) break;
             const uint64_t kdesc = sdesc_sw128(skv + ks * C::kTileBytes, 16, 1024);
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(384, 1)
           const SpanSeg w = *at;
           mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
 #pragma unroll 1
-          for (int j = w.j0; ok && j < w.j1; ++j, ++g) {
+          for (int j = w.j1 - 1; ok && j >= w.j0; --j, ++g) {
             const int vs = C::slot(1, g);
             if (!(ok = span_wait(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
             // rows that nobody sees: warp 11 zeroes them while P is being formed
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 clean = true;
                 tc_fence_after();
-                const bool add = j > (PAIR ? (t ? w.a0[1] : w.a0[0]) : w.j0 + 1);  // not the tile's first block
+                const bool add = j + 1 < (PAIR ? (t ? w.a1[1] : w.a1[0]) : w.j1 - 1);  // not the tile's first product
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_bf16_ts(tmem + (t ? C::kOCol1 : C::kOCol0), tmem + (t ? C::kPCol1 : C::kPCol0) + kk * 8,
@@ -709,13 +712,13 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
 #pragma unroll 1
-        for (int j = w.j0; ok && j < w.j1; j = j + 1 < w.j1 - 1 ? w.j1 - 1 : j + 1) {  // (its first and its last block)
+        for (int j = w.j1 - 1; ok && j >= w.j0; j = j - 1 > w.j0 ? w.j0 : j - 1) {  // (its last and its first block)
           if (!span_dirty(w, j)) continue;
           ok = __all_sync(0xffffffffu, span_wait(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
           if (!ok) break;
           ++cleaned;
           const int from = max(w.lo - j * 128, 0), to = max(min(w.hi - j * 128, 128), from);  // seen
-          uint8_t* tile = sKV + C::slot(1, g + j - w.j0) * C::kTileBytes;
+          uint8_t* tile = sKV + C::slot(1, g + w.j1 - 1 - j) * C::kTileBytes;
           const int unseen = (from + 128 - to) * 8;  // 16-byte chunks of an atom
           for (int i = lane; i < C::kAtoms * unseen; i += 32) {
             const int a = i >= unseen ? 1 : 0, k = i - a * unseen, c = k < from * 8 ? k : k - from * 8 + to * 8;
@@ -769,7 +772,7 @@ __global__ void __launch_bounds__(384, 1)
       int row_lo, row_hi, pos;
       float slope2 = 0.f;
       bool there = true;  // the row is written
-      const int jfirst = PAIR ? w.a0[t] : w.j0 + t, j1 = PAIR ? w.a1[t] : w.j1;
+      const int jfirst = (PAIR ? w.a1[t] : w.j1 - t) - 1, jend = PAIR ? w.a0[t] : w.j0;
       const int lo_cut = w.lo_cut[PAIR ? t : 0], hi_cut = w.hi_cut[PAIR ? t : 0];  // blocks that all rows see whole
       {
         const int b = w.b, row = min(w.row0 + (PAIR ? 128 * t : 0) + r, p.rows.R - 1), head = row / v.N;
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(384, 1)
       // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
       // block's largest one, so that l + lcorr normalises O (see fa_fwd_kernel)
       float l = 0.f, lcorr = 0.f;
-      for (int j = jfirst; j < j1; j += PAIR ? 1 : 2, ++uses) {
+      for (int j = jfirst; j >= jend; j -= PAIR ? 1 : 2, ++uses) {
         if (!__all_sync(0xffffffffu, span_wait(&bar->s_full[t], uses & 1, ctx, kSiteCrossS))) {
           alive = false;
           break;
@@ -918,7 +921,7 @@ __global__ void __launch_bounds__(384, 1)
         // P_t and O_t are in use until the tile's previous product has completed
         // (a segment's first block: its predecessor's epilogue has waited for
         // it; ALT: O_1 also until warpgroup 0 has read it)
-        if (j > jfirst) {
+        if (j < jfirst) {
           if (!__all_sync(0xffffffffu, span_wait(&bar->pv_done[t], (uses - 1) & 1, ctx, kSiteCrossPv))) {
             alive = false;
             break;
