@@ -338,9 +338,6 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.dq = direct ? static_cast<__nv_bfloat16*>(dq) : nullptr;
   p.B = B, p.H = H, p.Hkv = Hkv, p.N = N, p.nb = nb;
-  // heads handed out together: enough for four times the CTAs' number of items, so that the longest
-  // ones are handed out well before the last (see causal_group_heads)
-  p.group_heads = (int)std::min<long long>(Hkv, (4LL * sms + nb) / (nb + 1));
   p.scale_log2 = scale * 1.4426950408889634f;
   p.scale = scale;
   p.cap = span_cap(scale, cap);
@@ -349,7 +346,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   p.debug_stall = g_debug_stall.load();
   p.out_align32 = aligned32(dk) && aligned32(dv) && aligned32(dq);
   const long long blocks = (long long)B * H * nb * nb;  // (at most: what a mask leaves out is not known here)
-  p.ctas = (int)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
+  const unsigned grid = (unsigned)std::min<long long>(blocks, std::min(sms, fa::kCrossBwdMaxCtas));
   const long long rows = (long long)B * H * npad, per_block = 256 / (D / 8);
   const long long prep = std::min((rows + per_block - 1) / per_block, 152LL * 16) + ((long long)B * nb + 1) / 2;
   if (launch_early(fa::fa_span_bwd_prep_kernel<D>, dim3((unsigned)prep), 256, 0, stream,
@@ -358,7 +355,6 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
                    const_cast<int4*>(p.rows.bounds), B, npad, rows) != cudaSuccess)
     return FA_ERR_CUDA;
   if (launch_early(fa::fa_span_plan_kernel, dim3(1), 1024, 0, stream, p) != cudaSuccess) return FA_ERR_CUDA;
-  const unsigned grid = (unsigned)p.ctas;
   const fa_status st = cap > 0.f ? (slopes ? launch_span_bwd<D, 3>(maps, p, grid, stream) : launch_span_bwd<D, 2>(maps, p, grid, stream))
                                  : (slopes ? launch_span_bwd<D, 1>(maps, p, grid, stream) : launch_span_bwd<D, 0>(maps, p, grid, stream));
   if (st != FA_OK) return st;

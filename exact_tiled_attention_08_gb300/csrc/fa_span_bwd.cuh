@@ -61,8 +61,6 @@ struct SpanBwdParams {
   __nv_bfloat16 *dk, *dv;
   __nv_bfloat16* dq;       // one key block: written directly (scaled, bf16); else nullptr
   int B, H, Hkv, N, nb;    // nb: blocks of N
-  int group_heads;         // key/value heads whose items are handed out together
-  int ctas;
   float scale_log2;        // scale * log2(e)
   float scale;
   SpanCap cap;
@@ -168,15 +166,16 @@ __device__ __forceinline__ int2 span_bwd_hull(const SpanBwdParams& p, int b, int
   return last < 0 ? make_int2(0, 1) : make_int2(first, last + 1);
 }
 
-// What cutting pays for: an item longer than a CTA's share of everything ends after the
-// others.  Such items are cut into runs of about half a share (so at most kSpanBwdSlots runs
-// come of it), but none shorter than kSpanBwdRun blocks.
+// Items longer than half of a CTA's share of everything are cut into runs of about that
+// (so at most kSpanBwdSlots runs come of it), but none shorter than kSpanBwdRun blocks.
+// (Measured, cutting only where an item is longer than a whole share: 25 packed documents,
+// N=8192 H=32/8 d=128, 390 and 372 us; equal where nothing is that long.)
 constexpr int kSpanBwdRun = 4;
 
 // One CTA: hulls and costs, the cut length, and the runs in the order of the entries.
 __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constant__ SpanBwdParams p) {
   __shared__ long long work_of[32];
-  __shared__ int most_of[32], runs_of[32], cut_of[32], slots_of[32];
+  __shared__ int runs_of[32], cut_of[32], slots_of[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.nb, G = p.H / p.Hkv, chunk = (E + 1023) / 1024, e0 = min(E, tid * chunk), e1 = min(E, e0 + chunk);
   grid_wait();
@@ -202,11 +201,9 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
   __syncthreads();
   auto block_of = [&](int e, int b) { return sorted ? p.order[e] : e - b * p.nb; };
   long long work = 0;
-  int most = 0;
   for (int e = e0; e < e1; ++e) {
     const int2 h = p.hulls[e];
     work += h.y - h.x;
-    most = max(most, h.y - h.x);
   }
   auto sum = [&](long long x) {
 #pragma unroll
@@ -222,15 +219,11 @@ __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constan
     return x;
   };
   work = sum(work);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) work_of[warp] = work, most_of[warp] = most;
+  if (lane == 0) work_of[warp] = work;
   __syncthreads();
   work = sum(work_of[lane]) * G * p.Hkv;
-  most = __reduce_max_sync(0xffffffffu, most_of[lane]);
-  const long long share = (work + p.ctas - 1) / p.ctas;
-  const bool cuts = (long long)most * G > share;
   const int length = (int)min((long long)0x7fffffff, max((long long)kSpanBwdRun, (2 * work + kSpanBwdSlots - 1) / kSpanBwdSlots));
-  auto parts = [&](int cost) { return cuts && cost > length ? (cost + length - 1) / length : 1; };
+  auto parts = [&](int cost) { return cost > length ? (cost + length - 1) / length : 1; };
   // this thread's runs, cut entries and their runs, and those of all before it
   int runs = 0, cut = 0, slots = 0;
   for (int e = e0; e < e1; ++e) {
@@ -277,7 +270,9 @@ struct SpanBwdSeg {
   int end;                     // no more units
 };
 
-// Unit k: requests one after another; in a request groups of key/value heads, in a group run by run.
+// Unit k: requests one after another, in a request run by run, of all key/value heads.  (Groups of
+// heads, which keep fewer query rows in use at a time, are slower: N=4096 H=32 d=128, two requests,
+// causal, 713 us, in groups of 18 heads 727, of 4 781.)
 __device__ __forceinline__ bool span_bwd_unit(const SpanBwdParams& p, int k, SpanBwdSeg& s) {
   if (k >= p.plan->units) return false;
   const int run = k / p.Hkv;
@@ -287,12 +282,9 @@ __device__ __forceinline__ bool span_bwd_unit(const SpanBwdParams& p, int k, Spa
     if (p.first[mid] <= run) b = mid;
     else top = mid;
   }
-  const int r0 = p.first[b], n = p.first[b + 1] - r0;
-  const int off = k - r0 * p.Hkv, grp = off / (n * p.group_heads), heads = min(p.group_heads, p.Hkv - grp * p.group_heads);
-  const int in = off - grp * n * p.group_heads, r = in / heads;
   s.b = b;
-  s.kvh = grp * p.group_heads + in - r * heads;
-  const SpanRun x = p.runs[r0 + r];
+  s.kvh = k - run * p.Hkv;
+  const SpanRun x = p.runs[run];
   s.jb = x.jb, s.i0 = x.i0, s.cnt = x.cnt, s.n = x.f1 - x.f0;
   s.head = x.f0 / x.cnt;
   s.i = x.i0 + x.f0 - s.head * x.cnt;
