@@ -55,28 +55,25 @@ struct SpanTile {
   __device__ __forceinline__ bool empty() const { return lo >= hi; }
 };
 
-// Query rows are numbered in units: a query head's N rows, or (pages) the G N rows of
-// the heads that share a key/value head.
+// Query rows come in units: a query head's, or (pages) those of the heads that share a
+// key/value head.  A tile has whole tokens, row r is head r % heads of its token r / heads, so
+// that a request's new tokens fill as few tiles as they can, whatever the others bring.
 struct SpanRows {
   SpanView view;
   const int4* bounds;  // [B][tiles] SpanTile, or nullptr: the mask is a formula of the position
-  int R, tiles;        // rows of a unit, and tiles of 128 of them
+  int heads, tokens;   // heads of a unit; tokens of a tile
+  int tiles;           // tiles of a unit's N tokens
   int units, kv_div;   // units of a request; of a key/value head
+  // row of [B][H][N]
+  __device__ __forceinline__ size_t row(int b, int u, int head, int token) const {
+    return (((size_t)b * units + u) * heads + head) * view.N + token;
+  }
   __device__ __forceinline__ SpanTile tile(int b, int t) const {
     if (bounds) {
       const int4 x = bounds[(long long)b * tiles + t];
       return {x.x, x.y, x.z, x.w};
     }
-    // the tokens of the tile: of one head, or of several
-    const int row0 = t * 128, row1 = min(row0 + 127, R - 1), N = view.N;
-    int t0 = row0, t1 = row1;
-    if (R != N) {
-      const int h0 = row0 / N, h1 = row1 / N;
-      t0 = h0 == h1 ? row0 - h0 * N : 0;
-      t1 = h0 == h1 ? row1 - h0 * N : N - 1;
-    }
-    const int len = view.len(b);
-    t1 = min(t1, view.rows(b, len) - 1);
+    const int len = view.len(b), t0 = t * tokens, t1 = min(t0 + tokens, view.rows(b, len)) - 1;
     if (t0 > t1) return {0, 0, 0x7fffffff, 0};
     SpanTile s{0, view.C, 0, view.C};
     view.clip(len + t0, len + t1, s.lo, s.hi);

@@ -89,18 +89,42 @@ fa::SpanCap span_cap(float scale, float cap) {
   return c;
 }
 
+// Heads of a unit of the heads that share a key/value head: a divisor of their number, the largest
+// that leaves at most an eighth of the rows of a tile of 128 empty, or all rows in one tile.
+int span_unit_heads(int group, int N) {
+  for (int h = std::min(group, 128);; --h)
+    if (group % h == 0 && ((long long)h * N <= 128 || 128 / h * h >= 112)) return h;
+}
+
+// queries as a 4-D tensor (d, heads of a unit, tokens, units) for boxes of 64 columns of a tile's rows
+bool encode_units(CUtensorMap* map, const void* q, int units, int heads, int N, int tokens, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)N, (cuuint64_t)units};
+  const cuuint64_t strides[3] = {(cuuint64_t)N * d * 2, (cuuint64_t)d * 2, (cuuint64_t)heads * N * d * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)tokens, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Grid and workspace of the forward, as CrossFwdPlan; with spans by row their tiles' bounds first.
 struct SpanFwdPlan {
-  int tiles, row_tiles, part_rows, ctas;
+  int few;  // the kernel for 16 or 32 rows, or 0
+  int tokens, tiles, row_tiles, part_rows, ctas;
   bool pair, cuts;
   size_t meta_at, lse_at, o_at, total;
-  static SpanFwdPlan of(int B, int units, int R, int C, int d, bool bounds) {
+  static SpanFwdPlan of(int B, int H, int heads, int N, int C, int d, bool bounds) {
     SpanFwdPlan w;
-    w.tiles = (R + 127) / 128;
-    w.pair = R > 128;
+    const long long rows_all = (long long)heads * N;
+    w.few = rows_all <= 16 ? 16 : rows_all <= 32 ? 32 : 0;
+    w.tokens = (w.few ? w.few : 128) / heads;
+    w.tiles = (N + w.tokens - 1) / w.tokens;
+    w.pair = w.tiles > 1;
     w.row_tiles = w.pair ? (w.tiles + 1) / 2 : 1;
-    w.part_rows = w.pair ? 256 : R;
-    const long long blocks = (long long)B * units * w.row_tiles * ((C + 127LL) / 128 + fa::kCrossStart);
+    w.part_rows = w.pair ? 256 : (int)rows_all;
+    const long long blocks = (long long)B * (H / heads) * w.row_tiles * ((C + 127LL) / 128 + fa::kCrossStart);
     w.ctas = (int)std::min<long long>(blocks, fa::kCrossMaxCtas);
     w.cuts = C > 128;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -152,7 +176,7 @@ fa_status launch_span_few(const CUtensorMap* maps, fa::SpanFwdParams& p, unsigne
   const long long items = (long long)p.B * p.rows.units;
   int blocks = (p.rows.view.C + 127) / 128;
   if (p.B == 1 && paged && blocks > 2) blocks = (blocks + 1) / 2;
-  p.cluster = fa::cross_cluster(items, blocks, p.rows.R, p.B == 1 || !paged, std::min(sms, fa::kCrossMaxCtas),
+  p.cluster = fa::cross_cluster(items, blocks, p.rows.heads * p.rows.view.N, p.B == 1 || !paged, std::min(sms, fa::kCrossMaxCtas),
                                 few_cluster_fit<D, R>(dev));
   if (p.cluster > 1) {
     auto kernel = fa::fa_span_few_kernel<D, R, true>;
@@ -196,11 +220,10 @@ struct SpanCall {
 fa_status run_span_fwd(const SpanCall& a) {
   const fa::SpanView& view = a.rows.view;
   const bool by_row = view.begin || view.end;
-  const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.rows.units, a.rows.R, view.C, a.d, !view.table);
-  // (up to 32 rows per unit: the kernel that has the keys on the tensor memory's lanes)
-  const int few = a.rows.R <= 16 ? 16 : a.rows.R <= 32 ? 32 : 0;
+  const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.H, a.rows.heads, view.N, view.C, a.d, !view.table);
+  const int few = plan.few;
   CUtensorMap maps[3];
-  if (!encode_bhnd(&maps[0], a.q, a.B * a.rows.units, a.rows.R, a.d, few ? few : 128) ||
+  if (!encode_units(&maps[0], a.q, a.B * a.rows.units, a.rows.heads, view.N, plan.tokens, a.d) ||
       !encode_pages(&maps[1], a.k, a.tokens, a.Hkv, a.pages, a.box_rows, a.d) ||
       !encode_pages(&maps[2], a.v, a.tokens, a.Hkv, a.pages, a.box_rows, a.d))
     return FA_ERR_CUDA;
@@ -211,6 +234,7 @@ fa_status run_span_fwd(const SpanCall& a) {
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
   fa::SpanFwdParams p{};
   p.rows = a.rows;
+  p.rows.tokens = plan.tokens;
   p.rows.tiles = plan.tiles;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
@@ -218,8 +242,8 @@ fa_status run_span_fwd(const SpanCall& a) {
   p.part_lse = reinterpret_cast<float*>(ws + plan.lse_at);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_at);
   p.part_rows = plan.part_rows;
+  p.q_bytes = a.rows.heads * plan.tokens * a.d * 2;
   p.B = a.B;
-  p.H = a.H;
   p.row_tiles = plan.row_tiles;
   p.pages = a.pages;
   p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -324,7 +348,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   fa::SpanBwdParams p{};
   p.rows.view = view;
   p.rows.bounds = reinterpret_cast<int4*>(ws + w.bounds_at);
-  p.rows.R = N, p.rows.tiles = nb, p.rows.units = H, p.rows.kv_div = H / Hkv;
+  p.rows.heads = 1, p.rows.tokens = 128, p.rows.tiles = nb, p.rows.units = H, p.rows.kv_div = H / Hkv;
   p.lo = reinterpret_cast<int*>(ws + w.lo_at);
   p.hi = reinterpret_cast<int*>(ws + w.hi_at);
   p.plan = reinterpret_cast<fa::SpanBwdPlan*>(ws);
@@ -371,7 +395,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
 extern "C" {
 
 size_t fa_span_fwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
-  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanFwdPlan::of(B, H, N, N, d, true).total : 0;
+  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanFwdPlan::of(B, H, 1, N, N, d, true).total : 0;
 }
 
 fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
@@ -388,7 +412,7 @@ fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* ke
   if ((st = check_device_ptrs_given({key_begin, key_end, slopes})) != FA_OK) return st;
   SpanCall a{};
   a.rows.view = {key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
-  a.rows.R = N;
+  a.rows.heads = 1;
   a.rows.units = H;
   a.rows.kv_div = H / Hkv;
   a.q = q;
@@ -424,7 +448,9 @@ fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* ke
 
 size_t fa_paged_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d) {
   int R;
-  return check_cross_shape(B, H, Hkv, T, C, d, &R) == FA_OK ? SpanFwdPlan::of(B, Hkv, R, C, d, false).total : 0;
+  return check_cross_shape(B, H, Hkv, T, C, d, &R) == FA_OK
+             ? SpanFwdPlan::of(B, H, span_unit_heads(H / Hkv, T), T, C, d, false).total
+             : 0;
 }
 
 fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v_pages, const int* page_table,
@@ -449,9 +475,9 @@ fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v
   SpanCall a{};
   a.rows.view = {nullptr, nullptr, cache_lens, chunk_lens, page_table, table_width, pages.shift(), T,
                  (int)pages.capacity(), 1, window};
-  a.rows.R = R;
-  a.rows.units = Hkv;
-  a.rows.kv_div = 1;
+  a.rows.heads = span_unit_heads(H / Hkv, T);
+  a.rows.units = H / a.rows.heads;
+  a.rows.kv_div = a.rows.units / Hkv;
   a.q = q;
   a.k = page_rows(k_pages), a.v = page_rows(v_pages);
   a.box_rows = std::min(page_size, 128), a.tokens = page_size, a.pages = num_pages;

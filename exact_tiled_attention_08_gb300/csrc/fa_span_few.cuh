@@ -309,11 +309,11 @@ __global__ void __launch_bounds__(256, 1)
       if (tid < 32) {
         int lo = 0, hi = 0;
         float slope2 = 0.f;
-        if (tid < p.rows.R) {
-          const int head = tid / v.N, tok = tid - head * v.N;
+        const int tok = tid / p.rows.heads;
+        if (tok < fresh) {
           pos = len + tok;
-          if (tok < fresh) v.span(b, tok, pos, lo, hi);
-          if (p.slopes) slope2 = p.slopes[u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
+          v.span(b, tok, pos, lo, hi);
+          if (p.slopes) slope2 = p.slopes[(u - tok) * p.rows.heads + tid] * 1.4426950408889634f;
         }
         rows->lo[tid] = lo, rows->hi[tid] = hi, rows->slope2[tid] = slope2;
         rows->rel[g & 1][tid] = (float)(pos - (j1 - 1) * 128);
@@ -452,11 +452,13 @@ __global__ void __launch_bounds__(256, 1)
         break;
       }
       const bool first = flags & kSegFirst, whole = first && (flags & kSegLast);
-      const size_t grow = ((size_t)b * p.rows.units + u) * p.rows.R;
+      int head = 0, tok = 0;
       const size_t prow = ((size_t)2 * blockIdx.x + (first ? 1 : 0)) * p.part_rows;
 #pragma unroll
       for (int q = 0; q < R; ++q) {
-        if (q >= p.rows.R || q % v.N >= fresh) continue;
+        if (tok >= fresh) continue;
+        const size_t grow = p.rows.row(b, u, head, tok);
+        if (++head == p.rows.heads) head = 0, ++tok;
         const float sum = rows->part[0][q] + rows->part[1][q] + rows->part[2][q] + rows->part[3][q];
         const float inv = sum == 0.f ? 0.f : 1.f / sum, value = __uint_as_float(o[q]) * inv;
         const float lse2 = sum == 0.f ? -CUDART_INF_F : rows->ref[q] + log2f(sum);
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(256, 1)
           if (CLUSTER)
             sPart[q * (D + 4) + tid] = value;
           else if (whole)
-            p.o[(grow + q) * D + tid] = __float2bfloat16(value);
+            p.o[grow * D + tid] = __float2bfloat16(value);
           else
             p.part_o[(prow + q) * D + tid] = value;
         }
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(256, 1)
           if (CLUSTER)
             rows->lse[q] = lse2;
           else if (whole)
-            p.lse[grow + q] = lse2 * 0.6931471805599453f;
+            p.lse[grow] = lse2 * 0.6931471805599453f;
           else
             p.part_lse[prow + q] = lse2;
         }
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(256, 1)
         meta.split = 1;
         meta.b = b;
         meta.u = u;
-        meta.row0 = 0;
+        meta.token0 = 0;
         meta.last = bar->end + rest;
         meta.total = bar->total;
       }
@@ -505,8 +507,7 @@ __global__ void __launch_bounds__(256, 1)
     const int ctas = p.cluster, item = blockIdx.x / ctas, b = item / p.rows.units;
     const int fresh = v.rows(b, v.len(b));
     const float* parts = reinterpret_cast<const float*>(sKV) + lane * E;
-    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.R; row += ctas * (C::kThreads / 32)) {
-      if (row % v.N >= fresh) continue;
+    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.heads * fresh; row += ctas * (C::kThreads / 32)) {
       float l[kMost], o[kMost][E], mx = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < kMost; ++i)
@@ -530,7 +531,8 @@ __global__ void __launch_bounds__(256, 1)
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
         }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t grow = (size_t)item * p.rows.R + row;  // (one row tile per unit)
+      const int tok = row / p.rows.heads;
+      const size_t grow = p.rows.row(b, item - b * p.rows.units, row - tok * p.rows.heads, tok);
       uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

@@ -40,7 +40,7 @@ namespace fa {
 
 struct SpanMeta {     // of each CTA, for the combine kernel
   int split;          // its last item goes on in the next CTA
-  int b, u, row0;     // that item
+  int b, u, token0;   // that item
   long long last;     // the place behind the item's last block
   long long total;    // places of the sequence
 };
@@ -52,8 +52,9 @@ struct SpanFwdParams {
   SpanMeta* meta;    // [grid]
   float* part_lse;   // [2 grid][part_rows], base 2
   float* part_o;     // [2 grid][part_rows][d]
-  int part_rows;     // rows of a part: 256 (PAIR) or R (ALT)
-  int B, H;
+  int part_rows;     // rows of a part: 256 (PAIR) or a unit's (ALT)
+  int q_bytes;       // of a row tile's queries
+  int B;
   int row_tiles;     // row tiles (PAIR: pairs of them) per unit
   int cluster;       // fa_span_few_kernel: CTAs per item, joined in a cluster (1: none)
   int pages;         // pages in the pool
@@ -84,7 +85,7 @@ __device__ __forceinline__ long long span_rank(int round, int G, int c) {
 // longer fit the instruction cache.)
 enum : int { kSegFirst = 1, kSegLast = 2, kSegTwo = 4, kSegDirtyFront = 8, kSegDirtyBack = 16, kSegEnd = 32 };
 struct SpanSeg {
-  int b, u, row0;
+  int b, u, token0;
   int flags;           // the item's first and last block are in it; PAIR: there is a second row tile;
                        // rows of V in block j0 and j1 - 1 that nobody sees; no more segments
   int j0, j1, rest;    // blocks; the item's blocks behind them
@@ -98,7 +99,10 @@ enum : int { kSiteSpanSeg = 70, kSiteSpanSegFree };
 template <bool PAIR>
 struct SpanItem {
   SpanTile t[PAIR ? 2 : 1];
-  int lo, hi, base, n;  // keys seen; first block and number of blocks (at least one, so that rows without keys are written)
+  int lo, hi, base;  // keys seen; first block
+  int n;             // number of blocks: none without tokens, else at least one, so that rows without keys are written
+  int token0;
+  bool two;          // there are tokens in the second tile
   __device__ __forceinline__ SpanItem(const SpanFwdParams& p, int e) {
     const int b = e / p.row_tiles, rt = p.row_tiles - 1 - (e - b * p.row_tiles);
     t[0] = p.rows.tile(b, PAIR ? 2 * rt : rt);
@@ -109,8 +113,12 @@ struct SpanItem {
       else if (!t[1].empty()) lo = min(lo, t[1].lo), hi = max(hi, t[1].hi);
     }
     base = lo >> 7;
-    n = max(((hi + 127) >> 7) - base, 1);
+    const int there = p.rows.view.rows(b, p.rows.view.len(b));
+    token0 = (PAIR ? 2 * rt : rt) * p.rows.tokens;
+    two = PAIR && token0 + p.rows.tokens < there;
+    n = token0 < there ? max(((hi + 127) >> 7) - base, 1) : 0;
   }
+  __device__ __forceinline__ int places() const { return n > 0 ? n + kCrossStart : 0; }
 };
 
 // The next segment.  Ranks are numbered by entry (with `order`: entries by falling cost), all
@@ -133,16 +141,19 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t
     }
     const SpanItem<PAIR> item(p, e);
     s.b = e / p.row_tiles;
-    const int rt = p.row_tiles - 1 - (e - s.b * p.row_tiles);
-    s.row0 = rt * (PAIR ? 256 : 128);
+    s.token0 = item.token0;
     s.lo = item.lo, s.hi = item.hi;
     const int end_block = item.base + item.n;
     if (at.mode != kSpanShares) {
       s.j0 = item.base, s.j1 = end_block;
       --at.left;
       at.e = (int)span_rank(++at.j, gridDim.x, blockIdx.x);
+      if (item.n == 0) continue;
+    } else if (item.n == 0) {
+      ++at.e;  // (the entry's units all)
+      continue;
     } else {
-      const int places = item.n + kCrossStart, end = min(places, at.j + min(at.left, places));
+      const int places = item.places(), end = min(places, at.j + min(at.left, places));
       s.j0 = item.base + max(at.j - kCrossStart, 0);
       s.j1 = item.base + end - kCrossStart;
       at.left -= end - at.j;
@@ -155,7 +166,7 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t
     }
     s.rest = end_block - s.j1;
     s.flags = (s.j0 == item.base ? kSegFirst : 0) | (s.rest == 0 ? kSegLast : 0) |
-              (PAIR && s.row0 + 128 < p.rows.R ? kSegTwo : 0);
+              (item.two ? kSegTwo : 0);
     // (past the keys of a contiguous tensor the TMA has filled zeros)
     const int filled = p.rows.view.table ? s.j1 * 128 : min(p.rows.view.C, s.j1 * 128);
     if (s.lo > s.j0 * 128 || (s.j1 == s.j0 + 1 && s.hi < filled)) s.flags |= kSegDirtyFront;
@@ -226,11 +237,12 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
     }
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      const int n = sorted && pass > 0 ? one : SpanItem<PAIR>(p, e).n + kCrossStart;
+      const int n = sorted && pass > 0 ? one : SpanItem<PAIR>(p, e).places();
       if (pass == 0) {
         mine += n;
         one = n;
       } else if (pass < 3) {
+        if (n == 0) continue;
         const int b = e / p.row_tiles, at = sorted ? place_of : e;
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
@@ -406,11 +418,11 @@ __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUt
   auto load_q = [&](int qs) {
     if (lane == 0) {
       const int tiles = w.flags & kSegTwo ? 2 : 1;
-      mbar_arrive_expect_tx(&bar->q_full[qs], tiles * QBYTES);
+      mbar_arrive_expect_tx(&bar->q_full[qs], tiles * p.q_bytes);
       for (int t = 0; t < tiles; ++t)
         for (int a = 0; a < C::kAtoms; ++a)
-          tma_load_3d(sQ + (PAIR ? t : qs) * QBYTES + a * QATOM, map_q, &bar->q_full[qs], a * 64,
-                      w.row0 + 128 * t, w.b * p.rows.units + w.u);
+          tma_load_4d(sQ + (PAIR ? t : qs) * QBYTES + a * QATOM, map_q, &bar->q_full[qs], a * 64, 0,
+                      w.token0 + p.rows.tokens * t, w.b * p.rows.units + w.u);
     }
     __syncwarp();
   };
@@ -734,7 +746,7 @@ __global__ void __launch_bounds__(384, 1)
           meta.split = 1;
           meta.b = w.b;
           meta.u = w.u;
-          meta.row0 = w.row0;
+          meta.token0 = w.token0;
           meta.last = bar->end + w.rest;
           meta.total = bar->total;
         }
@@ -775,12 +787,12 @@ __global__ void __launch_bounds__(384, 1)
       const int jfirst = (PAIR ? w.a1[t] : w.j1 - t) - 1, jend = PAIR ? w.a0[t] : w.j0;
       const int lo_cut = w.lo_cut[PAIR ? t : 0], hi_cut = w.hi_cut[PAIR ? t : 0];  // blocks that all rows see whole
       {
-        const int b = w.b, row = min(w.row0 + (PAIR ? 128 * t : 0) + r, p.rows.R - 1), head = row / v.N;
-        const int tok = row - head * v.N, len = v.len(b);
+        const int b = w.b, i = r / p.rows.heads, token = w.token0 + (PAIR ? p.rows.tokens * t : 0) + i;
+        const int tok = min(token, v.N - 1), len = v.len(b);
         pos = len + tok;
         v.span(b, tok, pos, row_lo, row_hi);
-        if (MOD >= 2) there = tok < v.rows(b, len);
-        if (MOD & 1) slope2 = p.slopes[w.u * (p.H / p.rows.units) + head] * 1.4426950408889634f;
+        if (MOD >= 2) there = i < p.rows.tokens && token < v.rows(b, len);
+        if (MOD & 1) slope2 = p.slopes[w.u * p.rows.heads + r - i * p.rows.heads] * 1.4426950408889634f;
       }
       float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
       // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
@@ -962,7 +974,6 @@ __global__ void __launch_bounds__(384, 1)
       // ---- end of the segment
       const int flags = w.flags;
       const bool seg_first = flags & kSegFirst, whole = seg_first && (flags & kSegLast);
-      const int row = w.row0 + (PAIR ? 128 * t : 0) + r;
       const bool join = !PAIR && w.j1 - w.j0 >= 2;
       float lo = l + lcorr, a0 = 1.f, a1 = 0.f;
       if (join) {
@@ -993,8 +1004,9 @@ __global__ void __launch_bounds__(384, 1)
       a0 *= inv;
       a1 *= inv;
       const float lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-      const bool write = row < p.rows.R && row % v.N < v.rows(w.b, v.len(w.b));
-      const size_t grow = ((size_t)w.b * p.rows.units + w.u) * p.rows.R + row;
+      const int of_tile = r / p.rows.heads, token = w.token0 + (PAIR ? p.rows.tokens * t : 0) + of_tile;
+      const bool write = of_tile < p.rows.tokens && token < v.rows(w.b, v.len(w.b));
+      const size_t grow = p.rows.row(w.b, w.u, r - of_tile * p.rows.heads, token);
       const size_t prow = ((size_t)2 * blockIdx.x + (seg_first ? 1 : 0)) * p.part_rows + (PAIR ? 128 * t : 0) + r;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1072,12 +1084,13 @@ __global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_const
   const int parts = (int)((meta.last * min((long long)gridDim.x, meta.total) - 1) / meta.total) - (int)blockIdx.x + 1;
   const int lane = threadIdx.x & 31, local0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
   const int fresh = v.rows(meta.b, v.len(meta.b));
-  const size_t grow0 = ((size_t)meta.b * p.rows.units + meta.u) * p.rows.R + meta.row0 + local0;
   // part i: the last segment of CTA x, then the first of each CTA after it
   auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local0; };
   for (int r = 0; r < kRows; ++r) {
-    const int row = meta.row0 + local0 + r;
-    if (local0 + r >= p.part_rows || row >= p.rows.R || row % v.N >= fresh) continue;
+    const int local = local0 + r, second = PAIR ? local >> 7 : 0, of_tile = (local - second * 128) / p.rows.heads;
+    const int token = meta.token0 + second * p.rows.tokens + of_tile;
+    if (local >= p.part_rows || of_tile >= p.rows.tokens || token >= fresh) continue;
+    const size_t grow = p.rows.row(meta.b, meta.u, local - second * 128 - of_tile * p.rows.heads, token);
     float acc[E], sum = 0.f, ref = -CUDART_INF_F;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1112,10 +1125,10 @@ __global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_const
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + (grow0 + r) * D) + lane * (E / 2);
+    uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0) p.lse[grow0 + r] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
+    if (lane == 0) p.lse[grow] = (sum == 0.f ? -CUDART_INF_F : ref + log2f(sum)) * 0.6931471805599453f;
   }
 }
 

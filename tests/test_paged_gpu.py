@@ -364,3 +364,41 @@ def test_a_prompt_in_chunks_and_then_tokens():
             assert not off.numel() or off.max() <= 2 * (1e-4 + 130 * 2.0 ** -16 + 30 * 2.0 ** -21)
         done = [x + c for x, c in zip(done, chunks)]
     assert done == total
+
+
+@pytest.mark.parametrize("H, Hkv, T, lens, some, window, cap, slopes, d", [
+    # heads of a group that do and do not divide a row tile, groups in several units, chunks that
+    # fill from none to all of the tiles that the longest one has
+    (6, 2, 90, [700, 0, 300], [90, 0, 1], 0, 0.0, True, 64),
+    (5, 1, 51, [130, 61], [51, 26], 0, 30.0, False, 128),
+    (14, 2, 40, [0, 500, 77], [37, 2, 18], 100, 0.0, True, 128),
+    (3, 1, 5, [400], None, 0, 50.0, True, 64),
+    (10, 2, 3, [255, 4], [3, 1], 0, 0.0, True, 128),
+    (22, 2, 2, [300, 11, 60], [1, 2, 0], 0, 20.0, True, 64),
+    (7, 1, 18, [129], [17], 0, 0.0, False, 128),
+    (48, 1, 9, [350, 128], [9, 4], 0, 0.0, True, 64),
+    (96, 1, 3, [200], None, 0, 50.0, False, 128),
+    (127, 1, 2, [100], None, 0, 0.0, True, 64),
+    (131, 1, 2, [140], None, 0, 0.0, False, 64),
+    (144, 1, 1, [260], None, 0, 0.0, True, 128),
+    (16, 4, 700, [900, 40, 0, 1200, 3, 0], [1, 700, 0, 2, 33, 1], 0, 0.0, False, 128),
+    (8, 8, 300, [0, 0], [0, 300], 0, 0.0, True, 64),
+    (8, 2, 300, [50, 9], [0, 0], 0, 0.0, False, 64),
+])
+def test_units_of_a_group(H, Hkv, T, lens, some, window, cap, slopes, d):
+    B, size = len(lens), 16
+    chunks = [T] * B if some is None else some
+    width = max(1, max(-(-(n + c) // size) for n, c in zip(lens, chunks)))
+    table, count = tables(lens, chunks, size, width, H)
+    kp, vp = pool(H, count, Hkv, size, d, "tokens"), pool(H + 1, count, Hkv, size, d, "heads")
+    q = randn(H + 2, B, H, T, d)
+    for b, c in enumerate(chunks):
+        q[b, :, c:] = float("nan")
+    sl = slopes_of(H, slopes)
+    o, lse = torch.full((B, H, T, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((B, H, T), 7.0, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(B, H, Hkv, T, width * size, d), dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(q.cuda(), kp, vp, table.cuda(), torch.tensor(lens, **I32).cuda(),
+                    None if some is None else torch.tensor(some, **I32).cuda(), o, lse, ws, 1 / math.sqrt(d), window=window,
+                    cap=cap, slopes=None if sl is None else sl.cuda())
+    assert fa.fa_check_device_status() == fa.FA_OK
+    check_paged(q, kp, vp, table, o, lse, 1 / math.sqrt(d), lens, chunks, window, cap, sl, most=24)
