@@ -72,6 +72,8 @@ struct FewRows {
   float rel[2][32];       // positions from the first key of a block and of the one that follows
   float ref[32];          // the reference (log2 units), -inf: no key so far
   float part[4][32];      // of each warp: maxima, sums
+  float inv[32];          // at the end: 1 / sum
+  char* out[32];          // at the end: where the row goes, or nullptr
   float lse[32];          // CLUSTER: this CTA's part
 };
 static_assert(sizeof(FewRows) <= 2048 && offsetof(FewRows, ref) % 16 == 0, "statistics overflow their shared-memory slot");
@@ -87,6 +89,22 @@ __device__ __forceinline__ bool few_any(bool x) {
       : "r"((uint32_t)x)
       : "memory");
   return any != 0;
+}
+
+// lane q's (q < R) sum of l[q] over the warp
+template <int R>
+__device__ __forceinline__ float few_sum(float (&l)[R]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = R / 2; h > 0; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? l[i] : l[i + h], keep = up ? l[i + h] : l[i];
+      l[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+    }
+  }
+  return R == 16 ? l[0] + __shfl_xor_sync(0xffffffffu, l[0], 16) : l[0];
 }
 
 template <int R>
@@ -437,14 +455,11 @@ __global__ void __launch_bounds__(256, 1)
       }
       bad = !__all_sync(0xffffffffu, span_wait(&bar->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, ctx, kSiteCrossPv));
       tc_fence_after();
-      // ---- end of the segment: sums over the keys, then channel by channel
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        float s = l[q];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == q) rows->part[warp][q] = s;
-      }
+      // ---- end of the segment: sums over the keys, a thread per row for its statistics and a channel
+      // per thread for its values.  (With the statistics in an unrolled loop over the rows, of code that
+      // runs once per segment, a row of a segment took 0.6 us of instruction fetches.)
+      const float sums = few_sum<R>(l);
+      if (lane < R) rows->part[warp][lane] = sums;
       uint32_t o[R];
       few_tmem_ld<R>(tO, o);
       if (few_any(bad)) {
@@ -452,34 +467,42 @@ __global__ void __launch_bounds__(256, 1)
         break;
       }
       const bool first = flags & kSegFirst, whole = first && (flags & kSegLast);
-      int head = 0, tok = 0;
-      const size_t prow = ((size_t)2 * blockIdx.x + (first ? 1 : 0)) * p.part_rows;
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        if (tok >= fresh) continue;
-        const size_t grow = p.rows.row(b, u, head, tok);
-        if (++head == p.rows.heads) head = 0, ++tok;
-        const float sum = rows->part[0][q] + rows->part[1][q] + rows->part[2][q] + rows->part[3][q];
-        const float inv = sum == 0.f ? 0.f : 1.f / sum, value = __uint_as_float(o[q]) * inv;
-        const float lse2 = sum == 0.f ? -CUDART_INF_F : rows->ref[q] + log2f(sum);
-        if (tid < D) {
-          if (CLUSTER)
-            sPart[q * (D + 4) + tid] = value;
-          else if (whole)
-            p.o[grow * D + tid] = __float2bfloat16(value);
-          else
-            p.part_o[(prow + q) * D + tid] = value;
-        }
-        if (tid == 0) {
-          if (CLUSTER)
-            rows->lse[q] = lse2;
-          else if (whole)
+      if (tid < R) {
+        const float sum = rows->part[0][tid] + rows->part[1][tid] + rows->part[2][tid] + rows->part[3][tid];
+        const float lse2 = sum == 0.f ? -CUDART_INF_F : rows->ref[tid] + log2f(sum);
+        const int tok = tid / p.rows.heads;
+        rows->inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        char* out = nullptr;
+        if (CLUSTER) {
+          rows->lse[tid] = lse2;
+        } else if (tok < fresh) {
+          if (whole) {
+            const size_t grow = p.rows.row(b, u, tid - tok * p.rows.heads, tok);
+            out = reinterpret_cast<char*>(p.o + grow * D);
             p.lse[grow] = lse2 * 0.6931471805599453f;
-          else
-            p.part_lse[prow + q] = lse2;
+          } else {
+            const size_t prow = ((size_t)2 * blockIdx.x + (first ? 1 : 0)) * p.part_rows + tid;
+            out = reinterpret_cast<char*>(p.part_o + prow * D);
+            p.part_lse[prow] = lse2;
+          }
+        }
+        rows->out[tid] = out;
+      }
+      few_sync();
+      if (tid < D) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const float value = __uint_as_float(o[q]) * rows->inv[q];
+          if (CLUSTER) {
+            sPart[q * (D + 4) + tid] = value;
+          } else if (char* out = rows->out[q]) {
+            if (whole)
+              reinterpret_cast<__nv_bfloat16*>(out)[tid] = __float2bfloat16(value);
+            else
+              reinterpret_cast<float*>(out)[tid] = value;
+          }
         }
       }
-      few_sync();  // (the statistics have been read)
       if ((flags & (kSegFirst | kSegLast)) == kSegFirst) {
         // (the CTA's last segment: the item's other blocks follow its share)
         meta.split = 1;
