@@ -13,31 +13,34 @@
 
 namespace fa {
 
+// PAGED: keys in pages; else in [B][Hkv][N][d].  (The kernels are compiled for each of the two: what the other
+// form needs costs instruction fetches.  N=8192 H=32/8 d=128 causal, one request, capped: 560 and 496 us.)
+template <bool PAGED>
 struct SpanView {
   const int *begin, *end;      // [B][N] or nullptr: 0 and C
   const int *lens, *chunks;    // pages: tokens before the chunk [B]; new tokens [B], or nullptr: N
-  const int* table;            // pages: [B][width] page numbers, or nullptr: keys in [B][Hkv][N][d]
+  const int* table;            // pages: [B][width] page numbers
   int width, page_shift;       // pages: entries per request; log2 of a page's rows
   int N;                       // query rows per head
   int C;                       // keys: N, or width pages
   int causal, window;          // j <= p_i; |p_i - j| < window (0: any)
-  __device__ __forceinline__ int len(int b) const { return table ? min(max(lens[b], 0), C) : 0; }
+  __device__ __forceinline__ int len(int b) const { return PAGED ? min(max(lens[b], 0), C) : 0; }
   // query rows of request b that exist
   __device__ __forceinline__ int rows(int b, int len) const {
-    return table ? min(min(max(chunks ? chunks[b] : N, 0), N), C - len) : N;
+    return PAGED ? min(min(max(chunks ? chunks[b] : N, 0), N), C - len) : N;
   }
   // the keys that query i of request b sees (pos: its position); lo >= hi: none
   __device__ __forceinline__ void span(int b, int i, int pos, int& lo, int& hi) const {
-    lo = begin ? max(begin[(long long)b * N + i], 0) : 0;
-    hi = end ? min(end[(long long)b * N + i], C) : C;
+    lo = !PAGED && begin ? max(begin[(long long)b * N + i], 0) : 0;
+    hi = !PAGED && end ? min(end[(long long)b * N + i], C) : C;
     clip(pos, pos, lo, hi);
   }
   // what is left of [lo, hi) for queries at positions p0 .. p1
   __device__ __forceinline__ void clip(int p0, int p1, int& lo, int& hi) const {
-    if (causal) hi = min(hi, p1 + 1);
+    if (PAGED || causal) hi = min(hi, p1 + 1);
     if (window) {
       lo = max(lo, p0 - window + 1);
-      hi = (int)min((long long)hi, (long long)p1 + window);
+      if (!PAGED) hi = (int)min((long long)hi, (long long)p1 + window);
     }
   }
 };
@@ -58,22 +61,25 @@ struct SpanTile {
 // Query rows come in units: a query head's, or (pages) those of the heads that share a
 // key/value head.  A tile has whole tokens, row r is head r % heads of its token r / heads, so
 // that a request's new tokens fill as few tiles as they can, whatever the others bring.
+template <bool PAGED>
 struct SpanRows {
-  SpanView view;
+  SpanView<PAGED> view;
   const int4* bounds;  // [B][tiles] SpanTile, or nullptr: the mask is a formula of the position
-  int heads, tokens;   // heads of a unit; tokens of a tile
+  int unit_heads, tile_tokens;  // pages: heads of a unit; tokens of a tile
   int tiles;           // tiles of a unit's N tokens
   int units, kv_div;   // units of a request; of a key/value head
+  __device__ __forceinline__ int heads() const { return PAGED ? unit_heads : 1; }
+  __device__ __forceinline__ int tokens() const { return PAGED ? tile_tokens : 128; }
   // row of [B][H][N]
   __device__ __forceinline__ size_t row(int b, int u, int head, int token) const {
-    return (((size_t)b * units + u) * heads + head) * view.N + token;
+    return (((size_t)b * units + u) * heads() + head) * view.N + token;
   }
   __device__ __forceinline__ SpanTile tile(int b, int t) const {
-    if (bounds) {
+    if (!PAGED && bounds) {
       const int4 x = bounds[(long long)b * tiles + t];
       return {x.x, x.y, x.z, x.w};
     }
-    const int len = view.len(b), t0 = t * tokens, t1 = min(t0 + tokens, view.rows(b, len)) - 1;
+    const int len = view.len(b), t0 = t * tokens(), t1 = min(t0 + tokens(), view.rows(b, len)) - 1;
     if (t0 > t1) return {0, 0, 0x7fffffff, 0};
     SpanTile s{0, view.C, 0, view.C};
     view.clip(len + t0, len + t1, s.lo, s.hi);
@@ -103,7 +109,7 @@ __device__ __forceinline__ int4 span_tile_reduce(int lo, int hi, bool row, int4*
 }
 
 // Bounds of all tiles where the spans are given by row: a block of 128 threads per tile.
-__global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView v, int tiles, int4* bounds) {
+__global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView<false> v, int tiles, int4* bounds) {
   __shared__ int4 scratch[4];
   grid_wait();
   grid_trigger();

@@ -111,15 +111,15 @@ bool encode_units(CUtensorMap* map, const void* q, int units, int heads, int N, 
 
 // Grid and workspace of the forward, as CrossFwdPlan; with spans by row their tiles' bounds first.
 struct SpanFwdPlan {
-  int few;  // the kernel for 16 or 32 rows, or 0
+  bool few;  // the kernel for up to 16 rows of a unit
   int tokens, tiles, row_tiles, part_rows, ctas;
   bool pair, cuts;
   size_t meta_at, lse_at, o_at, total;
-  static SpanFwdPlan of(int B, int H, int heads, int N, int C, int d, bool bounds) {
+  static SpanFwdPlan of(int B, int H, int heads, int N, int C, int d, bool paged) {
     SpanFwdPlan w;
     const long long rows_all = (long long)heads * N;
-    w.few = rows_all <= 16 ? 16 : rows_all <= 32 ? 32 : 0;
-    w.tokens = (w.few ? w.few : 128) / heads;
+    w.few = paged && rows_all <= fa::kFewRows;
+    w.tokens = (w.few ? fa::kFewRows : 128) / heads;
     w.tiles = (N + w.tokens - 1) / w.tokens;
     w.pair = w.tiles > 1;
     w.row_tiles = w.pair ? (w.tiles + 1) / 2 : 1;
@@ -129,7 +129,7 @@ struct SpanFwdPlan {
     w.cuts = C > 128;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t rows = w.cuts ? (size_t)2 * w.ctas * w.part_rows : 0;
-    w.meta_at = bounds ? up((size_t)B * w.tiles * sizeof(int4)) : 0;
+    w.meta_at = !paged ? up((size_t)B * w.tiles * sizeof(int4)) : 0;
     w.lse_at = w.meta_at + up(w.ctas * sizeof(fa::SpanMeta));
     w.o_at = w.lse_at + up(rows * sizeof(float));
     w.total = w.o_at + up(rows * d * sizeof(float)) + 256;  // (the base is brought to a 256-byte boundary)
@@ -137,10 +137,10 @@ struct SpanFwdPlan {
   }
 };
 
-template <int D, int MOD, bool PAIR>
-fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams& p, unsigned grid, cudaStream_t stream) {
+template <int D, int MOD, bool PAIR, bool PAGED>
+fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams<PAGED>& p, unsigned grid, cudaStream_t stream) {
   using C = fa::CrossCfg<D>;
-  auto kernel = fa::fa_span_fwd_kernel<D, MOD, PAIR>;
+  auto kernel = fa::fa_span_fwd_kernel<D, MOD, PAIR, PAGED>;
   if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
@@ -151,60 +151,68 @@ fa_status launch_span_fwd(const CUtensorMap* maps, const fa::SpanFwdParams& p, u
              : FA_ERR_CUDA;
 }
 
-template <int D, int MOD>
-fa_status launch_span_form(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
-                           cudaStream_t stream) {
-  return pair ? launch_span_fwd<D, MOD, true>(maps, p, grid, stream) : launch_span_fwd<D, MOD, false>(maps, p, grid, stream);
-}
-
 // Clusters of 8, 4 and 2 CTAs of the kernel for few rows that the device holds at once, asked once per device.
-template <int D, int R>
+template <int D>
 fa::CrossClusterFit few_cluster_fit(int dev) {
-  using C = fa::FewCfg<D, R>;
+  using C = fa::FewCfg<D>;
   static std::atomic<unsigned long long> known[64];  // by device: the three numbers and a bit that says so
-  return cluster_fit(fa::fa_span_few_kernel<D, R, true>, C::kThreads, C::kSmemBytes, dev, known);
+  return cluster_fit(fa::fa_span_few_kernel<D, true>, C::kThreads, C::kSmemBytes, dev, known);
 }
 
-template <int D, int R>
-fa_status launch_span_few(const CUtensorMap* maps, fa::SpanFwdParams& p, unsigned grid, int sms, cudaStream_t stream) {
-  using C = fa::FewCfg<D, R>;
+template <int D>
+fa_status launch_span_few(const CUtensorMap* maps, fa::SpanFwdParams<true>& p, unsigned grid, int sms, cudaStream_t stream) {
+  using C = fa::FewCfg<D>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   // One request of a length that only the device knows counts as half of what its pages hold, as
   // in the cross forward.
-  const bool paged = p.rows.view.table != nullptr;
   const long long items = (long long)p.B * p.rows.units;
   int blocks = (p.rows.view.C + 127) / 128;
-  if (p.B == 1 && paged && blocks > 2) blocks = (blocks + 1) / 2;
-  p.cluster = fa::cross_cluster(items, blocks, p.rows.heads * p.rows.view.N, p.B == 1 || !paged, std::min(sms, fa::kCrossMaxCtas),
-                                few_cluster_fit<D, R>(dev));
+  if (p.B == 1 && blocks > 2) blocks = (blocks + 1) / 2;
+  p.cluster = fa::cross_cluster(items, blocks, p.part_rows, p.B == 1, std::min(sms, fa::kCrossMaxCtas),
+                                few_cluster_fit<D>(dev));
   if (p.cluster > 1) {
-    auto kernel = fa::fa_span_few_kernel<D, R, true>;
+    auto kernel = fa::fa_span_few_kernel<D, true>;
     if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
     return launch_early_clusters(kernel, dim3((unsigned)(items * p.cluster)), p.cluster, C::kThreads, C::kSmemBytes, stream,
                                  maps[0], maps[1], maps[2], p) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
   }
-  auto kernel = fa::fa_span_few_kernel<D, R, false>;
+  auto kernel = fa::fa_span_few_kernel<D, false>;
   if (set_smem(kernel, C::kSmemBytes) != cudaSuccess) return FA_ERR_CUDA;
   return launch_early(kernel, dim3(grid), C::kThreads, C::kSmemBytes, stream, maps[0], maps[1], maps[2], p) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
 
-template <int D>
-fa_status launch_span_mod(const CUtensorMap* maps, const fa::SpanFwdParams& p, bool pair, unsigned grid,
-                          cudaStream_t stream) {
+template <int D, bool PAIR, bool PAGED>
+fa_status launch_span_mod(const CUtensorMap* maps, const fa::SpanFwdParams<PAGED>& p, unsigned grid, cudaStream_t stream) {
   if (p.cap.top > 0.f)
-    return p.slopes ? launch_span_form<D, 3>(maps, p, pair, grid, stream)
-                    : launch_span_form<D, 2>(maps, p, pair, grid, stream);
-  return p.slopes ? launch_span_form<D, 1>(maps, p, pair, grid, stream)
-                  : launch_span_form<D, 0>(maps, p, pair, grid, stream);
+    return p.slopes ? launch_span_fwd<D, 3, PAIR>(maps, p, grid, stream) : launch_span_fwd<D, 2, PAIR>(maps, p, grid, stream);
+  return p.slopes ? launch_span_fwd<D, 1, PAIR>(maps, p, grid, stream) : launch_span_fwd<D, 0, PAIR>(maps, p, grid, stream);
 }
 
+// The forward's main kernel: two row tiles per item, one, or (pages) few rows.
+template <int D, bool PAGED>
+fa_status launch_span_form(const CUtensorMap* maps, fa::SpanFwdParams<PAGED>& p, const SpanFwdPlan& plan, unsigned grid,
+                           int sms, cudaStream_t stream) {
+  if constexpr (PAGED)
+    if (plan.few) return launch_span_few<D>(maps, p, grid, sms, stream);
+  return plan.pair ? launch_span_mod<D, true>(maps, p, grid, stream) : launch_span_mod<D, false>(maps, p, grid, stream);
+}
+
+template <int D, bool PAGED>
+fa_status launch_span_combine(const fa::SpanFwdParams<PAGED>& p, const SpanFwdPlan& plan, unsigned grid, cudaStream_t stream) {
+  const int per_block = plan.pair ? 32 : 8;  // rows of a block
+  const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
+  auto combine = plan.pair ? fa::fa_span_combine_kernel<D, true, PAGED> : fa::fa_span_combine_kernel<D, false, PAGED>;
+  return launch_early(combine, parts, 256, 0, stream, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <bool PAGED>
 struct SpanCall {
-  fa::SpanRows rows;
+  fa::SpanRows<PAGED> rows;
   const void* q;
   fa::PageRows k, v;
   int box_rows, tokens, pages;  // of the key and value tensors
@@ -217,13 +225,12 @@ struct SpanCall {
   cudaStream_t stream;
 };
 
-fa_status run_span_fwd(const SpanCall& a) {
-  const fa::SpanView& view = a.rows.view;
-  const bool by_row = view.begin || view.end;
-  const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.H, a.rows.heads, view.N, view.C, a.d, !view.table);
-  const int few = plan.few;
+template <bool PAGED>
+fa_status run_span_fwd(const SpanCall<PAGED>& a) {
+  const fa::SpanView<PAGED>& view = a.rows.view;
+  const SpanFwdPlan plan = SpanFwdPlan::of(a.B, a.H, a.rows.unit_heads, view.N, view.C, a.d, PAGED);
   CUtensorMap maps[3];
-  if (!encode_units(&maps[0], a.q, a.B * a.rows.units, a.rows.heads, view.N, plan.tokens, a.d) ||
+  if (!encode_units(&maps[0], a.q, a.B * a.rows.units, a.rows.unit_heads, view.N, plan.tokens, a.d) ||
       !encode_pages(&maps[1], a.k, a.tokens, a.Hkv, a.pages, a.box_rows, a.d) ||
       !encode_pages(&maps[2], a.v, a.tokens, a.Hkv, a.pages, a.box_rows, a.d))
     return FA_ERR_CUDA;
@@ -232,9 +239,9 @@ fa_status run_span_fwd(const SpanCall& a) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return FA_ERR_CUDA;
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
-  fa::SpanFwdParams p{};
+  fa::SpanFwdParams<PAGED> p{};
   p.rows = a.rows;
-  p.rows.tokens = plan.tokens;
+  p.rows.tile_tokens = plan.tokens;
   p.rows.tiles = plan.tiles;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
@@ -242,7 +249,7 @@ fa_status run_span_fwd(const SpanCall& a) {
   p.part_lse = reinterpret_cast<float*>(ws + plan.lse_at);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_at);
   p.part_rows = plan.part_rows;
-  p.q_bytes = a.rows.heads * plan.tokens * a.d * 2;
+  p.q_bytes = a.rows.unit_heads * plan.tokens * a.d * 2;
   p.B = a.B;
   p.row_tiles = plan.row_tiles;
   p.pages = a.pages;
@@ -253,32 +260,23 @@ fa_status run_span_fwd(const SpanCall& a) {
   p.debug_stall = g_debug_stall.load();
   p.o_align32 = aligned32(a.o);
   p.cluster = 1;
-  if (by_row) {
-    int4* bounds = reinterpret_cast<int4*>(ws);
-    p.rows.bounds = bounds;
-    if (launch_early(fa::fa_span_bounds_kernel, dim3((unsigned)plan.tiles * (unsigned)a.B), 128, 0, a.stream, view,
-                     plan.tiles, bounds) != cudaSuccess)
-      return FA_ERR_CUDA;
+  if constexpr (!PAGED) {
+    if (view.begin || view.end) {
+      int4* bounds = reinterpret_cast<int4*>(ws);
+      p.rows.bounds = bounds;
+      if (launch_early(fa::fa_span_bounds_kernel, dim3((unsigned)plan.tiles * (unsigned)a.B), 128, 0, a.stream, view,
+                       plan.tiles, bounds) != cudaSuccess)
+        return FA_ERR_CUDA;
+    }
   }
   const unsigned grid = (unsigned)std::min(plan.ctas, sms);
-  fa_status st;
-  if (few)
-    st = a.d == 128 ? (few == 16 ? launch_span_few<128, 16>(maps, p, grid, sms, a.stream)
-                                 : launch_span_few<128, 32>(maps, p, grid, sms, a.stream))
-                    : (few == 16 ? launch_span_few<64, 16>(maps, p, grid, sms, a.stream)
-                                 : launch_span_few<64, 32>(maps, p, grid, sms, a.stream));
-  else
-    st = a.d == 128 ? launch_span_mod<128>(maps, p, plan.pair, grid, a.stream)
-                    : launch_span_mod<64>(maps, p, plan.pair, grid, a.stream);
+  const fa_status st = a.d == 128 ? launch_span_form<128>(maps, p, plan, grid, sms, a.stream)
+                                  : launch_span_form<64>(maps, p, plan, grid, sms, a.stream);
   if (st != FA_OK || !plan.cuts || p.cluster > 1) return st;
   // Nothing is cut where whole items cannot take longer than what cutting costs (span_schedule's rule).
   const long long items = (long long)a.B * a.rows.units * plan.row_tiles;
   if ((items + grid - 1) / grid * ((view.C + 127LL) / 128 + fa::kCrossStart) <= fa::kCrossCut) return FA_OK;
-  const int per_block = plan.pair ? 32 : 8;  // rows of a block
-  const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
-  auto combine = a.d == 128 ? (plan.pair ? fa::fa_span_combine_kernel<128, true> : fa::fa_span_combine_kernel<128, false>)
-                            : (plan.pair ? fa::fa_span_combine_kernel<64, true> : fa::fa_span_combine_kernel<64, false>);
-  return launch_early(combine, parts, 256, 0, a.stream, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return a.d == 128 ? launch_span_combine<128>(p, plan, grid, a.stream) : launch_span_combine<64>(p, plan, grid, a.stream);
 }
 
 // workspace of the backward: the plan, the spans and their tiles' bounds, the dQ accumulator (more than
@@ -324,7 +322,7 @@ fa_status launch_span_bwd(const CUtensorMap* maps, const fa::SpanBwdParams& p, u
 }
 
 template <int D>
-fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void* q, const void* k, const void* v,
+fa_status run_span_bwd(const fa::SpanView<false>& view, const float* slopes, const void* q, const void* k, const void* v,
                        const void* o, const void* dout, const float* lse, void* dq, void* dk, void* dv, void* workspace,
                        int B, int H, int Hkv, float scale, float cap, cudaStream_t stream) {
   const int N = view.N, nb = (N + 127) / 128, npad = nb * 128;
@@ -348,7 +346,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
   fa::SpanBwdParams p{};
   p.rows.view = view;
   p.rows.bounds = reinterpret_cast<int4*>(ws + w.bounds_at);
-  p.rows.heads = 1, p.rows.tokens = 128, p.rows.tiles = nb, p.rows.units = H, p.rows.kv_div = H / Hkv;
+  p.rows.unit_heads = 1, p.rows.tile_tokens = 128, p.rows.tiles = nb, p.rows.units = H, p.rows.kv_div = H / Hkv;
   p.lo = reinterpret_cast<int*>(ws + w.lo_at);
   p.hi = reinterpret_cast<int*>(ws + w.hi_at);
   p.plan = reinterpret_cast<fa::SpanBwdPlan*>(ws);
@@ -395,7 +393,7 @@ fa_status run_span_bwd(const fa::SpanView& view, const float* slopes, const void
 extern "C" {
 
 size_t fa_span_fwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
-  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanFwdPlan::of(B, H, 1, N, N, d, true).total : 0;
+  return check_span_shape(B, H, Hkv, N, d) == FA_OK ? SpanFwdPlan::of(B, H, 1, N, N, d, false).total : 0;
 }
 
 fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
@@ -410,9 +408,9 @@ fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* ke
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, lse, workspace})) != FA_OK) return st;
   if ((st = check_device_ptrs_given({key_begin, key_end, slopes})) != FA_OK) return st;
-  SpanCall a{};
+  SpanCall<false> a{};
   a.rows.view = {key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
-  a.rows.heads = 1;
+  a.rows.unit_heads = 1;
   a.rows.units = H;
   a.rows.kv_div = H / Hkv;
   a.q = q;
@@ -441,7 +439,7 @@ fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* ke
     return FA_ERR_MISALIGNED;
   if ((st = check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, workspace})) != FA_OK) return st;
   if ((st = check_device_ptrs_given({key_begin, key_end, slopes})) != FA_OK) return st;
-  const fa::SpanView view{key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
+  const fa::SpanView<false> view{key_begin, key_end, nullptr, nullptr, nullptr, 0, 0, N, N, causal, window};
   return (d == 128 ? run_span_bwd<128> : run_span_bwd<64>)(view, slopes, q, k, v, o, dout, lse, dq, dk, dv, workspace, B, H,
                                                            Hkv, scale, cap, stream);
 }
@@ -449,7 +447,7 @@ fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* ke
 size_t fa_paged_fwd_workspace_bytes(int B, int H, int Hkv, int T, int C, int d) {
   int R;
   return check_cross_shape(B, H, Hkv, T, C, d, &R) == FA_OK
-             ? SpanFwdPlan::of(B, H, span_unit_heads(H / Hkv, T), T, C, d, false).total
+             ? SpanFwdPlan::of(B, H, span_unit_heads(H / Hkv, T), T, C, d, true).total
              : 0;
 }
 
@@ -472,11 +470,11 @@ fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v
   if ((st = check_device_ptrs({q, k_pages->ptr, v_pages->ptr, page_table, cache_lens, o, lse, workspace})) != FA_OK)
     return st;
   if ((st = check_device_ptrs_given({chunk_lens, slopes})) != FA_OK) return st;
-  SpanCall a{};
+  SpanCall<true> a{};
   a.rows.view = {nullptr, nullptr, cache_lens, chunk_lens, page_table, table_width, pages.shift(), T,
                  (int)pages.capacity(), 1, window};
-  a.rows.heads = span_unit_heads(H / Hkv, T);
-  a.rows.units = H / a.rows.heads;
+  a.rows.unit_heads = span_unit_heads(H / Hkv, T);
+  a.rows.units = H / a.rows.unit_heads;
   a.rows.kv_div = a.rows.units / Hkv;
   a.q = q;
   a.k = page_rows(k_pages), a.v = page_rows(v_pages);

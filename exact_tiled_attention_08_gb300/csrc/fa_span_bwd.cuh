@@ -49,7 +49,7 @@ constexpr int kSpanBwdSlots = 608;  // runs of cut items
 constexpr int kSpanBwdSegs = 2;
 
 struct SpanBwdParams {
-  SpanRows rows;           // (tiles of the query heads; bounds always given)
+  SpanRows<false> rows;           // (tiles of the query heads; bounds always given)
   const int *lo, *hi;      // [B][npad] spans of the queries
   SpanBwdPlan* plan;
   SpanRun* runs;           // [entries + kSpanBwdSlots], request by request
@@ -78,7 +78,7 @@ struct SpanBwdParams {
 template <int D>
 __global__ void __launch_bounds__(256)
     fa_span_bwd_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, float* delta_pad,
-                            float* lse2_pad, float* dq_acc, const SpanView v, int* lo_pad, int* hi_pad, int4* bounds,
+                            float* lse2_pad, float* dq_acc, const SpanView<false> v, int* lo_pad, int* hi_pad, int4* bounds,
                             int B, int npad, long long padded_rows) {
   constexpr int kThreadsPerRow = D / 8, kRows = 256 / kThreadsPerRow;
   __shared__ int4 scratch[8];  // (of the first four warps, and what the others leave)
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256)
 // The query blocks of a key block: from the first to the last that sees one of its keys
 // (none: the first, whose pairs are all masked, so that zeros are written).  By one warp.
 __device__ __forceinline__ int2 span_bwd_hull(const SpanBwdParams& p, int b, int jb) {
-  const SpanView& v = p.rows.view;
+  const SpanView<false>& v = p.rows.view;
   const int lane = threadIdx.x & 31;
   if (!v.begin && !v.end) {
     int i0 = 0, i1 = p.nb;

@@ -1,11 +1,11 @@
-// Forward of attention to spans of keys for units of at most 32 rows: a token, or a
-// few, of the query heads that share a key/value head.
+// Forward of attention to spans of keys in pages, for units of at most 16 rows: a token, or
+// a few, of the query heads that share a key/value head.
 //
 // What fa_span_fwd_kernel does for 128 rows would be empty rows here, and its
 // exponentials (128 keys of 128 rows a block) take longer than the block's 64 KB of keys
 // and values need from memory.  So the products are turned around: S^T = K Q^T has
-// the keys on the tensor memory's lanes and R = 16 or 32 columns of rows, a thread holds one
-// key's R scores, and O^T += V^T P^T has the d channels on the lanes.  P goes to
+// the keys on the tensor memory's lanes and 16 columns of rows, a thread holds one
+// key's 16 scores, and O^T += V^T P^T has the d channels on the lanes.  P goes to
 // shared memory as [row][key], where it is the B operand.
 //
 // The maximum of a row is over lanes now.  The four warps keep one reference per row in
@@ -26,12 +26,15 @@
 
 namespace fa {
 
-template <int D, int R>
+constexpr int kFewRows = 16;
+
+template <int D>
 struct FewCfg {
+  static constexpr int R = kFewRows;
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kAtoms = D / 64;
   static constexpr int kThreads = 256;  // four softmax warps, one that loads K, the issuing one, one that loads V
-  static constexpr int kKSlots = D == 128 ? 3 : 6, kVSlots = D == 128 && R == 32 ? 2 : kKSlots, kSlots = kKSlots + kVSlots;
+  static constexpr int kKSlots = D == 128 ? 3 : 6, kVSlots = kKSlots, kSlots = kKSlots + kVSlots;
   static __device__ __forceinline__ int slot(int kv, int g) { return kv ? kKSlots + g % kVSlots : g % kKSlots; }
   static __device__ __forceinline__ int use(int kv, int g) { return g / (kv ? kVSlots : kKSlots); }
   static constexpr int kQAtom = R * 128, kQBytes = kAtoms * kQAtom;  // atoms of 64 columns
@@ -91,12 +94,11 @@ __device__ __forceinline__ bool few_any(bool x) {
   return any != 0;
 }
 
-// lane q's (q < R) sum of l[q] over the warp
-template <int R>
-__device__ __forceinline__ float few_sum(float (&l)[R]) {
+// lane q's (q < 16) sum of l[q] over the warp
+__device__ __forceinline__ float few_sum(float (&l)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int h = R / 2; h > 0; h >>= 1) {
+  for (int h = 8; h > 0; h >>= 1) {
     const bool up = lane & h;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -104,27 +106,16 @@ __device__ __forceinline__ float few_sum(float (&l)[R]) {
       l[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
     }
   }
-  return R == 16 ? l[0] + __shfl_xor_sync(0xffffffffu, l[0], 16) : l[0];
+  return l[0] + __shfl_xor_sync(0xffffffffu, l[0], 16);
 }
 
-template <int R>
-__device__ __forceinline__ void few_tmem_ld(uint32_t at, uint32_t (&x)[R]) {
-  if constexpr (R == 16) {
-    tmem_ld16(at, x);
-    tmem_wait_ld();
-    reg_fence16(x);
-  } else {
-    tmem_ld32(at, x);
-    tmem_wait_ld();
-    reg_fence32(x);
-  }
+__device__ __forceinline__ void few_tmem_ld(uint32_t at, uint32_t (&x)[16]) {
+  tmem_ld16(at, x);
+  tmem_wait_ld();
+  reg_fence16(x);
 }
-template <int R>
-__device__ __forceinline__ void few_tmem_st(uint32_t at, const uint32_t (&x)[R]) {
-  if constexpr (R == 16)
-    tmem_st16(at, x);
-  else
-    tmem_st32(at, x);
+__device__ __forceinline__ void few_tmem_st(uint32_t at, const uint32_t (&x)[16]) {
+  tmem_st16(at, x);
   tmem_wait_st();
 }
 
@@ -136,17 +127,18 @@ __device__ __forceinline__ int few_order(float x) {
 __device__ __forceinline__ float few_order(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // The share of a cluster's item, by one thread.
-__device__ __forceinline__ void span_cluster_share(const SpanFwdParams& p, SpanPlace* place) {
+__device__ __forceinline__ void span_cluster_share(const SpanFwdParams<true>& p, SpanPlace* place) {
   const int k = blockIdx.x / p.cluster, rank = blockIdx.x - k * p.cluster, e = k / p.rows.units;
-  const int n = SpanItem<false>(p, e).n, j0 = rank * n / p.cluster, j1 = (rank + 1) * n / p.cluster;
+  const int n = SpanItem<false, true>(p, e).n, j0 = rank * n / p.cluster, j1 = (rank + 1) * n / p.cluster;
   *place = SpanPlace{e, k - e * p.rows.units, j0 + kCrossStart, j1 - j0, kSpanShares};
 }
 
-template <int D, int R, bool CLUSTER>
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(256, 1)
     fa_span_few_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
-  using C = FewCfg<D, R>;
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams<true> p) {
+  using C = FewCfg<D>;
+  constexpr int R = kFewRows;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
@@ -164,7 +156,7 @@ __global__ void __launch_bounds__(256, 1)
   uint8_t* sSchedule = reinterpret_cast<uint8_t*>(rows) + C::kStatBytes;
   FewBarriers* bar = reinterpret_cast<FewBarriers*>(sSchedule + C::kScheduleBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const SpanView& v = p.rows.view;
+  const SpanView<true>& v = p.rows.view;
 
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -212,37 +204,10 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t tmem = bar->tmem_base;
   const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
 
-  if (warp == 4) {
+  if (warp == 4 || warp == 6) {
     // ------------------------------------------------------------------ segments and TMA
-    span_load_warp<C, false, true, C::kQBytes, C::kQAtom>(p, &map_q, &map_k, &map_v, bar, nullptr, sQ, sKV, ctx);
-    __syncwarp();
-  } else if (warp == 6) {
-    // ------------------------------------------------------------------ TMA of the V tiles
-    // (A box costs the warp that asks for it some 50 cycles: with pages of 16 tokens one
-    // warp for K and V takes longer over a block than memory does.)
-    const SpanBoxes boxes(p, sKV);
-    const SpanSeg* at;
-    int g = 0;
-    bool ok = true;
-#pragma unroll 1
-    for (int n = 0; ok && __all_sync(0xffffffffu, span_segment(bar, n, ctx, at)); ++n) {
-      const SpanSeg w = *at;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
-      const int kvh = w.u / p.rows.kv_div;
-      int page = boxes.page(p, w, w.j1 - 1);
-#pragma unroll 1
-      for (int j = w.j1 - 1; j >= w.j0; --j, ++g) {
-        const int next = j > w.j0 ? boxes.page(p, w, j - 1) : 0;  // (asked for a block ahead)
-        if (!(ok = boxes.load<C>(&map_v, bar, 1, g, w, j, kvh, page, ctx))) break;
-        page = next;
-      }
-    }
-    if (lane == 0)
-#pragma unroll 1
-      for (int s = 0; s < C::kVSlots; ++s)
-        if (g > s) wait_drain_inl(&bar->kv_full[C::kKSlots + s], C::use(1, g - 1 - s) & 1, kDrainLimitNs);
-    __syncwarp();
+    span_load_warp<C, false, false, C::kQBytes, C::kQAtom>(p, warp == 6, &map_q, &map_k, &map_v, bar, nullptr, sQ, sKV, ctx,
+                                                           [](const SpanSeg&) {});
   } else if (warp == 5) {
     // ------------------------------------------------------------------ issuer: S^T of a block ahead of its neighbour's O^T
     if (lane == 0) {
@@ -327,11 +292,11 @@ __global__ void __launch_bounds__(256, 1)
       if (tid < 32) {
         int lo = 0, hi = 0;
         float slope2 = 0.f;
-        const int tok = tid / p.rows.heads;
+        const int tok = tid / p.rows.heads();
         if (tok < fresh) {
           pos = len + tok;
           v.span(b, tok, pos, lo, hi);
-          if (p.slopes) slope2 = p.slopes[(u - tok) * p.rows.heads + tid] * 1.4426950408889634f;
+          if (p.slopes) slope2 = p.slopes[(u - tok) * p.rows.heads() + tid] * 1.4426950408889634f;
         }
         rows->lo[tid] = lo, rows->hi[tid] = hi, rows->slope2[tid] = slope2;
         rows->rel[g & 1][tid] = (float)(pos - (j1 - 1) * 128);
@@ -347,7 +312,7 @@ __global__ void __launch_bounds__(256, 1)
         bad = bad || !__all_sync(0xffffffffu, span_wait(&bar->s_full[buf], (g >> 1) & 1, ctx, kSiteCrossS));
         tc_fence_after();
         uint32_t x[R];
-        few_tmem_ld<R>(tmem + buf * R + lane_off, x);
+        few_tmem_ld(tmem + buf * R + lane_off, x);
         tc_fence_before();
         mbar_arrive(&bar->s_free[buf]);
         // scores in log2 units
@@ -403,7 +368,7 @@ __global__ void __launch_bounds__(256, 1)
           if (again) bad = !__all_sync(0xffffffffu, span_wait(&bar->pv_done[buf ^ 1], ((g - 1) >> 1) & 1, ctx, kSiteCrossPv));
           tc_fence_after();
           uint32_t o[R];
-          if (again) few_tmem_ld<R>(tO, o);
+          if (again) few_tmem_ld(tO, o);
 #pragma unroll
           for (int q = 0; q < R; ++q) {
             const float was = rows->ref[q];
@@ -412,7 +377,7 @@ __global__ void __launch_bounds__(256, 1)
             l[q] *= alpha;
             if (again) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
           }
-          if (again) few_tmem_st<R>(tO, o);
+          if (again) few_tmem_st(tO, o);
           few_sync();
           if (tid < R)
             rows->ref[tid] = fmaxf(rows->ref[tid], fmaxf(fmaxf(rows->part[0][tid], rows->part[1][tid]),
@@ -436,9 +401,8 @@ __global__ void __launch_bounds__(256, 1)
           }
         }
         // rows of V that nobody sees may hold anything: this key's
-        const int filled = v.table ? 0x7fffffff : v.C;  // (behind the keys of a contiguous tensor the TMA has filled zeros)
-        const bool unseen = key < seg_lo || (key >= seg_hi && key < filled);
-        if (seg_lo > j * 128 || seg_hi < min(filled, j * 128 + 128)) {
+        const bool unseen = key < seg_lo || key >= seg_hi;
+        if (seg_lo > j * 128 || seg_hi < j * 128 + 128) {
           bad = bad || !__all_sync(0xffffffffu, span_wait(&bar->kv_full[C::slot(1, g)], C::use(1, g) & 1, ctx, kSiteCrossTail));
           if (unseen)
             for (int c = 0; c < C::kAtoms * 8; ++c)
@@ -458,10 +422,10 @@ __global__ void __launch_bounds__(256, 1)
       // ---- end of the segment: sums over the keys, a thread per row for its statistics and a channel
       // per thread for its values.  (With the statistics in an unrolled loop over the rows, of code that
       // runs once per segment, a row of a segment took 0.6 us of instruction fetches.)
-      const float sums = few_sum<R>(l);
+      const float sums = few_sum(l);
       if (lane < R) rows->part[warp][lane] = sums;
       uint32_t o[R];
-      few_tmem_ld<R>(tO, o);
+      few_tmem_ld(tO, o);
       if (few_any(bad)) {
         bad = true;
         break;
@@ -470,14 +434,14 @@ __global__ void __launch_bounds__(256, 1)
       if (tid < R) {
         const float sum = rows->part[0][tid] + rows->part[1][tid] + rows->part[2][tid] + rows->part[3][tid];
         const float lse2 = sum == 0.f ? -CUDART_INF_F : rows->ref[tid] + log2f(sum);
-        const int tok = tid / p.rows.heads;
+        const int tok = tid / p.rows.heads();
         rows->inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
         char* out = nullptr;
         if (CLUSTER) {
           rows->lse[tid] = lse2;
         } else if (tok < fresh) {
           if (whole) {
-            const size_t grow = p.rows.row(b, u, tid - tok * p.rows.heads, tok);
+            const size_t grow = p.rows.row(b, u, tid - tok * p.rows.heads(), tok);
             out = reinterpret_cast<char*>(p.o + grow * D);
             p.lse[grow] = lse2 * 0.6931471805599453f;
           } else {
@@ -530,7 +494,7 @@ __global__ void __launch_bounds__(256, 1)
     const int ctas = p.cluster, item = blockIdx.x / ctas, b = item / p.rows.units;
     const int fresh = v.rows(b, v.len(b));
     const float* parts = reinterpret_cast<const float*>(sKV) + lane * E;
-    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.heads * fresh; row += ctas * (C::kThreads / 32)) {
+    for (int row = (int)cluster_ctarank() + ctas * warp; row < p.rows.heads() * fresh; row += ctas * (C::kThreads / 32)) {
       float l[kMost], o[kMost][E], mx = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < kMost; ++i)
@@ -554,8 +518,8 @@ __global__ void __launch_bounds__(256, 1)
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[i][e], acc[e]);
         }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int tok = row / p.rows.heads;
-      const size_t grow = p.rows.row(b, item - b * p.rows.units, row - tok * p.rows.heads, tok);
+      const int tok = row / p.rows.heads();
+      const size_t grow = p.rows.row(b, item - b * p.rows.units, row - tok * p.rows.heads(), tok);
       uint32_t* orow = reinterpret_cast<uint32_t*>(p.o + grow * D) + lane * (E / 2);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) orow[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

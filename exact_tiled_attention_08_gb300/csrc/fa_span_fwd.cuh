@@ -4,8 +4,8 @@
 // The arithmetic, the roles and the pipeline are those of fa_cross_fwd_kernel (TMA
 // fills a ring of K and V tiles, one thread issues S = Q K^T, one O += P V, two softmax
 // warpgroups hold a row of scores per thread; two row tiles per item, PAIR, or one
-// whose key blocks go to the warpgroups in turn, ALT).  Up to 32 rows per unit go to
-// fa_span_few_kernel.  What differs:
+// whose key blocks go to the warpgroups in turn, ALT).  Up to 16 rows of a unit over
+// pages go to fa_span_few_kernel.  What differs:
 //
 // Work.  An item is a tile (pair) of query rows of a unit (SpanRows) with the blocks of
 // 128 keys that any of its rows sees; items cost what they have of them.  Where enough of them
@@ -17,7 +17,7 @@
 // d=64, four requests, causal, with slopes, 84 us).
 //
 // Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
-// (MOD 2) and the bias (MOD 1 and 2) change the scores in registers, before the maximum.
+// (MOD 2 and 3) and the bias (MOD 1 and 3) change the scores in registers, before the maximum.
 //
 // Pages.  A tile of 128 keys is 128 / page_size boxes, one per lane of the loading
 // warp, from where the page table says; pages that no row sees, and those outside the
@@ -25,7 +25,7 @@
 // without reading.
 //
 // Keys of an item's first and last block that none of its rows sees may hold
-// anything: their scores become -inf and warp 11 zeroes their rows of V.
+// anything: their scores become -inf and the warp that loads V zeroes their rows of it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -45,8 +45,9 @@ struct SpanMeta {     // of each CTA, for the combine kernel
   long long total;    // places of the sequence
 };
 
+template <bool PAGED>
 struct SpanFwdParams {
-  SpanRows rows;
+  SpanRows<PAGED> rows;
   __nv_bfloat16* o;
   float* lse;
   SpanMeta* meta;    // [grid]
@@ -96,14 +97,14 @@ struct SpanSeg {
 constexpr int kSpanSegs = 4;  // segments in shared memory
 enum : int { kSiteSpanSeg = 70, kSiteSpanSegFree };
 
-template <bool PAIR>
+template <bool PAIR, bool PAGED>
 struct SpanItem {
   SpanTile t[PAIR ? 2 : 1];
   int lo, hi, base;  // keys seen; first block
   int n;             // number of blocks: none without tokens, else at least one, so that rows without keys are written
   int token0;
   bool two;          // there are tokens in the second tile
-  __device__ __forceinline__ SpanItem(const SpanFwdParams& p, int e) {
+  __device__ __forceinline__ SpanItem(const SpanFwdParams<PAGED>& p, int e) {
     const int b = e / p.row_tiles, rt = p.row_tiles - 1 - (e - b * p.row_tiles);
     t[0] = p.rows.tile(b, PAIR ? 2 * rt : rt);
     lo = t[0].lo, hi = t[0].hi;
@@ -114,8 +115,8 @@ struct SpanItem {
     }
     base = lo >> 7;
     const int there = p.rows.view.rows(b, p.rows.view.len(b));
-    token0 = (PAIR ? 2 * rt : rt) * p.rows.tokens;
-    two = PAIR && token0 + p.rows.tokens < there;
+    token0 = (PAIR ? 2 * rt : rt) * p.rows.tokens();
+    two = PAIR && token0 + p.rows.tokens() < there;
     n = token0 < there ? max(((hi + 127) >> 7) - base, 1) : 0;
   }
   __device__ __forceinline__ int places() const { return n > 0 ? n + kCrossStart : 0; }
@@ -124,8 +125,8 @@ struct SpanItem {
 // The next segment.  Ranks are numbered by entry (with `order`: entries by falling cost), all
 // units of one after another, or head by head (all row tiles of a unit one after another, whose
 // keys the CTAs of a round then share in L2).  Places beside an item's blocks as in fa_cross_fwd.cuh.
-template <bool PAIR>
-__device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t* order, SpanPlace& at, SpanSeg& s) {
+template <bool PAIR, bool PAGED>
+__device__ __forceinline__ bool span_next(const SpanFwdParams<PAGED>& p, const uint16_t* order, SpanPlace& at, SpanSeg& s) {
   const int U = p.rows.units;
   while (at.left > 0) {
     int e = at.e;
@@ -139,7 +140,7 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t
       s.u = at.e - e * U;
       if (PAIR && at.mode == kSpanSorted) e = order[e];
     }
-    const SpanItem<PAIR> item(p, e);
+    const SpanItem<PAIR, PAGED> item(p, e);
     s.b = e / p.row_tiles;
     s.token0 = item.token0;
     s.lo = item.lo, s.hi = item.hi;
@@ -168,7 +169,7 @@ __device__ __forceinline__ bool span_next(const SpanFwdParams& p, const uint16_t
     s.flags = (s.j0 == item.base ? kSegFirst : 0) | (s.rest == 0 ? kSegLast : 0) |
               (item.two ? kSegTwo : 0);
     // (past the keys of a contiguous tensor the TMA has filled zeros)
-    const int filled = p.rows.view.table ? s.j1 * 128 : min(p.rows.view.C, s.j1 * 128);
+    const int filled = PAGED ? s.j1 * 128 : min(p.rows.view.C, s.j1 * 128);
     if (s.lo > s.j0 * 128 || (s.j1 == s.j0 + 1 && s.hi < filled)) s.flags |= kSegDirtyFront;
     if (s.hi < filled || (s.j1 == s.j0 + 1 && s.lo > s.j0 * 128)) s.flags |= kSegDirtyBack;
 #pragma unroll
@@ -202,8 +203,8 @@ __device__ __forceinline__ bool span_dirty(const SpanSeg& s, int j) {
 // numbering them, and the items go whole where that ends no later than even shares and the
 // join of what they cut.
 constexpr int kSpanRounds = 32;
-template <bool PAIR, int T>
-__device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scratch, SpanPlace* place, long long* all,
+template <bool PAIR, int T, bool PAGED>
+__device__ __forceinline__ void span_schedule(const SpanFwdParams<PAGED>& p, void* scratch, SpanPlace* place, long long* all,
                                               long long* share_end) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.row_tiles, U = p.rows.units, G = gridDim.x, c = blockIdx.x;
@@ -213,7 +214,7 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
     if (tid == 0) *place = SpanPlace{c, 0, 0, rounds + (span_rank(rounds, G, c) < count ? 1 : 0), mode};
   };
   if (count > (long long)kSpanRounds * G) {
-    const SpanView& v = p.rows.view;
+    const SpanView<PAGED>& v = p.rows.view;
     whole(PAIR && (v.window || !v.causal || v.begin) ? kSpanByHead : kSpanByEntry);
     return;
   }
@@ -237,7 +238,7 @@ __device__ __forceinline__ void span_schedule(const SpanFwdParams& p, void* scra
     }
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      const int n = sorted && pass > 0 ? one : SpanItem<PAIR>(p, e).places();
+      const int n = sorted && pass > 0 ? one : SpanItem<PAIR, PAGED>(p, e).places();
       if (pass == 0) {
         mine += n;
         one = n;
@@ -324,7 +325,7 @@ struct SpanBarriers {
   uint64_t merge_ready, merge_free;
   uint64_t drain[2];
   uint64_t never;
-  uint64_t seg_full[kSpanSegs], seg_empty[kSpanSegs];  // (read by the issuers, warp 11 and eight softmax warps)
+  uint64_t seg_full[kSpanSegs], seg_empty[kSpanSegs];  // (read by the issuers, the warp that loads V and eight softmax warps)
   SpanSeg seg[kSpanSegs];
   SpanPlace place;
   long long total, end;  // places of the sequence; end of the CTA's share
@@ -363,22 +364,20 @@ __device__ __forceinline__ bool span_segment(Bar* bar, int n, const WaitCtx& ctx
 }
 
 // A tile of 128 keys as TMA boxes, a lane per page.
+template <bool PAGED>
 struct SpanBoxes {
   int lane, shift, rows, count;
-  bool paged;
   uint8_t* ring;
-  __device__ __forceinline__ SpanBoxes(const SpanFwdParams& p, uint8_t* sKV) {
-    const SpanView& v = p.rows.view;
+  __device__ __forceinline__ SpanBoxes(const SpanFwdParams<PAGED>& p, uint8_t* sKV) {
     lane = threadIdx.x & 31;
-    paged = v.table != nullptr;
-    shift = v.page_shift;
-    rows = paged ? min(1 << shift, 128) : 128;
+    shift = p.rows.view.page_shift;
+    rows = PAGED ? min(1 << shift, 128) : 128;
     count = 128 / rows;
     ring = sKV;
   }
   // the page of this lane's part of block j, or -1: nothing there that a row sees
-  __device__ __forceinline__ int page(const SpanFwdParams& p, const SpanSeg& w, int j) const {
-    if (!paged) return w.b;
+  __device__ __forceinline__ int page(const SpanFwdParams<PAGED>& p, const SpanSeg& w, int j) const {
+    if (!PAGED) return w.b;
     if (lane >= count) return -1;
     const int key = j * 128 + lane * rows;
     if (key >= w.hi || key + rows <= w.lo) return -1;
@@ -395,7 +394,7 @@ struct SpanBoxes {
     if (lane == 0) mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
     __syncwarp();
     if (lane < count) {
-      const int row = !paged ? j * 128 : count > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
+      const int row = !PAGED ? j * 128 : count > 1 ? 0 : (j * 128) & ((1 << shift) - 1);
       for (int a = 0; a < C::kAtoms; ++a)
         tma_load_4d(ring + slot * C::kTileBytes + a * 16384 + lane * rows * 128, map, &bar->kv_full[slot], a * 64, row, kvh, page);
     }
@@ -403,18 +402,35 @@ struct SpanBoxes {
   }
 };
 
-// The loading warp: works out the segments, publishes them, and fills Q's two buffers (QBYTES
-// each, atoms of 64 columns QATOM bytes apart) and the ring of K and V tiles (SPLIT: of K tiles).
-template <class C, bool PAIR, bool SPLIT, int QBYTES, int QATOM, class Bar>
-__device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUtensorMap* map_q, const CUtensorMap* map_k,
-                                                 const CUtensorMap* map_v, Bar* bar, const uint16_t* order, uint8_t* sQ,
-                                           uint8_t* sKV, const WaitCtx& ctx) {
+// Rows of V that nobody sees, of the tile loaded as the `tile`-th; -1: none are waiting.
+struct SpanUnseen {
+  int tile, segment;
+  int from, to;  // rows [from, to) are seen
+};
+
+// The two loading warps, in one piece of code.  The first works out the segments, publishes them, and fills
+// Q's two buffers (QBYTES each, atoms of 64 columns QATOM bytes apart) and the K tiles of the ring.  The V
+// tiles are the second's with pages, else the first's as well.  (A box costs the warp that asks for it some
+// 50 cycles: with pages of 16 tokens one warp for both takes longer over a block than the rest of the
+// kernel, 594 instead of 466 us for 2048 tokens of two requests over 2000 and 16000, H=32/8 d=128; with
+// one box a tile the two are equal.)  CLEAN: the second zeroes rows of V that nobody sees, when
+// the warp that issues P V has come to their block and is asking.  It puts that off, to load on, but not
+// until it waits for something that only comes after that block: its tile's slot, or a segment that is
+// published when the block's is done with.  `done` is called with every segment of the second.  False: a
+// wait ran out.
+template <class C, bool PAIR, bool CLEAN, int QBYTES, int QATOM, bool PAGED, class Bar, class Done>
+__device__ __forceinline__ bool span_load_warp(const SpanFwdParams<PAGED>& p, bool second, const CUtensorMap* map_q,
+                                               const CUtensorMap* map_k, const CUtensorMap* map_v, Bar* bar, const uint16_t* order, uint8_t* sQ,
+                                               uint8_t* sKV, const WaitCtx& ctx, Done done) {
   const int lane = threadIdx.x & 31;
   SpanPlace at = bar->place;
   SpanSeg w{};
-  const SpanBoxes boxes(p, sKV);
-  int loads = 0, nq = 0;  // K and V tiles, in turn (SPLIT: K tiles)
+  const SpanBoxes<PAGED> boxes(p, sKV);
+  const int kv0 = second ? PAGED ? 1 : 2 : 0, kv1 = second || !PAGED ? 2 : 1;  // what this warp loads
+  int g = 0, loads = 0, segments = 0, nq = 0;  // blocks, tiles, segments, Q loads
   bool ok = true;
+  SpanUnseen unseen{-1, 0, 0, 0};
+  int cleaned = 0;
   auto load_q = [&](int qs) {
     if (lane == 0) {
       const int tiles = w.flags & kSegTwo ? 2 : 1;
@@ -422,65 +438,104 @@ __device__ __forceinline__ void span_load_warp(const SpanFwdParams& p, const CUt
       for (int t = 0; t < tiles; ++t)
         for (int a = 0; a < C::kAtoms; ++a)
           tma_load_4d(sQ + (PAIR ? t : qs) * QBYTES + a * QATOM, map_q, &bar->q_full[qs], a * 64, 0,
-                      w.token0 + p.rows.tokens * t, w.b * p.rows.units + w.u);
+                      w.token0 + p.rows.tokens() * t, w.b * p.rows.units + w.u);
     }
     __syncwarp();
+    ++nq;
+  };
+  auto clean = [&] {
+    if constexpr (CLEAN) {
+      if (!__all_sync(0xffffffffu, span_wait(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail))) return false;
+      ++cleaned;
+      uint8_t* tile = sKV + C::slot(1, unseen.tile) * C::kTileBytes;
+      const int from = unseen.from, to = unseen.to, chunks = (from + 128 - to) * 8;  // of 16 bytes of an atom
+      for (int i = lane; i < C::kAtoms * chunks; i += 32) {
+        const int a = i >= chunks ? 1 : 0, k = i - a * chunks, c = k < from * 8 ? k : k - from * 8 + to * 8;
+        *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->v_clean);
+      unseen.tile = -1;
+    }
+    return true;
   };
 #pragma unroll 1
   while (ok) {
-    const bool more = span_next<PAIR>(p, order, at, w);
-    if (!more) w.flags = kSegEnd;
-    // the segment for the other warps, once they have done with the one in its place
-    const int s = nq % kSpanSegs;
-    ok = __all_sync(0xffffffffu, span_wait(&bar->seg_empty[s], ((nq / kSpanSegs) & 1) ^ 1, ctx, kSiteSpanSegFree));
-    if (!ok) break;
-    if (lane == 0) {
-      bar->seg[s] = w;
-      mbar_arrive(&bar->seg_full[s]);
+    const int s = segments % kSpanSegs;
+    if (!second) {
+      const bool more = span_next<PAIR>(p, order, at, w);
+      if (!more) w.flags = kSegEnd;
+      // the segment for the other warps, once they have done with the one in its place
+      ok = __all_sync(0xffffffffu, span_wait(&bar->seg_empty[s], ((segments / kSpanSegs) & 1) ^ 1, ctx, kSiteSpanSegFree));
+      if (!ok) break;
+      if (lane == 0) {
+        bar->seg[s] = w;
+        mbar_arrive(&bar->seg_full[s]);
+      }
+      __syncwarp();
+      if (!more) break;
+      // a later segment's first key block needs only ring slots: it goes out
+      // before the queries, whose buffer an earlier segment may still be reading
+      if (segments == 0) load_q(0);
+    } else {
+      const SpanSeg* seg;
+      if (unseen.tile >= 0 && (!PAGED || segments - unseen.segment > 1) && !(ok = clean())) break;
+      if (!__all_sync(0xffffffffu, span_segment(bar, segments, ctx, seg))) {
+        ok = !*ctx.abort_flag;
+        break;
+      }
+      w = *seg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->seg_empty[s]);
     }
-    __syncwarp();
-    if (!more) break;
     const int kvh = w.u / p.rows.kv_div;
-    const int qs = PAIR ? 0 : nq & 1, use = PAIR ? nq : nq >> 1;
     int page = boxes.page(p, w, w.j1 - 1);
-    // a later segment's first key block needs only ring slots: it goes out
-    // before the queries, whose buffer an earlier segment may still be reading
-    if (nq == 0) load_q(qs);
-    ++nq;
 #pragma unroll 1
     for (int j = w.j1 - 1; ok && j >= w.j0; --j) {
       const int next = j > w.j0 ? boxes.page(p, w, j - 1) : 0;  // (asked for a block ahead)
+      const bool dirty = CLEAN && second && span_dirty(w, j);
+      if (unseen.tile >= 0 && (dirty || !PAGED || g - unseen.tile >= C::kVSlots) && !(ok = clean())) break;
 #pragma unroll 1
-      for (int kv = 0; kv < (SPLIT ? 1 : 2); ++kv) {
-        const int g = SPLIT ? loads : loads >> 1;
-        if (!(ok = boxes.load<C>(kv ? map_v : map_k, bar, kv, g, w, j, kvh, page, ctx))) break;
+      for (int kv = kv0; kv < kv1; ++kv) {
+        if (!(ok = boxes.template load<C>(kv ? map_v : map_k, bar, kv, g, w, j, kvh, page, ctx))) break;
         ++loads;
       }
-      if (ok && j == w.j1 - 1 && nq > 1) {
-        if (use > 0)
-          ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
-        if (ok)
-          load_q(qs);
-        else
-          --nq;  // (these queries were not asked for)
+      if (!ok) break;
+      if (dirty) {
+        const int from = max(w.lo - j * 128, 0);
+        unseen = {g, segments, from, max(min(w.hi - j * 128, 128), from)};
       }
+      ++g;
       page = next;
+      if (!second && j == w.j1 - 1 && segments > 0) {
+        const int qs = PAIR ? 0 : segments & 1, use = PAIR ? segments : segments >> 1;
+        if (use > 0) ok = __all_sync(0xffffffffu, span_wait(&bar->q_empty[qs], (use - 1) & 1, ctx, kSiteCrossQEmpty));
+        if (ok) load_q(qs);
+      }
     }
+    ++segments;
+    if (second) done(w);
   }
+  if (ok && unseen.tile >= 0) ok = clean();
   // every copy this warp started must land before the CTA can exit
   if (lane == 0) {
-    for (int s = 0; s < (PAIR ? 1 : 2); ++s) {
-      const int uses = PAIR ? nq : (nq + 1 - s) >> 1;
-      if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
-    }
+    if (!second)
+      for (int s = 0; s < (PAIR ? 1 : 2); ++s) {
+        const int uses = PAIR ? nq : (nq + 1 - s) >> 1;
+        if (uses > 0) wait_drain_inl(&bar->q_full[s], (uses - 1) & 1, kDrainLimitNs);
+      }
 #pragma unroll 1
     for (int s = 0; s < C::kSlots; ++s) {
       // loads into slot s
       const bool vslot = s >= C::kKSlots;
-      const int n = SPLIT ? (vslot ? 0 : loads) : vslot ? loads >> 1 : (loads + 1) >> 1, first = vslot ? s - C::kKSlots : s;
+      const int n = PAGED ? (vslot == second ? loads : 0) : vslot ? loads >> 1 : (loads + 1) >> 1;
+      const int first = vslot ? s - C::kKSlots : s;
       if (n > first) wait_drain_inl(&bar->kv_full[s], C::use(vslot, n - 1 - first) & 1, kDrainLimitNs);
     }
   }
+  __syncwarp();
+  return ok;
 }
 
 // multiplies a block's scores with mul and adds a bias of -slope2 |rel - c| to that of key c
@@ -524,10 +579,10 @@ __device__ __forceinline__ uint32_t span_bits(int from, int to) {
 }
 
 // PAIR: two row tiles per item.  MOD: 0 plain scores, 1 with a bias, 2 capped, 3 both.
-template <int D, int MOD, bool PAIR>
+template <int D, int MOD, bool PAIR, bool PAGED>
 __global__ void __launch_bounds__(384, 1)
     fa_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams p) {
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams<PAGED> p) {
   using C = CrossCfg<D>;
   // The issuing threads' loops over the two row tiles: one copy of the products at d = 128, where
   // the kernel's loops together outgrow the instruction cache (H=32/8 N=8192, two requests, causal:
@@ -549,7 +604,7 @@ __global__ void __launch_bounds__(384, 1)
   float* sMerge = reinterpret_cast<float*>(sKV + C::kSlots * C::kTileBytes);  // [3][128]
   SpanBarriers* bar = reinterpret_cast<SpanBarriers*>(reinterpret_cast<uint8_t*>(sMerge) + C::kMergeBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const SpanView& v = p.rows.view;
+  const SpanView<PAGED>& v = p.rows.view;
 
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -597,10 +652,25 @@ __global__ void __launch_bounds__(384, 1)
   const WaitCtx ctx{&bar->abort_flag, p.wait_limit_ns};
   if (warp >= 8) {
     setmaxnreg_dec<C::kMiscRegs>();
-    if (warp == 9) {
+    if (warp == 9 || warp == 11) {
       // ------------------------------------------------------------------ segments and TMA
-      span_load_warp<C, PAIR, false, C::kTileBytes, 16384>(p, &map_q, &map_k, &map_v, bar,
-                                                    reinterpret_cast<const uint16_t*>(sMerge), sQ, sKV, ctx);
+      const bool second = warp == 11;
+      SpanMeta meta{};
+      const bool ok = span_load_warp<C, PAIR, true, C::kTileBytes, 16384>(
+          p, second, &map_q, &map_k, &map_v, bar, reinterpret_cast<const uint16_t*>(sMerge), sQ, sKV, ctx,
+          [&](const SpanSeg& w) {
+            if ((w.flags & (kSegFirst | kSegLast)) == kSegFirst) {
+              // (the CTA's last segment: the item's other blocks follow its share)
+              meta.split = 1;
+              meta.b = w.b;
+              meta.u = w.u;
+              meta.token0 = w.token0;
+              meta.last = bar->end + w.rest;
+              meta.total = bar->total;
+            }
+          });
+      if (!ok) meta.split = 0;
+      if (second && lane == 0) p.meta[blockIdx.x] = meta;
       __syncwarp();
     } else if (warp == 8) {
       // ------------------------------------------------------------------ S issuer
@@ -654,7 +724,7 @@ __global__ void __launch_bounds__(384, 1)
         wait_drain_inl(&bar->drain[0], 0, kDrainLimitNs);
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else {
       // ------------------------------------------------------------------ P V issuer
       // O_t += P_t(j) V_j once the softmax of tile t wrote P_t(j)
       if (lane == 0) {
@@ -672,7 +742,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = w.j1 - 1; ok && j >= w.j0; --j, ++g) {
             const int vs = C::slot(1, g);
             if (!(ok = span_wait(&bar->kv_full[vs], C::use(1, g) & 1, ctx, kSiteCrossV))) break;
-            // rows that nobody sees: warp 11 zeroes them while P is being formed
+            // rows that nobody sees: the warp that loads V zeroes them while P is being formed
             const bool dirty = span_dirty(w, j);
             if (dirty) mbar_arrive(&bar->v_ask);
             const uint64_t vdesc = sdesc_sw128(skv + vs * C::kTileBytes, 16384, 1024);
@@ -708,51 +778,6 @@ __global__ void __launch_bounds__(384, 1)
         wait_drain_inl(&bar->drain[1], 0, kDrainLimitNs);
       }
       __syncwarp();
-    } else {
-      // ------------------------------------------------------------------ warp 11: rows of V that nobody sees
-      int g = 0, cleaned = 0;
-      bool ok = true;
-      SpanMeta meta{};
-      const SpanSeg* at;
-#pragma unroll 1
-      for (int n = 0; ok; ++n) {
-        if (!__all_sync(0xffffffffu, span_segment(bar, n, ctx, at))) {
-          ok = !*ctx.abort_flag;
-          break;
-        }
-        const SpanSeg w = *at;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
-#pragma unroll 1
-        for (int j = w.j1 - 1; ok && j >= w.j0; j = j - 1 > w.j0 ? w.j0 : j - 1) {  // (its last and its first block)
-          if (!span_dirty(w, j)) continue;
-          ok = __all_sync(0xffffffffu, span_wait(&bar->v_ask, cleaned & 1, ctx, kSiteCrossTail));
-          if (!ok) break;
-          ++cleaned;
-          const int from = max(w.lo - j * 128, 0), to = max(min(w.hi - j * 128, 128), from);  // seen
-          uint8_t* tile = sKV + C::slot(1, g + w.j1 - 1 - j) * C::kTileBytes;
-          const int unseen = (from + 128 - to) * 8;  // 16-byte chunks of an atom
-          for (int i = lane; i < C::kAtoms * unseen; i += 32) {
-            const int a = i >= unseen ? 1 : 0, k = i - a * unseen, c = k < from * 8 ? k : k - from * 8 + to * 8;
-            *reinterpret_cast<uint4*>(tile + a * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->v_clean);
-        }
-        g += w.j1 - w.j0;
-        if ((w.flags & (kSegFirst | kSegLast)) == kSegFirst) {
-          // (the CTA's last segment: the item's other blocks follow its share)
-          meta.split = 1;
-          meta.b = w.b;
-          meta.u = w.u;
-          meta.token0 = w.token0;
-          meta.last = bar->end + w.rest;
-          meta.total = bar->total;
-        }
-      }
-      if (!ok) meta.split = 0;
-      if (lane == 0) p.meta[blockIdx.x] = meta;
     }
   } else {
     setmaxnreg_inc<C::kSoftRegs>();
@@ -787,12 +812,12 @@ __global__ void __launch_bounds__(384, 1)
       const int jfirst = (PAIR ? w.a1[t] : w.j1 - t) - 1, jend = PAIR ? w.a0[t] : w.j0;
       const int lo_cut = w.lo_cut[PAIR ? t : 0], hi_cut = w.hi_cut[PAIR ? t : 0];  // blocks that all rows see whole
       {
-        const int b = w.b, i = r / p.rows.heads, token = w.token0 + (PAIR ? p.rows.tokens * t : 0) + i;
+        const int b = w.b, i = r / p.rows.heads(), token = w.token0 + (PAIR ? p.rows.tokens() * t : 0) + i;
         const int tok = min(token, v.N - 1), len = v.len(b);
         pos = len + tok;
         v.span(b, tok, pos, row_lo, row_hi);
-        if (MOD >= 2) there = i < p.rows.tokens && token < v.rows(b, len);
-        if (MOD & 1) slope2 = p.slopes[w.u * p.rows.heads + r - i * p.rows.heads] * 1.4426950408889634f;
+        if (MOD >= 2) there = i < p.rows.tokens() && token < v.rows(b, len);
+        if (MOD & 1) slope2 = p.slopes[w.u * p.rows.heads() + r - i * p.rows.heads()] * 1.4426950408889634f;
       }
       float m = -CUDART_INF_F;  // exponent reference (log2 units), a stale running max
       // l: sum of the fp32 probabilities; lcorr: the rounding errors of each
@@ -867,11 +892,11 @@ __global__ void __launch_bounds__(384, 1)
             mx = row_max();
           }
           if constexpr (MOD == 3) {
-            span_bias(sr, 1.f, slope2, pos - kbase, v.causal);
+            span_bias(sr, 1.f, slope2, pos - kbase, PAGED || v.causal);
             mx = row_max();
           }
         } else {
-          if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase, v.causal);
+          if constexpr (MOD == 1) span_bias(sr, p.scale_log2, slope2, pos - kbase, PAGED || v.causal);
           if (__builtin_expect(cut, 0)) hide(-CUDART_INF_F);
           if constexpr (C::kDualS && MOD == 0)
             mx = fmaxf(cut ? cross_max64(sr[0], sr[1]) : mx_a, cross_max64(sr[2], sr[3]));
@@ -1004,9 +1029,9 @@ __global__ void __launch_bounds__(384, 1)
       a0 *= inv;
       a1 *= inv;
       const float lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-      const int of_tile = r / p.rows.heads, token = w.token0 + (PAIR ? p.rows.tokens * t : 0) + of_tile;
-      const bool write = of_tile < p.rows.tokens && token < v.rows(w.b, v.len(w.b));
-      const size_t grow = p.rows.row(w.b, w.u, r - of_tile * p.rows.heads, token);
+      const int of_tile = r / p.rows.heads(), token = w.token0 + (PAIR ? p.rows.tokens() * t : 0) + of_tile;
+      const bool write = of_tile < p.rows.tokens() && token < v.rows(w.b, v.len(w.b));
+      const size_t grow = p.rows.row(w.b, w.u, r - of_tile * p.rows.heads(), token);
       const size_t prow = ((size_t)2 * blockIdx.x + (seg_first ? 1 : 0)) * p.part_rows + (PAIR ? 128 * t : 0) + r;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1071,8 +1096,8 @@ __global__ void __launch_bounds__(384, 1)
 // Joins the parts of the items that share ends cut: block x takes the item that
 // begins in CTA x's share and goes on behind it, kRows rows per warp.  O = sum of
 // the parts' O weighted by 2^(their LSE - the largest), in CTA order.
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_constant__ SpanFwdParams p) {
+template <int D, bool PAIR, bool PAGED>
+__global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_constant__ SpanFwdParams<PAGED> p) {
   constexpr int E = D / 32;
   constexpr int kRows = PAIR ? 4 : 1;  // rows of a warp
   constexpr int kBatch = 8;            // parts whose loads are in flight together
@@ -1080,17 +1105,17 @@ __global__ void __launch_bounds__(256) fa_span_combine_kernel(const __grid_const
   grid_trigger();
   const SpanMeta meta = p.meta[blockIdx.x];
   if (!meta.split) return;
-  const SpanView& v = p.rows.view;
+  const SpanView<PAGED>& v = p.rows.view;
   const int parts = (int)((meta.last * min((long long)gridDim.x, meta.total) - 1) / meta.total) - (int)blockIdx.x + 1;
   const int lane = threadIdx.x & 31, local0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
   const int fresh = v.rows(meta.b, v.len(meta.b));
   // part i: the last segment of CTA x, then the first of each CTA after it
   auto part = [&](int i) { return ((size_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.part_rows + local0; };
   for (int r = 0; r < kRows; ++r) {
-    const int local = local0 + r, second = PAIR ? local >> 7 : 0, of_tile = (local - second * 128) / p.rows.heads;
-    const int token = meta.token0 + second * p.rows.tokens + of_tile;
-    if (local >= p.part_rows || of_tile >= p.rows.tokens || token >= fresh) continue;
-    const size_t grow = p.rows.row(meta.b, meta.u, local - second * 128 - of_tile * p.rows.heads, token);
+    const int local = local0 + r, second = PAIR ? local >> 7 : 0, of_tile = (local - second * 128) / p.rows.heads();
+    const int token = meta.token0 + second * p.rows.tokens() + of_tile;
+    if (local >= p.part_rows || of_tile >= p.rows.tokens() || token >= fresh) continue;
+    const size_t grow = p.rows.row(meta.b, meta.u, local - second * 128 - of_tile * p.rows.heads(), token);
     float acc[E], sum = 0.f, ref = -CUDART_INF_F;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;

@@ -32,7 +32,7 @@ def interleave(roles, copies, products, rng, speeds):
     in_order, steps = rng.random(), 0
     while roles or copies or any(products):
         steps += 1
-        assert steps < 40000, "no role can go on"
+        assert steps < 400000, "no role can go on"
         names = [*roles, *(["copies"] if copies else []), *(i for i, x in enumerate(products) if x)]
         name = rng.choices(names, [speed[n] for n in names])[0]
         if name == "copies":
@@ -84,8 +84,9 @@ class Ring:
         self.empty[self.place(kv, g)[0]].arrive()
 
 
-def run_pairs(items, slots, dual, seed):
-    """`items`: of each the blocks, each tile's range of them (None: no such tile), and which are dirty."""
+def run_pairs(items, slots, dual, paged, seed):
+    """`items`: of each the blocks, each tile's range of them (None: no such tile), and which are dirty.
+    `paged`: K and V are loaded by two roles, else the second one only zeroes rows of V."""
     rng = random.Random(seed)
     copies, products = [], [[], []]
     tiles = Ring(slots, copies)
@@ -112,13 +113,43 @@ def run_pairs(items, slots, dual, seed):
                 return
             for j in range(item["blocks"]):
                 yield from tiles.load(0, g)
-                yield from tiles.load(1, g)
+                if not paged:
+                    yield from tiles.load(1, g)
                 if j == 0:
                     if n:
                         yield from wait(q_empty, n - 1)
                     q_full.expect()
                     copies.append(q_full.land)
                 g += 1
+
+    def values():
+        g, asked, unseen, of = 0, 0, None, 0
+
+        def clean():
+            yield from wait(v_ask, asked)
+            tiles.read(1, unseen)
+            cleaned.add(unseen)
+            yield
+            v_clean.arrive()
+
+        for n, item in enumerate(items):
+            if unseen is not None and (not paged or n - of > 1):
+                yield from clean()
+                asked, unseen = asked + 1, None
+            yield from segment(n)
+            seg_empty[n % segments].arrive()
+            for j in range(item["blocks"]):
+                dirty = j in item["dirty"]
+                if unseen is not None and (dirty or not paged or g - unseen >= slots[1]):
+                    yield from clean()
+                    asked, unseen = asked + 1, None
+                if paged:
+                    yield from tiles.load(1, g)
+                if dirty:
+                    unseen, of = g, n
+                g += 1
+        if unseen is not None:
+            yield from clean()
 
     def s_issuer():
         g, uses = 0, [0, 0]
@@ -171,21 +202,6 @@ def run_pairs(items, slots, dual, seed):
                 g += 1
                 yield
 
-    def cleaner():
-        g, asked = 0, 0
-        for n, item in enumerate(items):
-            yield from segment(n)
-            seg_empty[n % segments].arrive()
-            for j in range(item["blocks"]):
-                if j in item["dirty"]:
-                    yield from wait(v_ask, asked)
-                    asked += 1
-                    tiles.read(1, g + j)
-                    cleaned.add(g + j)
-                    yield
-                    v_clean.arrive()
-            g += item["blocks"]
-
     def softmax(t):
         uses = 0
         for n, item in enumerate(items):
@@ -205,7 +221,7 @@ def run_pairs(items, slots, dual, seed):
             for _ in range(4):  # (its warps)
                 seg_empty[n % segments].arrive()
 
-    roles = {f.__name__: f() for f in (producer, s_issuer, pv_issuer, cleaner)}
+    roles = {f.__name__: f() for f in (producer, values, s_issuer, pv_issuer)}
     roles.update({"softmax 0": softmax(0), "softmax 1": softmax(1)})
     interleave(roles, copies, products, rng, [*roles, "copies", 0, 1])
 
@@ -222,19 +238,18 @@ def random_items(r):
     return items
 
 
+@pytest.mark.parametrize("paged", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
-def test_no_wait_passes_early_in_pairs(d):
+def test_no_wait_passes_early_in_pairs(d, paged):
     for seed in range(150):
         r = random.Random(seed)
-        run_pairs(random_items(r), ring("fa_cross_fwd.cuh", d), d == 64, seed)
+        run_pairs(random_items(r), ring("fa_cross_fwd.cuh", d), d == 64, paged, seed)
 
 
-def few_slots(d, rows):
+def few_slots(d):
     text = open(os.path.join(build.CSRC_DIR, "fa_span_few.cuh")).read()
-    k = re.search(r"kKSlots = D == 128 \? (\d+) : (\d+), kVSlots = D == 128 && R == 32 \? (\d+) : kKSlots", text)
-    k = [int(x) for x in k.groups()]
-    kslots = k[0] if d == 128 else k[1]
-    return kslots, k[2] if d == 128 and rows == 32 else kslots
+    k = re.search(r"kKSlots = D == 128 \? (\d+) : (\d+), kVSlots = kKSlots", text)
+    return (int(k[1 if d == 128 else 2]),) * 2
 
 
 def run_few(items, slots, seed):
@@ -250,13 +265,16 @@ def run_few(items, slots, seed):
         for n, blocks in enumerate(items):
             for j in range(blocks):
                 yield from tiles.load(0, g)
-                yield from tiles.load(1, g)
                 if j == 0:
                     if n >= 2:
                         yield from wait(q_empty[n & 1], (n >> 1) - 1)
                     q_full[n & 1].expect()
                     copies.append(q_full[n & 1].land)
                 g += 1
+
+    def values():
+        for g in range(sum(items)):
+            yield from tiles.load(1, g)
 
     def issuer():
         g = 0
@@ -299,13 +317,12 @@ def run_few(items, slots, seed):
                 yield
             yield from wait(pv_done[(g - 1) & 1], (g - 1) >> 1)
 
-    roles = {f.__name__: f() for f in (producer, issuer, softmax)}
+    roles = {f.__name__: f() for f in (producer, values, issuer, softmax)}
     interleave(roles, copies, products, rng, [*roles, "copies", 0])
 
 
-@pytest.mark.parametrize("rows", [16, 32])
 @pytest.mark.parametrize("d", [64, 128])
-def test_no_wait_passes_early_with_few_rows(d, rows):
+def test_no_wait_passes_early_with_few_rows(d):
     for seed in range(150):
         r = random.Random(seed)
-        run_few([r.choice([1, 1, 2, 3, 7, 30]) for _ in range(r.choice([1, 2, 5, 9]))], few_slots(d, rows), seed)
+        run_few([r.choice([1, 1, 2, 3, 7, 30]) for _ in range(r.choice([1, 2, 5, 9]))], few_slots(d), seed)
