@@ -31,8 +31,8 @@ struct SpanView {
   }
   // the keys that query i of request b sees (pos: its position); lo >= hi: none
   __device__ __forceinline__ void span(int b, int i, int pos, int& lo, int& hi) const {
-    lo = !PAGED && begin ? max(begin[(long long)b * N + i], 0) : 0;
-    hi = !PAGED && end ? min(end[(long long)b * N + i], C) : C;
+    lo = !PAGED && begin ? min(max(begin[(long long)b * N + i], 0), C) : 0;
+    hi = !PAGED && end ? min(max(end[(long long)b * N + i], 0), C) : C;
     clip(pos, pos, lo, hi);
   }
   // what is left of [lo, hi) for queries at positions p0 .. p1

@@ -378,3 +378,26 @@ def test_two_calls_at_once():
     for (o, lse), g in outs:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         assert torch.equal(g[1], wantg[1]) and torch.equal(g[2], wantg[2])
+
+
+@pytest.mark.parametrize("N, cap", [(100, 0.0), (700, 0.0), (700, 50.0)])
+@pytest.mark.parametrize("window", [0, 2 ** 31 - 1])
+def test_spans_of_any_integers(N, cap, window):
+    """Values outside [0, N], up to those of the type, give the bits of 0 and N."""
+    B, H, Hkv, d = 2, 4, 2, 64
+    g = np.random.default_rng(N)
+    some = np.array([-2 ** 31, -2 ** 31 + 1, -2 ** 30, -1, 0, 1, N // 2, N, N + 1, 2 ** 30, 2 ** 31 - 1], np.int64)
+    begin, end = (torch.from_numpy(g.choice(some, (B, N)).astype(np.int32)).cuda() for _ in range(2))
+    begin[0], end[1] = -2 ** 31, 2 ** 31 - 1
+    q, k, v, do = (randn(i, B, h, N, d).cuda() for i, h in enumerate((H, Hkv, Hkv, H)))
+    outs = []
+    for b, e in ((begin, end), (begin.clamp(0, N), end.clamp(0, N))):
+        o, lse = fa.span_attention_forward(q, k, v, 0.125, b, e, window=window, cap=cap)
+        outs.append((o, lse, *fa.span_attention_backward(q, k, v, o, do, lse, 0.125, b, e, window=window, cap=cap)))
+    seen = (begin.clamp(0, N) < end.clamp(0, N))[:, None].expand(B, H, N)
+    o, lse, dq, dk, dv = outs[0]
+    assert (o[~seen] == 0).all() and (lse[~seen] == -math.inf).all() and (dq[~seen] == 0).all()
+    for x, y in zip((o, lse, dk, dv), (outs[1][0], outs[1][1], outs[1][3], outs[1][4])):
+        assert torch.equal(x, y)
+    # (dQ is summed in any order, in 32 bits, and rounded to bf16)
+    torch.testing.assert_close(dq.float(), outs[1][2].float(), rtol=2 ** -7, atol=1e-5 * float(dq.float().abs().max()))
