@@ -402,3 +402,25 @@ def test_units_of_a_group(H, Hkv, T, lens, some, window, cap, slopes, d):
                     cap=cap, slopes=None if sl is None else sl.cuda())
     assert fa.fa_check_device_status() == fa.FA_OK
     check_paged(q, kp, vp, table, o, lse, 1 / math.sqrt(d), lens, chunks, window, cap, sl, most=24)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dirty", [0.0, 0.2, 1.0])
+def test_many_items_of_a_block(d, dirty):
+    """More items of one block than a CTA keeps segments of, some of which end inside their block."""
+    B, H, Hkv, T, size = 400, 16, 4, 40, 16
+    g = np.random.default_rng(7)
+    lens = [int(g.integers(0, 88)) if g.random() < dirty else 88 for _ in range(B)]
+    table, count = tables(lens, [T] * B, size, 8, 3)
+    kp, vp = pool(1, count, Hkv, size, d, "heads"), pool(2, count, Hkv, size, d, "tokens")
+    for b, n in enumerate(lens):
+        if (n + T) % size:
+            page = int(table[b, (n + T) // size])
+            kp[page, :, (n + T) % size:], vp[page, :, (n + T) % size:] = float("nan"), float("nan")
+    q = randn(3, B, H, T, d).cuda()
+    o, lse = torch.full_like(q, 7.0), torch.full((B, H, T), 7.0, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(B, H, Hkv, T, 8 * size, d), dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(q, kp, vp, table.cuda(), torch.tensor(lens, **I32).cuda(), None, o, lse, ws, 1 / math.sqrt(d))
+    assert fa.fa_check_device_status() == fa.FA_OK
+    assert torch.isfinite(o).all()
+    check_paged(q, kp, vp, table, o, lse, 1 / math.sqrt(d), lens, [T] * B, 0, 0.0, None, most=40)
