@@ -1,7 +1,7 @@
 """Builds the C-ABI library ``lib/libfa.so`` from ``csrc/`` with nvcc for sm_103a.
 
-The library is one translation unit (``csrc/fa_ops.cu``, whose kernels ptxas takes on
-all cores) with the CUDA runtime linked statically, so it loads with ``ctypes`` on any host and depends on no
+The library is one translation unit (``csrc/fa_ops.cu``) with the CUDA runtime
+linked statically, so it loads with ``ctypes`` on any host and depends on no
 particular torch build.  Rebuilds only when a source is newer than the output.
 """
 
@@ -47,7 +47,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
-    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-split-compile=0", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE_DIR, "-o", tmp, os.path.join(CSRC_DIR, "fa_ops.cu")]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

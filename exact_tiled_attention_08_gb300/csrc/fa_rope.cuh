@@ -31,6 +31,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fa_cross.cuh"
 #include "fa_span.cuh"
 #include "sm103_ptx.cuh"
@@ -68,8 +70,10 @@ struct RopeParams {
   long long units;      // warps' units of work: token groups (rounded up to whole CTAs) * split.steps
   float eps, factor;
   int norm;
-  // pages (their tokens' first positions in starts, C = width pages; table nullptr:
-  // queries alone)
+};
+
+// Pages (their tokens' first positions in starts, C = width pages; table nullptr: queries alone).
+struct RopePagedParams : RopeParams {
   PageRows k_pages, v_pages;
   const int *table, *chunks;  // [B][width]; [B] or nullptr: N new tokens
   int width, page_shift, pages;
@@ -305,10 +309,12 @@ __device__ __forceinline__ void rope_fwd_heads(const RopeTurn<kInterleaved>& tur
   __syncwarp();  // the ring has been read
 }
 
-// kPaged: keys and values go to the pages of a cache.  (A kernel of its own, so that
-// contiguous caches keep their addresses and registers.)
-template <int D, bool kInterleaved, bool kNorm, bool kPaged>
-__global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kernel(const RopeParams p) {
+// Params: RopePagedParams where keys and values go to the pages of a cache, else RopeParams.  (Kernels of their
+// own, so that contiguous caches keep their addresses and registers: 16384 tokens of 48 heads of 128 with
+// the norm 69 us, 78 where addresses of pages are kept through the queries.)
+template <int D, bool kInterleaved, bool kNorm, class Params>
+__global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kernel(const Params p) {
+  constexpr bool kPaged = std::is_same<Params, RopePagedParams>::value;
   __shared__ unsigned long long turns[64];
   __shared__ __align__(16) uint8_t rings[kRopeThreads / 32][kRopeStages * 512];
   uint8_t* ring = rings[threadIdx.x >> 5];
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     const RopeToken t = rope_token<D>(p, unit);
     int start = p.starts ? __ldg(p.starts + t.b) : 0;
     bool here = t.valid;  // a token of the chunk
-    if (kPaged) {
+    if constexpr (kPaged) {
       start = min(max(start, 0), p.C);
       here = here && t.n < min(p.chunks ? __ldg(p.chunks + t.b) : p.N, p.C - start);
       if (!__any_sync(0xffffffffu, here)) continue;  // (padding is not read)
@@ -327,23 +333,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
     const int pos = p.positions ? __ldg(p.positions + (t.valid ? t.token : 0)) : start + t.n;
     const long long row = (long long)start + t.n;  // row of this token in k_out and v_out
     bool stored = here && row >= 0 && row < p.C;
-    // where the row of the first key/value head goes, and how far the next one's is
-    __nv_bfloat16 *k_to, *v_to;
-    long long k_next = (long long)p.C * D, v_next = k_next;
-    if (kPaged) {
-      int page = 0;
+    int page = 0;
+    if constexpr (kPaged) {
       if (stored && p.table) page = __ldg(p.table + (long long)t.b * p.width + (row >> p.page_shift));
       stored = stored && page >= 0 && page < p.pages;
       if (!stored) page = 0;
-      const long long in_page = row & ((1 << p.page_shift) - 1);
-      k_to = p.k_pages.ptr + page * p.k_pages.page + in_page * p.k_pages.token;
-      v_to = p.v_pages.ptr + page * p.v_pages.page + in_page * p.v_pages.token;
-      k_next = p.k_pages.head;
-      v_next = p.v_pages.head;
-    } else {
-      const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D;
-      k_to = p.k_out + cache;
-      v_to = p.v_out + cache;
     }
     int e0, e1;
     RopeTurn<kInterleaved>::place(p.rot, t.sub, e0, e1);
@@ -355,6 +349,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeFwdPerSm) fa_rope_fwd_kerne
                                                    p.q_out + ((long long)t.b * p.H * p.N + t.n) * D,
                                                    (long long)p.N * D, t.h0, min(t.h1, p.H), e0, e1,
                                                    kPaged ? here : t.valid, here, p.q_weight, p.eps);
+    // where the row of the first key/value head goes, and how far the next one's is
+    __nv_bfloat16 *k_to, *v_to;
+    long long k_next = (long long)p.C * D, v_next = k_next;
+    if constexpr (kPaged) {
+      const long long in_page = row & ((1 << p.page_shift) - 1);
+      k_to = p.k_pages.ptr + page * p.k_pages.page + in_page * p.k_pages.token;
+      v_to = p.v_pages.ptr + page * p.v_pages.page + in_page * p.v_pages.token;
+      k_next = p.k_pages.head;
+      v_next = p.v_pages.head;
+    } else {
+      const long long cache = ((long long)t.b * p.Hkv * p.C + row) * D;
+      k_to = p.k_out + cache;
+      v_to = p.v_out + cache;
+    }
     if (p.k.ptr)
       rope_fwd_heads<D, kInterleaved, kNorm, true>(turn, ring, in(p.k), p.k.head, k_to, k_next, max(t.h0 - p.H, 0),
                                                    min(t.h1 - p.H, p.Hkv), e0, e1, kPaged ? here : t.valid, stored,

@@ -85,24 +85,24 @@ void rope_units(fa::RopeParams& p, int d, long long warps, bool q, bool k, bool 
   }
 }
 
-template <int D, bool kNorm, bool kPaged>
-void launch_rope_fwd(const fa::RopeParams& p, unsigned grid, int interleaved, cudaStream_t stream) {
+template <int D, bool kNorm, class Params>
+void launch_rope_fwd(const Params& p, unsigned grid, int interleaved, cudaStream_t stream) {
   if (interleaved)
-    fa::fa_rope_fwd_kernel<D, true, kNorm, kPaged><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    fa::fa_rope_fwd_kernel<D, true, kNorm, Params><<<grid, fa::kRopeThreads, 0, stream>>>(p);
   else
-    fa::fa_rope_fwd_kernel<D, false, kNorm, kPaged><<<grid, fa::kRopeThreads, 0, stream>>>(p);
+    fa::fa_rope_fwd_kernel<D, false, kNorm, Params><<<grid, fa::kRopeThreads, 0, stream>>>(p);
 }
 
-template <bool kPaged>
-fa_status run_rope_fwd(fa::RopeParams& p, int d, bool q, bool k, bool v, int interleaved, cudaStream_t stream) {
+template <class Params>
+fa_status run_rope_fwd(Params& p, int d, bool q, bool k, bool v, int interleaved, cudaStream_t stream) {
   rope_units(p, d, kRopeFwdCtas * 8LL, q, k, v);
   const unsigned grid = (unsigned)std::min<long long>((p.units + 7) / 8, kRopeFwdCtas);
   if (d == 128)
-    p.norm ? launch_rope_fwd<128, true, kPaged>(p, grid, interleaved, stream)
-           : launch_rope_fwd<128, false, kPaged>(p, grid, interleaved, stream);
+    p.norm ? launch_rope_fwd<128, true>(p, grid, interleaved, stream)
+           : launch_rope_fwd<128, false>(p, grid, interleaved, stream);
   else
-    p.norm ? launch_rope_fwd<64, true, kPaged>(p, grid, interleaved, stream)
-           : launch_rope_fwd<64, false, kPaged>(p, grid, interleaved, stream);
+    p.norm ? launch_rope_fwd<64, true>(p, grid, interleaved, stream)
+           : launch_rope_fwd<64, false>(p, grid, interleaved, stream);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -162,7 +162,7 @@ fa_status fa_rope_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   p.eps = eps;
   p.factor = factor;
   p.norm = norm;
-  return run_rope_fwd<false>(p, d, q_out, k_out, v_out, interleaved, stream);
+  return run_rope_fwd(p, d, q_out, k_out, v_out, interleaved, stream);
 }
 
 fa_status fa_rope_paged_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const float* q_weight,
@@ -195,7 +195,7 @@ fa_status fa_rope_paged_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v
                                      k_weight, inv_freq, positions, page_table, cache_lens, chunk_lens, q_out,
                                      to_k ? k_pages->ptr : nullptr, to_v ? v_pages->ptr : nullptr})) != FA_OK)
     return st;
-  fa::RopeParams p{};
+  fa::RopePagedParams p{};
   p.q = rope_rows(q);
   p.k = rope_rows(k);
   p.v = rope_rows(v);
@@ -224,7 +224,7 @@ fa_status fa_rope_paged_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v
     p.page_shift = pages.shift();
     p.pages = num_pages;
   }
-  return run_rope_fwd<true>(p, d, q_out, to_k, to_v, interleaved, stream);
+  return run_rope_fwd(p, d, q_out, to_k, to_v, interleaved, stream);
 }
 
 size_t fa_rope_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d) {
