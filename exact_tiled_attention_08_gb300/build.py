@@ -47,6 +47,8 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
+    # (With -split-compile ptxas takes the kernels on all cores, but makes them slower: the rotation of 16384
+    # tokens of 48 heads 78 us instead of 69, the span backward 2.48 ms instead of 2.28.)
     cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE_DIR, "-o", tmp, os.path.join(CSRC_DIR, "fa_ops.cu")]
     if verbose:

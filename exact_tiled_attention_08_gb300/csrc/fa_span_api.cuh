@@ -121,7 +121,7 @@ struct SpanFwdPlan {
     w.few = paged && rows_all <= fa::kFewRows;
     w.tokens = (w.few ? fa::kFewRows : 128) / heads;
     w.tiles = (N + w.tokens - 1) / w.tokens;
-    w.pair = w.tiles > 1;
+    w.pair = !paged || w.tiles > 1;  // (a tile of contiguous keys alone has but one block)
     w.row_tiles = w.pair ? (w.tiles + 1) / 2 : 1;
     w.part_rows = w.pair ? 256 : (int)rows_all;
     const long long blocks = (long long)B * (H / heads) * w.row_tiles * ((C + 127LL) / 128 + fa::kCrossStart);
@@ -193,20 +193,24 @@ fa_status launch_span_mod(const CUtensorMap* maps, const fa::SpanFwdParams<PAGED
   return p.slopes ? launch_span_fwd<D, 1, PAIR>(maps, p, grid, stream) : launch_span_fwd<D, 0, PAIR>(maps, p, grid, stream);
 }
 
-// The forward's main kernel: two row tiles per item, one, or (pages) few rows.
+// The forward's main kernel: two row tiles per item, or (pages) one, or few rows.
 template <int D, bool PAGED>
 fa_status launch_span_form(const CUtensorMap* maps, fa::SpanFwdParams<PAGED>& p, const SpanFwdPlan& plan, unsigned grid,
                            int sms, cudaStream_t stream) {
-  if constexpr (PAGED)
+  if constexpr (PAGED) {
     if (plan.few) return launch_span_few<D>(maps, p, grid, sms, stream);
-  return plan.pair ? launch_span_mod<D, true>(maps, p, grid, stream) : launch_span_mod<D, false>(maps, p, grid, stream);
+    if (!plan.pair) return launch_span_mod<D, false>(maps, p, grid, stream);
+  }
+  return launch_span_mod<D, true>(maps, p, grid, stream);
 }
 
 template <int D, bool PAGED>
 fa_status launch_span_combine(const fa::SpanFwdParams<PAGED>& p, const SpanFwdPlan& plan, unsigned grid, cudaStream_t stream) {
   const int per_block = plan.pair ? 32 : 8;  // rows of a block
   const dim3 parts(grid, (unsigned)((plan.part_rows + per_block - 1) / per_block));
-  auto combine = plan.pair ? fa::fa_span_combine_kernel<D, true, PAGED> : fa::fa_span_combine_kernel<D, false, PAGED>;
+  auto combine = fa::fa_span_combine_kernel<D, true, PAGED>;
+  if constexpr (PAGED)
+    if (!plan.pair) combine = fa::fa_span_combine_kernel<D, false, PAGED>;
   return launch_early(combine, parts, 256, 0, stream, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

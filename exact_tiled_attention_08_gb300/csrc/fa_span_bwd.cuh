@@ -19,6 +19,10 @@
 // Scores as in the forward: P = 2^(s log2e - LSE log2e) with the capped and biased score
 // s, and dS = P o (dP - delta) o (1 - tanh^2); P (1 - tanh^2) is what is kept
 // between the two halves of the elementwise step.
+//
+// Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 2.28 ms, 1204 TFLOP/s (fa_bwd at H=32: 2.18),
+// capped 2.71 ms; 25 packed documents of one request, capped, 422 us, of which the main kernel takes 340.
+// The elementwise warps bound it.
 #pragma once
 
 #include <cuda_bf16.h>

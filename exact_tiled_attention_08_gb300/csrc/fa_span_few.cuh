@@ -19,7 +19,9 @@
 // through one another's shared memory, without the second kernel.
 //
 // What bounds it is memory, as far as there are blocks enough: the ring holds three K and
-// three V tiles at d = 128.
+// three V tiles at d = 128.  Measured on a GB300: 16 requests of 300 to 8100 tokens, H=32/8 d=128, a token
+// each, 60 us (4.5 TB/s with start and join), capped or not, pages of 16 or 64; fa_span_fwd_kernel
+// takes 66 us with pages of 64, capped 82.  (With 32 columns it was slower than that kernel: 76 and 67 us.)
 #pragma once
 
 #include "fa_span_fwd.cuh"
