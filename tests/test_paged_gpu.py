@@ -424,3 +424,56 @@ def test_many_items_of_a_block(d, dirty):
     assert fa.fa_check_device_status() == fa.FA_OK
     assert torch.isfinite(o).all()
     check_paged(q, kp, vp, table, o, lse, 1 / math.sqrt(d), lens, [T] * B, 0, 0.0, None, most=40)
+
+
+def test_offsets_past_32_bits():
+    """Rows far behind 2^31 elements of a pool, of the queries and of the outputs: the bits of a pool that has
+    only the pages in use, and of a request alone."""
+    B, H, Hkv, T, size, d, count = 3, 4, 2, 300, 64, 128, 150000
+    lens, width = [900, 0, 513], 20
+    g = torch.Generator("cuda").manual_seed(1)
+    need = [-(-(n + T) // size) for n in lens]
+    small = [torch.randn((sum(need), Hkv, size, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    where = torch.arange(count - 2 * sum(need), count, 2, device="cuda")[torch.randperm(sum(need), generator=torch.Generator().manual_seed(2)).cuda()]
+    big = [torch.empty((count, Hkv, size, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert int(where.min()) * Hkv * size * d > 2 ** 31
+    tables_ = []
+    for pages in (torch.arange(sum(need), device="cuda"), where):
+        table, at = torch.full((B, width), -1, device="cuda", **I32), 0
+        for b, n in enumerate(need):
+            table[b, :n] = pages[at:at + n].int()
+            at += n
+        tables_.append(table)
+    for x, y in zip(small, big):
+        y[where] = x
+    q = torch.randn((B, H, T, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    dl = torch.tensor(lens, **I32).cuda()
+    one = fa.paged_attention_forward(q, *small, tables_[0], dl, 0.1)
+    two = fa.paged_attention_forward(q, *big, tables_[1], dl, 0.1)
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    # new rows go to the far pages too
+    rows = torch.randn((B, T, H + 2 * Hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    heads = rows[:, :, :H], rows[:, :, H:H + Hkv], rows[:, :, H + Hkv:]
+    for pages, table in ((small, tables_[0]), (big, tables_[1])):
+        fa.fa_rope_paged_fwd(*heads, None, None, None, None, table, dl, None, torch.empty_like(q), *pages)
+    for x, y in zip(small, big):
+        assert torch.equal(x, y[where])
+
+
+def test_queries_past_32_bits():
+    """More than 2^31 elements of queries: the last request comes out as it does alone."""
+    B, H, Hkv, T, size, d = 70, 32, 4, 8000, 256, 128
+    assert B * H * T * d > 2 ** 31
+    g = torch.Generator("cuda").manual_seed(1)
+    kp, vp = (torch.randn((40, Hkv, size, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.arange(32, device="cuda", **I32).repeat(B, 1)
+    q = torch.randn((B, H, T, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    lens = torch.zeros(B, device="cuda", **I32)
+    chunks = torch.full((B,), 3, device="cuda", **I32)
+    chunks[-1] = T
+    o, lse = fa.paged_attention_forward(q, kp, vp, table, lens, 0.1, chunks, window=600)
+    # (alone an item may be cut into other parts, which rounds once more in fp32: a bf16 step of the largest)
+    p, ple = fa.paged_attention_forward(q[-1:], kp, vp, table[:1], lens[:1], 0.1, window=600)
+    assert float((o[-1:].float() - p.float()).abs().max()) <= 2 ** -7 * float(p.float().abs().max())
+    assert float((lse[-1:] - ple).abs().max()) <= 1e-4
+    assert (o[5, :, 3:] == 0).all() and (lse[5, :, 3:] == -math.inf).all()

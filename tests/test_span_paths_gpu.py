@@ -303,3 +303,21 @@ def test_a_training_step():
     got = host(dx[0, :, 0])
     # (as in test_span_gpu's differences, and the rounding of the rotated rows to bf16, relative to the scores' size)
     assert abs((got * u).sum() - (step(1e-4) - step(-1e-4)) / 2e-4) <= 64 * H2 * np.linalg.norm(got)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last group of heads comes out as it does alone."""
+    B, H, Hkv, N, d, window = 1, 300, 30, 60000, 128, 300
+    assert B * H * N * d > 2 ** 31
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v, do = (torch.randn((B, h, N, d), generator=g, device="cuda", dtype=torch.bfloat16) for h in (H, Hkv, Hkv, H))
+    o, lse = fa.span_attention_forward(q, k, v, 0.1, causal=True, window=window)
+    grads = fa.span_attention_backward(q, k, v, o, do, lse, 0.1, causal=True, window=window)
+    G = H // Hkv
+    one = [x[:, -n:].contiguous() for x, n in ((q, G), (k, 1), (v, 1), (do, G))]
+    p, ple = fa.span_attention_forward(*one[:3], 0.1, causal=True, window=window)
+    alone = fa.span_attention_backward(*one[:3], p, one[3], ple, 0.1, causal=True, window=window)
+    # (alone, items may be cut into other parts, which are added up in fp32: a bf16 step of the largest)
+    for x, y in zip((o[:, -G:], grads[0][:, -G:], grads[1][:, -1:], grads[2][:, -1:]), (p, *alone)):
+        assert float((x.float() - y.float()).abs().max()) <= 2 ** -7 * float(y.float().abs().max())
+    assert float((lse[:, -G:] - ple).abs().max()) <= 1e-4
