@@ -16,9 +16,9 @@
 // running maximum stays (from the first to the last it rises in every block: H=32/8 N=8192
 // d=128, two requests, causal, with slopes, 1022 and 951 us).
 //
-// Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 730 us, 1507 TFLOP/s, with slopes 739 us,
-// with a window of 1024 242 us; one request capped 477 us; 2048 new tokens of two requests over 2000 and 16000
-// in pages 461 us, 1459 TFLOP/s.  The softmax warps bound it (tensor cores 56 % busy, DRAM idle).
+// Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 701 us, 1568 TFLOP/s, with slopes 743 us,
+// with a window of 1024 237 us; one request capped 479 us; 2048 new tokens of two requests over 2000 and 16000
+// in pages 457 us, 1472 TFLOP/s.  The softmax warps bound it (tensor cores 56 % busy, DRAM idle).
 //
 // Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
 // (MOD 2 and 3) and the bias (MOD 1 and 3) change the scores in registers, before the maximum.
@@ -588,11 +588,11 @@ __global__ void __launch_bounds__(384, 1)
     fa_span_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SpanFwdParams<PAGED> p) {
   using C = CrossCfg<D>;
-  // The issuing threads' loops over the two row tiles: one copy of the products at d = 128, where
-  // the kernel's loops together outgrow the instruction cache (H=32/8 N=8192, two requests, causal:
-  // 814 us, and 904 with two copies, when it was tried); at d = 64 the shorter products outrun a loop
-  // (H=16 N=2048, four requests, with slopes: 76 and 78 us).
-  constexpr int kIssueUnroll = D == 64 ? 2 : 1;
+  // The issuing threads' loops over the two row tiles: one copy of the products where the kernel's loops
+  // together outgrow the instruction cache (H=32/8 N=8192 d=128, two requests, causal, with slopes: 743 us, and
+  // 785 with two copies; one request capped 479 and 566), else two (plain scores 701 us, and 735 with one copy;
+  // H=16 N=2048 d=64, four requests, 59 and 66 us).
+  constexpr int kIssueUnroll = D == 64 || MOD == 0 ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     // the 128-byte-swizzled tiles need 1024-byte alignment: report, do nothing
