@@ -910,7 +910,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         // mx cmx: the largest score; a row that sees nothing of the block has none
         const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;
-        if (MOD == 2 && fused && mx <= p.cap.hidden) mx = -CUDART_INF_F;
+        // (below a cap of 30, where nothing stands for hidden keys, the polynomial takes blocks seen whole alone)
+        if (MOD == 2 && fused && p.cap.hidden < 0.f && mx <= p.cap.hidden) mx = -CUDART_INF_F;
         const float m_new = fmaxf(m, mx * cmx);
         // conditional rescale: the reference moves only when the row maximum
         // rose by more than the threshold (always from -inf: no key so far)

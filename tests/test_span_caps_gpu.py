@@ -1,0 +1,100 @@
+"""Capped scores where a row's products are not spread around zero: rows without any product
+above zero.  Spans and pages, with gradients; bounds as in test_span_gpu."""
+
+import math
+
+import pytest
+import torch
+
+from exact_tiled_attention_08_gb300 import fa
+from test_paged_gpu import check_paged, pool, tables
+from test_span_gpu import check_bwd, check_fwd, inputs, masks
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from exact_tiled_attention_08_gb300.build import build_library
+
+    build_library()
+    fa.load_library()
+
+
+def direction(d):
+    return torch.where(torch.rand(d, generator=torch.Generator().manual_seed(d)) < 0.5, -1.0, 1.0)
+
+
+def shares(caps):
+    """Keys' lengths, the longest 1, and what the queries make up for it."""
+    top = float(caps.abs().max())
+    return (caps / top if top else torch.ones_like(caps)), top
+
+
+def directed(B, H, Hkv, N, d, caps, cap):
+    """q, k, v, do with scale q.k about caps[j] cap for key j of every query, scale = d^-1/2 (keys
+    differ by a twentieth of a unit in each channel)."""
+    q, k, v, do = inputs(B, H, Hkv, N, d, 0.0, 31)
+    u, (rows, top) = direction(d), shares(caps)
+    k = ((u + 0.05 * k.float()) * rows[None, None, :, None]).bfloat16()
+    q = (u * (cap * top / math.sqrt(d))).bfloat16().expand(B, H, N, d).contiguous()
+    return [x.cuda() for x in (q, k, v, do)]
+
+
+def both_ways(x, kind, cap, d):
+    q, k, v, do = x
+    B, H, N, _ = q.shape
+    begin, end, causal = masks(kind, B, N, 5)
+    args = dict(key_begin=None if begin is None else begin.cuda(), key_end=None if end is None else end.cuda(),
+                causal=causal, cap=cap)
+    scale = 1 / math.sqrt(d)
+    o, lse = fa.span_attention_forward(q, k, v, scale, **args)
+    check_fwd(q, k, v, o, lse, scale, begin, end, causal, 0, cap, None)
+    grads = fa.span_attention_backward(q, k, v, o, do, lse, scale, **args)
+    for g in grads:
+        assert torch.isfinite(g).all()
+    check_bwd(q, k, v, o, do, lse, grads, scale, begin, end, causal, 0, cap, None)
+
+
+def over_pages(T, pattern, cap, d):
+    B, H, Hkv, size, lens = 2, 4, 2, 32, [700, 385]
+    table, count = tables(lens, [T] * B, size, -(-(max(lens) + T) // size), 1)
+    u, (shared, top) = direction(d).cuda(), shares(caps_of(pattern, max(lens) + T + size))
+    kp, vp = pool(1, count, Hkv, size, d, "tokens"), pool(2, count, Hkv, size, d, "heads")
+    away = u + 0.05 * kp.float()
+    for b, n in enumerate(lens):
+        for i in range(-(-(n + T) // size)):
+            page = int(table[b, i])
+            kp[page] = (away[page] * shared[i * size:(i + 1) * size, None].cuda()).bfloat16()
+    q = (u * (cap * top / math.sqrt(d))).bfloat16().expand(B, H, T, d).contiguous()
+    scale = 1 / math.sqrt(d)
+    o, lse = fa.paged_attention_forward(q, kp, vp, table.cuda(), torch.tensor(lens, **I32).cuda(), scale, cap=cap)
+    check_paged(q, kp, vp, table, o, lse, scale, lens, [T] * B, 0, cap, None)
+
+
+def caps_of(pattern, N):
+    """What scale q.k is of each key, in caps."""
+    j = torch.arange(N)
+    return {"zero": torch.zeros(N),
+            "against": torch.full((N,), -0.3),
+            "turning": torch.where(j < N // 3, 0.1, -0.3)}[pattern]  # (keys are taken from the last to the first)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [5.0, 20.0, 29.0, 30.0, 50.0])
+@pytest.mark.parametrize("pattern", ["zero", "against", "turning"])
+@pytest.mark.parametrize("B, H, Hkv, N, kind", [(1, 2, 1, 1024, "full"), (4, 40, 40, 256, "full"), (1, 2, 1, 600, "prefix")])
+def test_no_product_above_zero(B, H, Hkv, N, kind, pattern, cap, d):
+    """Queries of zeros, and queries that all or most keys point away from: in few items, which shares
+    cut, and in many."""
+    both_ways(directed(B, H, Hkv, N, d, caps_of(pattern, N), cap), kind, cap, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [5.0, 20.0, 29.0, 30.0, 50.0])
+@pytest.mark.parametrize("pattern", ["zero", "against", "turning"])
+@pytest.mark.parametrize("T", [1, 17, 60, 150])
+def test_no_product_above_zero_over_pages(T, pattern, cap, d):
+    """A few rows, one row tile and pairs of them."""
+    over_pages(T, pattern, cap, d)
