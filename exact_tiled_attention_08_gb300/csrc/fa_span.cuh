@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(128) fa_span_bounds_kernel(const SpanView<fals
 // -0.2.  Products below -0.6, where the polynomial goes its own way downwards (to the
 // ninth power), then weigh less than e^-(0.53 - 0.2) 30 = 5e-5 in their row, and their weights'
 // errors, e^-(tanh|x| - 0.2) 30 times 30 |x G(x^2) - tanh x|, are below 1e-8 everywhere.  And a product of
-// -10 gives a weight of 0, so that it stands for a key that is not seen.
+// -10 gives a weight of 0 beside such a largest one, so that it stands for a key that is not seen.
 struct SpanCap {
   float mul;     // 2 log2(e) scale / cap
   float small;   // products up to there take the polynomial: 0.6 cap / scale

@@ -873,14 +873,20 @@ __global__ void __launch_bounds__(384, 1)
         auto row_max = [&] { return fmaxf(cross_max64(sr[0], sr[1]), cross_max64(sr[2], sr[3])); };
         // MOD 2 and 3: small products are capped by the polynomial, in MOD 2 inside the exponent's
         // argument below; others in place.  What is not seen has no say in it.
+        // (That the row sees nothing of the block is asked of its span, not of the maximum: products that it
+        // sees may lie below the one that stands for hidden keys, all of them.)
         bool fused = false;
+        bool none = false;
         float mx = 0.f;
         if constexpr (MOD >= 2) {
           bool small;
           if (MOD == 2 && p.cap.hidden < 0.f) {
-            if (__builtin_expect(cut, 0)) hide(p.cap.hidden);
+            if (__builtin_expect(cut, 0)) {
+              hide(p.cap.hidden);
+              none = max(row_lo, kbase) >= min(row_hi, kbase + 128);
+            }
             mx = row_max();
-            small = mx <= p.cap.small && (mx >= p.cap.low || mx <= p.cap.hidden);
+            small = mx <= p.cap.small && (mx >= p.cap.low || none);
           } else {
             mx = row_max();
             small = !cut && span_absmax(sr) <= p.cap.small;
@@ -910,8 +916,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         // mx cmx: the largest score; a row that sees nothing of the block has none
         const float cmx = MOD == 2 && fused ? span_cap_small(make_float2(mx, mx), p.cap).x : cj;
-        // (below a cap of 30, where nothing stands for hidden keys, the polynomial takes blocks seen whole alone)
-        if (MOD == 2 && fused && p.cap.hidden < 0.f && mx <= p.cap.hidden) mx = -CUDART_INF_F;
+        if (MOD == 2 && none) mx = -CUDART_INF_F;
         const float m_new = fmaxf(m, mx * cmx);
         // conditional rescale: the reference moves only when the row maximum
         // rose by more than the threshold (always from -inf: no key so far)

@@ -1,5 +1,6 @@
 """Capped scores where a row's products are not spread around zero: rows without any product
-above zero.  Spans and pages, with gradients; bounds as in test_span_gpu."""
+above zero, rows whose products all lie many caps below it.  Spans and pages, with gradients;
+bounds as in test_span_gpu."""
 
 import math
 
@@ -8,7 +9,7 @@ import torch
 
 from exact_tiled_attention_08_gb300 import fa
 from test_paged_gpu import check_paged, pool, tables
-from test_span_gpu import check_bwd, check_fwd, inputs, masks
+from test_span_gpu import check_bwd, check_fwd, inputs, masks, randn
 
 pytestmark = pytest.mark.gpu
 I32 = dict(dtype=torch.int32)
@@ -78,7 +79,11 @@ def caps_of(pattern, N):
     j = torch.arange(N)
     return {"zero": torch.zeros(N),
             "against": torch.full((N,), -0.3),
-            "turning": torch.where(j < N // 3, 0.1, -0.3)}[pattern]  # (keys are taken from the last to the first)
+            "turning": torch.where(j < N // 3, 0.1, -0.3),  # (keys are taken from the last to the first)
+            "low": torch.full((N,), -11.0),
+            "lowest": torch.full((N,), -40.0),
+            "levels": torch.tensor([-2.0, -11.0, -40.0])[j // 128 % 3],
+            "levels back": torch.tensor([-40.0, -11.0, -2.0])[j // 128 % 3]}[pattern]
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -97,4 +102,33 @@ def test_no_product_above_zero(B, H, Hkv, N, kind, pattern, cap, d):
 @pytest.mark.parametrize("T", [1, 17, 60, 150])
 def test_no_product_above_zero_over_pages(T, pattern, cap, d):
     """A few rows, one row tile and pairs of them."""
+    over_pages(T, pattern, cap, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [8.0, 30.0, 50.0])
+@pytest.mark.parametrize("pattern", ["low", "lowest", "levels", "levels back"])
+@pytest.mark.parametrize("N, kind", [(100, "causal"), (700, "causal"), (700, "docs"), (384, "full"), (700, "random")])
+def test_products_many_caps_below_zero(N, kind, pattern, cap, d):
+    """Rows that see nothing but products of -2, -11 and -40 caps: the scores are all about -cap."""
+    both_ways(directed(1, 4, 2, N, d, caps_of(pattern, N), cap), kind, cap, d)
+
+
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+@pytest.mark.parametrize("kind", ["causal", "docs", "random"])
+def test_a_few_rows_of_low_products(kind, cap):
+    """Rows 0, 37, 74, ... see products of -15 caps alone, their neighbours ordinary ones."""
+    d, N = 128, 500
+    q, k, v, do = directed(1, 4, 2, N, d, caps_of("low", N), cap)
+    low = q[:, :, ::37] * (15 / 11)
+    q = (randn(3, 1, 4, N, d) * 4).cuda()
+    q[:, :, ::37] = low
+    both_ways((q, k, v, do), kind, cap, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [5.0, 30.0, 50.0])
+@pytest.mark.parametrize("pattern", ["low", "lowest", "levels"])
+@pytest.mark.parametrize("T", [1, 17, 60, 150])
+def test_products_many_caps_below_zero_over_pages(T, pattern, cap, d):
     over_pages(T, pattern, cap, d)
