@@ -331,7 +331,7 @@ __device__ __forceinline__ uint32_t span_transpose(uint32_t v, int lane) {
 
 // Blocks seen in part, by one warp, 32 queries at a time: hidden products become -inf in tensor
 // memory (with a cap their tanh is -1, its derivative 0), and with a cap hidden
-// probabilities 0 behind that.  (Small code away from the loop: masks unrolled into it
+// probabilities 0 behind that (with a bias too those that are kept for dS).  (Small code away from the loop: masks unrolled into it
 // cost a block that is seen in part more than twice another's time.)
 __device__ __forceinline__ void span_bwd_hide_s(uint32_t at, const uint32_t (&seen)[2]) {
 #pragma unroll 1
@@ -844,7 +844,20 @@ __global__ void __launch_bounds__(512, 1)
             tmem_st8(tS + qc + 16, pk + 8);
           }
         }
-        if (MOD >= 2 && __builtin_expect(cut, 0)) span_bwd_hide_p(tS + 64 * grp, seen);
+        if (MOD >= 2 && __builtin_expect(cut, 0)) {
+          span_bwd_hide_p(tS + 64 * grp, seen);
+          // (Without a bias 2^(-cap - LSE) is at most 1, and times 1 - tanh^2 = 0.  With one a hidden key may be
+          // so much nearer than those that the row sees that it is infinite.)
+          if constexpr (MOD == 3) {
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (!((seen[ch] >> (2 * e)) & 1u)) pf[ch][e].x = 0.f;
+                if (!((seen[ch] >> (2 * e + 1)) & 1u)) pf[ch][e].y = 0.f;
+              }
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar->p_done);

@@ -1,6 +1,6 @@
 """Capped scores where a row's products are not spread around zero: rows without any product
-above zero, rows whose products all lie many caps below it.  Spans and pages, with gradients;
-bounds as in test_span_gpu."""
+above zero, rows whose products all lie many caps below it, hidden keys that are much nearer
+than every key a row sees.  Spans and pages, with gradients; bounds as in test_span_gpu."""
 
 import math
 
@@ -43,19 +43,19 @@ def directed(B, H, Hkv, N, d, caps, cap):
     return [x.cuda() for x in (q, k, v, do)]
 
 
-def both_ways(x, kind, cap, d):
+def both_ways(x, kind, cap, d, slopes=None, spans=None):
     q, k, v, do = x
     B, H, N, _ = q.shape
-    begin, end, causal = masks(kind, B, N, 5)
+    begin, end, causal = masks(kind, B, N, 5) if spans is None else (*spans, False)
     args = dict(key_begin=None if begin is None else begin.cuda(), key_end=None if end is None else end.cuda(),
-                causal=causal, cap=cap)
+                causal=causal, cap=cap, slopes=None if slopes is None else slopes.cuda())
     scale = 1 / math.sqrt(d)
     o, lse = fa.span_attention_forward(q, k, v, scale, **args)
-    check_fwd(q, k, v, o, lse, scale, begin, end, causal, 0, cap, None)
+    check_fwd(q, k, v, o, lse, scale, begin, end, causal, 0, cap, slopes)
     grads = fa.span_attention_backward(q, k, v, o, do, lse, scale, **args)
     for g in grads:
         assert torch.isfinite(g).all()
-    check_bwd(q, k, v, o, do, lse, grads, scale, begin, end, causal, 0, cap, None)
+    check_bwd(q, k, v, o, do, lse, grads, scale, begin, end, causal, 0, cap, slopes)
 
 
 def over_pages(T, pattern, cap, d):
@@ -132,3 +132,24 @@ def test_a_few_rows_of_low_products(kind, cap):
 @pytest.mark.parametrize("T", [1, 17, 60, 150])
 def test_products_many_caps_below_zero_over_pages(T, pattern, cap, d):
     over_pages(T, pattern, cap, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap, slope", [(30.0, 1.0), (30.0, 0.5), (5.0, 0.25), (5.0, 2.0), (0.0, 1.0)])
+@pytest.mark.parametrize("seen", ["far", "far documents", "near"])
+def test_hidden_keys_much_nearer_than_the_seen_ones(seen, cap, slope, d):
+    """Rows that see far keys alone, in tiles whose other rows see near ones: without its mask the bias would
+    make a hidden pair weigh more than fp32 holds.  (near: a bias that grows, and hidden keys that are far.)"""
+    N = 2048 if slope < 1 else 512
+    i = torch.arange(N, dtype=torch.int32)
+    even = i % 2 == 0
+    if seen == "far":
+        begin, end = torch.where(even, 0, N // 2), torch.where(even, 10, 3 * N // 4)
+    elif seen == "far documents":
+        begin, end = torch.zeros_like(i), torch.where(even, 10, N)
+    else:
+        begin, end = torch.where(even, N - 140, N - 256), torch.where(even, N - 120, N)
+        slope = -slope
+    slopes = torch.tensor([slope, slope / 2, 0.0, -slope / 8])
+    x = inputs(1, 4, 2, N, d, cap, 41)
+    both_ways([t.cuda() for t in x], None, cap, d, slopes, (begin.int()[None], end.int()[None]))
