@@ -34,11 +34,17 @@ fa_status check_pages(const fa_pages* r, const PageShape& s, int Hkv) {
   return aligned16(r->ptr) ? FA_OK : FA_ERR_MISALIGNED;
 }
 
+// 1 - 2 / (1 + e^2x), which the backward, few rows and blocks with large products take, is off by 2^-21 of the
+// cap however small the score (half of it from the rounding of 1 + e^2x and the two approximations at x = 0,
+// all of it at -1).  Up to this cap that is at most 2^-7 of a score, a change of a weight by two of bf16's
+// half steps.
+constexpr float kMaxCap = 16384.f;
+
 fa_status check_span_args(float scale, float cap, int window, int causal) {
   fa_status st = check_scale(scale, causal);
   if (st != FA_OK) return st;
-  if (!std::isfinite(cap) || cap < 0.f || window < 0) return FA_ERR_INVALID_ARG;
-  if (cap > 0.f && (!std::isnormal(scale / cap) || !std::isfinite(4.f * scale / cap) || !std::isfinite(4.f * cap))) return FA_ERR_INVALID_ARG;
+  if (!(cap >= 0.f && cap <= kMaxCap) || window < 0) return FA_ERR_INVALID_ARG;
+  if (cap > 0.f && (!std::isnormal(scale / cap) || !std::isfinite(4.f * scale / cap))) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 

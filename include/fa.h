@@ -396,8 +396,10 @@ fa_status fa_rope_bwd(const fa_rows* q, const fa_rows* k, const float* q_weight,
  *                [0, N] are taken as 0 and N.)
  *   slopes       in:  fp32 [H], or null
  *   o, lse       rows that see no key give O = 0 and LSE = -inf
- *   cap          0, or positive with 4 cap and 4 scale / cap finite and scale / cap normal;
- *                window >= 0
+ *   cap          0, or positive and at most 16384, with 4 scale / cap finite and scale / cap
+ *                normal.  The tanh is off by at most 2^-21, not relative to it: scores are off by
+ *                up to 2^-21 of the cap, small ones too, hence the limit.
+ *   window       >= 0
  *   workspace    as for fa_cross_fwd, of fa_span_fwd_workspace_bytes()
  * Scores of pairs outside the spans have no effect, whatever they are.  Rows of V
  * meet the queries of their tile with weight 0 where they are not seen, so a row

@@ -9,7 +9,7 @@ import torch
 
 from exact_tiled_attention_08_gb300 import fa
 from test_paged_gpu import check_paged, pool, tables
-from test_span_gpu import check_bwd, check_fwd, inputs, masks, randn
+from test_span_gpu import check_bwd, check_fwd, inputs, masks, randn, slopes_of
 
 pytestmark = pytest.mark.gpu
 I32 = dict(dtype=torch.int32)
@@ -153,3 +153,21 @@ def test_hidden_keys_much_nearer_than_the_seen_ones(seen, cap, slope, d):
     slopes = torch.tensor([slope, slope / 2, 0.0, -slope / 8])
     x = inputs(1, 4, 2, N, d, cap, 41)
     both_ways([t.cuda() for t in x], None, cap, d, slopes, (begin.int()[None], end.int()[None]))
+
+
+@pytest.mark.parametrize("cap", [1000.0, 16384.0])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_small_scores_under_a_large_cap(slopes, cap):
+    """The tanh's error, 2^-21 of the cap, is what the bounds count: in all forms, of scores up to 20 or so."""
+    d, H = 128, 4
+    sl = slopes_of(H, slopes)
+    for kind, N in (("causal", 700), ("docs", 300), ("full", 256)):
+        both_ways([x.cuda() for x in inputs(1, H, 2, N, d, cap, 51)], kind, cap, d, sl)
+    lens, size, scale = [700, 385], 32, 1 / math.sqrt(d)
+    for T in (1, 17, 60, 150):
+        table, count = tables(lens, [T] * 2, size, -(-(max(lens) + T) // size), 1)
+        kp, vp = pool(1, count, 2, size, d, "tokens"), pool(2, count, 2, size, d, "heads")
+        q = (randn(3, 2, H, T, d) * 4).cuda()
+        o, lse = fa.paged_attention_forward(q, kp, vp, table.cuda(), torch.tensor(lens, **I32).cuda(), scale, cap=cap,
+                                            slopes=None if sl is None else sl.cuda())
+        check_paged(q, kp, vp, table, o, lse, scale, lens, [T] * 2, 0, cap, sl)
