@@ -44,7 +44,7 @@ struct FewCfg {
   static constexpr uint32_t kTmemCols = 128;                         // S^T of two blocks, O^T
   static constexpr uint32_t kOCol = 2 * R;
   static_assert(3 * R <= kTmemCols, "tensor memory budget");
-  static constexpr int kStatBytes = 2048;
+  static constexpr int kStatBytes = 1024;
   static constexpr int kScheduleBytes = 1536;
   // (16 KB behind the ring: with d = 64 the V^T operand's upper 64 rows are whatever lies there)
   static constexpr int kTail = 2 * kQBytes + 2 * kPBytes + kStatBytes + kScheduleBytes + 1024;
@@ -72,16 +72,18 @@ static_assert(sizeof(FewBarriers) <= 1024, "barriers overflow their shared-memor
 
 // Of the segment's rows, in shared memory.
 struct FewRows {
-  int lo[32], hi[32];
-  float slope2[32];
-  float rel[2][32];       // positions from the first key of a block and of the one that follows
-  float ref[32];          // the reference (log2 units), -inf: no key so far
-  float part[4][32];      // of each warp: maxima, sums
-  float inv[32];          // at the end: 1 / sum
-  char* out[32];          // at the end: where the row goes, or nullptr
-  float lse[32];          // CLUSTER: this CTA's part
+  int lo[kFewRows], hi[kFewRows];
+  float slope2[kFewRows];
+  float rel[2][kFewRows];  // positions from the first key of a block and of the one that follows
+  float ref[kFewRows];     // the reference (log2 units), -inf: no key so far
+  float part[4][kFewRows];  // of each warp: maxima, sums
+  float inv[kFewRows];     // at the end: 1 / sum
+  char* out[kFewRows];     // at the end: where the row goes, or nullptr
+  float lse[kFewRows];     // CLUSTER: this CTA's part
 };
-static_assert(sizeof(FewRows) <= 2048 && offsetof(FewRows, ref) % 16 == 0, "statistics overflow their shared-memory slot");
+static_assert(sizeof(FewRows) <= 1024, "statistics overflow their shared-memory slot");
+static_assert(offsetof(FewRows, slope2) % 16 == 0 && offsetof(FewRows, rel) % 16 == 0 && offsetof(FewRows, ref) % 16 == 0,
+              "read four rows at a time");
 
 // the four softmax warps: a barrier, and one that says whether any thread of them has x
 __device__ __forceinline__ void few_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   grid_wait();
   if (CLUSTER) {
-    if (tid < 32) rows->lse[tid] = -CUDART_INF_F;  // no part so far
+    if (tid < R) rows->lse[tid] = -CUDART_INF_F;  // no part so far
     if (tid == 0) span_cluster_share(p, &bar->place);
   } else {
     span_schedule<false, C::kThreads>(p, sSchedule, &bar->place, &bar->total, &bar->end);
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(256, 1)
       if (lane == 0) mbar_arrive(&bar->seg_empty[n % kSpanSegs]);
       const int len = v.len(b), fresh = v.rows(b, len);
       int pos = 0;  // of row `tid`
-      if (tid < 32) {
+      if (tid < R) {
         int lo = 0, hi = 0;
         float slope2 = 0.f;
         const int tok = tid / p.rows.heads();
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(256, 1)
           for (int q = 0; q < R; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * p.scale_log2);
         }
         if (p.slopes) {
-          if (tid < 32) rows->rel[buf ^ 1][tid] = (float)(pos - j * 128 + 128);  // (a barrier before it is read)
+          if (tid < R) rows->rel[buf ^ 1][tid] = (float)(pos - j * 128 + 128);  // (a barrier before it is read)
 #pragma unroll
           for (int q4 = 0; q4 < R; q4 += 4) {
             const float4 rel = *reinterpret_cast<const float4*>(rows->rel[buf] + q4);
