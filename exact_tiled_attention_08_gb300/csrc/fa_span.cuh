@@ -15,7 +15,7 @@ namespace fa {
 
 // PAGED: keys in pages; else in [B][Hkv][N][d].  (The kernels are compiled for each of the two: what the other
 // form needs costs instruction fetches.  N=8192 H=32/8 d=128 causal, one request, capped: 560 and 496 us
-// when it was tried, 477 now.)
+// when it was tried, 479 now.)
 template <bool PAGED>
 struct SpanView {
   const int *begin, *end;      // [B][N] or nullptr: 0 and C

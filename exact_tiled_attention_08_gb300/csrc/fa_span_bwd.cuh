@@ -21,7 +21,8 @@
 // between the two halves of the elementwise step.
 //
 // Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 2.28 ms, 1204 TFLOP/s (fa_bwd at H=32: 2.18),
-// capped 2.71 ms; 25 packed documents of one request, capped, 422 us, of which the main kernel takes 340.
+// capped 2.71 ms, capped and with slopes 2.95; 25 packed documents of one request, capped, 421 us, of which the
+// main kernel takes 340.
 // The elementwise warps bound it.
 #pragma once
 
@@ -176,7 +177,9 @@ __device__ __forceinline__ int2 span_bwd_hull(const SpanBwdParams& p, int b, int
 // N=8192 H=32/8 d=128, 390 and 372 us; equal where nothing is that long.)
 constexpr int kSpanBwdRun = 4;
 
-// One CTA: hulls and costs, the cut length, and the runs in the order of the entries.
+// One CTA: hulls and costs, the cut length, and the runs in the order of the entries.  With spans by row it
+// looks at all of a request's blocks for each of them, twice: 7 us at 64 blocks, and it grows with their square
+// (documents of 512 tokens, H=8/1 d=128: N=131072 0.13 of 1.04 ms, N=524288 1.8 of 5.4 ms).
 __global__ void __launch_bounds__(1024) fa_span_plan_kernel(const __grid_constant__ SpanBwdParams p) {
   __shared__ long long work_of[32];
   __shared__ int runs_of[32], cut_of[32], slots_of[32];

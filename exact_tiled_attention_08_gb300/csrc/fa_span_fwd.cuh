@@ -16,9 +16,11 @@
 // running maximum stays (from the first to the last it rises in every block: H=32/8 N=8192
 // d=128, two requests, causal, with slopes, 1022 and 951 us).
 //
-// Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 701 us, 1568 TFLOP/s, with slopes 743 us,
-// with a window of 1024 237 us; one request capped 479 us; 2048 new tokens of two requests over 2000 and 16000
-// in pages 457 us, 1472 TFLOP/s.  The softmax warps bound it (tensor cores 56 % busy, DRAM idle).
+// Measured on a GB300 (two requests, H=32/8 N=8192 d=128, causal): 703 us, 1565 TFLOP/s, with slopes 742 us,
+// with a window of 1024 237 us; one request capped at 50 479 us, at 20 (where blocks on the diagonal take the
+// exponential) 528 us; 2048 new tokens of two requests over 2000 and 16000 in pages of 64 457 us, 1470 TFLOP/s.
+// These are loops over the same tensors; with others from call to call the last takes 487 us, 1380 TFLOP/s.
+// The softmax warps bound it (tensor cores 56 % busy, DRAM idle).
 //
 // Scores.  Blocks that some row sees in part are masked by the row's own span; the cap
 // (MOD 2 and 3) and the bias (MOD 1 and 3) change the scores in registers, before the maximum.

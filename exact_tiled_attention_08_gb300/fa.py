@@ -627,8 +627,8 @@ def fa_span_fwd(q, k, v, key_begin, key_end, o, lse, workspace, scale: float, *,
                 cap: float = 0.0, slopes=None, stream=None) -> None:
     """Self-attention of q [B,H,N,d] over k, v [B,Hkv,N,d] in which query i sees the keys
     key_begin[b,i] <= j < key_end[b,i] (int32 [B,N] or None: 0 and N), j <= i (causal)
-    and |i - j| < window (0: any); scores cap tanh(scale q.k / cap) (0: no cap) minus
-    slopes[h] |i - j| (fp32 [H] or None); o like q, lse [B,H,N] fp32."""
+    and |i - j| < window (0: any); scores cap tanh(scale q.k / cap) (0: no cap, at most
+    16384) minus slopes[h] |i - j| (fp32 [H] or None); o like q, lse [B,H,N] fp32."""
     B, H, Hkv, N, d = _span_sizes(q, k)
     dev, bf, rows, keys = q.device, torch.bfloat16, (B, H, N, d), (B, Hkv, N, d)
     _call("fa_span_fwd", dev, stream, _ptr(q, "q", bf, rows, dev), _ptr(k, "k", bf, keys, dev),

@@ -426,7 +426,8 @@ fa_status fa_span_fwd(const void* q, const void* k, const void* v, const int* ke
  * Q, K, V and dO meet products with weight 0 where a pair is not seen: an infinity
  * or NaN in any row of them may make any gradient of its request NaN.
  * dQ is summed with fp32 atomics, so it is not bitwise repeatable from run to
- * run; dK and dV are.
+ * run; dK and dV are.  With spans by row one thread block plans the work, in a time
+ * that grows with the square of N (0.13 ms at N = 131072, 1.8 ms at 524288).
  */
 size_t fa_span_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d);
 fa_status fa_span_bwd(const void* q, const void* k, const void* v, const int* key_begin, const int* key_end,
