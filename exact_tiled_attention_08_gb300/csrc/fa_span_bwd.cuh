@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(512, 1)
         if (MOD >= 2 && __builtin_expect(cut, 0)) {
           span_bwd_hide_p(tS + 64 * grp, seen);
           // (Without a bias 2^(-cap - LSE) is at most 1, and times 1 - tanh^2 = 0.  With one a hidden key may be
-          // so much nearer than those that the row sees that it is infinite.)
+          // so much nearer than those that the row sees (farther, if the slope is negative) that it is infinite.)
           if constexpr (MOD == 3) {
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch)

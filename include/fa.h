@@ -491,7 +491,7 @@ fa_status fa_paged_fwd(const void* q, const fa_pages* k_pages, const fa_pages* v
  *   positions    in:  int32 [B][N], or null: cache_lens[b] + n
  *   page_table, cache_lens, chunk_lens  as for fa_paged_fwd; page_table and
  *                cache_lens may be null where k and v are left out (cache_lens
- *                then counts as 0)
+ *                then counts as 0); no capacity bounds the new tokens there
  *   k_pages, v_pages  out: pages whose rows share no memory.  Rows of positions
  *                outside [0, C) and of pages outside [0, num_pages) are not
  *                written; rows of tokens >= the request's number of new ones are
